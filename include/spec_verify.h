@@ -366,6 +366,139 @@ int spec_page_pool_release(spec_page_pool* pool, int b, int slots);
 const int32_t* spec_page_pool_table(const spec_page_pool* pool);
 int spec_page_pool_free_pages(const spec_page_pool* pool);
 
+/* ------------------------------------------------------------ 8-bit paged KV */
+/* A paged cache in 8 bits: half the bytes that a verification's attention
+ * reads and twice the contexts that fit.  Pages, table and lengths as in
+ * spec_paged_kv_cache (the host page pool serves both); a cached value is
+ * code x scale:
+ *   k, v              e4m3 codes [n_layers][n_pages][n_kv_heads][64][head_dim]
+ *                     (spec_kv8_bytes each), 16-byte aligned;
+ *   k_scale, v_scale  fp32 [n_layers][n_pages][n_kv_heads][64 / SPEC_KV8_BLOCK]
+ *                     (spec_kv8_scale_bytes each), 16-byte aligned: one power
+ *                     of two in [2^-40, 2^40] per block of SPEC_KV8_BLOCK slots
+ *                     and KV head.
+ * The scale of a block is the smallest such power s with |x| <= 448 s for the
+ * finite values of its rows (2^-40 where all are zero); larger values and
+ * infinities are held as +-448 s, NaN as NaN.  The scales of blocks that hold
+ * no row below len[b] are not read.  Limits: max_pages * 64 <= 2^20 slots, n_pages *
+ * n_kv_heads * 64 < 2^31, batch <= 65535.  Every call below takes any
+ * workspace of this library as d_ws (its status word is used) and works on
+ * the current device; `cfg` gives the layer count and the head shape.
+ * Two sequences may share pages that neither appends to (a common prefix); a
+ * page that receives rows belongs to one sequence alone.
+ *
+ * One pass: for each layer spec_kv8_append then spec_kv8_attention, both at
+ * the lengths before the pass; then spec_kv8_advance, the accept, and
+ * spec_kv8_truncate or spec_kv8_tree_commit.  spec_verify_forward_kv8 is a
+ * whole pass including the advance. */
+#define SPEC_KV8_BLOCK 16
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int32_t* len;
+  const int32_t* table;
+  int batch;
+  int n_pages;
+  int max_pages;
+} spec_kv8_cache;
+
+/* Bytes of the k codes (and of v) and of the k scales (and of v). */
+size_t spec_kv8_bytes(const spec_model_config* cfg, int n_pages);
+size_t spec_kv8_scale_bytes(const spec_model_config* cfg, int n_pages);
+
+/* A rotary embedding: the first rotary_dim of a head's dimensions (a multiple
+ * of 4, at most head_dim; the others pass through) in pairs, (i, i +
+ * rotary_dim/2) or, interleaved != 0, (2i, 2i + 1), turned by position *
+ * theta^(-2i/rotary_dim).  factor >= 1 scales the frequencies for contexts
+ * longer than trained: all divided by it (orig_len = 0), or by wavelength
+ * (orig_len > 0): kept where orig_len covers at least high_freq turns,
+ * divided where at most low_freq, mixed linearly between (high_freq >
+ * low_freq > 0). */
+typedef struct {
+  int rotary_dim;
+  int interleaved;
+  int orig_len;
+  double theta;
+  double factor;
+  double low_freq;
+  double high_freq;
+} spec_rope_config;
+
+/* Fill the caller's d_table (fp32 [rotary_dim/2][2], 8-byte aligned) with the frequencies
+ * that spec_kv8_append reads: made once per embedding. */
+int spec_rope_table(const spec_rope_config* rope, float* d_table, void* stream);
+
+/* Rotate the new tokens' q and k and append k and v to one layer's pages.
+ *   d_q, d_k, d_v  rows of token b*n + j, heads side by side; bf16, or fp32
+ *             with is_f32 != 0; rows q_ld / k_ld / v_ld elements apart (parts
+ *             of one projection's output, say); base and row distance
+ *             16-byte aligned.
+ *   d_depth   int32 [batch][n] position offsets (a draft tree's depths), or
+ *             NULL: token j is at position len[b] + j.
+ *   d_q_out   bf16 [batch*n][n_heads*head_dim]: q rotated, rounded once.
+ * Token j's rows go to slot len[b] + j; len is not changed.  A block that
+ * already holds rows keeps the larger of its scale and the one its new rows
+ * need; when it grows, the rows held are re-rounded at it.  A sequence whose
+ * slots pass the capacity or lie on a page id outside the pool sets
+ * SPEC_DEV_KV_OVERFLOW / SPEC_DEV_BAD_PAGE and gets nothing written to the
+ * cache (its q_out is unspecified).  1 <= n <= 128. */
+int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
+                    const void* d_q, int64_t q_ld, const void* d_k, int64_t k_ld, const void* d_v,
+                    int64_t v_ld, int is_f32, const int32_t* d_depth,
+                    const spec_rope_config* rope, const float* d_table, uint16_t* d_q_out,
+                    void* d_ws, void* stream);
+
+/* Attention of the n new tokens of each sequence over slots [0, len[b] + n) of
+ * one layer: o = softmax(scale * q k^T) v per head, query heads sharing KV
+ * heads in order (n_heads / n_kv_heads each).
+ *   d_q    bf16 rows (spec_kv8_append's d_q_out), q_ld elements apart;
+ *   d_o    bf16 rows, o_ld elements apart; both 16-byte aligned;
+ *   d_anc  uint64 [batch][n] ancestor masks (spec_tree_masks; n <= 64), or
+ *          NULL: token j sees the cached slots and new slots 0 .. j.
+ *   scale  > 0, or 0 for 1/sqrt(head_dim).
+ * Scores, softmax and sums are in fp32 or finer; q as given, each weight
+ * p within 2^-11 of its value.  A row that sees no slot (a mask without its own bit, an
+ * empty cache) is zero.  Slots at or past len[b] + n and slots a row does not
+ * see have no influence, whatever they hold; a NaN code that it sees makes
+ * the row's affected outputs NaN, an infinite or NaN q its whole row.  A
+ * sequence that does not fit (as in spec_kv8_append) gets zero rows and a
+ * status bit; a page id outside the pool below len[b] sets SPEC_DEV_BAD_PAGE
+ * and leaves its rows unspecified. */
+int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
+                       const uint16_t* d_q, int64_t q_ld, const uint64_t* d_anc, float scale,
+                       uint16_t* d_o, int64_t o_ld, void* d_ws, void* stream);
+
+/* len[b] += n after the layers of a pass; a sequence that does not fit, or
+ * with a page id outside the pool in [0, len[b] + n), is left and flagged. */
+int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream);
+
+/* Rollback as spec_paged_kv_truncate. */
+int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws,
+                      void* stream);
+
+/* The draft-tree round's commit as spec_kv_tree_commit, on the 8-bit cache
+ * (len[b] includes the n_nodes slots): the accepted rows move together in
+ * every layer and len[b] = L0 + 1 + m.  A destination block takes the largest
+ * scale among the blocks its rows come from, and its own if it holds rows up
+ * to the root; rows are re-rounded where that is larger than theirs. */
+int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv,
+                         const int32_t* d_path, const int32_t* d_n_accepted, int n_nodes,
+                         void* d_ws, void* stream);
+
+/* spec_verify_forward on the 8-bit cache (chain: d_anc and d_depth NULL; tree:
+ * both, n <= 64 nodes), n new tokens per sequence.  The per-step schedule of
+ * spec_verify_forward_paged with spec_kv8_append and spec_kv8_attention in
+ * each layer (q rounded once to bf16; the model's own rotary table).
+ * Limits as spec_verify_forward but for the capacity, which is the cache's.
+ * Workspace: spec_kv8_workspace_bytes(cfg, batch, n). */
+size_t spec_kv8_workspace_bytes(const spec_model_config* cfg, int batch, int n);
+int spec_verify_forward_kv8(const spec_model* model, const int32_t* d_tokens,
+                            const uint64_t* d_anc, const int32_t* d_depth, int batch, int n,
+                            const spec_kv8_cache* kv, float* d_logits, void* d_ws,
+                            size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ draft trees */
 /* Verification of a draft TREE instead of a chain ([aci] Tree-Based Drafting;
  * [engine] Speculation Depth Tuning and Tree Drafting): several candidates

@@ -52,6 +52,19 @@ class spec_paged_kv_cache(ctypes.Structure):
 
 
 PAGE_SLOTS = 64
+KV8_BLOCK = 16
+class spec_kv8_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("len", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("batch", ctypes.c_int), ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class spec_rope_config(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("orig_len", ctypes.c_int),
+                ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_freq", ctypes.c_double),
+                ("high_freq", ctypes.c_double)]
+
+
 _LIB = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
@@ -87,6 +100,20 @@ _SIGS = {
     "spec_page_pool_release": (_I, [_P, _I, _I]),
     "spec_page_pool_table": (ctypes.POINTER(ctypes.c_int32), [_P]),
     "spec_page_pool_free_pages": (_I, [_P]),
+    "spec_kv8_bytes": (_SZ, [ctypes.POINTER(spec_model_config), _I]),
+    "spec_kv8_scale_bytes": (_SZ, [ctypes.POINTER(spec_model_config), _I]),
+    "spec_rope_table": (_I, [ctypes.POINTER(spec_rope_config), _P, _P]),
+    "spec_kv8_append": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_kv8_cache), _I, _I,
+                             _P, ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _I, _P,
+                             ctypes.POINTER(spec_rope_config), _P, _P, _P, _P]),
+    "spec_kv8_attention": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_kv8_cache), _I, _I,
+                                _P, ctypes.c_int64, _P, _F, _P, ctypes.c_int64, _P, _P]),
+    "spec_kv8_advance": (_I, [ctypes.POINTER(spec_kv8_cache), _I, _P, _P]),
+    "spec_kv8_truncate": (_I, [ctypes.POINTER(spec_kv8_cache), _P, _I, _P, _P]),
+    "spec_kv8_tree_commit": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_kv8_cache), _P, _P,
+                                  _I, _P, _P]),
+    "spec_kv8_workspace_bytes": (_SZ, [ctypes.POINTER(spec_model_config), _I, _I]),
+    "spec_verify_forward_kv8": (_I, [_P, _P, _P, _P, _I, _I, ctypes.POINTER(spec_kv8_cache), _P, _P, _SZ, _P]),
     "spec_gamma_ctl_create": (_I, [_I, _I, _I, _I, _I, _I, ctypes.c_double, ctypes.c_double,
                                    ctypes.c_double, ctypes.POINTER(_P)]),
     "spec_gamma_ctl_destroy": (_I, [_P]),
@@ -332,6 +359,152 @@ def spec_verify_forward_paged(handle: int, tokens, batch: int, gamma: int, kv: "
 def spec_paged_kv_truncate(kv: "PagedKVCache", n_accepted, gamma: int, ws, stream=None):
     _check(lib().spec_paged_kv_truncate(ctypes.byref(kv.c()), _ptr(n_accepted), gamma, _ptr(ws),
                                         _stream(stream)), "spec_paged_kv_truncate")
+
+
+class KV8Cache:
+    """8-bit paged target cache: k, v e4m3 [layers][n_pages][Hkv][64][hd] with
+    power-of-two scales fp32 [layers][n_pages][Hkv][4] (one per 16 slots), len
+    int32 [B], the device page table int32 [B][max_pages], and a host page
+    pool as in PagedKVCache."""
+
+    def __init__(self, cfg: ModelConfig, batch: int, n_pages: int, max_pages: int, device="cuda"):
+        self.cfg, self.batch, self.n_pages, self.max_pages = cfg, batch, n_pages, max_pages
+        shape = (cfg.n_layers, n_pages, cfg.n_kv_heads, PAGE_SLOTS, cfg.head_dim)
+        self.k = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.v = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        self.k_scale = torch.ones(shape[:3] + (PAGE_SLOTS // KV8_BLOCK,), dtype=torch.float32, device=device)
+        self.v_scale = torch.ones_like(self.k_scale)
+        assert self.k.numel() == int(lib().spec_kv8_bytes(ctypes.byref(cfg.c()), n_pages))
+        self.len = torch.zeros(batch, dtype=torch.int32, device=device)
+        self.table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
+        self.pool = None
+        h = ctypes.c_void_p()
+        _check(lib().spec_page_pool_create(n_pages, batch, max_pages, ctypes.byref(h)),
+               "spec_page_pool_create")
+        self.pool = h.value
+
+    capacity = PagedKVCache.capacity
+    reserve = PagedKVCache.reserve
+    release = PagedKVCache.release
+    host_table = PagedKVCache.host_table
+    free_pages = PagedKVCache.free_pages
+    sync = PagedKVCache.sync
+    close = PagedKVCache.close
+    __del__ = PagedKVCache.__del__
+
+    def c(self) -> spec_kv8_cache:
+        return spec_kv8_cache(*(_ptr(t) for t in (self.k, self.v, self.k_scale, self.v_scale, self.len,
+                                                  self.table)), self.batch, self.n_pages, self.max_pages)
+
+
+class RopeTable:
+    """A rotary embedding's description and its device frequency table
+    (spec_rope_table), made once and passed to every spec_kv8_append."""
+
+    def __init__(self, rotary_dim: int, theta: float, interleaved: bool = False, factor: float = 1.0,
+                 low_freq: float = 1.0, high_freq: float = 4.0, orig_len: int = 0, device="cuda", stream=None):
+        self.config = spec_rope_config(rotary_dim, int(interleaved), orig_len, theta, factor, low_freq, high_freq)
+        self.table = torch.empty(max(rotary_dim, 0) // 2, 2, dtype=torch.float32, device=device)
+        with _on(self.table):
+            _check(lib().spec_rope_table(ctypes.byref(self.config), _ptr(self.table), _stream(stream)),
+                   "spec_rope_table")
+
+
+def _rows(t, rows: int, width: int, types, what: str):
+    """(address, elements between rows) of a 2-D CUDA tensor of whole rows."""
+    if not t.is_cuda or t.dtype not in types or t.shape != (rows, width) or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected a CUDA tensor {(rows, width)} of {types} with unit column stride")
+    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), width)
+
+
+def _plain(t, shape, dtype, what: str):
+    """Address of a contiguous CUDA tensor of this shape and type (None stays None)."""
+    if t is None:
+        return None
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError(f"{what}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
+    return _ptr(t)
+
+
+def _on(t):
+    """The device of tensor t as the current one: launches go to the caller's device."""
+    return torch.cuda.device(t.device)
+
+
+def _kv8_same(kv: "KV8Cache", *tensors):
+    """Every tensor of a call lives on the cache's device."""
+    for t in tensors:
+        if t is not None and t.device != kv.len.device:
+            raise ValueError(f"expected every tensor on {kv.len.device}, got one on {t.device}")
+
+
+def spec_kv8_append(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, k, v, rope: "RopeTable", q_out, ws,
+                    depth=None, stream=None):
+    """Rotate q and k of n new tokens per sequence, append k and v to `layer`'s pages, q to q_out (bf16)."""
+    m, hd = kv.batch * n, cfg.head_dim
+    _kv8_same(kv, q, k, v, rope.table, q_out, ws, depth)
+    types = (q.dtype,) if q.dtype in (torch.bfloat16, torch.float32) else (torch.bfloat16, torch.float32)
+    qp, q_ld = _rows(q, m, cfg.n_heads * hd, types, "q")
+    kp, k_ld = _rows(k, m, cfg.n_kv_heads * hd, types, "k")
+    vp, v_ld = _rows(v, m, cfg.n_kv_heads * hd, types, "v")
+    with _on(kv.len):
+        _check(lib().spec_kv8_append(
+            ctypes.byref(cfg.c()), ctypes.byref(kv.c()), layer, n, qp, q_ld, kp, k_ld, vp, v_ld,
+            int(q.dtype == torch.float32), _plain(depth, (kv.batch, n), torch.int32, "depth"),
+            ctypes.byref(rope.config), _ptr(rope.table),
+            _plain(q_out, (m, cfg.n_heads * hd), torch.bfloat16, "q_out"), _ptr(ws), _stream(stream)),
+            "spec_kv8_append")
+
+
+def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, out, ws, anc=None,
+                       scale: float = 0.0, stream=None):
+    """Attention of n new tokens per sequence (q, out bf16 rows) over `layer`'s pages."""
+    m, width = kv.batch * n, cfg.n_heads * cfg.head_dim
+    _kv8_same(kv, q, out, ws, anc)
+    qp, q_ld = _rows(q, m, width, (torch.bfloat16,), "q")
+    op, o_ld = _rows(out, m, width, (torch.bfloat16,), "out")
+    with _on(kv.len):
+        _check(lib().spec_kv8_attention(ctypes.byref(cfg.c()), ctypes.byref(kv.c()), layer, n, qp, q_ld,
+                                        _plain(anc, (kv.batch, n), torch.int64, "anc"), scale, op, o_ld, _ptr(ws),
+                                        _stream(stream)), "spec_kv8_attention")
+
+
+def spec_kv8_advance(kv: "KV8Cache", n: int, ws, stream=None):
+    _kv8_same(kv, ws)
+    with _on(kv.len):
+        _check(lib().spec_kv8_advance(ctypes.byref(kv.c()), n, _ptr(ws), _stream(stream)), "spec_kv8_advance")
+
+
+def spec_kv8_truncate(kv: "KV8Cache", n_accepted, gamma: int, ws, stream=None):
+    _kv8_same(kv, n_accepted, ws)
+    with _on(kv.len):
+        _check(lib().spec_kv8_truncate(ctypes.byref(kv.c()), _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"),
+                                       gamma, _ptr(ws), _stream(stream)), "spec_kv8_truncate")
+
+
+def spec_kv8_tree_commit(cfg: ModelConfig, kv: "KV8Cache", path, n_accepted, n_nodes: int, ws, stream=None):
+    """Move the accepted path's rows together in every layer and set the lengths."""
+    _kv8_same(kv, path, n_accepted, ws)
+    with _on(kv.len):
+        _check(lib().spec_kv8_tree_commit(
+            ctypes.byref(cfg.c()), ctypes.byref(kv.c()), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
+            _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), n_nodes, _ptr(ws), _stream(stream)),
+            "spec_kv8_tree_commit")
+
+
+def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
+    return int(lib().spec_kv8_workspace_bytes(ctypes.byref(cfg.c()), batch, n))
+
+
+def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cache", logits, ws, anc=None,
+                            depth=None, stream=None):
+    """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
+    _kv8_same(kv, tokens, logits, ws, anc, depth)
+    with _on(kv.len):
+        _check(lib().spec_verify_forward_kv8(
+            handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),
+            _plain(depth, (batch, n), torch.int32, "depth"), batch, n, ctypes.byref(kv.c()), _ptr(logits), _ptr(ws),
+            ws.numel(), _stream(stream)), "spec_verify_forward_kv8")
 
 
 class GammaController:

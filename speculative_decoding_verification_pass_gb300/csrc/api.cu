@@ -107,6 +107,8 @@ int mk_att_chunks_max(int pairs, int slot_chunks) {
 
 size_t align_up(size_t x, size_t a = kAlign) { return (x + a - 1) / a * a; }
 int round_up(int x, int a) { return (x + a - 1) / a * a; }
+// blocks of SPEC_KV8_BLOCK slots that n consecutive slots can touch
+int kv8_blocks(int n) { return (n + 2 * SPEC_KV8_BLOCK - 2) / SPEC_KV8_BLOCK; }
 
 bool cfg_ok(const spec_model_config* c) {
   if (!c) return false;
@@ -555,25 +557,34 @@ struct PageDesc {
   int max_pages = 0, n_pages = 0;
 };
 
+// An 8-bit paged cache of the pass (its pages in PageDesc); qkv is the fp32
+// projection output that spec_kv8_append's kernel reads.
+struct Kv8Desc {
+  uint8_t *k, *v;
+  float *k_scale, *v_scale;
+  float* qkv;
+};
+
 // The verification forward; d_anc / d_depth describe a draft tree per
 // sequence (nullptr: the chain, node j at position len + j seeing new slots
 // 0..j); pg the page table of a paged cache (kv->capacity = its logical
-// capacity).
+// capacity); k8 the 8-bit cache in kv's place (per-step schedule).
 static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, const uint64_t* d_anc,
                                const int32_t* d_depth, int batch, int gamma, const spec_kv_cache* kv,
                                float* d_logits, void* d_ws, size_t ws_bytes, void* stream,
-                               const PageDesc& pg = PageDesc{}) {
+                               const PageDesc& pg = PageDesc{}, const Kv8Desc* k8 = nullptr) {
   if (!m || !d_tokens || !kv || !d_logits || !d_ws) return SPEC_EINVAL;
   if (batch < 0 || gamma < 0) return SPEC_EINVAL;
   const spec_model_config& c = m->cfg;
   if (c.n_layers == 0) return SPEC_ENOTSUP;
   if (!kv->k || !kv->v || !kv->len) return SPEC_EINVAL;
   if (kv->batch != batch || kv->capacity <= 0) return SPEC_EINVAL;
-  if (kv->capacity > kAttnChunk * kAttnMaxChunks) return SPEC_ESIZE;
+  if (!k8 && kv->capacity > kAttnChunk * kAttnMaxChunks) return SPEC_ESIZE;
   const int n = gamma + 1;
   if (n > kMaxN || static_cast<long long>(batch) * n > kMaxM) return SPEC_ESIZE;
   if (batch == 0) return SPEC_OK;
-  const WsPlan P = plan_ws(c, batch, gamma, kv->capacity);
+  // the 8-bit cache's attention keeps its partials on the chip
+  const WsPlan P = plan_ws(c, batch, gamma, k8 ? 1 : kv->capacity);
   if (ws_bytes < P.total) return SPEC_ESIZE;
   if (reinterpret_cast<uintptr_t>(d_ws) % kAlign) return SPEC_EINVAL;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -603,7 +614,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
   {
     const int ntok = round_up(M, 16);
     const int fpt = d / 128;
-    const bool shape_ok = mk_enabled() && M <= 128 && P.R <= kMkAttRows && c.n_layers <= kMkMaxLayers &&
+    const bool shape_ok = !k8 && mk_enabled() && M <= 128 && P.R <= kMkAttRows && c.n_layers <= kMkMaxLayers &&
                           (fpt & (fpt - 1)) == 0 && fpt <= 128;
     // one CTA per SM with a deep ring (the ring also absorbs grid barriers)
     int stages = shape_ok ? forward_max_stages(ntok, hd, static_cast<size_t>(mk_smem_kb()) * 1024) : 0;
@@ -747,7 +758,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
   ep.d = d;
   ep.V = c.vocab;
   ep.cap = kv->capacity;
-  ep.kv_table = pg.table;
+  ep.kv_table = pg.table;  // checked for every slot of the pass, whichever cache it holds
   ep.kv_max_pages = pg.max_pages;
   ep.kv_n_pages = pg.n_pages;
   SPEC_CUDA(launch_embed(ep, st, pdl));
@@ -767,7 +778,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
   // decode shapes of head dim 128 past the persistent kernel (more than 128
   // token rows): the attention on the tensor cores, as launches of its own
   MkParams* tq = nullptr;
-  if (hd == 128 && P.R <= kMkAttRows && batch <= 128 && mk_att_tc_enabled()) {
+  if (!k8 && hd == 128 && P.R <= kMkAttRows && batch <= 128 && mk_att_tc_enabled()) {
     tq = new MkParams();
     MkParams& A = *tq;
     A.B = batch;
@@ -814,7 +825,74 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
   for (int l = 0; l < c.n_layers; ++l) {
     uint16_t* kc = static_cast<uint16_t*>(kv->k) + l * layer_kv;
     uint16_t* vc = static_cast<uint16_t*>(kv->v) + l * layer_kv;
-    {  // QKV projection: RMSNorm scale, RoPE, KV append
+    if (k8) {  // QKV projection to fp32, then rotation and append, then attention
+      GemmParams p = g0;
+      p.epi = EPI_STORE;
+      p.ssq_in = ssq;
+      p.out = k8->qkv;
+      p.ldo = m->qkv_rows;
+      int r = run_gemm(cx, &m->tm_qkv[l], hb, hb_lo, M, m->qkv_rows, d, p);
+      if (r) return r;
+      const size_t rows = static_cast<size_t>(pg.n_pages) * Hkv * SPEC_PAGE_SLOTS * l;
+      Kv8AppendParams a{};
+      a.q = k8->qkv;
+      a.k = k8->qkv + qd;
+      a.v = k8->qkv + qd + Hkv * hd;
+      a.q_ld = a.k_ld = a.v_ld = m->qkv_rows;
+      a.f32 = 1;
+      a.q_out = q;
+      a.kc = k8->k + rows * hd;
+      a.vc = k8->v + rows * hd;
+      a.ks = k8->k_scale + rows / SPEC_KV8_BLOCK;
+      a.vs = k8->v_scale + rows / SPEC_KV8_BLOCK;
+      a.base = pos_base;
+      a.seq_ok = seq_ok;
+      a.depth = d_depth;
+      a.table = pg.table;
+      a.rope = reinterpret_cast<const float2*>(B + L.rope);
+      a.status = status;
+      a.max_pages = pg.max_pages;
+      a.n_pages = pg.n_pages;
+      a.B = batch;
+      a.n = n;
+      a.H = H;
+      a.Hkv = Hkv;
+      a.hd = a.rd = hd;
+      a.nb = kv8_blocks(n);
+      SPEC_CUDA(launch_kv8_append(a, st));
+      Kv8AttnParams t{};
+      t.q = q;
+      t.o = o;
+      t.q_ld = t.o_ld = qd;
+      t.kc = a.kc;
+      t.vc = a.vc;
+      t.ks = a.ks;
+      t.vs = a.vs;
+      t.base = pos_base;
+      t.anc = d_anc;
+      t.table = pg.table;
+      t.status = status;
+      t.max_pages = pg.max_pages;
+      t.n_pages = pg.n_pages;
+      t.B = batch;
+      t.n = n;
+      t.H = H;
+      t.Hkv = Hkv;
+      t.hd = hd;
+      t.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
+      TimedLaunch tl{};
+      if (cx.timing) {
+        tl.a = take_event(const_cast<spec_model*>(m));
+        tl.b = take_event(const_cast<spec_model*>(m));
+        tl.kind = 1;
+        cudaEventRecord(tl.a, st);
+      }
+      SPEC_CUDA(launch_kv8_attention(t, st));
+      if (cx.timing) {
+        cudaEventRecord(tl.b, st);
+        const_cast<spec_model*>(m)->pending.push_back(tl);
+      }
+    } else {  // QKV projection: RMSNorm scale, RoPE, KV append
       GemmParams p = g0;
       p.epi = EPI_QKV;
       p.ssq_in = ssq;
@@ -837,7 +915,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
       int r = run_gemm(cx, &m->tm_qkv[l], hb, hb_lo, M, m->qkv_rows, d, p);
       if (r) return r;
     }
-    {  // attention over the cache
+    if (!k8) {  // attention over the cache
       AttnParams a{};
       a.q = q;
       a.q_lo = q_lo;
@@ -890,7 +968,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
       p.hb_lo = hb_lo;
       p.g_next = reinterpret_cast<const float*>(B + L.g_mlp[l]);
       p.ssq_out = ssq;
-      int r = run_gemm(cx, &m->tm_o[l], o, o_lo, M, d, qd, p);
+      int r = run_gemm(cx, &m->tm_o[l], o, k8 ? nullptr : o_lo, M, d, qd, p);
       if (r) return r;
     }
     {  // gate/up + SwiGLU
@@ -1328,6 +1406,229 @@ int spec_timing_read(spec_model* m, double ms[3], int64_t launches[3], double by
   }
   m->pending.clear();
   return SPEC_OK;
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------ 8-bit paged KV cache
+namespace {
+
+constexpr int kKv8MaxSlots = 1 << 20;
+
+// Shape and cache checks shared by the entry points of the 8-bit cache.
+int kv8_checks(const spec_model_config* c, const spec_kv8_cache* kv) {
+  if (!kv || !kv->len || !kv->table) return SPEC_EINVAL;
+  if (kv->batch < 0 || kv->n_pages <= 0 || kv->max_pages <= 0) return SPEC_EINVAL;
+  if (kv->batch > 65535 || kv->max_pages > kKv8MaxSlots / SPEC_PAGE_SLOTS) return SPEC_ESIZE;
+  if (!c) return SPEC_OK;
+  if (!cfg_ok(c) || c->n_layers == 0) return SPEC_EINVAL;
+  if (!kv->k || !kv->v || !kv->k_scale || !kv->v_scale) return SPEC_EINVAL;
+  for (const void* a : {static_cast<const void*>(kv->k), static_cast<const void*>(kv->v),
+                        static_cast<const void*>(kv->k_scale), static_cast<const void*>(kv->v_scale)})
+    if (reinterpret_cast<uintptr_t>(a) % 16) return SPEC_EINVAL;
+  // a layer's row coordinates are 32-bit
+  if (static_cast<long long>(kv->n_pages) * c->n_kv_heads * SPEC_PAGE_SLOTS >= (1ll << 31)) return SPEC_ESIZE;
+  return SPEC_OK;
+}
+
+// rows of `elem`-byte elements: base and row distance 16-byte aligned, rows apart
+bool rows_ok(const void* p, int64_t ld, int64_t width, int elem) {
+  return p && reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld >= width && ld <= (1ll << 40) && ld * elem % 16 == 0;
+}
+
+bool rope_ok(const spec_rope_config* r) {
+  if (!r || r->rotary_dim < 4 || r->rotary_dim % 4 || r->rotary_dim > 128 || r->orig_len < 0) return false;
+  if (!(r->theta > 1.0) || std::isinf(r->theta) || !(r->factor >= 1.0) || std::isinf(r->factor)) return false;
+  return r->orig_len == 0 || (r->low_freq > 0.0 && r->high_freq > r->low_freq && !std::isinf(r->high_freq));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_kv8_bytes(const spec_model_config* cfg, int n_pages) { return spec_paged_kv_bytes(cfg, n_pages) / 2; }
+
+size_t spec_kv8_scale_bytes(const spec_model_config* cfg, int n_pages) {
+  if (!cfg_ok(cfg) || n_pages < 0) return 0;
+  return static_cast<size_t>(cfg->n_layers) * n_pages * (cfg->n_layers ? cfg->n_kv_heads : 0) *
+         (SPEC_PAGE_SLOTS / SPEC_KV8_BLOCK) * sizeof(float);
+}
+
+int spec_rope_table(const spec_rope_config* rope, float* d_table, void* stream) {
+  if (!d_table || reinterpret_cast<uintptr_t>(d_table) % 8 || !rope_ok(rope)) return SPEC_EINVAL;
+  SPEC_CUDA(launch_kv8_rope(reinterpret_cast<float2*>(d_table), rope->rotary_dim, rope->theta, rope->factor,
+                            rope->low_freq, rope->high_freq, rope->orig_len, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n, const void* d_q,
+                    int64_t q_ld, const void* d_k, int64_t k_ld, const void* d_v, int64_t v_ld, int is_f32,
+                    const int32_t* d_depth, const spec_rope_config* rope, const float* d_table, uint16_t* d_q_out,
+                    void* d_ws, void* stream) {
+  if (!cfg || !d_table || !d_q_out || !d_ws) return SPEC_EINVAL;
+  if (const int r = kv8_checks(cfg, kv)) return r;
+  const int hd = cfg->d_model / cfg->n_heads, elem = is_f32 ? 4 : 2;
+  if (layer < 0 || layer >= cfg->n_layers || n < 1) return SPEC_EINVAL;
+  if (!rope_ok(rope) || rope->rotary_dim > hd) return SPEC_EINVAL;
+  if (!rows_ok(d_q, q_ld, static_cast<int64_t>(cfg->n_heads) * hd, elem) ||
+      !rows_ok(d_k, k_ld, static_cast<int64_t>(cfg->n_kv_heads) * hd, elem) ||
+      !rows_ok(d_v, v_ld, static_cast<int64_t>(cfg->n_kv_heads) * hd, elem) ||
+      reinterpret_cast<uintptr_t>(d_q_out) % 16 || reinterpret_cast<uintptr_t>(d_table) % 8)
+    return SPEC_EINVAL;
+  if (n > kMaxN) return SPEC_ESIZE;
+  if (kv->batch == 0) return SPEC_OK;
+  const size_t rows = static_cast<size_t>(kv->n_pages) * cfg->n_kv_heads * SPEC_PAGE_SLOTS * layer;
+  Kv8AppendParams p{};
+  p.q = d_q;
+  p.k = d_k;
+  p.v = d_v;
+  p.q_ld = q_ld;
+  p.k_ld = k_ld;
+  p.v_ld = v_ld;
+  p.f32 = is_f32 ? 1 : 0;
+  p.q_out = d_q_out;
+  p.kc = static_cast<uint8_t*>(kv->k) + rows * hd;
+  p.vc = static_cast<uint8_t*>(kv->v) + rows * hd;
+  p.ks = kv->k_scale + rows / SPEC_KV8_BLOCK;
+  p.vs = kv->v_scale + rows / SPEC_KV8_BLOCK;
+  p.base = kv->len;
+  p.depth = d_depth;
+  p.table = kv->table;
+  p.rope = reinterpret_cast<const float2*>(d_table);
+  p.status = static_cast<int32_t*>(d_ws);
+  p.max_pages = kv->max_pages;
+  p.n_pages = kv->n_pages;
+  p.B = kv->batch;
+  p.n = n;
+  p.H = cfg->n_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.hd = hd;
+  p.rd = rope->rotary_dim;
+  p.inter = rope->interleaved ? 1 : 0;
+  p.nb = kv8_blocks(n);
+  SPEC_CUDA(launch_kv8_append(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n, const uint16_t* d_q,
+                       int64_t q_ld, const uint64_t* d_anc, float scale, uint16_t* d_o, int64_t o_ld, void* d_ws,
+                       void* stream) {
+  if (!cfg || !d_ws) return SPEC_EINVAL;
+  if (const int r = kv8_checks(cfg, kv)) return r;
+  const int hd = cfg->d_model / cfg->n_heads;
+  const int64_t width = static_cast<int64_t>(cfg->n_heads) * hd;
+  if (layer < 0 || layer >= cfg->n_layers || n < 1) return SPEC_EINVAL;
+  if (!rows_ok(d_q, q_ld, width, 2) || !rows_ok(d_o, o_ld, width, 2)) return SPEC_EINVAL;
+  if (!(scale >= 0.f) || std::isinf(scale)) return SPEC_EINVAL;
+  if (n > (d_anc ? kTreeMaxNodes : kMaxN)) return SPEC_ESIZE;
+  if (kv->batch == 0) return SPEC_OK;
+  const size_t rows = static_cast<size_t>(kv->n_pages) * cfg->n_kv_heads * SPEC_PAGE_SLOTS * layer;
+  Kv8AttnParams p{};
+  p.q = d_q;
+  p.o = d_o;
+  p.q_ld = q_ld;
+  p.o_ld = o_ld;
+  p.kc = static_cast<const uint8_t*>(kv->k) + rows * hd;
+  p.vc = static_cast<const uint8_t*>(kv->v) + rows * hd;
+  p.ks = kv->k_scale + rows / SPEC_KV8_BLOCK;
+  p.vs = kv->v_scale + rows / SPEC_KV8_BLOCK;
+  p.base = kv->len;
+  p.anc = d_anc;
+  p.table = kv->table;
+  p.status = static_cast<int32_t*>(d_ws);
+  p.max_pages = kv->max_pages;
+  p.n_pages = kv->n_pages;
+  p.B = kv->batch;
+  p.n = n;
+  p.H = cfg->n_heads;
+  p.Hkv = cfg->n_kv_heads;
+  p.hd = hd;
+  p.scale_log2 =
+      static_cast<float>(1.4426950408889634 * (scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(hd))));
+  SPEC_CUDA(launch_kv8_attention(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) {
+  if (!d_ws || n < 1) return SPEC_EINVAL;
+  if (const int r = kv8_checks(nullptr, kv)) return r;
+  if (n > kMaxN) return SPEC_ESIZE;
+  if (kv->batch == 0) return SPEC_OK;
+  SPEC_CUDA(launch_kv8_advance(kv->len, kv->table, kv->batch, n, kv->max_pages, kv->n_pages,
+                               static_cast<int32_t*>(d_ws), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws, void* stream) {
+  if (const int r = kv8_checks(nullptr, kv)) return r;
+  spec_kv_cache view{};
+  view.len = kv->len;
+  view.batch = kv->batch;
+  return spec_kv_truncate(&view, d_n_accepted, gamma, d_ws, stream);
+}
+
+int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv, const int32_t* d_path,
+                         const int32_t* d_n_accepted, int n_nodes, void* d_ws, void* stream) {
+  if (!cfg || !d_path || !d_n_accepted || !d_ws || n_nodes < 1) return SPEC_EINVAL;
+  if (const int r = kv8_checks(cfg, kv)) return r;
+  if (n_nodes > kTreeMaxNodes || cfg->n_layers > 65535) return SPEC_ESIZE;
+  if (kv->batch == 0) return SPEC_OK;
+  Kv8CommitParams p{};
+  p.kc = static_cast<uint8_t*>(kv->k);
+  p.vc = static_cast<uint8_t*>(kv->v);
+  p.ks = kv->k_scale;
+  p.vs = kv->v_scale;
+  p.len = kv->len;
+  p.path = d_path;
+  p.n_acc = d_n_accepted;
+  p.table = kv->table;
+  p.status = static_cast<int32_t*>(d_ws);
+  p.max_pages = kv->max_pages;
+  p.n_pages = kv->n_pages;
+  p.L = cfg->n_layers;
+  p.B = kv->batch;
+  p.Hkv = cfg->n_kv_heads;
+  p.hd = cfg->d_model / cfg->n_heads;
+  p.n = n_nodes;
+  SPEC_CUDA(launch_kv8_commit(p, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+size_t spec_kv8_workspace_bytes(const spec_model_config* cfg, int batch, int n) {
+  if (!cfg_ok(cfg) || cfg->n_layers == 0 || batch < 0 || n < 1) return 0;
+  const size_t hd = cfg->d_model / cfg->n_heads;
+  const size_t qkv = static_cast<size_t>(batch) * n * (cfg->n_heads + 2 * cfg->n_kv_heads) * hd * sizeof(float);
+  return plan_ws(*cfg, batch, n - 1, 1).total + align_up(qkv);
+}
+
+int spec_verify_forward_kv8(const spec_model* m, const int32_t* d_tokens, const uint64_t* d_anc,
+                            const int32_t* d_depth, int batch, int n, const spec_kv8_cache* kv, float* d_logits,
+                            void* d_ws, size_t ws_bytes, void* stream) {
+  if (!m || !d_ws || n < 1 || (d_anc == nullptr) != (d_depth == nullptr)) return SPEC_EINVAL;
+  if (m->cfg.n_layers == 0) return SPEC_ENOTSUP;
+  if (const int r = kv8_checks(&m->cfg, kv)) return r;
+  if (batch < 0 || kv->batch != batch) return SPEC_EINVAL;
+  if (n > (d_anc ? kTreeMaxNodes : kMaxN) || static_cast<long long>(batch) * n > kMaxM) return SPEC_ESIZE;
+  if (batch == 0) return SPEC_OK;
+  if (ws_bytes < spec_kv8_workspace_bytes(&m->cfg, batch, n)) return SPEC_ESIZE;
+  spec_kv_cache view{};
+  view.k = kv->k;
+  view.v = kv->v;
+  view.len = kv->len;
+  view.batch = batch;
+  view.capacity = kv->max_pages * SPEC_PAGE_SLOTS;
+  PageDesc pg;
+  pg.table = kv->table;
+  pg.max_pages = kv->max_pages;
+  pg.n_pages = kv->n_pages;
+  Kv8Desc k8{};
+  k8.k = static_cast<uint8_t*>(kv->k);
+  k8.v = static_cast<uint8_t*>(kv->v);
+  k8.k_scale = kv->k_scale;
+  k8.v_scale = kv->v_scale;
+  k8.qkv = reinterpret_cast<float*>(static_cast<uint8_t*>(d_ws) + plan_ws(m->cfg, batch, n - 1, 1).total);
+  return verify_forward_impl(m, d_tokens, d_anc, d_depth, batch, n - 1, &view, d_logits, d_ws, ws_bytes, stream, pg,
+                             &k8);
 }
 
 }  // extern "C"

@@ -298,4 +298,54 @@ struct TreeCommitParams {
 };
 cudaError_t launch_tree_commit(const TreeCommitParams& p, cudaStream_t stream);
 
+// ------------------------------------------------------ 8-bit paged KV cache
+struct Kv8AppendParams {
+  const void *q, *k, *v;      // rows of a token's heads, bf16 or fp32 (f32)
+  long long q_ld, k_ld, v_ld; // elements between two tokens' rows
+  int f32;
+  uint16_t* q_out;            // [B*n][H*hd] bf16
+  uint8_t *kc, *vc;           // this layer's codes [n_pages][Hkv][64][hd]
+  float *ks, *vs;             // this layer's scales [n_pages][Hkv][4]
+  const int32_t* base;        // [B] slots held before the new ones
+  const int32_t* seq_ok;      // [B] 0: leave the sequence alone, or nullptr
+  const int32_t* depth;       // [B][n] rotary position offsets, or nullptr (0 .. n-1)
+  const int32_t* table;       // [B][max_pages]
+  const float2* rope;         // [rd/2] turns per position (hi, lo)
+  int32_t* status;
+  int max_pages, n_pages, B, n, H, Hkv, hd, rd, inter;
+  int nb;                     // blocks that n slots can touch
+};
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream);
+
+struct Kv8AttnParams {
+  const uint16_t* q;          // [B*n] rows of H*hd bf16, q_ld apart
+  uint16_t* o;
+  long long q_ld, o_ld;
+  const uint8_t *kc, *vc;     // this layer's codes
+  const float *ks, *vs;       // this layer's scales
+  const int32_t* base;        // [B] slots before the new ones
+  const uint64_t* anc;        // [B][n] ancestor masks, or nullptr (chain)
+  const int32_t* table;
+  int32_t* status;
+  int max_pages, n_pages, B, n, H, Hkv, hd;
+  float scale_log2;           // log2(e) * the score scale
+};
+cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream);
+
+struct Kv8CommitParams {
+  uint8_t *kc, *vc;           // all layers
+  float *ks, *vs;
+  int32_t* len;
+  const int32_t* path;        // [B][n]
+  const int32_t* n_acc;       // [B]
+  const int32_t* table;
+  int32_t* status;
+  int max_pages, n_pages, L, B, Hkv, hd, n;
+};
+cudaError_t launch_kv8_commit(const Kv8CommitParams& p, cudaStream_t stream);
+cudaError_t launch_kv8_advance(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,
+                               int32_t* status, cudaStream_t stream);
+cudaError_t launch_kv8_rope(float2* dst, int rd, double theta, double factor, double low, double high, int orig_len,
+                            cudaStream_t stream);
+
 }  // namespace spec

@@ -1,0 +1,402 @@
+// The 8-bit paged KV cache: append with rotation, draft-tree commit and
+// length updates.  (Attention over it is in kv8_attention.cu.)
+#include "internal.h"
+#include "kv8_common.cuh"
+
+namespace spec {
+namespace {
+
+// ------------------------------------------------------------------ rotary
+// Frequency of pair i in turns per position, split as hi + lo floats:
+//   f = theta^(-2i / rd) / 2 pi
+// scaled for long contexts by `factor`: every frequency divided by it
+// (orig_len = 0), or, by wavelength, kept where orig_len * f >= high_freq
+// turns, divided where <= low_freq, and mixed linearly between.
+__global__ void kv8_rope_kernel(float2* dst, int rd, double theta, double factor, double low, double high,
+                                int orig_len) {
+  const int i = blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= rd / 2) return;
+  const double two_pi = 6.283185307179586;
+  double f = pow(theta, -2.0 * i / rd) / two_pi;
+  if (factor != 1.0) {
+    double w = 0.0;
+    if (orig_len > 0) {
+      w = (orig_len * f - low) / (high - low);
+      w = w < 0.0 ? 0.0 : (w > 1.0 ? 1.0 : w);
+    }
+    f = f * w + f / factor * (1.0 - w);
+  }
+  const float hi = static_cast<float>(f);
+  dst[i] = make_float2(hi, static_cast<float>(f - static_cast<double>(hi)));
+}
+
+// ------------------------------------------------------------------ append
+// One warp per unit.  A q unit is one token and a few of its heads; a k or v
+// unit is one block of 16 slots of one (sequence, KV head), so that the
+// warp alone sees every row that the block's scale depends on:
+//   s = max over the block's new rows of the smallest 2^e with |x| <= 448 2^e
+//   (and the scale it has, if it holds rows from before),
+//   code = e4m3(x / s); rows held before are re-rounded when s has grown.
+// A row is spread over hd / 4 lanes, each with two rotary pairs (p, p + 1), so
+// the rotation needs no exchange: half layout dims (p, p + 1) and
+// (p + rd/2, p + 1 + rd/2), interleaved layout or unrotated dims 2p .. 2p + 3.
+constexpr int kAppThreads = 128;
+constexpr int kAppHeads = 4;  // head rows per lane of a q unit
+
+SPEC_DEVINL float2 load2(const void* p, long long i, int f32) {
+  if (f32) return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + i));
+  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i));
+  return make_float2(bf16lo(w), bf16hi(w));
+}
+
+// Sine and cosine of pos turns x (fr.x + fr.y): pos * fr.x = t + its rounding
+// error exactly (fma), whole turns leave exactly, and the half-turn functions
+// take the reduced angle within 2 ulps, so that a rotated value is off by
+// little more than its own fp32 rounding at any position.  (A code is a
+// rounding to 4 bits: a coarser angle moves values over its borders.)
+SPEC_DEVINL void kv8_sincos(int pos, float2 fr, float* sn, float* cs) {
+  const float fp = static_cast<float>(pos);
+  const float t = fp * fr.x;
+  const float terr = fmaf(fp, fr.x, -t) + fp * fr.y;
+  sincospif(2.f * ((t - rintf(t)) + terr), sn, cs);
+}
+
+// bf16 bits of a value that may be infinite or NaN.
+SPEC_DEVINL uint32_t bf16_any(float x) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(x));
+  return r & 0xFFFFu;
+}
+
+struct Pair4 {  // dims d0, d0 + 1 and d1, d1 + 1 of one row
+  int d0, d1;
+  bool rot, inter;
+  int i0;  // first pair's frequency index
+};
+SPEC_DEVINL Pair4 pair4(int li, int rd, int inter) {
+  Pair4 q;
+  q.i0 = 2 * li;
+  q.rot = q.i0 < rd / 2;
+  q.inter = inter || !q.rot;
+  q.d0 = q.inter ? 4 * li : 2 * li;
+  q.d1 = q.inter ? q.d0 + 2 : q.d0 + rd / 2;
+  return q;
+}
+SPEC_DEVINL void rotate4(const Pair4& q, float (&x)[4], const float (&c)[2], const float (&s)[2]) {
+  if (!q.rot) return;
+  if (q.inter) {  // pairs (x0, x1), (x2, x3)
+    const float a0 = x[0], a1 = x[2];
+    x[0] = a0 * c[0] - x[1] * s[0];
+    x[1] = x[1] * c[0] + a0 * s[0];
+    x[2] = a1 * c[1] - x[3] * s[1];
+    x[3] = x[3] * c[1] + a1 * s[1];
+  } else {  // pairs (x0, x2), (x1, x3)
+    const float a0 = x[0], a1 = x[1];
+    x[0] = a0 * c[0] - x[2] * s[0];
+    x[2] = x[2] * c[0] + a0 * s[0];
+    x[1] = a1 * c[1] - x[3] * s[1];
+    x[3] = x[3] * c[1] + a1 * s[1];
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8AppendParams p) {
+  constexpr int LPR = HD / 4, RPW = 32 / LPR, IT = kKv8Block / RPW;
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
+  long long u = static_cast<long long>(blockIdx.x) * (kAppThreads / 32) + (threadIdx.x >> 5);
+  const Pair4 pr = pair4(li, p.rd, p.inter);
+  float2 fr[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) fr[k] = pr.rot ? __ldg(p.rope + pr.i0 + k) : make_float2(0.f, 0.f);
+  const long long kv_units = 2ll * p.B * p.Hkv * p.nb;
+  if (u >= kv_units) {  // ---- q: rotate and round to bf16
+    u -= kv_units;
+    const int groups = (p.H + kAppHeads * RPW - 1) / (kAppHeads * RPW);
+    const int m = static_cast<int>(u / groups), g = static_cast<int>(u % groups);
+    if (m >= p.B * p.n) return;
+    const int b = m / p.n;
+    float x[kAppHeads][4];
+#pragma unroll
+    for (int k = 0; k < kAppHeads; ++k) {
+      const int h = (g * kAppHeads + k) * RPW + sub;
+      if (h < p.H) {
+        const long long at = static_cast<long long>(m) * p.q_ld + h * HD;
+        const float2 a = load2(p.q, at + pr.d0, p.f32), c = load2(p.q, at + pr.d1, p.f32);
+        x[k][0] = a.x, x[k][1] = a.y, x[k][2] = c.x, x[k][3] = c.y;
+      }
+    }
+    const int pos = p.base[b] + (p.depth ? __ldg(p.depth + m) : m - b * p.n);
+    float cs[2], sn[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) kv8_sincos(pos, fr[k], &sn[k], &cs[k]);
+#pragma unroll
+    for (int k = 0; k < kAppHeads; ++k) {
+      const int h = (g * kAppHeads + k) * RPW + sub;
+      if (h >= p.H) continue;
+      rotate4(pr, x[k], cs, sn);
+      uint16_t* o = p.q_out + (static_cast<long long>(m) * p.H + h) * HD;
+      *reinterpret_cast<uint32_t*>(o + pr.d0) = bf16_any(x[k][0]) | (bf16_any(x[k][1]) << 16);
+      *reinterpret_cast<uint32_t*>(o + pr.d1) = bf16_any(x[k][2]) | (bf16_any(x[k][3]) << 16);
+    }
+    return;
+  }
+  // ---- one block of 16 slots of k (which 0) or v (1)
+  const int which = static_cast<int>(u & 1);
+  u >>= 1;
+  const int h = static_cast<int>(u % p.Hkv);
+  u /= p.Hkv;
+  const int blk_i = static_cast<int>(u % p.nb), b = static_cast<int>(u / p.nb);
+  const int L = p.base[b];
+  int32_t bad = kv8_fit(L, p.n, p.table, p.max_pages, p.n_pages, b);
+  if (p.seq_ok && !p.seq_ok[b]) return;  // flagged when the pass began
+  if (bad) {
+    if (lane == 0) set_status(p.status, bad);
+    return;
+  }
+  const int slot0 = (L / kKv8Block + blk_i) * kKv8Block;  // the block's first slot
+  if (slot0 >= L + p.n) return;
+  const void* src = which ? p.v : p.k;
+  const long long ld = which ? p.v_ld : p.k_ld;
+  const Pair4 at = which ? pair4(li, 0, 1) : pr;
+  float x[IT][4];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = slot0 + i * RPW + sub - L;  // the row's token
+    x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+    if (j >= 0 && j < p.n) {
+      const long long o = (static_cast<long long>(b) * p.n + j) * ld + h * HD;
+      const float2 a = load2(src, o + at.d0, p.f32), c = load2(src, o + at.d1, p.f32);
+      x[i][0] = a.x, x[i][1] = a.y, x[i][2] = c.x, x[i][3] = c.y;
+    }
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int j = slot0 + i * RPW + sub - L;
+    if (at.rot && j >= 0 && j < p.n) {
+      const int pos = L + (p.depth ? __ldg(p.depth + b * p.n + j) : j);
+      float cs[2], sn[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) kv8_sincos(pos, fr[k], &sn[k], &cs[k]);
+      rotate4(at, x[i], cs, sn);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a = fabsf(x[i][k]);
+      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);  // finite values alone set the scale
+    }
+  }
+  amax = warp_max(amax);
+  const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
+  const int page = map.page(b, slot0);
+  uint8_t* codes = (which ? p.vc : p.kc) + map.row(page, h, slot0);
+  float* sp = (which ? p.vs : p.ks) + map.scale(page, h, slot0);
+  const int kept = max(0, L - slot0);  // rows the block holds from before
+  float s = kv8_scale(amax);
+  float s_old = s;
+  if (kept) {
+    s_old = *sp;
+    s = fmaxf(s, s_old);
+  }
+  const float inv = pow2_inv(s), ratio = s_old * inv;
+  __syncwarp();  // every lane has read the scale before lane 0 replaces it
+#pragma unroll
+  for (int i = 0; i < IT; ++i) {
+    const int r = i * RPW + sub, j = slot0 + r - L;
+    uint8_t* row = codes + static_cast<long long>(r) * HD;
+    if (j >= 0 && j < p.n) {
+      const uint32_t w = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
+      if (at.inter) {
+        *reinterpret_cast<uint32_t*>(row + at.d0) = w;
+      } else {
+        *reinterpret_cast<uint16_t*>(row + at.d0) = static_cast<uint16_t>(w);
+        *reinterpret_cast<uint16_t*>(row + at.d1) = static_cast<uint16_t>(w >> 16);
+      }
+    } else if (r < kept && ratio < 1.f) {
+      uint32_t* w = reinterpret_cast<uint32_t*>(row + 4 * li);
+      *w = kv8_rescale4(*w, ratio);
+    }
+  }
+  if (lane == 0) *sp = s;
+}
+
+// ------------------------------------------------------------------ commit
+// Moves the accepted path's rows L0 + path[d - 1] -> L0 + d (d = 1 .. m) of one
+// (layer, sequence, KV head), keys and values.  A destination block's scale is
+// the largest of those its rows come with: the rows moved in, and its own if
+// it keeps rows (slots up to the root, L0).  Every row is read before any is
+// written: rows and scales go through registers and shared memory.
+constexpr int kMoveThreads = 128;
+constexpr int kMoveBlocks = (kTreeMaxNodes + 2 * kKv8Block - 2) / kKv8Block;  // blocks n slots can touch
+
+// 0 when the path of sequence b can be committed, else the status bit.
+SPEC_DEVINL int32_t kv8_path_bad(const Kv8CommitParams& p, int b, int len, int m) {
+  if (m < 0 || m >= p.n) return SPEC_DEV_BAD_TREE;
+  const int32_t* path = p.path + static_cast<long long>(b) * p.n;
+  int prev = 0;
+  for (int d = 0; d < m; ++d) {
+    const int s = __ldg(path + d);
+    if (s <= prev || s >= p.n) return SPEC_DEV_BAD_TREE;
+    prev = s;
+  }
+  if (len < p.n) return SPEC_DEV_KV_OVERFLOW;
+  return kv8_fit(len - p.n, p.n, p.table, p.max_pages, p.n_pages, b);
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kMoveThreads) kv8_commit_kernel(const Kv8CommitParams p) {
+  constexpr int VEC = HD / 16;                                             // 16-byte words per row
+  constexpr int PER = 2 * (kTreeMaxNodes - 1) * VEC / kMoveThreads + 1;   // words per thread
+  __shared__ float s_src[2][kTreeMaxNodes], s_dst[2][kMoveBlocks], s_own[2];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, layer = blockIdx.y;
+  const int tid = threadIdx.x;
+  const int len = p.len[b], m = __ldg(p.n_acc + b);
+  if (m <= 0 || kv8_path_bad(p, b, len, m)) return;  // the length update reports it
+  const int L0 = len - p.n;
+  const int32_t* path = p.path + static_cast<long long>(b) * p.n;
+  const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
+  const long long lrow = static_cast<long long>(layer) * p.n_pages * p.Hkv * kPageSlots * HD;
+  const long long lsc = static_cast<long long>(layer) * p.n_pages * p.Hkv * kKv8Sub;
+  uint8_t* const codes[2] = {p.kc + lrow, p.vc + lrow};
+  float* const scales[2] = {p.ks + lsc, p.vs + lsc};
+  const int per_side = m * VEC;
+  uint4 w[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int e = tid + k * kMoveThreads;
+    if (e < 2 * per_side) {
+      const int side = e >= per_side, rem = e - side * per_side;
+      const int src = L0 + __ldg(path + rem / VEC);
+      w[k] = reinterpret_cast<const uint4*>(codes[side] + map.row(map.page(b, src), h, src))[rem % VEC];
+    }
+  }
+  for (int e = tid; e < 2 * m; e += kMoveThreads) {
+    const int side = e >= m, d = e - side * m;
+    const int src = L0 + __ldg(path + d);
+    s_src[side][d] = scales[side][map.scale(map.page(b, src), h, src)];
+  }
+  if (tid < 2) s_own[tid] = scales[tid][map.scale(map.page(b, L0), h, L0)];
+  __syncthreads();
+  const int blk0 = L0 / kKv8Block;
+  const int nblk = (L0 + m) / kKv8Block - blk0 + 1;
+  for (int e = tid; e < 2 * nblk; e += kMoveThreads) {
+    const int side = e >= nblk, i = e - side * nblk;
+    const int d0 = max(1, (blk0 + i) * kKv8Block - L0), d1 = min(m, (blk0 + i + 1) * kKv8Block - 1 - L0);
+    float s = i == 0 ? s_own[side] : 0.f;  // the root's block keeps rows
+    for (int d = d0; d <= d1; ++d) s = fmaxf(s, s_src[side][d - 1]);
+    s_dst[side][i] = s;
+    if (d0 <= d1) {
+      const int t = (blk0 + i) * kKv8Block;
+      scales[side][map.scale(map.page(b, t), h, t)] = s;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int e = tid + k * kMoveThreads;
+    if (e >= 2 * per_side) continue;
+    const int side = e >= per_side, rem = e - side * per_side, d = rem / VEC + 1;
+    const float ratio = s_src[side][d - 1] * pow2_inv(s_dst[side][(L0 + d) / kKv8Block - blk0]);
+    uint4 v = w[k];
+    if (ratio < 1.f)
+      v = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
+                     kv8_rescale4(v.w, ratio));
+    reinterpret_cast<uint4*>(codes[side] + map.row(map.page(b, L0 + d), h, L0 + d))[rem % VEC] = v;
+  }
+  // rows that the root's block holds, if its scale has grown
+  const int t0 = blk0 * kKv8Block, kept = L0 - t0 + 1;
+  for (int e = tid; e < 2 * kept * VEC; e += kMoveThreads) {
+    const int side = e >= kept * VEC, rem = e - side * kept * VEC;
+    const float ratio = s_own[side] * pow2_inv(s_dst[side][0]);
+    if (ratio >= 1.f) continue;
+    const int t = t0 + rem / VEC;
+    uint4* a = reinterpret_cast<uint4*>(codes[side] + map.row(map.page(b, t), h, t)) + rem % VEC;
+    const uint4 v = *a;
+    *a = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
+                    kv8_rescale4(v.w, ratio));
+  }
+}
+
+// len = L0 + 1 + m, after the copies (a launch of its own: they read len).
+__global__ void kv8_commit_len_kernel(const Kv8CommitParams p) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= p.B) return;
+  const int len = p.len[b], m = p.n_acc[b];
+  if (const int32_t bad = kv8_path_bad(p, b, len, m)) {
+    set_status(p.status, bad);
+    return;
+  }
+  p.len[b] = len - p.n + 1 + m;
+}
+
+// len += n for every sequence whose slots and pages (all of [0, len + n)) are
+// in order: what opens a whole pass's length update.
+__global__ void kv8_advance_kernel(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,
+                                   int32_t* status) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  if (b >= B) return;
+  const int L = len[b];
+  const int cap = max_pages * kPageSlots;
+  const int32_t bad = L > cap ? SPEC_DEV_KV_OVERFLOW : seq_fit(L, n, cap, table, max_pages, n_pages, b);
+  if (bad)
+    set_status(status, bad);
+  else
+    len[b] = L + n;
+}
+
+template <class... A>
+cudaError_t launch_dep(void (*fn)(A...), dim3 grid, int threads, cudaStream_t stream, A... a) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, fn, a...);
+}
+
+}  // namespace
+
+cudaError_t launch_kv8_rope(float2* dst, int rd, double theta, double factor, double low, double high, int orig_len,
+                            cudaStream_t stream) {
+  kv8_rope_kernel<<<(rd / 2 + 63) / 64, 64, 0, stream>>>(dst, rd, theta, factor, low, high, orig_len);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
+  const int rpw = 32 / (p.hd / 4);
+  const long long units = 2ll * p.B * p.Hkv * p.nb +
+                          static_cast<long long>(p.B) * p.n * ((p.H + kAppHeads * rpw - 1) / (kAppHeads * rpw));
+  const long long grid = (units + kAppThreads / 32 - 1) / (kAppThreads / 32);
+  if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+  return launch_dep(p.hd == 128 ? kv8_append_kernel<128> : kv8_append_kernel<64>, dim3(static_cast<unsigned>(grid)),
+                    kAppThreads, stream, p);
+}
+
+cudaError_t launch_kv8_commit(const Kv8CommitParams& p, cudaStream_t stream) {
+  if (p.n > 1) {
+    const cudaError_t e = launch_dep(p.hd == 128 ? kv8_commit_kernel<128> : kv8_commit_kernel<64>,
+                                     dim3(p.B * p.Hkv, p.L), kMoveThreads, stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_dep(kv8_commit_len_kernel, dim3((p.B + 127) / 128), 128, stream, p);
+}
+
+cudaError_t launch_kv8_advance(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,
+                               int32_t* status, cudaStream_t stream) {
+  return launch_dep(kv8_advance_kernel, dim3((B + 127) / 128), 128, stream, len, table, B, n, max_pages, n_pages,
+                    status);
+}
+
+}  // namespace spec
