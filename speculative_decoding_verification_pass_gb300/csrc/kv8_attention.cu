@@ -3,93 +3,767 @@
 //   p_j = exp(s_j - max s) over the slots that the row's token may see
 // (the cached ones, and of the new ones its own and earlier, or those of its
 // ancestor mask); a row that sees nothing is zero.
+//
+// The cache is read once, by TMA, into shared memory, and enters the tensor
+// cores as it is stored: both products are tcgen05.mma kind::f8f6f4 with e4m3
+// operands and fp32 accumulators in TMEM, so no key or value is ever
+// converted.  The other operand is split into e4m3 pieces that add up to it:
+//   q row = 2^k (hi + lo)            bf16 has 8 significant bits, a piece 4: exact but
+//                                    for elements 2^-18 below the row's largest
+//   p     = 2^-8 (hi + mid + lo)     a weight to 2^-12 of itself (2^-18 of the largest)
+// and the pieces lie side by side in the N dimension, so a tile of keys or
+// values is read from shared memory once whatever their number.
+//
+// One CTA takes the RT query rows (n tokens x the query heads of a KV head) of
+// one (sequence, KV head) over a run of 128-key tiles; the runs of one row tile
+// are a thread-block cluster, whose CTAs merge their partial sums through
+// distributed shared memory: no workspace, no second launch.
+//   S^T [128 keys][RT hi | RT lo]          = K [keys][hd] x Q^T
+//   O^T [128 dims][RT hi | mid | lo]       = V^T [dims][keys] x P
+// Thread t of the four softmax warps owns TMEM lane t: key t of S^T, then
+// dimension t of O^T.  A key's scales so belong to one thread: ks multiplies its
+// scores, and vs enters as an exponent,
+//   p'_j = p_j vs_j = 2^(s_j + log2 vs_j - M'),  M' = max (s_j + log2 vs_j),
+// which keeps the weights that enter the product within (0, 1]; the sum of the
+// p_j themselves adds p'_j / vs_j in fp32.  Warp 4 issues the TMA loads, warp 5
+// the MMAs; S is double-buffered in TMEM, so the scores of tile i + 1 are
+// computed while the softmax of tile i runs.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+
 #include "internal.h"
 #include "kv8_common.cuh"
 
 namespace spec {
 namespace {
 
-// One CTA per (sequence, query row): a thread scores one key of a block of
-// 128, then owns one output dimension.
-constexpr int kRowThreads = 128;
+constexpr int kTile = 128;                  // keys per tile
+constexpr int kSoft = 128;                  // softmax threads
+constexpr int kAttThreads = kSoft + 64;     // + TMA warp + MMA warp
+constexpr int kPRow = 128;                  // bytes of a key's row of P
+constexpr int kMaxCluster = 16;
 
-template <int HD>
-__global__ void __launch_bounds__(kRowThreads) kv8_attention_kernel(const Kv8AttnParams p) {
-  __shared__ float sq[HD], sp[kRowThreads], red[4];
+SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+SPEC_DEVINL void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+SPEC_DEVINL void tmem_ld_x64(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+template <int N>
+SPEC_DEVINL void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
+  if constexpr (N == 16) tmem_ld_x16(taddr, r);
+  if constexpr (N == 32) tmem_ld_x32(taddr, r);
+  if constexpr (N == 64) tmem_ld_x64(taddr, r);
+}
+
+// D[tmem] (+)= A[smem] * B[smem] of e4m3 operands, issued by one thread.
+SPEC_DEVINL void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 -> fp32, M x N; tra / trb:
+// operand stored MN-major.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool tra, bool trb) {
+  return (1u << 4) | (tra ? 1u << 15 : 0u) | (trb ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+// Shared-memory descriptor of rows of ROWB bytes (128 or 64) with the swizzle
+// of that span: 8-row groups ROWB * 8 apart (stride offset); lbo: distance
+// between two spans along an MN-major operand's own dimension.
+template <int ROWB>
+SPEC_DEVINL uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
+  uint64_t d = 0;
+  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
+  d |= static_cast<uint64_t>((ROWB * 8) >> 4) << 32;
+  d |= static_cast<uint64_t>(1) << 46;
+  d |= static_cast<uint64_t>(ROWB == 128 ? 2 : 4) << 61;
+  return d;
+}
+// Byte offset of 16-byte chunk c of row i in such rows.
+template <int ROWB>
+SPEC_DEVINL uint32_t swz_off(int i, int c) {
+  if constexpr (ROWB == 128)
+    return static_cast<uint32_t>(i * 128 + ((c ^ (i & 7)) << 4));
+  else
+    return static_cast<uint32_t>(i * 64 + ((c ^ ((i >> 1) & 3)) << 4));
+}
+
+SPEC_DEVINL void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+SPEC_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+SPEC_DEVINL void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+SPEC_DEVINL uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+SPEC_DEVINL float peer_f32(uint32_t a) {
+  float v;
+  asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  return v;
+}
+SPEC_DEVINL float4 peer_f32x4(uint32_t a) {
+  float4 v;
+  asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  return v;
+}
+
+// Named barrier that also tells every thread whether any of them raised v.
+SPEC_DEVINL bool named_bar_any(int id, int nthreads, bool v) {
+  int any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(any)
+      : "r"(id), "r"(nthreads), "r"(v ? 1 : 0)
+      : "memory");
+  return any != 0;
+}
+
+// Reduce RT values per lane over the warp's 32 lanes with op; lane l then
+// holds the result of value l % RT (halving: each step sends half of what is
+// left; 31 shuffles for 32 values, 16 for 16).
+template <int RT, class Op>
+SPEC_DEVINL float warp_rows_reduce(float (&v)[RT], Op op) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = RT / 2; o >= 1; o >>= 1) {
+    const bool upper = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float send = upper ? v[i] : v[i + o];
+      const float keep = upper ? v[i + o] : v[i];
+      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+    }
+  }
+  float x = v[0];
+#pragma unroll
+  for (int o = RT; o < 32; o <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+template <int HD, int RT>
+struct AttSmem {
+  static constexpr int kStages = HD == 128 ? 2 : 4;
+  static constexpr uint32_t kTileB = kTile * HD;  // bytes of a K or V tile
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kP = kQ + 2 * RT * HD;
+  static constexpr uint32_t kK = kP + kTile * kPRow;
+  static constexpr uint32_t kV = kK + kStages * kTileB;
+  static constexpr uint32_t kMisc = kV + kStages * kTileB;
+  struct Misc {
+    uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages];
+    uint64_t s_full[2], s_free[2], p_full, o_full, drain;
+    uint64_t anc[RT];
+    alignas(16) float red[2][4][RT];  // per-warp maxima (sums at the end); this and the next three are read as float4
+    float rmax[4][RT];         // each warp's copy of the rows' running M' - 8
+    float alpha[2][4][RT];     // ... and of the rescale of this tile and the one before
+    float cq[RT];              // score factor of a row: 2^k scale log2(e)
+    float stat[2][RT];         // this CTA's M' and sum
+    float peer[2][kMaxCluster][RT];
+    uint32_t nan[RT][HD / 32]; // outputs that a NaN value code reaches
+    uint32_t tmem;
+    int abort, any_nan;
+  };
+  // partial sums [RT][HD] fp32, over the K ring once every MMA is done
+  static constexpr uint32_t kO = kK;
+  static_assert(offsetof(Misc, rmax) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 &&
+                    alignof(Misc) == 16 && kMisc % 1024 == 0,
+                "row arrays are read as float4");
+  static_assert(RT * HD * 4 <= 2 * kStages * kTileB, "the partial sums lie over the ring");
+  static constexpr uint32_t kBytes = kMisc + sizeof(Misc) + 1024;  // + alignment of the base
+  static constexpr uint32_t kTmemCols = RT == 32 ? 256 : 128;      // 2 x 2 RT (S) + 3 RT (O)
+};
+
+struct AttMaps {
+  CUtensorMap k, v;
+};
+
+template <int HD, int RT>
+__global__ void __launch_bounds__(kAttThreads, 2)
+    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int C) {
+  using S = AttSmem<HD, RT>;
+  constexpr int NS = S::kStages;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  auto& sm = *reinterpret_cast<typename S::Misc*>(smem_raw + (base - smem_u32(smem_raw)) + S::kMisc);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = blockIdx.x % C, rtile = blockIdx.x / C, h = blockIdx.y, b = blockIdx.z;
+  const int G = p.H / p.Hkv, R = p.n * G, rbase = rtile * RT;
+
+  if (tid == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&sm.full_k[i], 1);
+      mbar_init(&sm.full_v[i], 1);
+      mbar_init(&sm.empty_k[i], 1);
+      mbar_init(&sm.empty_v[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sm.s_full[i], 1);
+      mbar_init(&sm.s_free[i], kSoft);
+    }
+    mbar_init(&sm.p_full, kSoft);
+    mbar_init(&sm.o_full, 1);
+    mbar_init(&sm.drain, 1);
+    fence_mbar_init();
+    sm.abort = 0;
+    sm.any_nan = 0;
+  }
+  if (warp == 4) {
+    if (lane == 0) {
+      prefetch_tmap(&maps.k);
+      prefetch_tmap(&maps.v);
+    }
+    __syncwarp();
+    tmem_alloc(&sm.tmem, S::kTmemCols);
+    tmem_relinquish();
+  }
   grid_dep_wait();
   grid_dep_launch();
-  const int row = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;  // row = token j, head hq
-  const int j = row / p.H, hq = row % p.H, h = hq / (p.H / p.Hkv);
+
   const int L = p.base[b];
-  const long long m = static_cast<long long>(b) * p.n + j;
-  uint16_t* out = p.o + m * p.o_ld + hq * HD;
-  const int32_t bad = kv8_fit(L, p.n, p.table, p.max_pages, p.n_pages, b);
-  if (bad) {
-    if (tid == 0) set_status(p.status, bad);
-    if (tid < HD) out[tid] = 0;
-    return;
-  }
-  const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
-  if (tid < HD) sq[tid] = bf16_to_f32(p.q[m * p.q_ld + hq * HD + tid]) * p.scale_log2;
-  const uint64_t am = p.anc ? p.anc[m] : 0ull;
-  __syncthreads();
-  float mx = -INFINITY, l = 0.f, acc = 0.f;
-  const int T = L + p.n;
-  for (int t0 = 0; t0 < T; t0 += kRowThreads) {
-    const int t = t0 + tid;
-    const bool see = t < T && key_visible(t, L, j, p.anc, am);
-    float s = -INFINITY;
-    if (see) {
-      const int pg = map.page(b, t);
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(p.kc + map.row(pg, h, t));
-      float d = 0.f;
-      for (int c = 0; c < HD / 4; ++c) {
-        const float2 x = e4m3x2_to_f32(k[c]), y = e4m3x2_to_f32(k[c] >> 16);
-        d += x.x * sq[4 * c] + x.y * sq[4 * c + 1] + y.x * sq[4 * c + 2] + y.y * sq[4 * c + 3];
-      }
-      s = d * p.ks[map.scale(pg, h, t)];
+  const int32_t unfit = kv8_fit(L, p.n, p.table, p.max_pages, p.n_pages, b);
+  if (unfit && tid == 0) set_status(p.status, unfit);
+  const int T = unfit ? 0 : L + p.n;  // slots [0, T)
+  const int tiles = (T + kTile - 1) / kTile;
+  const int i0 = static_cast<int>(static_cast<long long>(tiles) * rank / C);
+  const int nt = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / C) - i0;  // this CTA's tiles
+  const int32_t* table = p.table + static_cast<long long>(b) * p.max_pages;
+  const auto page_of = [&](int t) {  // the page of slot t, clamped into the pool
+    const int pg = __ldg(table + min(t / kPageSlots, p.max_pages - 1));
+    if (pg < 0 || pg >= p.n_pages) {
+      if (t < T) set_status(p.status, SPEC_DEV_BAD_PAGE);
+      return pg < 0 ? 0 : p.n_pages - 1;
     }
-    float w = warp_max(s);
-    if ((tid & 31) == 0) red[tid >> 5] = w;
-    __syncthreads();
-    const float mn = fmaxf(mx, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float alpha = mx == -INFINITY ? 0.f : exp2f(mx - mn);
-    mx = mn;
-    const float e = see ? exp2f(s - mn) : 0.f;
-    sp[tid] = e;
-    l = l * alpha + e;
-    __syncthreads();
+    return pg;
+  };
+
+  // ---- the query rows as e4m3 pieces: row r = token r / G, head h * G + r % G
+  if (tid < RT * (kSoft / RT < HD / 16 ? kSoft / RT : HD / 16)) {
+    constexpr int TPR = kSoft / RT < HD / 16 ? kSoft / RT : HD / 16, E = HD / TPR;  // threads per row, their elements
+    const int r = tid / TPR, part = tid % TPR, rr = rbase + r;
+    float x[E];
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (rr < R)
+        w = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.n + rr / G) * p.q_ld +
+                                            (h * G + rr % G) * HD + part * E + c * 8);
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[8 * c + 2 * k] = bf16lo(v[k]);
+        x[8 * c + 2 * k + 1] = bf16hi(v[k]);
+      }
+    }
+    float mx = 0.f;
+    bool odd = false;  // an infinite or NaN element: the whole row is NaN
+#pragma unroll
+    for (int k = 0; k < E; ++k) {
+      odd |= !(fabsf(x[k]) <= 3.402823466e38f);
+      mx = fmaxf(mx, fabsf(x[k]));
+    }
+#pragma unroll
+    for (int o = 1; o < TPR; o <<= 1) {
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      odd |= __shfl_xor_sync(0xffffffffu, odd ? 1 : 0, o) != 0;
+    }
+    // 2^-k brings the largest element into [128, 256) (k at least -100: a row
+    // of smaller elements scores zero to fp32's last bit anyway)
+    const int k2 = max(static_cast<int>(__float_as_uint(mx) >> 23) - 127 - 7, -100);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - k2) << 23);
+#pragma unroll
+    for (int c = 0; c < E / 16; ++c) {
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float a = odd ? 0.f : x[16 * c + 2 * k] * down, d = odd ? 0.f : x[16 * c + 2 * k + 1] * down;
+        const uint32_t w = e4m3x2(a, d);
+        const float2 f = e4m3x2_to_f32(w);
+        const uint32_t u = e4m3x2(a - f.x, d - f.y);
+        if (k & 1) {
+          hi[k / 2] |= w << 16;
+          lo[k / 2] |= u << 16;
+        } else {
+          hi[k / 2] = w;
+          lo[k / 2] = u;
+        }
+      }
+      const int ch = part * (E / 16) + c;
+      st_shared_v4(base + S::kQ + swz_off<HD>(r, ch), hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(base + S::kQ + swz_off<HD>(RT + r, ch), lo[0], lo[1], lo[2], lo[3]);
+    }
+    if (part == 0) {
+      sm.cq[r] = odd ? __uint_as_float(0x7FC00000u)
+                     : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+      sm.anc[r] = (p.anc && rr < R) ? p.anc[static_cast<long long>(b) * p.n + rr / G] : 0ull;
+#pragma unroll
+      for (int c = 0; c < HD / 32; ++c) sm.nan[r][c] = 0u;
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
+
+  float acc[RT], l[RT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) acc[r] = l[r] = 0.f;
+  float mrun = -INFINITY;  // lane r: row r's running maximum M'
+
+  if (warp == 4) {
+    // ------------------------------------------------------- TMA producer
+    if (lane == 0) {
+      const uint64_t pol = l2_policy_evict_first();
+      int issued = 0;
+      const auto load = [&](const CUtensorMap* m, uint32_t dst, uint64_t* bar, int i) {
+        const int t = (i0 + i) * kTile;
+        const int np = T - t > kPageSlots ? 2 : 1;  // a page past the end is not read
+        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np * kPageSlots * HD));
+        for (int g = 0; g < np; ++g)
+          tma_load_2d_s(dst + g * kPageSlots * HD, m, bar, 0, (page_of(t + g * kPageSlots) * p.Hkv + h) * kPageSlots,
+                        pol);
+      };
+      for (int i = 0; i < nt; ++i) {
+        const int s = i % NS;
+        const uint32_t par = static_cast<uint32_t>((i / NS - 1) & 1);
+        if (i >= NS && !mbar_wait(&sm.empty_k[s], par, &sm.abort)) break;
+        load(&maps.k, base + S::kK + s * S::kTileB, &sm.full_k[s], i);
+        issued = 2 * i + 1;
+        if (i >= NS && !mbar_wait(&sm.empty_v[s], par, &sm.abort)) break;
+        load(&maps.v, base + S::kV + s * S::kTileB, &sm.full_v[s], i);
+        issued = 2 * i + 2;
+      }
+      if (sm.abort) {  // loads in flight land before the CTA leaves (bounded as every wait)
+        int none = 0;
+        for (int k = max(0, issued - 2 * NS); k < issued; ++k) {
+          const int i = k / 2;
+          mbar_wait(k & 1 ? &sm.full_v[i % NS] : &sm.full_k[i % NS], static_cast<uint32_t>((i / NS) & 1), &none);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 5) {
+    // --------------------------------------------------------- MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t id_s = idesc_e4m3(kTile, 2 * RT, false, false);
+      constexpr uint32_t id_o = idesc_e4m3(kTile, 3 * RT, true, true);
+      const auto issue_o = [&](int i) {
+        const int s = i % NS;
+        if (!mbar_wait(&sm.full_v[s], static_cast<uint32_t>((i / NS) & 1), &sm.abort)) return false;
+        if (!mbar_wait(&sm.p_full, static_cast<uint32_t>(i & 1), &sm.abort)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < kTile / 32; ++kk)
+          // head dim 64: the 128 rows of the A operand are the 64 dimensions twice
+          umma_e4m3(tmem + 4 * RT, sdesc_rows<HD>(base + S::kV + s * S::kTileB + kk * 32 * HD, 0),
+                    sdesc_rows<kPRow>(base + S::kP + kk * 32 * kPRow, 0), id_o, kk > 0 ? 1u : 0u);
+        umma_commit(&sm.empty_v[s]);
+        umma_commit(&sm.o_full);
+        return true;
+      };
+      bool ok = true;
+      for (int i = 0; i < nt && ok; ++i) {
+        const int s = i % NS;
+        ok = mbar_wait(&sm.full_k[s], static_cast<uint32_t>((i / NS) & 1), &sm.abort) &&
+             (i < 2 || mbar_wait(&sm.s_free[i & 1], static_cast<uint32_t>((i / 2 - 1) & 1), &sm.abort));
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < HD / 32; ++kk)
+          umma_e4m3(tmem + (i & 1) * 2 * RT, sdesc_rows<HD>(base + S::kK + s * S::kTileB + kk * 32, 16),
+                    sdesc_rows<HD>(base + S::kQ + kk * 32, 16), id_s, kk > 0 ? 1u : 0u);
+        umma_commit(&sm.empty_k[s]);
+        umma_commit(&sm.s_full[i & 1]);
+        if (i) ok = issue_o(i - 1);
+      }
+      if (ok && nt) ok = issue_o(nt - 1);
+      if (!ok) {  // MMAs in flight end before TMEM and shared memory go
+        int none = 0;
+        umma_commit(&sm.drain);
+        mbar_wait(&sm.drain, 0, &none);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------- softmax and accumulation
+    // A wait that gives up sets the abort flag; the threads leave the loop
+    // together at its barrier.
+    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
+    const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
+    const int sub = (tid % kPageSlots) / kKv8Block;
+    const auto scale_at = [&](int pg) { return (static_cast<long long>(pg) * p.Hkv + h) * kKv8Sub + sub; };
+    const auto add_o = [&](int i) {  // acc = acc * alpha_i + O_i
+      mbar_wait(&sm.o_full, static_cast<uint32_t>(i & 1), &sm.abort);
+      tc_fence_after();
+      const float* al = sm.alpha[i & 1][warp];
+      uint32_t o[RT];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        tmem_ld(tmem + lane_addr + (4 + q) * RT, o);
+#pragma unroll
+        for (int r = 0; r < RT; r += 4) {
+          float4 a = make_float4(1.f, 1.f, 1.f, 1.f);
+          if (q == 0) a = *reinterpret_cast<const float4*>(al + r);
+          acc[r] = fmaf(acc[r], a.x, __uint_as_float(o[r]));
+          acc[r + 1] = fmaf(acc[r + 1], a.y, __uint_as_float(o[r + 1]));
+          acc[r + 2] = fmaf(acc[r + 2], a.z, __uint_as_float(o[r + 2]));
+          acc[r + 3] = fmaf(acc[r + 3], a.w, __uint_as_float(o[r + 3]));
+        }
+      }
+    };
+    // this thread's scales, one tile ahead, and its page, two ahead
+    int pg1 = nt > 0 ? page_of(i0 * kTile + tid) : 0;
+    float ks_n = nt > 0 ? __ldg(p.ks + scale_at(pg1)) : 1.f, vs_n = nt > 0 ? __ldg(p.vs + scale_at(pg1)) : 1.f;
+    pg1 = nt > 1 ? page_of((i0 + 1) * kTile + tid) : 0;
+    bool stopped = false;
+    for (int i = 0; i < nt; ++i) {
+      const int buf = i & 1, t0 = (i0 + i) * kTile, t = t0 + tid;
+      const float ks = ks_n, vs = vs_n;
+      if (i + 1 < nt) {
+        ks_n = __ldg(p.ks + scale_at(pg1));
+        vs_n = __ldg(p.vs + scale_at(pg1));
+        if (i + 2 < nt) pg1 = page_of(t0 + 2 * kTile + tid);
+      }
+      const float lvs = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
+      const float ivs = pow2_inv(vs);
+      float s[RT];
+      mbar_wait(&sm.s_full[buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
+      tc_fence_after();
+      {
+        uint32_t w[2 * RT];
+        tmem_ld(tmem + lane_addr + buf * 2 * RT, w);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = __uint_as_float(w[r]) + __uint_as_float(w[RT + r]);
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.s_free[buf]);
+#pragma unroll
+      for (int r = 0; r < RT; r += 4) {
+        const float4 c = *reinterpret_cast<const float4*>(sm.cq + r);
+        s[r] = fmaf(s[r] * ks, c.x, lvs);
+        s[r + 1] = fmaf(s[r + 1] * ks, c.y, lvs);
+        s[r + 2] = fmaf(s[r + 2] * ks, c.z, lvs);
+        s[r + 3] = fmaf(s[r + 3] * ks, c.w, lvs);
+      }
+      const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
+      if (masked) {
+        uint32_t vis = 0u;  // bit r: row rbase + r sees slot t
+        if (t < T) {
+          vis = RT == 32 ? 0xFFFFFFFFu : (1u << RT) - 1u;
+          if (t >= L) {
+            const int k = t - L;
+            if (p.anc) {
+              vis = 0u;
+              if (k < 64)
+                for (int r = 0; r < RT; ++r) vis |= static_cast<uint32_t>((sm.anc[r] >> k) & 1ull) << r;
+            } else {  // row rr (token rr / G) sees new slot k iff rr >= k * G
+              const int first = k * G - rbase;
+              if (first > 0) vis = first >= 32 ? 0u : vis & (0xFFFFFFFFu << first);
+            }
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) s[r] = (vis >> r) & 1u ? s[r] : -INFINITY;
+        // This thread's value row, if not every row sees it: zero past the
+        // end (pages hold anything there), and NaN codes taken out (their
+        // weight of 0 would not clear them) and noted for the rows that see them.
+        const uint32_t vt = base + S::kV + (i % NS) * S::kTileB;
+        mbar_wait(&sm.full_v[i % NS], static_cast<uint32_t>((i / NS) & 1), &sm.abort);
+        if (t >= L) {
+#pragma unroll 1
+          for (int c = 0; c < HD / 16; ++c) {
+            const uint32_t a = vt + swz_off<HD>(tid, c);
+            if (t >= T) {
+              st_shared_v4(a, 0, 0, 0, 0);
+              continue;
+            }
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+              uint32_t w;
+              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(a + 4 * k) : "memory");
+              const uint32_t m = w & 0x7F7F7F7Fu;
+              const uint32_t hit = (m + 0x01010101u) & 0x80808080u;  // bytes 0x7F: the NaN codes
+              if (!hit) continue;
+              sm.any_nan = 1;
+              for (int q = 0; q < 4; ++q) {
+                if (!((hit >> (8 * q + 7)) & 1u)) continue;
+                w &= ~(0xFFu << (8 * q));
+                const int d = c * 16 + k * 4 + q;
+                for (int r = 0; r < RT; ++r)
+                  if ((vis >> r) & 1u) atomicOr(&sm.nan[r][d / 32], 1u << (d % 32));
+              }
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + 4 * k), "r"(w) : "memory");
+            }
+          }
+        }
+      }
+      // ---- row maxima over the tile's 128 keys
+      {
+        float v[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) v[r] = s[r];
+        const float m = warp_rows_reduce(v, [](float a, float c) { return fmaxf(a, c); });
+        if (lane < RT) sm.red[buf][warp][lane] = m;
+      }
+      if (named_bar_any(1, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
+        stopped = true;
+        break;
+      }
+      if (lane < RT) {
+        const float m = fmaxf(fmaxf(sm.red[buf][0][lane], sm.red[buf][1][lane]),
+                              fmaxf(sm.red[buf][2][lane], sm.red[buf][3][lane]));
+        const float mn = fmaxf(mrun, m);
+        sm.alpha[buf][warp][lane] = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
+        sm.rmax[warp][lane] = mn == -INFINITY ? 0.f : mn - 8.f;
+        mrun = mn;
+      }
+      __syncwarp();
+      // ---- weights (times 2^8) and their sums
+#pragma unroll
+      for (int r = 0; r < RT; r += 4) {
+        const float4 m = *reinterpret_cast<const float4*>(&sm.rmax[warp][r]);
+        const float4 a = *reinterpret_cast<const float4*>(&sm.alpha[buf][warp][r]);
+        s[r] = exp2f(s[r] - m.x);
+        s[r + 1] = exp2f(s[r + 1] - m.y);
+        s[r + 2] = exp2f(s[r + 2] - m.z);
+        s[r + 3] = exp2f(s[r + 3] - m.w);
+        // a key that nobody may see (its scale is not read as one) adds nothing
+        l[r] = fmaf(l[r], a.x, s[r] == 0.f ? 0.f : s[r] * ivs);
+        l[r + 1] = fmaf(l[r + 1], a.y, s[r + 1] == 0.f ? 0.f : s[r + 1] * ivs);
+        l[r + 2] = fmaf(l[r + 2], a.z, s[r + 2] == 0.f ? 0.f : s[r + 2] * ivs);
+        l[r + 3] = fmaf(l[r + 3], a.w, s[r + 3] == 0.f ? 0.f : s[r + 3] * ivs);
+      }
+      if (i) add_o(i - 1);  // and P is free
+      // ---- P: this key's row, hi | mid | lo
+#pragma unroll
+      for (int c = 0; c < RT / 16; ++c) {
+        uint32_t w[3][4];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          float x = s[16 * c + 2 * k], y = s[16 * c + 2 * k + 1];
+#pragma unroll
+          for (int q = 0; q < 3; ++q) {
+            const uint32_t u = e4m3x2(x, y);
+            if (q < 2) {
+              const float2 f = e4m3x2_to_f32(u);
+              x -= f.x;
+              y -= f.y;
+            }
+            w[q][k / 2] = k & 1 ? w[q][k / 2] | (u << 16) : u;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          st_shared_v4(base + S::kP + swz_off<kPRow>(tid, q * (RT / 16) + c), w[q][0], w[q][1], w[q][2], w[q][3]);
+      }
+      fence_async_smem();
+      tc_fence_before();
+      mbar_arrive(&sm.p_full);
+    }
+    if (nt && !stopped) add_o(nt - 1);
+    // ---- this CTA's row sums
+    const float ls = warp_rows_reduce(l, [](float a, float c) { return a + c; });
+    named_bar(1, kSoft);  // the last tile's maxima have been read
+    if (lane < RT) sm.red[0][warp][lane] = ls;
+    named_bar(1, kSoft);
+    if (tid < RT) {
+      sm.stat[0][tid] = mrun;
+      sm.stat[1][tid] = (sm.red[0][0][tid] + sm.red[0][1][tid]) + (sm.red[0][2][tid] + sm.red[0][3][tid]);
+    }
+    if (sm.any_nan && tid < HD) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if ((sm.nan[r][tid / 32] >> (tid % 32)) & 1u) acc[r] = __uint_as_float(0x7FC00000u);
+    }
     if (tid < HD) {
-      acc *= alpha;
-      for (int i = 0; i < min(kRowThreads, T - t0); ++i) {
-        if (!key_visible(t0 + i, L, j, p.anc, am)) continue;
-        const int pg = map.page(b, t0 + i);
-        const float v = e4m3x2_to_f32(p.vc[map.row(pg, h, t0 + i) + tid]).x;
-        acc += sp[i] * v * p.vs[map.scale(pg, h, t0 + i)];
-      }
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::kO + (r * HD + tid) * 4), "f"(acc[r]) : "memory");
     }
+  }
+
+  // ---- merge: the cluster's CTAs share the (row, 4 dimensions) items
+  __syncwarp();
+  if (C > 1)
+    cluster_sync_all();
+  else
     __syncthreads();
+  const uint32_t stat = smem_u32(&sm.stat[0][0]);
+  for (int e = tid; e < 2 * C * RT; e += kAttThreads) {
+    const int which = e / (C * RT), c = (e / RT) % C, r = e % RT;
+    const uint32_t a = stat + (which * RT + r) * 4;
+    sm.peer[which][c][r] = C > 1 ? peer_f32(peer_addr(a, c)) : sm.stat[which][r];
   }
-  l = warp_sum(l);
-  if ((tid & 31) == 0) red[tid >> 5] = l;
   __syncthreads();
-  const float lt = (red[0] + red[1]) + (red[2] + red[3]);
-  if (tid < HD) {
-    const float o = lt == 0.f ? 0.f : acc / lt;
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(0.f), "f"(o));
-    out[tid] = static_cast<uint16_t>(r);
+  const int rows = min(RT, R - rbase);
+  for (int e = rank * kAttThreads + tid; e < rows * (HD / 4); e += C * kAttThreads) {
+    const int r = e / (HD / 4), d = e % (HD / 4) * 4;
+    const uint32_t a = base + S::kO + (r * HD + d) * 4;
+    float m = -INFINITY;
+    for (int c = 0; c < C; ++c) m = fmaxf(m, sm.peer[0][c][r]);
+    float lt = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = 0; c < C; ++c) {
+      const float mc = sm.peer[0][c][r];
+      const float w = mc == -INFINITY ? 0.f : exp2f(mc - m);
+      const float4 x = peer_f32x4(C > 1 ? peer_addr(a, c) : peer_addr(a, 0));
+      lt = fmaf(w, sm.peer[1][c][r], lt);
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing is zero
+    const int rr = rbase + r;
+    uint2 u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y * inv), "f"(o.x * inv));
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w * inv), "f"(o.z * inv));
+    *reinterpret_cast<uint2*>(p.o + (static_cast<long long>(b) * p.n + rr / G) * p.o_ld + (h * G + rr % G) * HD + d) =
+        u;
   }
+  if (C > 1) cluster_sync_all();  // peers' shared memory stays until every CTA has read it
+  if (tid == 0 && sm.abort) set_status(p.status, SPEC_DEV_TIMEOUT);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    tmem_dealloc(tmem, S::kTmemCols);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// One layer's codes as [rows][hd] bytes, boxes of one page of one head (64 rows).
+bool page_map(CUtensorMap* m, const void* codes, long long rows, int hd) {
+  const auto fn = tmap_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(hd)};
+  cuuint32_t box[2] = {static_cast<cuuint32_t>(hd), kPageSlots};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct AttSetup {
+  cudaError_t err;
+  int max_cluster;  // largest cluster size that can be placed
+  int sms;
+};
+
+cudaLaunchConfig_t att_config(dim3 grid, uint32_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2], int C) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kAttThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
+template <int HD, int RT>
+cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
+  constexpr uint32_t smem = AttSmem<HD, RT>::kBytes;
+  static PerDevice<AttSetup> setup;
+  AttSetup s{};
+  if (!setup.get(
+          [] {
+            AttSetup r{cudaSuccess, 1, 0};
+            int dev = 0;
+            if ((r.err = cudaGetDevice(&dev)) != cudaSuccess) return r;
+            if ((r.err = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return r;
+            const auto fn = kv8_attention_kernel<HD, RT>;
+            if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                              static_cast<int>(smem))) != cudaSuccess)
+              return r;
+            if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+              return r;
+            for (int c = kMaxCluster; c > 1; c /= 2) {
+              cudaLaunchAttribute attr[2];
+              cudaLaunchConfig_t cfg = att_config(dim3(c), smem, nullptr, attr, c);
+              cfg.numAttrs = 1;
+              int n = 0;
+              if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0) {
+                r.max_cluster = c;
+                break;
+              }
+            }
+            return r;
+          },
+          &s))
+    return cudaErrorInvalidDevice;
+  if (s.err != cudaSuccess) return s.err;
+  const int R = p.n * (p.H / p.Hkv), rtiles = (R + RT - 1) / RT;
+  // as many CTAs per row tile as keep two resident per SM, and no more than tiles
+  const long long groups = static_cast<long long>(p.B) * p.Hkv * rtiles;
+  const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
+  int C = 1;
+  while (2 * C <= s.max_cluster && 2 * C <= tiles && groups * 2 * C <= 2ll * s.sms) C *= 2;
+  AttMaps maps;
+  const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
+  if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
+  cudaLaunchAttribute attr[2];
+  const cudaLaunchConfig_t cfg = att_config(dim3(C * rtiles, p.Hkv, p.B), smem, stream, attr, C);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, C);
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream) {
-  if (p.hd == 128)
-    kv8_attention_kernel<128><<<dim3(p.n * p.H, p.B), kRowThreads, 0, stream>>>(p);
-  else
-    kv8_attention_kernel<64><<<dim3(p.n * p.H, p.B), kRowThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const bool small = p.n * (p.H / p.Hkv) <= 16;
+  if (p.hd == 128) return small ? launch_tile<128, 16>(p, stream) : launch_tile<128, 32>(p, stream);
+  return small ? launch_tile<64, 16>(p, stream) : launch_tile<64, 32>(p, stream);
 }
 
 }  // namespace spec
