@@ -10,7 +10,8 @@
 // converted.  The other operand is split into e4m3 pieces that add up to it:
 //   q row = 2^k (hi + lo)            bf16 has 8 significant bits, a piece 4: exact but
 //                                    for elements 2^-18 below the row's largest
-//   p     = 2^-8 (hi + mid + lo)     a weight to 2^-12 of itself (2^-18 of the largest)
+//   p     = 2^-7 (hi + mid + lo)     an fp16 weight's 11 bits (2^-17 of the row's
+//                                    reference at the least)
 // and the pieces lie side by side in the N dimension, so a tile of keys or
 // values is read from shared memory once whatever their number.
 //
@@ -19,15 +20,19 @@
 // are a thread-block cluster, whose CTAs merge their partial sums through
 // distributed shared memory: no workspace, no second launch.
 //   S^T [128 keys][RT hi | RT lo]          = K [keys][hd] x Q^T
-//   O^T [128 dims][RT hi | mid | lo]       = V^T [dims][keys] x P
+//   O^T [128 dims][RT hi | mid | lo]      += V^T [dims][keys] x P
 // Thread t of the four softmax warps owns TMEM lane t: key t of S^T, then
 // dimension t of O^T.  A key's scales so belong to one thread: ks multiplies its
 // scores, and vs enters as an exponent,
-//   p'_j = p_j vs_j = 2^(s_j + log2 vs_j - M'),  M' = max (s_j + log2 vs_j),
-// which keeps the weights that enter the product within (0, 1]; the sum of the
-// p_j themselves adds p'_j / vs_j in fp32.  Warp 4 issues the TMA loads, warp 5
-// the MMAs; S is double-buffered in TMEM, so the scores of tile i + 1 are
-// computed while the softmax of tile i runs.
+//   p'_j = p_j vs_j = 2^(s_j + log2 vs_j - M),
+// which keeps the weights that enter the product in the pieces' range; the sum
+// of the p_j themselves adds p'_j / vs_j in fp32.  The reference M of a row
+// need not be its maximum: weights up to 2^1.8 M fit the pieces, so M is set
+// one above the maximum of the first tile and raised only when a score passes
+// it by 1.75 (one barrier per tile asks whether any did).  Until then O^T adds
+// up in TMEM and no thread reads it.  Warp 4 issues the TMA loads, warp 5 the
+// MMAs; S and P are double-buffered, so the scores of tile i + 1 and the
+// products of tile i - 1 run beside the softmax of tile i.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -43,37 +48,91 @@ constexpr int kSoft = 128;                  // softmax threads
 constexpr int kAttThreads = kSoft + 64;     // + TMA warp + MMA warp
 constexpr int kPRow = 128;                  // bytes of a key's row of P
 constexpr int kMaxCluster = 16;
+constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights times 2^7 that fit e4m3
+constexpr float kNoRef = -3.402823466e38f;  // M of a row that has seen no slot: any score passes it
 
-SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+SPEC_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
-SPEC_DEVINL void tmem_ld_x32(uint32_t taddr, uint32_t (&r)[32]) {
+SPEC_DEVINL void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
-SPEC_DEVINL void tmem_ld_x64(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
-      : "r"(taddr)
-      : "memory");
-}
-
+// N consecutive columns of the thread's lane (N a multiple of 8), ready for use.
 template <int N>
 SPEC_DEVINL void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 16) tmem_ld_x16(taddr, r);
-  if constexpr (N == 32) tmem_ld_x32(taddr, r);
-  if constexpr (N == 64) tmem_ld_x64(taddr, r);
+  int at = 0;
+#pragma unroll
+  for (; at + 32 <= N; at += 32) tmem_ld_x32(taddr + at, r + at);
+  if constexpr (N % 32 >= 16) {
+    tmem_ld_x16(taddr + at, r + at);
+    at += 16;
+  }
+  if constexpr (N % 16 >= 8) tmem_ld_x8(taddr + at, r + at);
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));  // no use moves above the wait
+}
+
+// Two fp32 operations in one instruction.
+SPEC_DEVINL float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.ftz.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+SPEC_DEVINL float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.ftz.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+SPEC_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.ftz.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+// fp16 pairs: two fp32 rounded, the difference, to e4m3 and back (`a` low).
+SPEC_DEVINL uint32_t f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+SPEC_DEVINL uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+SPEC_DEVINL uint32_t f16x2_to_e4m3x2(uint32_t a) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
+  return r;
+}
+SPEC_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t a) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(a)));
+  return r;
 }
 
 // D[tmem] (+)= A[smem] * B[smem] of e4m3 operands, issued by one thread.
@@ -150,26 +209,44 @@ SPEC_DEVINL bool named_bar_any(int id, int nthreads, bool v) {
   return any != 0;
 }
 
-// Reduce RT values per lane over the warp's 32 lanes with op; lane l then
-// holds the result of value l % RT (halving: each step sends half of what is
-// left; 31 shuffles for 32 values, 16 for 16).
+// Reduce RT values per lane (a multiple of 8) over the warp's 32 lanes with op;
+// lane l < RT then holds the result of value l.  Halving: each step sends half
+// of what is left, first within groups of 8 values, then across the groups.
 template <int RT, class Op>
-SPEC_DEVINL float warp_rows_reduce(float (&v)[RT], Op op) {
+SPEC_DEVINL float warp_rows_reduce(const float (&v)[RT], float none, Op op) {
   const int lane = threadIdx.x & 31;
+  float g[4];
 #pragma unroll
-  for (int o = RT / 2; o >= 1; o >>= 1) {
-    const bool upper = (lane & o) != 0;
-#pragma unroll
-    for (int i = 0; i < o; ++i) {
-      const float send = upper ? v[i] : v[i + o];
-      const float keep = upper ? v[i + o] : v[i];
-      v[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+  for (int q = 0; q < 4; ++q) {
+    if (q >= RT / 8) {
+      g[q] = none;
+      continue;
     }
-  }
-  float x = v[0];
+    float x[8];
 #pragma unroll
-  for (int o = RT; o < 32; o <<= 1) x = op(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
+    for (int i = 0; i < 8; ++i) x[i] = v[8 * q + i];
+#pragma unroll
+    for (int o = 4; o >= 1; o >>= 1) {
+      const bool upper = (lane & o) != 0;
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const float send = upper ? x[i] : x[i + o];
+        const float keep = upper ? x[i + o] : x[i];
+        x[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, o));
+      }
+    }
+    g[q] = x[0];
+  }
+  const bool up16 = (lane & 16) != 0, up8 = (lane & 8) != 0;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float send = up16 ? g[i] : g[i + 2];
+    const float keep = up16 ? g[i + 2] : g[i];
+    g[i] = op(keep, __shfl_xor_sync(0xffffffffu, send, 16));
+  }
+  const float send = up8 ? g[0] : g[1];
+  const float keep = up8 ? g[1] : g[0];
+  return op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
 }
 
 template <int HD, int RT>
@@ -178,31 +255,34 @@ struct AttSmem {
   static constexpr uint32_t kTileB = kTile * HD;  // bytes of a K or V tile
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kP = kQ + 2 * RT * HD;
-  static constexpr uint32_t kK = kP + kTile * kPRow;
+  static constexpr uint32_t kPB = kTile * kPRow;  // bytes of one P buffer
+  static constexpr uint32_t kK = kP + 2 * kPB;
   static constexpr uint32_t kV = kK + kStages * kTileB;
   static constexpr uint32_t kMisc = kV + kStages * kTileB;
   struct Misc {
     uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages];
-    uint64_t s_full[2], s_free[2], p_full, o_full, drain;
+    uint64_t s_full[2], s_free[2], p_full[2], o_full[2], drain;
     uint64_t anc[RT];
-    alignas(16) float red[2][4][RT];  // per-warp maxima (sums at the end); this and the next three are read as float4
-    float rmax[4][RT];         // each warp's copy of the rows' running M' - 8
-    float alpha[2][4][RT];     // ... and of the rescale of this tile and the one before
+    alignas(16) float red[4][RT];  // per-warp maxima (sums at the end); this and the next three are read as float4
+    float mneg[4][RT];         // each warp's copy of 7 - M
+    float alpha[4][RT];        // ... and of the factor of a rise of M
     float cq[RT];              // score factor of a row: 2^k scale log2(e)
     float stat[2][RT];         // this CTA's M' and sum
     float peer[2][kMaxCluster][RT];
     uint32_t nan[RT][HD / 32]; // outputs that a NaN value code reaches
     uint32_t tmem;
-    int abort, any_nan;
+    int abort, any_nan, fresh;  // fresh: the tile whose products start O from zero
   };
   // partial sums [RT][HD] fp32, over the K ring once every MMA is done
   static constexpr uint32_t kO = kK;
-  static_assert(offsetof(Misc, rmax) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 &&
+  static_assert(offsetof(Misc, mneg) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 &&
                     alignof(Misc) == 16 && kMisc % 1024 == 0,
                 "row arrays are read as float4");
   static_assert(RT * HD * 4 <= 2 * kStages * kTileB, "the partial sums lie over the ring");
   static constexpr uint32_t kBytes = kMisc + sizeof(Misc) + 1024;  // + alignment of the base
-  static constexpr uint32_t kTmemCols = RT == 32 ? 256 : 128;      // 2 x 2 RT (S) + 3 RT (O)
+  static constexpr int kNO = (3 * RT + 15) / 16 * 16;              // O columns (M = 128 takes multiples of 16)
+  static constexpr uint32_t kTmemCols = RT >= 24 ? 256 : (RT == 16 ? 128 : 64);
+  static_assert(4 * RT + kNO <= static_cast<int>(kTmemCols), "two S buffers and O");
 };
 
 struct AttMaps {
@@ -231,13 +311,14 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_free[i], kSoft);
+      mbar_init(&sm.p_full[i], kSoft);
+      mbar_init(&sm.o_full[i], 1);
     }
-    mbar_init(&sm.p_full, kSoft);
-    mbar_init(&sm.o_full, 1);
     mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.abort = 0;
     sm.any_nan = 0;
+    sm.fresh = 0;
   }
   if (warp == 4) {
     if (lane == 0) {
@@ -269,8 +350,10 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   };
 
   // ---- the query rows as e4m3 pieces: row r = token r / G, head h * G + r % G
-  if (tid < RT * (kSoft / RT < HD / 16 ? kSoft / RT : HD / 16)) {
-    constexpr int TPR = kSoft / RT < HD / 16 ? kSoft / RT : HD / 16, E = HD / TPR;  // threads per row, their elements
+  constexpr int TPR = RT <= 16 && HD == 128 ? 8 : 4;  // threads per query row
+  static_assert(RT * TPR <= kSoft && RT * TPR % 32 == 0 && HD / TPR % 16 == 0, "whole warps, 16 elements a thread");
+  if (tid < RT * TPR) {
+    constexpr int E = HD / TPR;  // elements per thread
     const int r = tid / TPR, part = tid % TPR, rr = rbase + r;
     float x[E];
 #pragma unroll
@@ -324,6 +407,8 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       st_shared_v4(base + S::kQ + swz_off<HD>(RT + r, ch), lo[0], lo[1], lo[2], lo[3]);
     }
     if (part == 0) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) sm.mneg[c][r] = -kNoRef;
       sm.cq[r] = odd ? __uint_as_float(0x7FC00000u)
                      : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
       sm.anc[r] = (p.anc && rr < R) ? p.anc[static_cast<long long>(b) * p.n + rr / G] : 0ull;
@@ -340,7 +425,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   float acc[RT], l[RT];
 #pragma unroll
   for (int r = 0; r < RT; ++r) acc[r] = l[r] = 0.f;
-  float mrun = -INFINITY;  // lane r: row r's running maximum M'
+  float mrun = kNoRef;  // lane r: row r's reference M
 
   if (warp == 4) {
     // ------------------------------------------------------- TMA producer
@@ -378,19 +463,21 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // --------------------------------------------------------- MMA issuer
     if (lane == 0) {
       constexpr uint32_t id_s = idesc_e4m3(kTile, 2 * RT, false, false);
-      constexpr uint32_t id_o = idesc_e4m3(kTile, 3 * RT, true, true);
+      constexpr uint32_t id_o = idesc_e4m3(kTile, S::kNO, true, true);
       const auto issue_o = [&](int i) {
         const int s = i % NS;
         if (!mbar_wait(&sm.full_v[s], static_cast<uint32_t>((i / NS) & 1), &sm.abort)) return false;
-        if (!mbar_wait(&sm.p_full, static_cast<uint32_t>(i & 1), &sm.abort)) return false;
+        if (!mbar_wait(&sm.p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort)) return false;
         tc_fence_after();
+        const bool fresh = *static_cast<volatile int*>(&sm.fresh) == i;
 #pragma unroll
         for (int kk = 0; kk < kTile / 32; ++kk)
           // head dim 64: the 128 rows of the A operand are the 64 dimensions twice
           umma_e4m3(tmem + 4 * RT, sdesc_rows<HD>(base + S::kV + s * S::kTileB + kk * 32 * HD, 0),
-                    sdesc_rows<kPRow>(base + S::kP + kk * 32 * kPRow, 0), id_o, kk > 0 ? 1u : 0u);
+                    sdesc_rows<kPRow>(base + S::kP + (i & 1) * S::kPB + kk * 32 * kPRow, 0), id_o,
+                    kk > 0 || !fresh ? 1u : 0u);
         umma_commit(&sm.empty_v[s]);
-        umma_commit(&sm.o_full);
+        umma_commit(&sm.o_full[i & 1]);
         return true;
       };
       bool ok = true;
@@ -424,23 +511,15 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
     const int sub = (tid % kPageSlots) / kKv8Block;
     const auto scale_at = [&](int pg) { return (static_cast<long long>(pg) * p.Hkv + h) * kKv8Sub + sub; };
-    const auto add_o = [&](int i) {  // acc = acc * alpha_i + O_i
-      mbar_wait(&sm.o_full, static_cast<uint32_t>(i & 1), &sm.abort);
+    const auto add_o = [&](int i) {  // acc += what O holds, tile i's products the last
+      mbar_wait(&sm.o_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
       tc_fence_after();
-      const float* al = sm.alpha[i & 1][warp];
       uint32_t o[RT];
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
         tmem_ld(tmem + lane_addr + (4 + q) * RT, o);
 #pragma unroll
-        for (int r = 0; r < RT; r += 4) {
-          float4 a = make_float4(1.f, 1.f, 1.f, 1.f);
-          if (q == 0) a = *reinterpret_cast<const float4*>(al + r);
-          acc[r] = fmaf(acc[r], a.x, __uint_as_float(o[r]));
-          acc[r + 1] = fmaf(acc[r + 1], a.y, __uint_as_float(o[r + 1]));
-          acc[r + 2] = fmaf(acc[r + 2], a.z, __uint_as_float(o[r + 2]));
-          acc[r + 3] = fmaf(acc[r + 3], a.w, __uint_as_float(o[r + 3]));
-        }
+        for (int r = 0; r < RT; ++r) acc[r] += __uint_as_float(o[r]);
       }
     };
     // this thread's scales, one tile ahead, and its page, two ahead
@@ -456,46 +535,62 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         vs_n = __ldg(p.vs + scale_at(pg1));
         if (i + 2 < nt) pg1 = page_of(t0 + 2 * kTile + tid);
       }
-      const float lvs = static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
-      const float ivs = pow2_inv(vs);
-      float s[RT];
+      const bool none = t >= T;  // past the end: no scale to read
+      const float lvs = none ? 0.f : static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
+      const float ivs = none ? 0.f : pow2_inv(vs);
+      const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
+      uint32_t vis = 0xFFFFFFFFu;          // bit r: row rbase + r sees slot t
+      if (masked && t >= L) {
+        const int k = t - L;
+        if (t >= T) {
+          vis = 0u;
+        } else if (p.anc) {
+          vis = 0u;
+          if (k < 64)
+            for (int r = 0; r < RT; ++r) vis |= static_cast<uint32_t>((sm.anc[r] >> k) & 1ull) << r;
+        } else {  // row rr (token rr / G) sees new slot k iff rr >= k * G
+          const int first = k * G - rbase;
+          if (first > 0) vis = first >= 32 ? 0u : 0xFFFFFFFFu << first;
+        }
+      }
       mbar_wait(&sm.s_full[buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
       tc_fence_after();
-      {
+      float s[RT];
+      const auto scores = [&] {  // s_j + log2 vs_j of this key for the tile's rows
         uint32_t w[2 * RT];
         tmem_ld(tmem + lane_addr + buf * 2 * RT, w);
+        const float2 ks2 = make_float2(ks, ks), lvs2 = make_float2(lvs, lvs);
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = __uint_as_float(w[r]) + __uint_as_float(w[RT + r]);
-      }
-      tc_fence_before();
-      mbar_arrive(&sm.s_free[buf]);
+        for (int r = 0; r < RT; r += 4) {
+          const float4 c = *reinterpret_cast<const float4*>(sm.cq + r);
 #pragma unroll
-      for (int r = 0; r < RT; r += 4) {
-        const float4 c = *reinterpret_cast<const float4*>(sm.cq + r);
-        s[r] = fmaf(s[r] * ks, c.x, lvs);
-        s[r + 1] = fmaf(s[r + 1] * ks, c.y, lvs);
-        s[r + 2] = fmaf(s[r + 2] * ks, c.z, lvs);
-        s[r + 3] = fmaf(s[r + 3] * ks, c.w, lvs);
-      }
-      const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
-      if (masked) {
-        uint32_t vis = 0u;  // bit r: row rbase + r sees slot t
-        if (t < T) {
-          vis = RT == 32 ? 0xFFFFFFFFu : (1u << RT) - 1u;
-          if (t >= L) {
-            const int k = t - L;
-            if (p.anc) {
-              vis = 0u;
-              if (k < 64)
-                for (int r = 0; r < RT; ++r) vis |= static_cast<uint32_t>((sm.anc[r] >> k) & 1ull) << r;
-            } else {  // row rr (token rr / G) sees new slot k iff rr >= k * G
-              const int first = k * G - rbase;
-              if (first > 0) vis = first >= 32 ? 0u : vis & (0xFFFFFFFFu << first);
-            }
+          for (int q = 0; q < 4; q += 2) {
+            const float2 u = add2(make_float2(__uint_as_float(w[r + q]), __uint_as_float(w[r + q + 1])),
+                                  make_float2(__uint_as_float(w[RT + r + q]), __uint_as_float(w[RT + r + q + 1])));
+            const float2 x = fma2(mul2(u, ks2), q ? make_float2(c.z, c.w) : make_float2(c.x, c.y), lvs2);
+            s[r + q] = x.x;
+            s[r + q + 1] = x.y;
           }
         }
+        if (masked) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r) s[r] = (vis >> r) & 1u ? s[r] : -INFINITY;
+          for (int r = 0; r < RT; ++r) s[r] = (vis >> r) & 1u ? s[r] : -INFINITY;
+        }
+      };
+      const auto exponents = [&] {  // s - M + 7, and the largest of them
+        float top = -INFINITY;
+#pragma unroll
+        for (int r = 0; r < RT; r += 4) {
+          const float4 m = *reinterpret_cast<const float4*>(&sm.mneg[warp][r]);
+          const float2 a = add2(make_float2(s[r], s[r + 1]), make_float2(m.x, m.y));
+          const float2 c = add2(make_float2(s[r + 2], s[r + 3]), make_float2(m.z, m.w));
+          s[r] = a.x, s[r + 1] = a.y, s[r + 2] = c.x, s[r + 3] = c.y;
+          top = fmaxf(fmaxf(top, fmaxf(a.x, a.y)), fmaxf(c.x, c.y));
+        }
+        return top;
+      };
+      scores();
+      if (masked) {
         // This thread's value row, if not every row sees it: zero past the
         // end (pages hold anything there), and NaN codes taken out (their
         // weight of 0 would not clear them) and noted for the rows that see them.
@@ -529,78 +624,79 @@ __global__ void __launch_bounds__(kAttThreads, 2)
           }
         }
       }
-      // ---- row maxima over the tile's 128 keys
-      {
-        float v[RT];
-#pragma unroll
-        for (int r = 0; r < RT; ++r) v[r] = s[r];
-        const float m = warp_rows_reduce(v, [](float a, float c) { return fmaxf(a, c); });
-        if (lane < RT) sm.red[buf][warp][lane] = m;
-      }
-      if (named_bar_any(1, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
-        stopped = true;
-        break;
-      }
-      if (lane < RT) {
-        const float m = fmaxf(fmaxf(sm.red[buf][0][lane], sm.red[buf][1][lane]),
-                              fmaxf(sm.red[buf][2][lane], sm.red[buf][3][lane]));
-        const float mn = fmaxf(mrun, m);
-        sm.alpha[buf][warp][lane] = mrun == -INFINITY ? 0.f : exp2f(mrun - mn);
-        sm.rmax[warp][lane] = mn == -INFINITY ? 0.f : mn - 8.f;
-        mrun = mn;
-      }
-      __syncwarp();
-      // ---- weights (times 2^8) and their sums
-#pragma unroll
-      for (int r = 0; r < RT; r += 4) {
-        const float4 m = *reinterpret_cast<const float4*>(&sm.rmax[warp][r]);
-        const float4 a = *reinterpret_cast<const float4*>(&sm.alpha[buf][warp][r]);
-        s[r] = exp2f(s[r] - m.x);
-        s[r + 1] = exp2f(s[r + 1] - m.y);
-        s[r + 2] = exp2f(s[r + 2] - m.z);
-        s[r + 3] = exp2f(s[r + 3] - m.w);
-        // a key that nobody may see (its scale is not read as one) adds nothing
-        l[r] = fmaf(l[r], a.x, s[r] == 0.f ? 0.f : s[r] * ivs);
-        l[r + 1] = fmaf(l[r + 1], a.y, s[r + 1] == 0.f ? 0.f : s[r + 1] * ivs);
-        l[r + 2] = fmaf(l[r + 2], a.z, s[r + 2] == 0.f ? 0.f : s[r + 2] * ivs);
-        l[r + 3] = fmaf(l[r + 3], a.w, s[r + 3] == 0.f ? 0.f : s[r + 3] * ivs);
-      }
-      if (i) add_o(i - 1);  // and P is free
-      // ---- P: this key's row, hi | mid | lo
-#pragma unroll
-      for (int c = 0; c < RT / 16; ++c) {
-        uint32_t w[3][4];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float x = s[16 * c + 2 * k], y = s[16 * c + 2 * k + 1];
-#pragma unroll
-          for (int q = 0; q < 3; ++q) {
-            const uint32_t u = e4m3x2(x, y);
-            if (q < 2) {
-              const float2 f = e4m3x2_to_f32(u);
-              x -= f.x;
-              y -= f.y;
-            }
-            w[q][k / 2] = k & 1 ? w[q][k / 2] | (u << 16) : u;
-          }
+      // ---- does any exponent pass the pieces' range?
+      const bool raise = exponents() > kTopExp;
+      if (named_bar_any(1, kSoft, raise || *static_cast<volatile int*>(&sm.abort) != 0)) {
+        // raise M to one above each row's maximum; what is summed so far shrinks by alpha
+        if (named_bar_any(2, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
+          stopped = true;
+          break;
         }
+        scores();
+        const float m = warp_rows_reduce(s, -INFINITY, [](float a, float c) { return fmaxf(a, c); });
+        if (lane < RT) sm.red[warp][lane] = m;
+        named_bar(1, kSoft);
+        if (lane < RT) {
+          const float mt = fmaxf(fmaxf(sm.red[0][lane], sm.red[1][lane]), fmaxf(sm.red[2][lane], sm.red[3][lane]));
+          const float mn = fmaxf(mrun, mt + 1.f);
+          sm.alpha[warp][lane] = exp2f(mrun - mn);
+          sm.mneg[warp][lane] = 7.f - mn;
+          mrun = mn;
+        }
+        __syncwarp();
+        if (i) add_o(i - 1);
+        if (tid == 0) sm.fresh = i;
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-          st_shared_v4(base + S::kP + swz_off<kPRow>(tid, q * (RT / 16) + c), w[q][0], w[q][1], w[q][2], w[q][3]);
+        for (int r = 0; r < RT; ++r) {
+          const float a = sm.alpha[warp][r];
+          acc[r] *= a;
+          l[r] *= a;
+        }
+        exponents();
+      }
+      tc_fence_before();
+      mbar_arrive(&sm.s_free[buf]);
+      // ---- weights (times 2^7) and their sums; P: this key's row, hi | mid | lo
+      uint32_t w[3][RT / 4];
+#pragma unroll
+      for (int r = 0; r < RT; r += 2) {
+        const float2 e = make_float2(exp2f(s[r]), exp2f(s[r + 1]));
+        const float2 sum = fma2(e, make_float2(ivs, ivs), make_float2(l[r], l[r + 1]));
+        l[r] = sum.x, l[r + 1] = sum.y;
+        uint32_t f = f16x2(e.x, e.y);
+#pragma unroll
+        for (int q = 0; q < 3; ++q) {
+          const uint32_t u = f16x2_to_e4m3x2(f);
+          if (q < 2) f = f16x2_sub(f, e4m3x2_to_f16x2(u));
+          w[q][r / 4] = r % 4 ? w[q][r / 4] | (u << 16) : u;
+        }
+      }
+      // P of tile i - 2 has been read
+      if (i >= 2) mbar_wait(&sm.o_full[buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
+      const uint32_t prow = base + S::kP + buf * S::kPB;
+      const auto word = [&](int k) { return w[k / (RT / 4)][k % (RT / 4)]; };
+#pragma unroll
+      for (int c = 0; c < 3 * RT / 16; ++c)
+        st_shared_v4(prow + swz_off<kPRow>(tid, c), word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
+      if constexpr (3 * RT % 16 != 0) {
+        constexpr int c = 3 * RT / 16;
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(prow + swz_off<kPRow>(tid, c)), "r"(word(4 * c)),
+                     "r"(word(4 * c + 1))
+                     : "memory");
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(&sm.p_full);
+      mbar_arrive(&sm.p_full[buf]);
     }
     if (nt && !stopped) add_o(nt - 1);
     // ---- this CTA's row sums
-    const float ls = warp_rows_reduce(l, [](float a, float c) { return a + c; });
+    const float ls = warp_rows_reduce(l, 0.f, [](float a, float c) { return a + c; });
     named_bar(1, kSoft);  // the last tile's maxima have been read
-    if (lane < RT) sm.red[0][warp][lane] = ls;
+    if (lane < RT) sm.red[warp][lane] = ls;
     named_bar(1, kSoft);
     if (tid < RT) {
       sm.stat[0][tid] = mrun;
-      sm.stat[1][tid] = (sm.red[0][0][tid] + sm.red[0][1][tid]) + (sm.red[0][2][tid] + sm.red[0][3][tid]);
+      sm.stat[1][tid] = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
     }
     if (sm.any_nan && tid < HD) {
 #pragma unroll
@@ -631,13 +727,13 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   for (int e = rank * kAttThreads + tid; e < rows * (HD / 4); e += C * kAttThreads) {
     const int r = e / (HD / 4), d = e % (HD / 4) * 4;
     const uint32_t a = base + S::kO + (r * HD + d) * 4;
-    float m = -INFINITY;
+    float m = kNoRef;
     for (int c = 0; c < C; ++c) m = fmaxf(m, sm.peer[0][c][r]);
     float lt = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = 0; c < C; ++c) {
       const float mc = sm.peer[0][c][r];
-      const float w = mc == -INFINITY ? 0.f : exp2f(mc - m);
+      const float w = exp2f(mc - m);  // 1 if no CTA has seen a slot: their sums are zero
       const float4 x = peer_f32x4(C > 1 ? peer_addr(a, c) : peer_addr(a, 0));
       lt = fmaf(w, sm.peer[1][c][r], lt);
       o.x = fmaf(w, x.x, o.x);
@@ -758,12 +854,25 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, C);
 }
 
+template <int HD>
+cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
+  // the row tile that leaves the fewest rows empty, the larger of equal ones
+  const int R = p.n * (p.H / p.Hkv);
+  int best = 32;
+  for (int rt = 24; rt >= 8; rt -= 8)
+    if ((R + rt - 1) / rt * rt < (R + best - 1) / best * best) best = rt;
+  switch (best) {
+    case 8: return launch_tile<HD, 8>(p, stream);
+    case 16: return launch_tile<HD, 16>(p, stream);
+    case 24: return launch_tile<HD, 24>(p, stream);
+    default: return launch_tile<HD, 32>(p, stream);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream) {
-  const bool small = p.n * (p.H / p.Hkv) <= 16;
-  if (p.hd == 128) return small ? launch_tile<128, 16>(p, stream) : launch_tile<128, 32>(p, stream);
-  return small ? launch_tile<64, 16>(p, stream) : launch_tile<64, 32>(p, stream);
+  return p.hd == 128 ? launch_rows<128>(p, stream) : launch_rows<64>(p, stream);
 }
 
 }  // namespace spec
