@@ -10,8 +10,7 @@
 // converted.  The other operand is split into e4m3 pieces that add up to it:
 //   q row = 2^k (hi + lo)            bf16 has 8 significant bits, a piece 4: exact but
 //                                    for elements 2^-18 below the row's largest
-//   p     = 2^-7 (hi + mid + lo)     an fp16 weight's 11 bits (2^-17 of the row's
-//                                    reference at the least)
+//   p     = hi + 2^-4 mid + 2^-8 lo  an fp16 weight's 11 bits (2^-18 at the least)
 // and the pieces lie side by side in the N dimension, so a tile of keys or
 // values is read from shared memory once whatever their number.
 //
@@ -27,15 +26,17 @@
 //   p'_j = p_j vs_j = 2^(s_j + log2 vs_j - M),
 // which keeps the weights that enter the product in the pieces' range; the sum
 // of the p_j themselves adds p'_j / vs_j in fp32.  The reference M of a row
-// need not be its maximum: weights up to 2^1.8 M fit the pieces, so M is set
-// one above the maximum of the first tile and raised only when a score passes
-// it by 1.75 (one barrier per tile asks whether any did).  Until then O^T adds
+// need not be its maximum: the pieces hold weights up to 448, so M is set to put
+// the maximum of the first tile at 2^2 and raised only when a weight would pass
+// 2^8.75 (one barrier per tile asks whether any does).  Until then O^T adds
 // up in TMEM and no thread reads it.  Warp 4 issues the TMA loads, warp 5 the
 // MMAs; S and P are double-buffered, so the scores of tile i + 1 and the
 // products of tile i - 1 run beside the softmax of tile i.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <cstdio>
+#include <cstdlib>
 
 #include "internal.h"
 #include "kv8_common.cuh"
@@ -45,10 +46,14 @@ namespace {
 
 constexpr int kTile = 128;                  // keys per tile
 constexpr int kSoft = 128;                  // softmax threads
-constexpr int kAttThreads = kSoft + 64;     // + TMA warp + MMA warp
-constexpr int kPRow = 128;                  // bytes of a key's row of P
+constexpr int kAttThreads = kSoft + 96;     // + TMA warp + two MMA warps
+constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 constexpr int kMaxCluster = 16;
-constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights times 2^7 that fit e4m3
+constexpr int kSortSeqs = 96;               // sequences that are put in order of length
+constexpr int kSmemCta = 227 * 1024;        // dynamic shared memory of a CTA alone on its SM,
+constexpr int kSmemHalf = 113 * 1024;       // ... and of two (1 KB of each CTA's share is the system's)
+constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
+constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
 constexpr float kNoRef = -3.402823466e38f;  // M of a row that has seen no slot: any score passes it
 
 SPEC_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
@@ -65,27 +70,31 @@ SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
       : "r"(taddr)
       : "memory");
 }
-SPEC_DEVINL void tmem_ld_x32(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-// N consecutive columns of the thread's lane (N a multiple of 8), ready for use.
+// N columns of the thread's lane at each of two places, ready for use.
 template <int N>
-SPEC_DEVINL void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  int at = 0;
-#pragma unroll
-  for (; at + 32 <= N; at += 32) tmem_ld_x32(taddr + at, r + at);
-  if constexpr (N % 32 >= 16) {
-    tmem_ld_x16(taddr + at, r + at);
-    at += 16;
+SPEC_DEVINL void tmem_ld2(uint32_t ta, uint32_t tb, uint32_t (&a)[N], uint32_t (&b)[N]) {
+  if constexpr (N == 8) {
+    tmem_ld_x8(ta, a);
+    tmem_ld_x8(tb, b);
+  } else {
+    tmem_ld_x16(ta, a);
+    tmem_ld_x16(tb, b);
   }
-  if constexpr (N % 16 >= 8) tmem_ld_x8(taddr + at, r + at);
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));  // no use moves above the wait
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));  // no use moves above the wait
+}
+SPEC_DEVINL void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
+               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+SPEC_DEVINL void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+SPEC_DEVINL void tmem_ld_wait(uint32_t (&a)[8], uint32_t (&b)[8], uint32_t (&c)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]));
 }
 
 // Two fp32 operations in one instruction.
@@ -113,15 +122,20 @@ SPEC_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
-// fp16 pairs: two fp32 rounded, the difference, to e4m3 and back (`a` low).
+// fp16 pairs: two fp32 rounded, product, a b + c, to e4m3 and back (`a` low).
 SPEC_DEVINL uint32_t f16x2(float a, float b) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-SPEC_DEVINL uint32_t f16x2_sub(uint32_t a, uint32_t b) {
+SPEC_DEVINL uint32_t f16x2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+SPEC_DEVINL uint32_t f16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
   return r;
 }
 SPEC_DEVINL uint32_t f16x2_to_e4m3x2(uint32_t a) {
@@ -150,7 +164,7 @@ __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool tra, bool t
   return (1u << 4) | (tra ? 1u << 15 : 0u) | (trb ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
          (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Shared-memory descriptor of rows of ROWB bytes (128 or 64) with the swizzle
+// Shared-memory descriptor of rows of ROWB bytes (128, 64 or 32) with the swizzle
 // of that span: 8-row groups ROWB * 8 apart (stride offset); lbo: distance
 // between two spans along an MN-major operand's own dimension.
 template <int ROWB>
@@ -160,17 +174,20 @@ SPEC_DEVINL uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
   d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
   d |= static_cast<uint64_t>((ROWB * 8) >> 4) << 32;
   d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(ROWB == 128 ? 2 : 4) << 61;
+  d |= static_cast<uint64_t>(ROWB == 128 ? 2 : (ROWB == 64 ? 4 : 6)) << 61;
   return d;
 }
 // Byte offset of 16-byte chunk c of row i in such rows.
 template <int ROWB>
 SPEC_DEVINL uint32_t swz_off(int i, int c) {
-  if constexpr (ROWB == 128)
-    return static_cast<uint32_t>(i * 128 + ((c ^ (i & 7)) << 4));
-  else
-    return static_cast<uint32_t>(i * 64 + ((c ^ ((i >> 1) & 3)) << 4));
+  if constexpr (ROWB == 128) return static_cast<uint32_t>(i * 128 + ((c ^ (i & 7)) << 4));
+  if constexpr (ROWB == 64) return static_cast<uint32_t>(i * 64 + ((c ^ ((i >> 1) & 3)) << 4));
+  return static_cast<uint32_t>(i * 32 + ((c ^ ((i >> 2) & 1)) << 4));
 }
+// ... and of chunk c of key i's row of P, which is cut into spans of 32 bytes
+// ([128 keys][32 bytes] each): three pieces of 24 rows then take 96 bytes a key
+// where a 128-byte span would take 128.
+SPEC_DEVINL uint32_t p_off(int i, int c) { return (c >> 1) * (kTile * kPSpan) + swz_off<kPSpan>(i, c & 1); }
 
 SPEC_DEVINL void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -194,6 +211,49 @@ SPEC_DEVINL float4 peer_f32x4(uint32_t a) {
   asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
   return v;
 }
+
+SPEC_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// Bound of a loop that polls barriers: more() after every turn that found
+// nothing to do; false once *abort is set or nothing was found for the wait
+// limit (and *abort then is set).
+struct Poll {
+  uint32_t turns = 0;
+  unsigned long long t0 = 0;
+  SPEC_DEVINL bool more(volatile int* abort) {
+    if ((++turns & 63u) != 0u) return true;
+    if (*abort) return false;
+    const unsigned long long now = globaltimer();
+    if (turns == 64u) t0 = now;
+    if (now - t0 <= kWaitLimitNs) return true;
+    *abort = 1;
+    return false;
+  }
+  SPEC_DEVINL void reset() { turns = 0; }
+};
+
+// A place in the ring: stage and the parity of the fill being awaited there
+// (counted along: a division by a stage count known only at run time costs the
+// one issuing thread ~100 cycles).
+struct Ring {
+  int s = 0;
+  uint32_t par = 0;
+  SPEC_DEVINL void next(int stages) {
+    if (++s == stages) {
+      s = 0;
+      par ^= 1u;
+    }
+  }
+};
 
 // Named barrier that also tells every thread whether any of them raised v.
 SPEC_DEVINL bool named_bar_any(int id, int nthreads, bool v) {
@@ -251,35 +311,36 @@ SPEC_DEVINL float warp_rows_reduce(const float (&v)[RT], float none, Op op) {
 
 template <int HD, int RT>
 struct AttSmem {
-  static constexpr int kStages = HD == 128 ? 2 : 4;
+  static constexpr int kMaxStages = 5;  // of K, and of V
   static constexpr uint32_t kTileB = kTile * HD;  // bytes of a K or V tile
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kP = kQ + 2 * RT * HD;
-  static constexpr uint32_t kPB = kTile * kPRow;  // bytes of one P buffer
+  static constexpr uint32_t kPB = (3 * RT + kPSpan - 1) / kPSpan * (kTile * kPSpan);  // bytes of one P buffer
   static constexpr uint32_t kK = kP + 2 * kPB;
-  static constexpr uint32_t kV = kK + kStages * kTileB;
-  static constexpr uint32_t kMisc = kV + kStages * kTileB;
+  // then nk K tiles, nv V tiles and Misc
   struct Misc {
-    uint64_t full_k[kStages], full_v[kStages], empty_k[kStages], empty_v[kStages];
-    uint64_t s_full[2], s_free[2], p_full[2], o_full[2], drain;
+    uint64_t full_k[kMaxStages], full_v[kMaxStages], empty_k[kMaxStages], empty_v[kMaxStages];
+    uint64_t s_full[2], s_free[2], p_full[2], o_full[2], drain[2];
     uint64_t anc[RT];
-    alignas(16) float red[4][RT];  // per-warp maxima (sums at the end); this and the next three are read as float4
-    float mneg[4][RT];         // each warp's copy of 7 - M
-    float alpha[4][RT];        // ... and of the factor of a rise of M
+    alignas(16) float red[4][RT];  // per-warp maxima (sums at the end); this and the next two are read as float4
+    float mneg[4][RT];         // each warp's copy of -M
     float cq[RT];              // score factor of a row: 2^k scale log2(e)
     float stat[2][RT];         // this CTA's M' and sum
-    float peer[2][kMaxCluster][RT];
-    uint32_t nan[RT][HD / 32]; // outputs that a NaN value code reaches
+    long long out[RT];         // where the row's output starts, -1: no such row
+    union {                    // before the loop, and from it on
+      int len[kSortSeqs];
+      uint32_t nan[RT][HD / 32];  // outputs that a NaN value code reaches
+    };
     uint32_t tmem;
-    int abort, any_nan, fresh;  // fresh: the tile whose products start O from zero
+    alignas(8) int pages[32];  // page ids of the tiles being loaded, two chunks of 16
+    int seq, seq_len, unfit, abort, any_nan;
   };
   // partial sums [RT][HD] fp32, over the K ring once every MMA is done
   static constexpr uint32_t kO = kK;
-  static_assert(offsetof(Misc, mneg) % 16 == 0 && offsetof(Misc, alpha) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 &&
-                    alignof(Misc) == 16 && kMisc % 1024 == 0,
+  static_assert(offsetof(Misc, mneg) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 && alignof(Misc) == 16 && kK % 1024 == 0,
                 "row arrays are read as float4");
-  static_assert(RT * HD * 4 <= 2 * kStages * kTileB, "the partial sums lie over the ring");
-  static constexpr uint32_t kBytes = kMisc + sizeof(Misc) + 1024;  // + alignment of the base
+  static_assert(RT * HD * 4 <= 4 * kTileB, "the partial sums lie over a ring of two stages or more");
+  static constexpr uint32_t bytes(int nk, int nv) { return kK + (nk + nv) * kTileB + sizeof(Misc) + 1024; }  // + alignment of the base
   static constexpr int kNO = (3 * RT + 15) / 16 * 16;              // O columns (M = 128 takes multiples of 16)
   static constexpr uint32_t kTmemCols = RT >= 24 ? 256 : (RT == 16 ? 128 : 64);
   static_assert(4 * RT + kNO <= static_cast<int>(kTmemCols), "two S buffers and O");
@@ -291,18 +352,19 @@ struct AttMaps {
 
 template <int HD, int RT>
 __global__ void __launch_bounds__(kAttThreads, 2)
-    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int C) {
+    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int C, const int NK, const int NV,
+                         const int longest_first) {
   using S = AttSmem<HD, RT>;
-  constexpr int NS = S::kStages;
   extern __shared__ uint8_t smem_raw[];
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  auto& sm = *reinterpret_cast<typename S::Misc*>(smem_raw + (base - smem_u32(smem_raw)) + S::kMisc);
+  const uint32_t ring_k = base + S::kK, ring_v = ring_k + NK * S::kTileB;
+  auto& sm = *reinterpret_cast<typename S::Misc*>(smem_raw + (ring_v + NV * S::kTileB - smem_u32(smem_raw)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x % C, rtile = blockIdx.x / C, h = blockIdx.y, b = blockIdx.z;
+  const int rank = blockIdx.x % C, rtile = blockIdx.x / C, h = blockIdx.y;
   const int G = p.H / p.Hkv, R = p.n * G, rbase = rtile * RT;
 
   if (tid == 0) {
-    for (int i = 0; i < NS; ++i) {
+    for (int i = 0; i < S::kMaxStages; ++i) {
       mbar_init(&sm.full_k[i], 1);
       mbar_init(&sm.full_v[i], 1);
       mbar_init(&sm.empty_k[i], 1);
@@ -313,12 +375,11 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       mbar_init(&sm.s_free[i], kSoft);
       mbar_init(&sm.p_full[i], kSoft);
       mbar_init(&sm.o_full[i], 1);
+      mbar_init(&sm.drain[i], 1);
     }
-    mbar_init(&sm.drain, 1);
     fence_mbar_init();
     sm.abort = 0;
     sm.any_nan = 0;
-    sm.fresh = 0;
   }
   if (warp == 4) {
     if (lane == 0) {
@@ -328,14 +389,34 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     __syncwarp();
     tmem_alloc(&sm.tmem, S::kTmemCols);
     tmem_relinquish();
+    tc_fence_before();
   }
+  __syncthreads();  // barriers set up
   grid_dep_wait();
   grid_dep_launch();
 
-  const int L = p.base[b];
-  const int32_t unfit = kv8_fit(L, p.n, p.table, p.max_pages, p.n_pages, b);
-  if (unfit && tid == 0) set_status(p.status, unfit);
-  const int T = unfit ? 0 : L + p.n;  // slots [0, T)
+  // Where the grid does not fit the GPU at once, its longest sequences go first
+  // (blocks start in index order): block z takes the sequence with z longer ones.
+  int b = blockIdx.z;
+  if (longest_first) {
+    if (tid < p.B) sm.len[tid] = p.base[tid];
+    __syncthreads();
+    if (tid < p.B) {
+      const int mine = sm.len[tid];
+      int before = 0;
+      for (int j = 0; j < p.B; ++j) before += sm.len[j] > mine || (sm.len[j] == mine && j < tid);
+      if (before == static_cast<int>(blockIdx.z)) {
+        sm.seq = tid;
+        sm.seq_len = mine;
+      }
+    }
+    __syncthreads();
+    b = sm.seq;
+  }
+  const int L = longest_first ? sm.seq_len : p.base[b];
+  const int cap = p.max_pages * kPageSlots;
+  const bool over = L < 0 || L > cap - p.n;
+  const int T = over ? 0 : L + p.n;  // slots [0, T)
   const int tiles = (T + kTile - 1) / kTile;
   const int i0 = static_cast<int>(static_cast<long long>(tiles) * rank / C);
   const int nt = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / C) - i0;  // this CTA's tiles
@@ -411,95 +492,129 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       for (int c = 0; c < 4; ++c) sm.mneg[c][r] = -kNoRef;
       sm.cq[r] = odd ? __uint_as_float(0x7FC00000u)
                      : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+      sm.out[r] =
+          rr < R ? (static_cast<long long>(b) * p.n + rr / G) * p.o_ld + static_cast<long long>(h * G + rr % G) * HD : -1;
       sm.anc[r] = (p.anc && rr < R) ? p.anc[static_cast<long long>(b) * p.n + rr / G] : 0ull;
 #pragma unroll
       for (int c = 0; c < HD / 32; ++c) sm.nan[r][c] = 0u;
     }
     fence_async_smem();
   }
-  tc_fence_before();
-  __syncthreads();
+  // q, the row arrays and the TMEM address are ready (the TMA warp goes ahead)
+  if (warp != 4) named_bar(3, kSoft + 64);
   tc_fence_after();
   const uint32_t tmem = sm.tmem;
 
-  float acc[RT], l[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) acc[r] = l[r] = 0.f;
   float mrun = kNoRef;  // lane r: row r's reference M
 
   if (warp == 4) {
     // ------------------------------------------------------- TMA producer
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_first();
-      int issued = 0;
-      const auto load = [&](const CUtensorMap* m, uint32_t dst, uint64_t* bar, int i) {
-        const int t = (i0 + i) * kTile;
-        const int np = T - t > kPageSlots ? 2 : 1;  // a page past the end is not read
-        mbar_arrive_expect_tx(bar, static_cast<uint32_t>(np * kPageSlots * HD));
-        for (int g = 0; g < np; ++g)
-          tma_load_2d_s(dst + g * kPageSlots * HD, m, bar, 0, (page_of(t + g * kPageSlots) * p.Hkv + h) * kPageSlots,
-                        pol);
-      };
-      for (int i = 0; i < nt; ++i) {
-        const int s = i % NS;
-        const uint32_t par = static_cast<uint32_t>((i / NS - 1) & 1);
-        if (i >= NS && !mbar_wait(&sm.empty_k[s], par, &sm.abort)) break;
-        load(&maps.k, base + S::kK + s * S::kTileB, &sm.full_k[s], i);
-        issued = 2 * i + 1;
-        if (i >= NS && !mbar_wait(&sm.empty_v[s], par, &sm.abort)) break;
-        load(&maps.v, base + S::kV + s * S::kTileB, &sm.full_v[s], i);
-        issued = 2 * i + 2;
+    // Page ids come 16 at a time (8 tiles), the next 16 on their way: a
+    // lookup per page in line with the loads took ~500 cycles each.
+    const uint64_t pol = l2_policy_evict_first();
+    const int entries = (T + kPageSlots - 1) / kPageSlots - 2 * i0;  // pages from this CTA's first slot on
+    const auto page_at = [&](int e) { return e < entries ? page_of(i0 * kTile + e * kPageSlots) : 0; };
+    int next = nt > 0 && lane < 16 ? page_at(lane) : 0;
+    int ki = 0, vi = 0, chunk = -1;
+    Poll idle;
+    Ring kr, vr;
+    const auto load = [&](const CUtensorMap* m, uint32_t dst, uint64_t* bar, int i) {
+      const bool two = entries - 2 * i > 1;  // a page past the end is not read
+      const int2 pg = *reinterpret_cast<const int2*>(&sm.pages[(2 * i) % 32]);
+      mbar_arrive_expect_tx(bar, (two ? 2u : 1u) * kPageSlots * HD);
+      tma_load_2d_s(dst, m, bar, 0, (pg.x * p.Hkv + h) * kPageSlots, pol);
+      if (two) tma_load_2d_s(dst + kPageSlots * HD, m, bar, 0, (pg.y * p.Hkv + h) * kPageSlots, pol);
+    };
+    // K and V each as soon as their stage is free (K's is when the scores are
+    // in TMEM, V's when its products are)
+    while (vi < nt) {
+      // the chunk before is kept, for V: it follows K by no more than the K
+      // stages and the 3 tiles between the scores and the products
+      if (ki < nt && ki % 8 == 0 && ki != chunk) {
+        chunk = ki;
+        __syncwarp();
+        if (lane < 16) {
+          sm.pages[(2 * ki + lane) % 32] = next;
+          next = page_at(2 * ki + 16 + lane);
+        }
+        __syncwarp();
       }
+      int did = 0, go = 1;
+      if (lane == 0) {
+        if (ki < nt && (ki < NK || mbar_test(&sm.empty_k[kr.s], kr.par ^ 1u))) {
+          load(&maps.k, ring_k + kr.s * S::kTileB, &sm.full_k[kr.s], ki);
+          kr.next(NK);
+          did = 1;
+        }
+        if (vi < ki + did && (vi < NV || mbar_test(&sm.empty_v[vr.s], vr.par ^ 1u))) {
+          load(&maps.v, ring_v + vr.s * S::kTileB, &sm.full_v[vr.s], vi);
+          vr.next(NV);
+          did |= 2;
+        }
+        if (did)
+          idle.reset();
+        else
+          go = idle.more(&sm.abort);
+      }
+      did = __shfl_sync(0xffffffffu, did, 0);
+      ki += did & 1;
+      vi += did >> 1;
+      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+    }
+    if (lane == 0) {
       if (sm.abort) {  // loads in flight land before the CTA leaves (bounded as every wait)
         int none = 0;
-        for (int k = max(0, issued - 2 * NS); k < issued; ++k) {
-          const int i = k / 2;
-          mbar_wait(k & 1 ? &sm.full_v[i % NS] : &sm.full_k[i % NS], static_cast<uint32_t>((i / NS) & 1), &none);
-        }
+        for (int i = max(0, ki - NK); i < ki; ++i)
+          mbar_wait(&sm.full_k[i % NK], static_cast<uint32_t>((i / NK) & 1), &none);
+        for (int i = max(0, vi - NV); i < vi; ++i)
+          mbar_wait(&sm.full_v[i % NV], static_cast<uint32_t>((i / NV) & 1), &none);
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
-    // --------------------------------------------------------- MMA issuer
+  } else if (warp >= 5) {
+    // -------------------------------- MMA issuers: scores (5), products (6)
+    // A thread issues one MMA per ~90 cycles whatever its N, so the two
+    // products of a tile come from two threads.
     if (lane == 0) {
-      constexpr uint32_t id_s = idesc_e4m3(kTile, 2 * RT, false, false);
-      constexpr uint32_t id_o = idesc_e4m3(kTile, S::kNO, true, true);
-      const auto issue_o = [&](int i) {
-        const int s = i % NS;
-        if (!mbar_wait(&sm.full_v[s], static_cast<uint32_t>((i / NS) & 1), &sm.abort)) return false;
-        if (!mbar_wait(&sm.p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort)) return false;
-        tc_fence_after();
-        const bool fresh = *static_cast<volatile int*>(&sm.fresh) == i;
-#pragma unroll
-        for (int kk = 0; kk < kTile / 32; ++kk)
-          // head dim 64: the 128 rows of the A operand are the 64 dimensions twice
-          umma_e4m3(tmem + 4 * RT, sdesc_rows<HD>(base + S::kV + s * S::kTileB + kk * 32 * HD, 0),
-                    sdesc_rows<kPRow>(base + S::kP + (i & 1) * S::kPB + kk * 32 * kPRow, 0), id_o,
-                    kk > 0 || !fresh ? 1u : 0u);
-        umma_commit(&sm.empty_v[s]);
-        umma_commit(&sm.o_full[i & 1]);
-        return true;
-      };
+      const bool scores = warp == 5;
+      const int stages = scores ? NK : NV;
+      Ring ring;
       bool ok = true;
-      for (int i = 0; i < nt && ok; ++i) {
-        const int s = i % NS;
-        ok = mbar_wait(&sm.full_k[s], static_cast<uint32_t>((i / NS) & 1), &sm.abort) &&
-             (i < 2 || mbar_wait(&sm.s_free[i & 1], static_cast<uint32_t>((i / 2 - 1) & 1), &sm.abort));
-        if (!ok) break;
-        tc_fence_after();
+      const uint64_t a0 = scores ? sdesc_rows<HD>(ring_k, 16) : sdesc_rows<HD>(ring_v, 0);
+      const uint64_t b0 = scores ? sdesc_rows<HD>(base + S::kQ, 16) : sdesc_rows<kPSpan>(base + S::kP, kTile * kPSpan);
+      for (int i = 0; i < nt; ++i) {
+        const uint64_t a = a0 + static_cast<uint32_t>(ring.s) * (S::kTileB >> 4);
+        if (scores) {
+          ok = (i < 2 || mbar_wait(&sm.s_free[i & 1], static_cast<uint32_t>((i / 2 - 1) & 1), &sm.abort)) &&
+               mbar_wait(&sm.full_k[ring.s], ring.par, &sm.abort);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < HD / 32; ++kk)
-          umma_e4m3(tmem + (i & 1) * 2 * RT, sdesc_rows<HD>(base + S::kK + s * S::kTileB + kk * 32, 16),
-                    sdesc_rows<HD>(base + S::kQ + kk * 32, 16), id_s, kk > 0 ? 1u : 0u);
-        umma_commit(&sm.empty_k[s]);
-        umma_commit(&sm.s_full[i & 1]);
-        if (i) ok = issue_o(i - 1);
+          for (int kk = 0; kk < HD / 32; ++kk)
+            umma_e4m3(tmem + (i & 1) * 2 * RT, a + kk * 2, b0 + kk * 2, idesc_e4m3(kTile, 2 * RT, false, false),
+                      kk > 0 ? 1u : 0u);
+          umma_commit(&sm.s_full[i & 1]);
+          umma_commit(&sm.empty_k[ring.s]);
+        } else {
+          ok = mbar_wait(&sm.full_v[ring.s], ring.par, &sm.abort) &&
+               mbar_wait(&sm.p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bp = b0 + static_cast<uint32_t>(i & 1) * (S::kPB >> 4);
+#pragma unroll
+          for (int kk = 0; kk < kTile / 32; ++kk)
+            // head dim 64: the 128 rows of the A operand are the 64 dimensions twice
+            umma_e4m3(tmem + 4 * RT, a + kk * (32 * HD >> 4), bp + kk * (32 * kPSpan >> 4),
+                      idesc_e4m3(kTile, S::kNO, true, true), i > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(&sm.o_full[i & 1]);
+          umma_commit(&sm.empty_v[ring.s]);
+        }
+        ring.next(stages);
       }
-      if (ok && nt) ok = issue_o(nt - 1);
       if (!ok) {  // MMAs in flight end before TMEM and shared memory go
         int none = 0;
-        umma_commit(&sm.drain);
-        mbar_wait(&sm.drain, 0, &none);
+        umma_commit(&sm.drain[scores ? 0 : 1]);
+        mbar_wait(&sm.drain[scores ? 0 : 1], 0, &none);
       }
     }
     __syncwarp();
@@ -511,65 +626,83 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
     const int sub = (tid % kPageSlots) / kKv8Block;
     const auto scale_at = [&](int pg) { return (static_cast<long long>(pg) * p.Hkv + h) * kKv8Sub + sub; };
-    const auto add_o = [&](int i) {  // acc += what O holds, tile i's products the last
-      mbar_wait(&sm.o_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
-      tc_fence_after();
-      uint32_t o[RT];
-#pragma unroll
-      for (int q = 0; q < 3; ++q) {
-        tmem_ld(tmem + lane_addr + (4 + q) * RT, o);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) acc[r] += __uint_as_float(o[r]);
+    const auto seen = [&](int t) {  // bit r: row rbase + r sees slot t
+      if (t < L) return 0xFFFFFFFFu;
+      if (t >= T) return 0u;
+      const int k = t - L;
+      if (p.anc) {
+        uint32_t m = 0u;
+        if (k < 64)
+#pragma unroll 1
+          for (int r = 0; r < RT; ++r) m |= static_cast<uint32_t>((sm.anc[r] >> k) & 1ull) << r;
+        return m;
       }
+      const int first = k * G - rbase;  // row rr (token rr / G) sees new slot k iff rr >= k * G
+      return first <= 0 ? 0xFFFFFFFFu : (first >= 32 ? 0u : 0xFFFFFFFFu << first);
     };
-    // this thread's scales, one tile ahead, and its page, two ahead
-    int pg1 = nt > 0 ? page_of(i0 * kTile + tid) : 0;
-    float ks_n = nt > 0 ? __ldg(p.ks + scale_at(pg1)) : 1.f, vs_n = nt > 0 ? __ldg(p.vs + scale_at(pg1)) : 1.f;
-    pg1 = nt > 1 ? page_of((i0 + 1) * kTile + tid) : 0;
+    // the pages that the new slots lie on, looked at in the end
+    const int new_pages = over ? 0 : (T - 1) / kPageSlots - L / kPageSlots + 1;
+    const int new_page = tid < new_pages ? __ldg(table + L / kPageSlots + tid) : 0;
+    // rows r .. r + 7 of O, the pieces put together
+    const auto o_rows = [&](int r, float (&o)[8]) {
+      uint32_t w[3][8];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) tmem_ld_x8(tmem + lane_addr + (4 + q) * RT + r, w[q]);
+      tmem_ld_wait(w[0], w[1], w[2]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        o[k] = fmaf(__uint_as_float(w[2][k]), 0.00390625f,
+                    fmaf(__uint_as_float(w[1][k]), 0.0625f, __uint_as_float(w[0][k])));
+    };
+    float l[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) l[r] = 0.f;
+    // this thread's scales, one tile ahead, and its page, two ahead (the TMA
+    // warp flags ids outside the pool; here they are clamped)
+    const int last_page = p.max_pages - 1;
+    const auto page_id = [&](int i) { return __ldg(table + min(((i0 + i) * kTile + tid) / kPageSlots, last_page)); };
+    const auto scale_of = [&](const float* sc, int pg) {
+      return __ldg(sc + scale_at(min(max(pg, 0), p.n_pages - 1)));
+    };
+    int pg1 = nt > 0 ? page_id(0) : 0;
+    float ks_n = nt > 0 ? scale_of(p.ks, pg1) : 1.f, vs_n = nt > 0 ? scale_of(p.vs, pg1) : 1.f;
+    pg1 = nt > 1 ? page_id(1) : 0;
     bool stopped = false;
-    for (int i = 0; i < nt; ++i) {
+    Ring vring;
+    for (int i = 0; i < nt; ++i, vring.next(NV)) {
       const int buf = i & 1, t0 = (i0 + i) * kTile, t = t0 + tid;
       const float ks = ks_n, vs = vs_n;
       if (i + 1 < nt) {
-        ks_n = __ldg(p.ks + scale_at(pg1));
-        vs_n = __ldg(p.vs + scale_at(pg1));
-        if (i + 2 < nt) pg1 = page_of(t0 + 2 * kTile + tid);
+        ks_n = scale_of(p.ks, pg1);
+        vs_n = scale_of(p.vs, pg1);
+        pg1 = page_id(i + 2);
       }
       const bool none = t >= T;  // past the end: no scale to read
       const float lvs = none ? 0.f : static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
       const float ivs = none ? 0.f : pow2_inv(vs);
       const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
-      uint32_t vis = 0xFFFFFFFFu;          // bit r: row rbase + r sees slot t
-      if (masked && t >= L) {
-        const int k = t - L;
-        if (t >= T) {
-          vis = 0u;
-        } else if (p.anc) {
-          vis = 0u;
-          if (k < 64)
-            for (int r = 0; r < RT; ++r) vis |= static_cast<uint32_t>((sm.anc[r] >> k) & 1ull) << r;
-        } else {  // row rr (token rr / G) sees new slot k iff rr >= k * G
-          const int first = k * G - rbase;
-          if (first > 0) vis = first >= 32 ? 0u : 0xFFFFFFFFu << first;
-        }
-      }
+      const uint32_t vis = masked ? seen(t) : 0xFFFFFFFFu;
       mbar_wait(&sm.s_full[buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
       tc_fence_after();
       float s[RT];
       const auto scores = [&] {  // s_j + log2 vs_j of this key for the tile's rows
-        uint32_t w[2 * RT];
-        tmem_ld(tmem + lane_addr + buf * 2 * RT, w);
         const float2 ks2 = make_float2(ks, ks), lvs2 = make_float2(lvs, lvs);
+        constexpr int GR = RT >= 24 ? 8 : RT;  // rows at a time (registers)
 #pragma unroll
-        for (int r = 0; r < RT; r += 4) {
-          const float4 c = *reinterpret_cast<const float4*>(sm.cq + r);
+        for (int r0 = 0; r0 < RT; r0 += GR) {
+          uint32_t hi[GR], lo[GR];
+          tmem_ld2(tmem + lane_addr + buf * 2 * RT + r0, tmem + lane_addr + buf * 2 * RT + RT + r0, hi, lo);
 #pragma unroll
-          for (int q = 0; q < 4; q += 2) {
-            const float2 u = add2(make_float2(__uint_as_float(w[r + q]), __uint_as_float(w[r + q + 1])),
-                                  make_float2(__uint_as_float(w[RT + r + q]), __uint_as_float(w[RT + r + q + 1])));
-            const float2 x = fma2(mul2(u, ks2), q ? make_float2(c.z, c.w) : make_float2(c.x, c.y), lvs2);
-            s[r + q] = x.x;
-            s[r + q + 1] = x.y;
+          for (int r = 0; r < GR; r += 4) {
+            const float4 c = *reinterpret_cast<const float4*>(sm.cq + r0 + r);
+#pragma unroll
+            for (int q = 0; q < 4; q += 2) {
+              const float2 u = add2(make_float2(__uint_as_float(hi[r + q]), __uint_as_float(hi[r + q + 1])),
+                                    make_float2(__uint_as_float(lo[r + q]), __uint_as_float(lo[r + q + 1])));
+              const float2 x = fma2(mul2(u, ks2), q ? make_float2(c.z, c.w) : make_float2(c.x, c.y), lvs2);
+              s[r0 + r + q] = x.x;
+              s[r0 + r + q + 1] = x.y;
+            }
           }
         }
         if (masked) {
@@ -577,7 +710,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
           for (int r = 0; r < RT; ++r) s[r] = (vis >> r) & 1u ? s[r] : -INFINITY;
         }
       };
-      const auto exponents = [&] {  // s - M + 7, and the largest of them
+      const auto exponents = [&] {  // s - M, and the largest of them
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
@@ -591,96 +724,119 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       };
       scores();
       if (masked) {
-        // This thread's value row, if not every row sees it: zero past the
-        // end (pages hold anything there), and NaN codes taken out (their
-        // weight of 0 would not clear them) and noted for the rows that see them.
-        const uint32_t vt = base + S::kV + (i % NS) * S::kTileB;
-        mbar_wait(&sm.full_v[i % NS], static_cast<uint32_t>((i / NS) & 1), &sm.abort);
-        if (t >= L) {
+        // Value rows that not every query row sees: zero past the end (pages
+        // hold anything there), and NaN codes of new slots taken out (a weight
+        // of 0 would not clear them) and noted for the rows that see them.
+        const uint32_t vt = ring_v + vring.s * S::kTileB;
+        mbar_wait(&sm.full_v[vring.s], vring.par, &sm.abort);
+        constexpr int VEC = HD / 16;
+        const int row0 = max(L - t0, 0);
+        for (int e = row0 * VEC + tid; e < kTile * VEC; e += kSoft) {
+          const int row = e / VEC, c = e % VEC;
+          const uint32_t a = vt + swz_off<HD>(row, c);
+          if (t0 + row >= T) {
+            st_shared_v4(a, 0, 0, 0, 0);
+            continue;
+          }
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(a)
+                       : "memory");
+          uint32_t hit = 0u;  // bytes 0x7F (but for the sign): the NaN codes
+#pragma unroll
+          for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+          if (!hit) continue;
+          sm.any_nan = 1;
+          const uint32_t m = seen(t0 + row);
 #pragma unroll 1
-          for (int c = 0; c < HD / 16; ++c) {
-            const uint32_t a = vt + swz_off<HD>(tid, c);
-            if (t >= T) {
-              st_shared_v4(a, 0, 0, 0, 0);
-              continue;
-            }
+          for (int k = 0; k < 16; ++k) {
+            uint32_t byte;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(byte) : "r"(a + k) : "memory");
+            if ((byte & 0x7Fu) != 0x7Fu) continue;
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(a + k), "r"(0) : "memory");
+            const int d = c * 16 + k;
 #pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-              uint32_t w;
-              asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w) : "r"(a + 4 * k) : "memory");
-              const uint32_t m = w & 0x7F7F7F7Fu;
-              const uint32_t hit = (m + 0x01010101u) & 0x80808080u;  // bytes 0x7F: the NaN codes
-              if (!hit) continue;
-              sm.any_nan = 1;
-              for (int q = 0; q < 4; ++q) {
-                if (!((hit >> (8 * q + 7)) & 1u)) continue;
-                w &= ~(0xFFu << (8 * q));
-                const int d = c * 16 + k * 4 + q;
-                for (int r = 0; r < RT; ++r)
-                  if ((vis >> r) & 1u) atomicOr(&sm.nan[r][d / 32], 1u << (d % 32));
-              }
-              asm volatile("st.shared.b32 [%0], %1;" ::"r"(a + 4 * k), "r"(w) : "memory");
-            }
+            for (int r = 0; r < RT; ++r)
+              if ((m >> r) & 1u) atomicOr(&sm.nan[r][d / 32], 1u << (d % 32));
           }
         }
       }
       // ---- does any exponent pass the pieces' range?
-      const bool raise = exponents() > kTopExp;
+      const bool raise = i == 0 || exponents() > kTopExp;  // (the first tile sets M)
       if (named_bar_any(1, kSoft, raise || *static_cast<volatile int*>(&sm.abort) != 0)) {
-        // raise M to one above each row's maximum; what is summed so far shrinks by alpha
+        // raise M to each row's maximum (at 2^2); what is summed so far shrinks by alpha
         if (named_bar_any(2, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
           stopped = true;
           break;
         }
-        scores();
+        if (i) scores();
+        float alpha = 1.f;  // lane r: row r's
         const float m = warp_rows_reduce(s, -INFINITY, [](float a, float c) { return fmaxf(a, c); });
         if (lane < RT) sm.red[warp][lane] = m;
         named_bar(1, kSoft);
         if (lane < RT) {
           const float mt = fmaxf(fmaxf(sm.red[0][lane], sm.red[1][lane]), fmaxf(sm.red[2][lane], sm.red[3][lane]));
-          const float mn = fmaxf(mrun, mt + 1.f);
-          sm.alpha[warp][lane] = exp2f(mrun - mn);
-          sm.mneg[warp][lane] = 7.f - mn;
+          const float mn = fmaxf(mrun, mt - kStartExp);
+          alpha = exp2f(mrun - mn);
+          sm.mneg[warp][lane] = -mn;
           mrun = mn;
         }
         __syncwarp();
-        if (i) add_o(i - 1);
-        if (tid == 0) sm.fresh = i;
+        if (i) {  // O and l shrink with it (O's pieces become one)
+          mbar_wait(&sm.o_full[(i - 1) & 1], static_cast<uint32_t>(((i - 1) >> 1) & 1), &sm.abort);
+          tc_fence_after();
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float a = sm.alpha[warp][r];
-          acc[r] *= a;
-          l[r] *= a;
+          for (int r = 0; r < RT; r += 8) {
+            float o[8];
+            o_rows(r, o);
+            uint32_t w[8], z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float a = __shfl_sync(0xffffffffu, alpha, r + k);
+              l[r + k] *= a;
+              w[k] = __float_as_uint(o[k] * a);
+              z[k] = 0u;
+            }
+            tmem_st_x8(tmem + lane_addr + 4 * RT + r, w);
+            tmem_st_x8(tmem + lane_addr + 5 * RT + r, z);
+            tmem_st_x8(tmem + lane_addr + 6 * RT + r, z);
+          }
+          tmem_st_wait();
         }
         exponents();
       }
       tc_fence_before();
       mbar_arrive(&sm.s_free[buf]);
-      // ---- weights (times 2^7) and their sums; P: this key's row, hi | mid | lo
+      // ---- weights and their sums; P: this key's row, hi | mid | lo
       uint32_t w[3][RT / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
         const float2 e = make_float2(exp2f(s[r]), exp2f(s[r + 1]));
         const float2 sum = fma2(e, make_float2(ivs, ivs), make_float2(l[r], l[r + 1]));
         l[r] = sum.x, l[r + 1] = sum.y;
-        uint32_t f = f16x2(e.x, e.y);
-#pragma unroll
-        for (int q = 0; q < 3; ++q) {
-          const uint32_t u = f16x2_to_e4m3x2(f);
-          if (q < 2) f = f16x2_sub(f, e4m3x2_to_f16x2(u));
-          w[q][r / 4] = r % 4 ? w[q][r / 4] | (u << 16) : u;
-        }
+        // p = hi + mid / 16 + lo / 256, each the nearest e4m3 of what is left
+        // times 1, 16 and 256 (fp16 holds every difference exactly)
+        const uint32_t f = f16x2(e.x, e.y);
+        const uint32_t u0 = f16x2_to_e4m3x2(f);
+        const uint32_t f1 = f16x2_fma(e4m3x2_to_f16x2(u0), 0xBC00BC00u, f);  // - hi
+        const uint32_t u1 = f16x2_to_e4m3x2(f16x2_mul(f1, 0x4C004C00u));     // x 16
+        const uint32_t f2 = f16x2_fma(e4m3x2_to_f16x2(u1), 0xAC00AC00u, f1); // - mid / 16
+        const uint32_t u2 = f16x2_to_e4m3x2(f16x2_mul(f2, 0x5C005C00u));     // x 256
+        w[0][r / 4] = r % 4 ? w[0][r / 4] | (u0 << 16) : u0;
+        w[1][r / 4] = r % 4 ? w[1][r / 4] | (u1 << 16) : u1;
+        w[2][r / 4] = r % 4 ? w[2][r / 4] | (u2 << 16) : u2;
       }
       // P of tile i - 2 has been read
       if (i >= 2) mbar_wait(&sm.o_full[buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
-      const uint32_t prow = base + S::kP + buf * S::kPB;
+      const uint32_t pbuf = base + S::kP + buf * S::kPB;
       const auto word = [&](int k) { return w[k / (RT / 4)][k % (RT / 4)]; };
 #pragma unroll
       for (int c = 0; c < 3 * RT / 16; ++c)
-        st_shared_v4(prow + swz_off<kPRow>(tid, c), word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
+        st_shared_v4(pbuf + p_off(tid, c), word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
       if constexpr (3 * RT % 16 != 0) {
         constexpr int c = 3 * RT / 16;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(prow + swz_off<kPRow>(tid, c)), "r"(word(4 * c)),
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(pbuf + p_off(tid, c)), "r"(word(4 * c)),
                      "r"(word(4 * c + 1))
                      : "memory");
       }
@@ -688,68 +844,103 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       tc_fence_before();
       mbar_arrive(&sm.p_full[buf]);
     }
-    if (nt && !stopped) add_o(nt - 1);
     // ---- this CTA's row sums
     const float ls = warp_rows_reduce(l, 0.f, [](float a, float c) { return a + c; });
-    named_bar(1, kSoft);  // the last tile's maxima have been read
+    // (and the last maxima have been read)
+    const bool bad_page = named_bar_any(2, kSoft, new_page < 0 || new_page >= p.n_pages);
+    const bool unfit = over || bad_page;  // zero rows
+    if (tid == 0) {
+      sm.unfit = unfit;
+      if (unfit) set_status(p.status, over ? SPEC_DEV_KV_OVERFLOW : SPEC_DEV_BAD_PAGE);
+    }
     if (lane < RT) sm.red[warp][lane] = ls;
     named_bar(1, kSoft);
     if (tid < RT) {
       sm.stat[0][tid] = mrun;
       sm.stat[1][tid] = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
     }
-    if (sm.any_nan && tid < HD) {
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-        if ((sm.nan[r][tid / 32] >> (tid % 32)) & 1u) acc[r] = __uint_as_float(0x7FC00000u);
+    if (C == 1) named_bar(1, kSoft);
+    // ---- O: dimension tid of every row, to the output, or to shared memory for the merge
+    if (nt && !stopped) {
+      mbar_wait(&sm.o_full[(nt - 1) & 1], static_cast<uint32_t>(((nt - 1) >> 1) & 1), &sm.abort);
+      tc_fence_after();
     }
-    if (tid < HD) {
+    const bool any_nan = sm.any_nan != 0;
+#pragma unroll 1
+    for (int r = 0; r < RT; r += 8) {
+      float o[8];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::kO + (r * HD + tid) * 4), "f"(acc[r]) : "memory");
+      for (int k = 0; k < 8; ++k) o[k] = 0.f;
+      if (nt) o_rows(r, o);
+      if (tid < HD) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (any_nan && ((sm.nan[r + k][tid / 32] >> (tid % 32)) & 1u)) o[k] = __uint_as_float(0x7FC00000u);
+          if (C > 1) {
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::kO + ((r + k) * HD + tid) * 4), "f"(o[k])
+                         : "memory");
+          } else if (sm.out[r + k] >= 0) {
+            const float lt = sm.stat[1][r + k];
+            const float x = lt == 0.f || unfit ? 0.f : o[k] * (1.f / lt);  // a row that sees nothing is zero
+            uint32_t u;
+            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(0.f), "f"(x));
+            p.o[sm.out[r + k] + tid] = static_cast<uint16_t>(u);
+          }
+        }
+      }
     }
   }
 
+  if (C > 1) {
+    const int rows = min(RT, R - rbase);
   // ---- merge: the cluster's CTAs share the (row, 4 dimensions) items
-  __syncwarp();
-  if (C > 1)
+    __syncwarp();
     cluster_sync_all();
-  else
-    __syncthreads();
-  const uint32_t stat = smem_u32(&sm.stat[0][0]);
-  for (int e = tid; e < 2 * C * RT; e += kAttThreads) {
-    const int which = e / (C * RT), c = (e / RT) % C, r = e % RT;
-    const uint32_t a = stat + (which * RT + r) * 4;
-    sm.peer[which][c][r] = C > 1 ? peer_f32(peer_addr(a, c)) : sm.stat[which][r];
-  }
-  __syncthreads();
-  const int rows = min(RT, R - rbase);
-  for (int e = rank * kAttThreads + tid; e < rows * (HD / 4); e += C * kAttThreads) {
-    const int r = e / (HD / 4), d = e % (HD / 4) * 4;
-    const uint32_t a = base + S::kO + (r * HD + d) * 4;
-    float m = kNoRef;
-    for (int c = 0; c < C; ++c) m = fmaxf(m, sm.peer[0][c][r]);
-    float lt = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = 0; c < C; ++c) {
-      const float mc = sm.peer[0][c][r];
-      const float w = exp2f(mc - m);  // 1 if no CTA has seen a slot: their sums are zero
-      const float4 x = peer_f32x4(C > 1 ? peer_addr(a, c) : peer_addr(a, 0));
-      lt = fmaf(w, sm.peer[1][c][r], lt);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
+    const uint32_t stat = smem_u32(&sm.stat[0][0]);
+    for (int e = rank * kAttThreads + tid; e < rows * (HD / 4); e += C * kAttThreads) {
+      const int r = e / (HD / 4), d = e % (HD / 4) * 4;
+      // every peer's reference, sum and four partial sums, all loads in flight together
+      float mc[kMaxCluster], lc[kMaxCluster];
+      float4 x[kMaxCluster];
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        mc[c] = kNoRef;
+        lc[c] = 0.f;
+        x[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < C) {
+          mc[c] = peer_f32(peer_addr(stat + r * 4, c));
+          lc[c] = peer_f32(peer_addr(stat + (RT + r) * 4, c));
+          x[c] = peer_f32x4(peer_addr(base + S::kO + (r * HD + d) * 4, c));
+        }
+      }
+      float m = kNoRef, lt = 0.f;
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) m = fmaxf(m, mc[c]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < kMaxCluster; ++c) {
+        if (c >= C) break;
+        const float w = exp2f(mc[c] - m);  // 1 if no CTA has seen a slot: their sums are zero
+        lt = fmaf(w, lc[c], lt);
+        o.x = fmaf(w, x[c].x, o.x);
+        o.y = fmaf(w, x[c].y, o.y);
+        o.z = fmaf(w, x[c].z, o.z);
+        o.w = fmaf(w, x[c].w, o.w);
+      }
+      const bool zero = lt == 0.f || sm.unfit;  // a row that sees nothing
+      const float inv = 1.f / lt;
+      o.x = zero ? 0.f : o.x * inv;
+      o.y = zero ? 0.f : o.y * inv;
+      o.z = zero ? 0.f : o.z * inv;
+      o.w = zero ? 0.f : o.w * inv;
+      uint2 u;
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y), "f"(o.x));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w), "f"(o.z));
+      *reinterpret_cast<uint2*>(p.o + sm.out[r] + d) = u;
     }
-    const float inv = lt == 0.f ? 0.f : 1.f / lt;  // a row that sees nothing is zero
-    const int rr = rbase + r;
-    uint2 u;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y * inv), "f"(o.x * inv));
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w * inv), "f"(o.z * inv));
-    *reinterpret_cast<uint2*>(p.o + (static_cast<long long>(b) * p.n + rr / G) * p.o_ld + (h * G + rr % G) * HD + d) =
-        u;
+    __syncwarp();
+    cluster_sync_all();  // peers' shared memory stays until every CTA has read it
   }
-  if (C > 1) cluster_sync_all();  // peers' shared memory stays until every CTA has read it
   if (tid == 0 && sm.abort) set_status(p.status, SPEC_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
@@ -810,7 +1001,7 @@ cudaLaunchConfig_t att_config(dim3 grid, uint32_t smem, cudaStream_t stream, cud
 
 template <int HD, int RT>
 cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
-  constexpr uint32_t smem = AttSmem<HD, RT>::kBytes;
+  using S = AttSmem<HD, RT>;
   static PerDevice<AttSetup> setup;
   AttSetup s{};
   if (!setup.get(
@@ -821,13 +1012,13 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
             if ((r.err = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return r;
             const auto fn = kv8_attention_kernel<HD, RT>;
             if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              static_cast<int>(smem))) != cudaSuccess)
+                                              kSmemCta)) != cudaSuccess)
               return r;
             if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
               return r;
             for (int c = kMaxCluster; c > 1; c /= 2) {
               cudaLaunchAttribute attr[2];
-              cudaLaunchConfig_t cfg = att_config(dim3(c), smem, nullptr, attr, c);
+              cudaLaunchConfig_t cfg = att_config(dim3(c), kSmemHalf, nullptr, attr, c);
               cfg.numAttrs = 1;
               int n = 0;
               if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0) {
@@ -846,12 +1037,19 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
   int C = 1;
   while (2 * C <= s.max_cluster && 2 * C <= tiles && groups * 2 * C <= 2ll * s.sms) C *= 2;
+  if (getenv("KV8_C")) C = atoi(getenv("KV8_C"));
+  const int fit = static_cast<int>((kSmemHalf - S::bytes(0, 0)) / S::kTileB);
+  int nv = std::min((fit + 1) / 2, S::kMaxStages), nk = std::min(fit / 2, S::kMaxStages);
+  if (getenv("KV8_NK")) nk = atoi(getenv("KV8_NK")), nv = atoi(getenv("KV8_NV"));
+  if (getenv("KV8_SAY")) printf("RT %d HD %d misc %d fit %d nk %d nv %d bytes %u\n", RT, HD, (int)sizeof(typename S::Misc), fit, nk, nv, S::bytes(nk, nv));
+  int sort = p.B > 1 && p.B <= kSortSeqs && groups * C > 2ll * s.sms ? 1 : 0;
+  if (getenv("KV8_SORT")) sort = sort && atoi(getenv("KV8_SORT"));
   AttMaps maps;
   const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = att_config(dim3(C * rtiles, p.Hkv, p.B), smem, stream, attr, C);
-  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, C);
+  const cudaLaunchConfig_t cfg = att_config(dim3(C * rtiles, p.Hkv, p.B), S::bytes(nk, nv), stream, attr, C);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, C, nk, nv, sort);
 }
 
 template <int HD>
