@@ -392,9 +392,36 @@ class KV8Cache:
     close = PagedKVCache.close
     __del__ = PagedKVCache.__del__
 
+    def _shapes(self):
+        pages = (self.cfg.n_layers, self.n_pages, self.cfg.n_kv_heads)
+        codes = (pages + (PAGE_SLOTS, self.cfg.head_dim), torch.float8_e4m3fn)
+        scales = (pages + (PAGE_SLOTS // KV8_BLOCK,), torch.float32)
+        return {"k": codes, "v": codes, "k_scale": scales, "v_scale": scales,
+                "len": ((self.batch,), torch.int32), "table": ((self.batch, self.max_pages), torch.int32)}
+
+    def __setattr__(self, name, value):
+        """A buffer is looked at when it is put in place, not at every call."""
+        if isinstance(value, torch.Tensor):
+            shape, dtype = self._shapes().get(name, (None, None))
+            if shape is not None and (tuple(value.shape) != shape or value.dtype != dtype
+                                      or not value.is_contiguous()):
+                raise ValueError(f"{name}: expected a contiguous {shape} {dtype} tensor")
+        object.__setattr__(self, name, value)
+
     def c(self) -> spec_kv8_cache:
-        return spec_kv8_cache(*(_ptr(t) for t in (self.k, self.v, self.k_scale, self.v_scale, self.len,
-                                                  self.table)), self.batch, self.n_pages, self.max_pages)
+        return spec_kv8_cache(self.k.data_ptr(), self.v.data_ptr(), self.k_scale.data_ptr(),
+                              self.v_scale.data_ptr(), self.len.data_ptr(), self.table.data_ptr(),
+                              self.batch, self.n_pages, self.max_pages)
+
+    def _call(self, cfg, tensors):
+        """(device, cfg reference, cache reference) of a call on these tensors, which lie on the cache's device."""
+        dev = self.len.get_device()
+        if dev < 0:
+            raise ValueError("expected a cache on a CUDA device")
+        for t in (self.k, self.v, self.k_scale, self.v_scale, self.table, *tensors):
+            if t is not None and t.get_device() != dev:
+                raise ValueError(f"expected every tensor of the call on cuda:{dev}")
+        return dev, ctypes.byref(cfg.c()) if cfg is not None else None, ctypes.byref(self.c())
 
 
 class RopeTable:
@@ -405,54 +432,71 @@ class RopeTable:
                  low_freq: float = 1.0, high_freq: float = 4.0, orig_len: int = 0, device="cuda", stream=None):
         self.config = spec_rope_config(rotary_dim, int(interleaved), orig_len, theta, factor, low_freq, high_freq)
         self.table = torch.empty(max(rotary_dim, 0) // 2, 2, dtype=torch.float32, device=device)
-        with _on(self.table):
-            _check(lib().spec_rope_table(ctypes.byref(self.config), _ptr(self.table), _stream(stream)),
+        dev = self.table.get_device()
+        if dev < 0:
+            raise ValueError("expected a CUDA device")
+        with _on(dev):
+            _check(lib().spec_rope_table(ctypes.byref(self.config), _ptr(self.table), _raw_stream(stream, dev)),
                    "spec_rope_table")
 
 
-def _rows(t, rows: int, width: int, types, what: str):
-    """(address, elements between rows) of a 2-D CUDA tensor of whole rows."""
-    if not t.is_cuda or t.dtype not in types or t.shape != (rows, width) or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{what}: expected a CUDA tensor {(rows, width)} of {types} with unit column stride")
+def _rows(t, rows: int, width: int, dtype, what: str):
+    """(address, elements between rows) of a 2-D tensor of whole rows."""
+    if t.dtype != dtype or t.dim() != 2 or t.size(0) != rows or t.size(1) != width or t.stride(1) != 1:
+        raise ValueError(f"{what}: expected a {(rows, width)} {dtype} tensor with unit column stride")
     return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), width)
 
 
 def _plain(t, shape, dtype, what: str):
-    """Address of a contiguous CUDA tensor of this shape and type (None stays None)."""
+    """Address of a contiguous tensor of this shape and type (None stays None)."""
     if t is None:
         return None
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
-        raise ValueError(f"{what}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    return _ptr(t)
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous {tuple(shape)} {dtype} tensor")
+    return t.data_ptr()
 
 
-def _on(t):
-    """The device of tensor t as the current one: launches go to the caller's device."""
-    return torch.cuda.device(t.device)
+class _Here:
+    """The call's device is the current one already."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *_):
+        return False
 
 
-def _kv8_same(kv: "KV8Cache", *tensors):
-    """Every tensor of a call lives on the cache's device."""
-    for t in tensors:
-        if t is not None and t.device != kv.len.device:
-            raise ValueError(f"expected every tensor on {kv.len.device}, got one on {t.device}")
+_HERE = _Here()
+
+
+def _on(dev: int):
+    """Device `dev` as the current one: launches go to the current device."""
+    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+
+
+def _raw_stream(stream, dev: int):
+    """The stream's handle; None: device dev's current stream."""
+    if stream is None:
+        return torch.cuda.current_stream(dev).cuda_stream
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def spec_kv8_append(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, k, v, rope: "RopeTable", q_out, ws,
                     depth=None, stream=None):
     """Rotate q and k of n new tokens per sequence, append k and v to `layer`'s pages, q to q_out (bf16)."""
     m, hd = kv.batch * n, cfg.head_dim
-    _kv8_same(kv, q, k, v, rope.table, q_out, ws, depth)
-    types = (q.dtype,) if q.dtype in (torch.bfloat16, torch.float32) else (torch.bfloat16, torch.float32)
-    qp, q_ld = _rows(q, m, cfg.n_heads * hd, types, "q")
-    kp, k_ld = _rows(k, m, cfg.n_kv_heads * hd, types, "k")
-    vp, v_ld = _rows(v, m, cfg.n_kv_heads * hd, types, "v")
-    with _on(kv.len):
+    width, kv_width = cfg.n_heads * hd, cfg.n_kv_heads * hd
+    f32 = q.dtype == torch.float32
+    dtype = torch.float32 if f32 else torch.bfloat16
+    dev, c, cache = kv._call(cfg, (q, k, v, rope.table, q_out, ws, depth))
+    qp, q_ld = _rows(q, m, width, dtype, "q")
+    kp, k_ld = _rows(k, m, kv_width, dtype, "k")
+    vp, v_ld = _rows(v, m, kv_width, dtype, "v")
+    with _on(dev):
         _check(lib().spec_kv8_append(
-            ctypes.byref(cfg.c()), ctypes.byref(kv.c()), layer, n, qp, q_ld, kp, k_ld, vp, v_ld,
-            int(q.dtype == torch.float32), _plain(depth, (kv.batch, n), torch.int32, "depth"),
-            ctypes.byref(rope.config), _ptr(rope.table),
-            _plain(q_out, (m, cfg.n_heads * hd), torch.bfloat16, "q_out"), _ptr(ws), _stream(stream)),
+            c, cache, layer, n, qp, q_ld, kp, k_ld, vp, v_ld, int(f32),
+            _plain(depth, (kv.batch, n), torch.int32, "depth"), ctypes.byref(rope.config), rope.table.data_ptr(),
+            _plain(q_out, (m, width), torch.bfloat16, "q_out"), ws.data_ptr(), _raw_stream(stream, dev)),
             "spec_kv8_append")
 
 
@@ -460,36 +504,36 @@ def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, 
                        scale: float = 0.0, stream=None):
     """Attention of n new tokens per sequence (q, out bf16 rows) over `layer`'s pages."""
     m, width = kv.batch * n, cfg.n_heads * cfg.head_dim
-    _kv8_same(kv, q, out, ws, anc)
-    qp, q_ld = _rows(q, m, width, (torch.bfloat16,), "q")
-    op, o_ld = _rows(out, m, width, (torch.bfloat16,), "out")
-    with _on(kv.len):
-        _check(lib().spec_kv8_attention(ctypes.byref(cfg.c()), ctypes.byref(kv.c()), layer, n, qp, q_ld,
-                                        _plain(anc, (kv.batch, n), torch.int64, "anc"), scale, op, o_ld, _ptr(ws),
-                                        _stream(stream)), "spec_kv8_attention")
+    dev, c, cache = kv._call(cfg, (q, out, ws, anc))
+    qp, q_ld = _rows(q, m, width, torch.bfloat16, "q")
+    op, o_ld = _rows(out, m, width, torch.bfloat16, "out")
+    with _on(dev):
+        _check(lib().spec_kv8_attention(c, cache, layer, n, qp, q_ld,
+                                        _plain(anc, (kv.batch, n), torch.int64, "anc"), scale, op, o_ld,
+                                        ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_attention")
 
 
 def spec_kv8_advance(kv: "KV8Cache", n: int, ws, stream=None):
-    _kv8_same(kv, ws)
-    with _on(kv.len):
-        _check(lib().spec_kv8_advance(ctypes.byref(kv.c()), n, _ptr(ws), _stream(stream)), "spec_kv8_advance")
+    dev, _, cache = kv._call(None, (ws,))
+    with _on(dev):
+        _check(lib().spec_kv8_advance(cache, n, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_advance")
 
 
 def spec_kv8_truncate(kv: "KV8Cache", n_accepted, gamma: int, ws, stream=None):
-    _kv8_same(kv, n_accepted, ws)
-    with _on(kv.len):
-        _check(lib().spec_kv8_truncate(ctypes.byref(kv.c()), _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"),
-                                       gamma, _ptr(ws), _stream(stream)), "spec_kv8_truncate")
+    dev, _, cache = kv._call(None, (n_accepted, ws))
+    with _on(dev):
+        _check(lib().spec_kv8_truncate(cache, _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), gamma,
+                                       ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_truncate")
 
 
 def spec_kv8_tree_commit(cfg: ModelConfig, kv: "KV8Cache", path, n_accepted, n_nodes: int, ws, stream=None):
     """Move the accepted path's rows together in every layer and set the lengths."""
-    _kv8_same(kv, path, n_accepted, ws)
-    with _on(kv.len):
+    dev, c, cache = kv._call(cfg, (path, n_accepted, ws))
+    with _on(dev):
         _check(lib().spec_kv8_tree_commit(
-            ctypes.byref(cfg.c()), ctypes.byref(kv.c()), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
-            _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), n_nodes, _ptr(ws), _stream(stream)),
-            "spec_kv8_tree_commit")
+            c, cache, _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
+            _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), n_nodes, ws.data_ptr(),
+            _raw_stream(stream, dev)), "spec_kv8_tree_commit")
 
 
 def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
@@ -499,12 +543,12 @@ def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
 def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cache", logits, ws, anc=None,
                             depth=None, stream=None):
     """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
-    _kv8_same(kv, tokens, logits, ws, anc, depth)
-    with _on(kv.len):
+    dev, _, cache = kv._call(None, (tokens, logits, ws, anc, depth))
+    with _on(dev):
         _check(lib().spec_verify_forward_kv8(
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),
-            _plain(depth, (batch, n), torch.int32, "depth"), batch, n, ctypes.byref(kv.c()), _ptr(logits), _ptr(ws),
-            ws.numel(), _stream(stream)), "spec_verify_forward_kv8")
+            _plain(depth, (batch, n), torch.int32, "depth"), batch, n, cache, _ptr(logits), _ptr(ws),
+            ws.numel(), _raw_stream(stream, dev)), "spec_verify_forward_kv8")
 
 
 class GammaController:

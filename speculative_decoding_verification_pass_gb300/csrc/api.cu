@@ -878,6 +878,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
       t.n = n;
       t.H = H;
       t.Hkv = Hkv;
+      t.G = H / Hkv;
       t.hd = hd;
       t.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(hd)));
       TimedLaunch tl{};
@@ -1542,6 +1543,7 @@ int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, i
   p.n = n;
   p.H = cfg->n_heads;
   p.Hkv = cfg->n_kv_heads;
+  p.G = p.H / p.Hkv;
   p.hd = hd;
   p.scale_log2 =
       static_cast<float>(1.4426950408889634 * (scale > 0.f ? scale : 1.0 / std::sqrt(static_cast<double>(hd))));

@@ -328,6 +328,7 @@ struct Kv8AttnParams {
   const int32_t* table;
   int32_t* status;
   int max_pages, n_pages, B, n, H, Hkv, hd;
+  int G;                      // H / Hkv
   float scale_log2;           // log2(e) * the score scale
 };
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream);

@@ -35,8 +35,6 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
-#include <cstdio>
-#include <cstdlib>
 
 #include "internal.h"
 #include "kv8_common.cuh"
@@ -49,7 +47,8 @@ constexpr int kSoft = 128;                  // softmax threads
 constexpr int kAttThreads = kSoft + 96;     // + TMA warp + two MMA warps
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 constexpr int kMaxCluster = 16;
-constexpr int kSortSeqs = 96;               // sequences that are put in order of length
+constexpr int kSortSeqs = 96;               // sequences that are put in order of length (a multiple of 4)
+constexpr int kMinTiles = 2;                // tiles of a CTA at least, where they are shared
 constexpr int kSmemCta = 227 * 1024;        // dynamic shared memory of a CTA alone on its SM,
 constexpr int kSmemHalf = 113 * 1024;       // ... and of two (1 KB of each CTA's share is the system's)
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
@@ -325,22 +324,22 @@ struct AttSmem {
     alignas(16) float red[4][RT];  // per-warp maxima (sums at the end); this and the next two are read as float4
     float mneg[4][RT];         // each warp's copy of -M
     float cq[RT];              // score factor of a row: 2^k scale log2(e)
-    float stat[2][RT];         // this CTA's M' and sum
-    long long out[RT];         // where the row's output starts, -1: no such row
+    alignas(16) float stat[2][RT];   // this CTA's M and sum per row
+    alignas(16) long long out[RT];         // where the row's output starts, -1: no such row
     union {                    // before the loop, and from it on
-      int len[kSortSeqs];
+      alignas(16) int len[kSortSeqs];
       uint32_t nan[RT][HD / 32];  // outputs that a NaN value code reaches
     };
     uint32_t tmem;
     alignas(8) int pages[32];  // page ids of the tiles being loaded, two chunks of 16
-    int seq, seq_len, unfit, abort, any_nan;
+    int seq, seq_len, unit, unfit, abort, any_nan;
   };
   // partial sums [RT][HD] fp32, over the K ring once every MMA is done
   static constexpr uint32_t kO = kK;
   static_assert(offsetof(Misc, mneg) % 16 == 0 && offsetof(Misc, cq) % 16 == 0 && alignof(Misc) == 16 && kK % 1024 == 0,
                 "row arrays are read as float4");
   static_assert(RT * HD * 4 <= 4 * kTileB, "the partial sums lie over a ring of two stages or more");
-  static constexpr uint32_t bytes(int nk, int nv) { return kK + (nk + nv) * kTileB + sizeof(Misc) + 1024; }  // + alignment of the base
+  static constexpr uint32_t bytes(int nk, int nv) { return kK + (nk + nv) * kTileB + sizeof(Misc); }
   static constexpr int kNO = (3 * RT + 15) / 16 * 16;              // O columns (M = 128 takes multiples of 16)
   static constexpr uint32_t kTmemCols = RT >= 24 ? 256 : (RT == 16 ? 128 : 64);
   static_assert(4 * RT + kNO <= static_cast<int>(kTmemCols), "two S buffers and O");
@@ -352,16 +351,16 @@ struct AttMaps {
 
 template <int HD, int RT>
 __global__ void __launch_bounds__(kAttThreads, 2)
-    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int C, const int NK, const int NV,
-                         const int longest_first) {
+    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int lc, const int NK, const int NV,
+                         const int share) {
   using S = AttSmem<HD, RT>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  const uint32_t base = smem_u32(smem_raw);  // swizzled tiles lie on their own span's boundaries
   const uint32_t ring_k = base + S::kK, ring_v = ring_k + NK * S::kTileB;
   auto& sm = *reinterpret_cast<typename S::Misc*>(smem_raw + (ring_v + NV * S::kTileB - smem_u32(smem_raw)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x % C, rtile = blockIdx.x / C, h = blockIdx.y;
-  const int G = p.H / p.Hkv, R = p.n * G, rbase = rtile * RT;
+  const int rank = blockIdx.x & ((1 << lc) - 1), rtile = blockIdx.x >> lc, h = blockIdx.y;
+  const int G = p.G, R = p.n * G, rbase = rtile * RT;
 
   if (tid == 0) {
     for (int i = 0; i < S::kMaxStages; ++i) {
@@ -381,45 +380,93 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     sm.abort = 0;
     sm.any_nan = 0;
   }
-  if (warp == 4) {
-    if (lane == 0) {
-      prefetch_tmap(&maps.k);
-      prefetch_tmap(&maps.v);
-    }
-    __syncwarp();
+  if (tid == 32 * 4) {
+    prefetch_tmap(&maps.k);
+    prefetch_tmap(&maps.v);
+  }
+  if (warp == 6) {
     tmem_alloc(&sm.tmem, S::kTmemCols);
     tmem_relinquish();
     tc_fence_before();
   }
-  __syncthreads();  // barriers set up
+  __syncthreads();  // barriers and TMEM set up
+  tc_fence_after();
+  const uint32_t tmem = sm.tmem;
   grid_dep_wait();
   grid_dep_launch();
 
-  // Where the grid does not fit the GPU at once, its longest sequences go first
-  // (blocks start in index order): block z takes the sequence with z longer ones.
+  // Which sequence, and how many of the cluster's CTAs share its tiles.  With
+  // the lengths at hand (up to kSortSeqs), the longest sequences go first
+  // (blocks start in index order: block z takes the sequence with z longer
+  // ones), and every CTA gets about the share of all tiles that fills the GPU
+  // once; the CTAs that a short sequence does not need leave.
+  const int cap = p.max_pages * kPageSlots;
+  const auto tiles_of = [&](int len) { return len < 0 || len > cap - p.n ? 0 : (len + p.n + kTile - 1) / kTile; };
+  const int slots = lc ? share / (p.Hkv * (gridDim.x >> lc)) : 0;  // CTAs of the GPU per sequence, KV head and row tile
   int b = blockIdx.z;
-  if (longest_first) {
-    if (tid < p.B) sm.len[tid] = p.base[tid];
+  if (p.B > 1 && p.B <= kSortSeqs) {
+    if (tid < kSortSeqs) sm.len[tid] = tid < p.B ? p.base[tid] : -1;
     __syncthreads();
     if (tid < p.B) {
       const int mine = sm.len[tid];
-      int before = 0;
-      for (int j = 0; j < p.B; ++j) before += sm.len[j] > mine || (sm.len[j] == mine && j < tid);
+      int before = 0, total = 0;
+      for (int j = 0; j < p.B; j += 4) {  // (the rows past B count as empty)
+        const int4 v = *reinterpret_cast<const int4*>(&sm.len[j]);
+        const int o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) before += o[k] > mine || (o[k] == mine && j + k < tid);
+        if (lc)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) total += tiles_of(o[k]);
+      }
       if (before == static_cast<int>(blockIdx.z)) {
         sm.seq = tid;
         sm.seq_len = mine;
+        if (lc) sm.unit = max(kMinTiles, (total + slots - 1) / max(slots, 1));
       }
     }
     __syncthreads();
     b = sm.seq;
   }
-  const int L = longest_first ? sm.seq_len : p.base[b];
-  const int cap = p.max_pages * kPageSlots;
+  // ---- the query rows: row r = token r / G, head h * G + r % G (loads on their
+  // way before the length is known)
+  constexpr int TPR = RT <= 16 && HD == 128 ? 8 : 4;  // threads per query row
+  constexpr int E = HD / TPR;                         // ... and their elements
+  static_assert(RT * TPR <= kSoft && RT * TPR % 32 == 0 && E % 16 == 0, "whole warps, 16 elements a thread");
+  const int qr = tid / TPR, qpart = tid % TPR;
+  uint4 qw[E / 8];
+  long long out_at = -1;
+  unsigned long long am = 0ull;
+  if (tid < RT * TPR) {
+    const int rr = rbase + qr, tok = rr / G, head = h * G + rr - tok * G;
+#pragma unroll
+    for (int c = 0; c < E / 8; ++c) qw[c] = make_uint4(0, 0, 0, 0);
+    if (rr < R) {
+      const long long m = static_cast<long long>(b) * p.n + tok;
+      const uint16_t* q = p.q + m * p.q_ld + head * HD + qpart * E;
+#pragma unroll
+      for (int c = 0; c < E / 8; ++c) qw[c] = *reinterpret_cast<const uint4*>(q + c * 8);
+      if (qpart == 0 && p.anc) am = p.anc[m];
+      out_at = m * p.o_ld + head * HD;
+    }
+  }
+
+  const bool sorted = p.B > 1 && p.B <= kSortSeqs;
+  const int L = sorted ? sm.seq_len : p.base[b];
   const bool over = L < 0 || L > cap - p.n;
   const int T = over ? 0 : L + p.n;  // slots [0, T)
   const int tiles = (T + kTile - 1) / kTile;
-  const int i0 = static_cast<int>(static_cast<long long>(tiles) * rank / C);
-  const int nt = static_cast<int>(static_cast<long long>(tiles) * (rank + 1) / C) - i0;  // this CTA's tiles
+  int C = 1, i0 = 0, nt = tiles;  // CTAs that share the tiles; this one's
+  if (lc) {
+    const int unit = sorted ? sm.unit : max(kMinTiles, p.B > 1 ? 0 : (tiles + slots - 1) / max(slots, 1));
+    C = min(1 << lc, max(1, (tiles + unit - 1) / unit));
+    if (rank >= C) {  // (its peers' barriers go on without it)
+      if (warp == 6) tmem_dealloc(tmem, S::kTmemCols);
+      return;
+    }
+    i0 = tiles * rank / C;  // (tiles * C <= 2^13 * 2^4)
+    nt = tiles * (rank + 1) / C - i0;
+  }
   const int32_t* table = p.table + static_cast<long long>(b) * p.max_pages;
   const auto page_of = [&](int t) {  // the page of slot t, clamped into the pool
     const int pg = __ldg(table + min(t / kPageSlots, p.max_pages - 1));
@@ -430,20 +477,12 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     return pg;
   };
 
-  // ---- the query rows as e4m3 pieces: row r = token r / G, head h * G + r % G
-  constexpr int TPR = RT <= 16 && HD == 128 ? 8 : 4;  // threads per query row
-  static_assert(RT * TPR <= kSoft && RT * TPR % 32 == 0 && HD / TPR % 16 == 0, "whole warps, 16 elements a thread");
+  // ---- ... as e4m3 pieces
   if (tid < RT * TPR) {
-    constexpr int E = HD / TPR;  // elements per thread
-    const int r = tid / TPR, part = tid % TPR, rr = rbase + r;
     float x[E];
 #pragma unroll
     for (int c = 0; c < E / 8; ++c) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (rr < R)
-        w = *reinterpret_cast<const uint4*>(p.q + (static_cast<long long>(b) * p.n + rr / G) * p.q_ld +
-                                            (h * G + rr % G) * HD + part * E + c * 8);
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t v[4] = {qw[c].x, qw[c].y, qw[c].z, qw[c].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         x[8 * c + 2 * k] = bf16lo(v[k]);
@@ -483,27 +522,25 @@ __global__ void __launch_bounds__(kAttThreads, 2)
           lo[k / 2] = u;
         }
       }
-      const int ch = part * (E / 16) + c;
-      st_shared_v4(base + S::kQ + swz_off<HD>(r, ch), hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(base + S::kQ + swz_off<HD>(RT + r, ch), lo[0], lo[1], lo[2], lo[3]);
+      const int ch = qpart * (E / 16) + c;
+      st_shared_v4(base + S::kQ + swz_off<HD>(qr, ch), hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(base + S::kQ + swz_off<HD>(RT + qr, ch), lo[0], lo[1], lo[2], lo[3]);
     }
-    if (part == 0) {
+    if (qpart == 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) sm.mneg[c][r] = -kNoRef;
-      sm.cq[r] = odd ? __uint_as_float(0x7FC00000u)
-                     : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
-      sm.out[r] =
-          rr < R ? (static_cast<long long>(b) * p.n + rr / G) * p.o_ld + static_cast<long long>(h * G + rr % G) * HD : -1;
-      sm.anc[r] = (p.anc && rr < R) ? p.anc[static_cast<long long>(b) * p.n + rr / G] : 0ull;
+      for (int c = 0; c < 4; ++c) sm.mneg[c][qr] = -kNoRef;
+      sm.cq[qr] = odd ? __uint_as_float(0x7FC00000u)
+                      : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
+      sm.out[qr] = out_at;
+      sm.anc[qr] = am;
 #pragma unroll
-      for (int c = 0; c < HD / 32; ++c) sm.nan[r][c] = 0u;
+      for (int c = 0; c < HD / 32; ++c) sm.nan[qr][c] = 0u;
     }
     fence_async_smem();
   }
-  // q, the row arrays and the TMEM address are ready (the TMA warp goes ahead)
+  // q and the row arrays are ready (the TMA warp needs neither)
   if (warp != 4) named_bar(3, kSoft + 64);
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;
 
   float mrun = kNoRef;  // lane r: row r's reference M
 
@@ -729,15 +766,9 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         // of 0 would not clear them) and noted for the rows that see them.
         const uint32_t vt = ring_v + vring.s * S::kTileB;
         mbar_wait(&sm.full_v[vring.s], vring.par, &sm.abort);
-        constexpr int VEC = HD / 16;
-        const int row0 = max(L - t0, 0);
-        for (int e = row0 * VEC + tid; e < kTile * VEC; e += kSoft) {
-          const int row = e / VEC, c = e % VEC;
-          const uint32_t a = vt + swz_off<HD>(row, c);
-          if (t0 + row >= T) {
-            st_shared_v4(a, 0, 0, 0, 0);
-            continue;
-          }
+        const uint32_t row0 = max(L - t0, 0), row1 = min(T - t0, kTile);
+        for (uint32_t a = vt + row1 * HD + tid * 16; a < vt + kTile * HD; a += kSoft * 16) st_shared_v4(a, 0, 0, 0, 0);
+        for (uint32_t a = vt + row0 * HD + tid * 16; a < vt + row1 * HD; a += kSoft * 16) {
           uint32_t w[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -748,6 +779,8 @@ __global__ void __launch_bounds__(kAttThreads, 2)
           for (int k = 0; k < 4; ++k) hit |= ((w[k] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
           if (!hit) continue;
           sm.any_nan = 1;
+          const int row = static_cast<int>((a - vt) / HD);
+          const int c = static_cast<int>(swz_off<HD>(row, (a - vt) % HD / 16) % HD) / 16;  // (its own inverse)
           const uint32_t m = seen(t0 + row);
 #pragma unroll 1
           for (int k = 0; k < 16; ++k) {
@@ -763,10 +796,10 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         }
       }
       // ---- does any exponent pass the pieces' range?
-      const bool raise = i == 0 || exponents() > kTopExp;  // (the first tile sets M)
-      if (named_bar_any(1, kSoft, raise || *static_cast<volatile int*>(&sm.abort) != 0)) {
+      // (the first tile sets M)
+      if (i == 0 || named_bar_any(1, kSoft, exponents() > kTopExp || *static_cast<volatile int*>(&sm.abort) != 0)) {
         // raise M to each row's maximum (at 2^2); what is summed so far shrinks by alpha
-        if (named_bar_any(2, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
+        if (i && named_bar_any(2, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
           stopped = true;
           break;
         }
@@ -856,8 +889,9 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     if (lane < RT) sm.red[warp][lane] = ls;
     named_bar(1, kSoft);
     if (tid < RT) {
-      sm.stat[0][tid] = mrun;
-      sm.stat[1][tid] = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+      const float lt = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
+      sm.stat[0][tid] = C > 1 ? mrun : (lt == 0.f || unfit ? 0.f : 1.f / lt);  // alone: the factor of a row
+      sm.stat[1][tid] = lt;
     }
     if (C == 1) named_bar(1, kSoft);
     // ---- O: dimension tid of every row, to the output, or to shared memory for the merge
@@ -865,32 +899,46 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       mbar_wait(&sm.o_full[(nt - 1) & 1], static_cast<uint32_t>(((nt - 1) >> 1) & 1), &sm.abort);
       tc_fence_after();
     }
-    const bool any_nan = sm.any_nan != 0;
-#pragma unroll 1
-    for (int r = 0; r < RT; r += 8) {
-      float o[8];
+    float acc[RT];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[k] = 0.f;
-      if (nt) o_rows(r, o);
-      if (tid < HD) {
+    for (int r = 0; r < RT; ++r) acc[r] = 0.f;
+    if (nt) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if (any_nan && ((sm.nan[r + k][tid / 32] >> (tid % 32)) & 1u)) o[k] = __uint_as_float(0x7FC00000u);
-          if (C > 1) {
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::kO + ((r + k) * HD + tid) * 4), "f"(o[k])
-                         : "memory");
-          } else if (sm.out[r + k] >= 0) {
-            const float lt = sm.stat[1][r + k];
-            const float x = lt == 0.f || unfit ? 0.f : o[k] * (1.f / lt);  // a row that sees nothing is zero
-            uint32_t u;
-            asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(0.f), "f"(x));
-            p.o[sm.out[r + k] + tid] = static_cast<uint16_t>(u);
-          }
+      for (int r = 0; r < RT; r += 8) {
+        float o[8];
+        o_rows(r, o);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[r + k] = o[k];
+      }
+    }
+    if (sm.any_nan && tid < HD) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        if ((sm.nan[r][tid / 32] >> (tid % 32)) & 1u) acc[r] = __uint_as_float(0x7FC00000u);
+    }
+    if (tid < HD) {
+      if (C > 1) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(base + S::kO + (r * HD + tid) * 4), "f"(acc[r]) : "memory");
+      } else {
+        uint16_t* o = p.o + tid;
+#pragma unroll
+        for (int r = 0; r < RT; r += 2) {
+          const float2 f = *reinterpret_cast<const float2*>(&sm.stat[0][r]);
+          const longlong2 at = *reinterpret_cast<const longlong2*>(&sm.out[r]);
+          // (a factor of zero is a row that sees nothing, whatever its sum holds)
+          const float x = f.x == 0.f ? 0.f : acc[r] * f.x, y = f.y == 0.f ? 0.f : acc[r + 1] * f.y;
+          uint32_t u;
+          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(y), "f"(x));
+          if (at.x >= 0) o[at.x] = static_cast<uint16_t>(u);
+          if (at.y >= 0) o[at.y] = static_cast<uint16_t>(u >> 16);
         }
       }
     }
   }
 
+  __syncwarp();
   if (C > 1) {
     const int rows = min(RT, R - rbase);
   // ---- merge: the cluster's CTAs share the (row, 4 dimensions) items
@@ -944,7 +992,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   if (tid == 0 && sm.abort) set_status(p.status, SPEC_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == 6) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
@@ -1031,31 +1079,29 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
           &s))
     return cudaErrorInvalidDevice;
   if (s.err != cudaSuccess) return s.err;
-  const int R = p.n * (p.H / p.Hkv), rtiles = (R + RT - 1) / RT;
-  // as many CTAs per row tile as keep two resident per SM, and no more than tiles
+  const int R = p.n * p.G, rtiles = (R + RT - 1) / RT;
+  // Clusters of up to 16 CTAs per row tile, as many CTAs as the GPU holds (two
+  // per SM), each of two tiles at least at full capacity.  (More, the surplus
+  // leaving at once, costs more than the even shares give: batch 16 29 us
+  // against 21.)
   const long long groups = static_cast<long long>(p.B) * p.Hkv * rtiles;
   const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
-  int C = 1;
-  while (2 * C <= s.max_cluster && 2 * C <= tiles && groups * 2 * C <= 2ll * s.sms) C *= 2;
-  if (getenv("KV8_C")) C = atoi(getenv("KV8_C"));
+  int lc = 0;
+  while ((2 << lc) <= s.max_cluster && (2 << lc) * kMinTiles <= tiles && (groups << (lc + 1)) <= 2ll * s.sms) ++lc;
   const int fit = static_cast<int>((kSmemHalf - S::bytes(0, 0)) / S::kTileB);
-  int nv = std::min((fit + 1) / 2, S::kMaxStages), nk = std::min(fit / 2, S::kMaxStages);
-  if (getenv("KV8_NK")) nk = atoi(getenv("KV8_NK")), nv = atoi(getenv("KV8_NV"));
-  if (getenv("KV8_SAY")) printf("RT %d HD %d misc %d fit %d nk %d nv %d bytes %u\n", RT, HD, (int)sizeof(typename S::Misc), fit, nk, nv, S::bytes(nk, nv));
-  int sort = p.B > 1 && p.B <= kSortSeqs && groups * C > 2ll * s.sms ? 1 : 0;
-  if (getenv("KV8_SORT")) sort = sort && atoi(getenv("KV8_SORT"));
+  const int nv = std::min((fit + 1) / 2, S::kMaxStages), nk = std::min(fit / 2, S::kMaxStages);
   AttMaps maps;
   const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = att_config(dim3(C * rtiles, p.Hkv, p.B), S::bytes(nk, nv), stream, attr, C);
-  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, C, nk, nv, sort);
+  const cudaLaunchConfig_t cfg = att_config(dim3(rtiles << lc, p.Hkv, p.B), S::bytes(nk, nv), stream, attr, 1 << lc);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, lc, nk, nv, 2 * s.sms);
 }
 
 template <int HD>
 cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
   // the row tile that leaves the fewest rows empty, the larger of equal ones
-  const int R = p.n * (p.H / p.Hkv);
+  const int R = p.n * p.G;
   int best = 32;
   for (int rt = 24; rt >= 8; rt -= 8)
     if ((R + rt - 1) / rt * rt < (R + best - 1) / best * best) best = rt;
