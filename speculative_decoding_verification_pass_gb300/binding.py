@@ -392,20 +392,20 @@ class KV8Cache:
     close = PagedKVCache.close
     __del__ = PagedKVCache.__del__
 
-    def _shapes(self):
-        pages = (self.cfg.n_layers, self.n_pages, self.cfg.n_kv_heads)
-        codes = (pages + (PAGE_SLOTS, self.cfg.head_dim), torch.float8_e4m3fn)
-        scales = (pages + (PAGE_SLOTS // KV8_BLOCK,), torch.float32)
-        return {"k": codes, "v": codes, "k_scale": scales, "v_scale": scales,
-                "len": ((self.batch,), torch.int32), "table": ((self.batch, self.max_pages), torch.int32)}
-
     def __setattr__(self, name, value):
         """A buffer is looked at when it is put in place, not at every call."""
         if isinstance(value, torch.Tensor):
-            shape, dtype = self._shapes().get(name, (None, None))
-            if shape is not None and (tuple(value.shape) != shape or value.dtype != dtype
-                                      or not value.is_contiguous()):
-                raise ValueError(f"{name}: expected a contiguous {shape} {dtype} tensor")
+            pages = (self.cfg.n_layers, self.n_pages, self.cfg.n_kv_heads)
+            codes = (pages + (PAGE_SLOTS, self.cfg.head_dim), torch.float8_e4m3fn)
+            scales = (pages + (PAGE_SLOTS // KV8_BLOCK,), torch.float32)
+            shape, dtype = {"k": codes, "v": codes, "k_scale": scales, "v_scale": scales,
+                            "len": ((self.batch,), torch.int32),
+                            "table": ((self.batch, self.max_pages), torch.int32)}.get(name, (value.shape, value.dtype))
+            first = self.__dict__.get("k", value)
+            if value.shape != shape or value.dtype != dtype or not value.is_contiguous() or not value.is_cuda:
+                raise ValueError(f"{name}: expected a contiguous {tuple(shape)} {dtype} CUDA tensor")
+            if value.device != first.device:
+                raise ValueError(f"{name}: expected a tensor on {first.device}")
         object.__setattr__(self, name, value)
 
     def c(self) -> spec_kv8_cache:
@@ -413,15 +413,13 @@ class KV8Cache:
                               self.v_scale.data_ptr(), self.len.data_ptr(), self.table.data_ptr(),
                               self.batch, self.n_pages, self.max_pages)
 
-    def _call(self, cfg, tensors):
-        """(device, cfg reference, cache reference) of a call on these tensors, which lie on the cache's device."""
+    def _device(self, *tensors) -> int:
+        """The cache's device, on which the call's tensors lie too."""
         dev = self.len.get_device()
-        if dev < 0:
-            raise ValueError("expected a cache on a CUDA device")
-        for t in (self.k, self.v, self.k_scale, self.v_scale, self.table, *tensors):
+        for t in tensors:
             if t is not None and t.get_device() != dev:
                 raise ValueError(f"expected every tensor of the call on cuda:{dev}")
-        return dev, ctypes.byref(cfg.c()) if cfg is not None else None, ctypes.byref(self.c())
+        return dev
 
 
 class RopeTable:
@@ -440,11 +438,11 @@ class RopeTable:
                    "spec_rope_table")
 
 
-def _rows(t, rows: int, width: int, dtype, what: str):
-    """(address, elements between rows) of a 2-D tensor of whole rows."""
-    if t.dtype != dtype or t.dim() != 2 or t.size(0) != rows or t.size(1) != width or t.stride(1) != 1:
+def _rows(t, rows: int, width: int, dtype, what: str) -> int:
+    """Elements between the rows of a 2-D tensor of whole rows."""
+    if t.dtype != dtype or t.shape != (rows, width) or t.stride(1) != 1:
         raise ValueError(f"{what}: expected a {(rows, width)} {dtype} tensor with unit column stride")
-    return t.data_ptr(), t.stride(0) if rows > 1 else max(t.stride(0), width)
+    return t.stride(0) if rows > 1 else max(t.stride(0), width)
 
 
 def _plain(t, shape, dtype, what: str):
@@ -474,64 +472,68 @@ def _on(dev: int):
     return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
 
 
-def _raw_stream(stream, dev: int):
+# the handle of a device's current stream, without a Stream object where torch has that call
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
+def _raw_stream(stream, dev: int) -> int:
     """The stream's handle; None: device dev's current stream."""
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return _current_raw_stream(dev)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def spec_kv8_append(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, k, v, rope: "RopeTable", q_out, ws,
                     depth=None, stream=None):
     """Rotate q and k of n new tokens per sequence, append k and v to `layer`'s pages, q to q_out (bf16)."""
-    m, hd = kv.batch * n, cfg.head_dim
-    width, kv_width = cfg.n_heads * hd, cfg.n_kv_heads * hd
-    f32 = q.dtype == torch.float32
-    dtype = torch.float32 if f32 else torch.bfloat16
-    dev, c, cache = kv._call(cfg, (q, k, v, rope.table, q_out, ws, depth))
-    qp, q_ld = _rows(q, m, width, dtype, "q")
-    kp, k_ld = _rows(k, m, kv_width, dtype, "k")
-    vp, v_ld = _rows(v, m, kv_width, dtype, "v")
+    m, width = kv.batch * n, cfg.d_model
+    kv_width = width // cfg.n_heads * cfg.n_kv_heads
+    dtype = torch.float32 if q.dtype == torch.float32 else torch.bfloat16
+    dev = kv._device(q, k, v, rope.table, q_out, ws, depth)
+    q_ld, k_ld, v_ld = (_rows(q, m, width, dtype, "q"), _rows(k, m, kv_width, dtype, "k"),
+                        _rows(v, m, kv_width, dtype, "v"))
     with _on(dev):
         _check(lib().spec_kv8_append(
-            c, cache, layer, n, qp, q_ld, kp, k_ld, vp, v_ld, int(f32),
-            _plain(depth, (kv.batch, n), torch.int32, "depth"), ctypes.byref(rope.config), rope.table.data_ptr(),
-            _plain(q_out, (m, width), torch.bfloat16, "q_out"), ws.data_ptr(), _raw_stream(stream, dev)),
-            "spec_kv8_append")
+            cfg.c(), kv.c(), layer, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+            dtype == torch.float32, _plain(depth, (kv.batch, n), torch.int32, "depth"), rope.config,
+            rope.table.data_ptr(), _plain(q_out, (m, width), torch.bfloat16, "q_out"), ws.data_ptr(),
+            _raw_stream(stream, dev)), "spec_kv8_append")
 
 
 def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, out, ws, anc=None,
                        scale: float = 0.0, stream=None):
     """Attention of n new tokens per sequence (q, out bf16 rows) over `layer`'s pages."""
-    m, width = kv.batch * n, cfg.n_heads * cfg.head_dim
-    dev, c, cache = kv._call(cfg, (q, out, ws, anc))
-    qp, q_ld = _rows(q, m, width, torch.bfloat16, "q")
-    op, o_ld = _rows(out, m, width, torch.bfloat16, "out")
+    m, width = kv.batch * n, cfg.d_model
+    dev = kv._device(q, out, ws, anc)
+    q_ld, o_ld = _rows(q, m, width, torch.bfloat16, "q"), _rows(out, m, width, torch.bfloat16, "out")
     with _on(dev):
-        _check(lib().spec_kv8_attention(c, cache, layer, n, qp, q_ld,
-                                        _plain(anc, (kv.batch, n), torch.int64, "anc"), scale, op, o_ld,
-                                        ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_attention")
+        _check(lib().spec_kv8_attention(
+            cfg.c(), kv.c(), layer, n, q.data_ptr(), q_ld, _plain(anc, (kv.batch, n), torch.int64, "anc"), scale,
+            out.data_ptr(), o_ld, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_attention")
 
 
 def spec_kv8_advance(kv: "KV8Cache", n: int, ws, stream=None):
-    dev, _, cache = kv._call(None, (ws,))
+    """len += n after the layers of a pass."""
+    dev = kv._device(ws)
     with _on(dev):
-        _check(lib().spec_kv8_advance(cache, n, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_advance")
+        _check(lib().spec_kv8_advance(kv.c(), n, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_advance")
 
 
 def spec_kv8_truncate(kv: "KV8Cache", n_accepted, gamma: int, ws, stream=None):
-    dev, _, cache = kv._call(None, (n_accepted, ws))
+    """Rollback: len -= gamma - n_accepted."""
+    dev = kv._device(n_accepted, ws)
     with _on(dev):
-        _check(lib().spec_kv8_truncate(cache, _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), gamma,
+        _check(lib().spec_kv8_truncate(kv.c(), _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), gamma,
                                        ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_truncate")
 
 
 def spec_kv8_tree_commit(cfg: ModelConfig, kv: "KV8Cache", path, n_accepted, n_nodes: int, ws, stream=None):
     """Move the accepted path's rows together in every layer and set the lengths."""
-    dev, c, cache = kv._call(cfg, (path, n_accepted, ws))
+    dev = kv._device(path, n_accepted, ws)
     with _on(dev):
         _check(lib().spec_kv8_tree_commit(
-            c, cache, _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
+            cfg.c(), kv.c(), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
             _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), n_nodes, ws.data_ptr(),
             _raw_stream(stream, dev)), "spec_kv8_tree_commit")
 
@@ -543,11 +545,11 @@ def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
 def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cache", logits, ws, anc=None,
                             depth=None, stream=None):
     """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
-    dev, _, cache = kv._call(None, (tokens, logits, ws, anc, depth))
+    dev = kv._device(tokens, logits, ws, anc, depth)
     with _on(dev):
         _check(lib().spec_verify_forward_kv8(
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),
-            _plain(depth, (batch, n), torch.int32, "depth"), batch, n, cache, _ptr(logits), _ptr(ws),
+            _plain(depth, (batch, n), torch.int32, "depth"), batch, n, kv.c(), _ptr(logits), _ptr(ws),
             ws.numel(), _raw_stream(stream, dev)), "spec_verify_forward_kv8")
 
 
