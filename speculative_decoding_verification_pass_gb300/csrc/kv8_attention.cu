@@ -44,7 +44,8 @@ namespace {
 
 constexpr int kTile = 128;                  // keys per tile
 constexpr int kSoft = 128;                  // softmax threads
-constexpr int kAttThreads = kSoft + 96;     // + TMA warp + two MMA warps
+constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O issuing warps
+constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;  // (warps)
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 constexpr int kMaxCluster = 16;
 constexpr int kSortSeqs = 96;               // sequences that are put in order of length (a multiple of 4)
@@ -211,35 +212,6 @@ SPEC_DEVINL float4 peer_f32x4(uint32_t a) {
   return v;
 }
 
-SPEC_DEVINL bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// Bound of a loop that polls barriers: more() after every turn that found
-// nothing to do; false once *abort is set or nothing was found for the wait
-// limit (and *abort then is set).
-struct Poll {
-  uint32_t turns = 0;
-  unsigned long long t0 = 0;
-  SPEC_DEVINL bool more(volatile int* abort) {
-    if ((++turns & 63u) != 0u) return true;
-    if (*abort) return false;
-    const unsigned long long now = globaltimer();
-    if (turns == 64u) t0 = now;
-    if (now - t0 <= kWaitLimitNs) return true;
-    *abort = 1;
-    return false;
-  }
-  SPEC_DEVINL void reset() { turns = 0; }
-};
-
 // A place in the ring: stage and the parity of the fill being awaited there
 // (counted along: a division by a stage count known only at run time costs the
 // one issuing thread ~100 cycles).
@@ -331,7 +303,7 @@ struct AttSmem {
       uint32_t nan[RT][HD / 32];  // outputs that a NaN value code reaches
     };
     uint32_t tmem;
-    alignas(8) int pages[32];  // page ids of the tiles being loaded, two chunks of 16
+    alignas(8) int pages[2][16];  // page ids of the 8 tiles being loaded, of K and of V
     int seq, seq_len, unit, unfit, abort, any_nan;
   };
   // partial sums [RT][HD] fp32, over the K ring once every MMA is done
@@ -380,11 +352,11 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     sm.abort = 0;
     sm.any_nan = 0;
   }
-  if (tid == 32 * 4) {
+  if (tid == 32 * kLoadK) {
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
   }
-  if (warp == 6) {
+  if (warp == kIssueO) {
     tmem_alloc(&sm.tmem, S::kTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -461,7 +433,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     const int unit = sorted ? sm.unit : max(kMinTiles, p.B > 1 ? 0 : (tiles + slots - 1) / max(slots, 1));
     C = min(1 << lc, max(1, (tiles + unit - 1) / unit));
     if (rank >= C) {  // (its peers' barriers go on without it)
-      if (warp == 6) tmem_dealloc(tmem, S::kTmemCols);
+      if (warp == kIssueO) tmem_dealloc(tmem, S::kTmemCols);
       return;
     }
     i0 = tiles * rank / C;  // (tiles * C <= 2^13 * 2^4)
@@ -538,82 +510,69 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     }
     fence_async_smem();
   }
-  // q and the row arrays are ready (the TMA warp needs neither)
-  if (warp != 4) named_bar(3, kSoft + 64);
+  // q and the row arrays are ready (the loading warps need neither)
+  if (warp != kLoadK && warp != kLoadV) named_bar(3, kSoft + 64);
   tc_fence_after();
 
   float mrun = kNoRef;  // lane r: row r's reference M
 
-  if (warp == 4) {
-    // ------------------------------------------------------- TMA producer
+  if (warp == kLoadK || warp == kLoadV) {
+    // ------------------------------------------- TMA: the tiles of K, or of V
     // Page ids come 16 at a time (8 tiles), the next 16 on their way: a
     // lookup per page in line with the loads took ~500 cycles each.
+    const bool is_k = warp == kLoadK;
+    const CUtensorMap* map = is_k ? &maps.k : &maps.v;
+    uint64_t* const full = is_k ? sm.full_k : sm.full_v;
+    uint64_t* const empty = is_k ? sm.empty_k : sm.empty_v;
+    int* const pages = sm.pages[is_k ? 0 : 1];
+    const uint32_t ring = is_k ? ring_k : ring_v;
+    const int stages = is_k ? NK : NV;
     const uint64_t pol = l2_policy_evict_first();
     const int entries = (T + kPageSlots - 1) / kPageSlots - 2 * i0;  // pages from this CTA's first slot on
     const auto page_at = [&](int e) { return e < entries ? page_of(i0 * kTile + e * kPageSlots) : 0; };
     int next = nt > 0 && lane < 16 ? page_at(lane) : 0;
-    int ki = 0, vi = 0, chunk = -1;
-    Poll idle;
-    Ring kr, vr;
-    const auto load = [&](const CUtensorMap* m, uint32_t dst, uint64_t* bar, int i) {
-      const bool two = entries - 2 * i > 1;  // a page past the end is not read
-      const int2 pg = *reinterpret_cast<const int2*>(&sm.pages[(2 * i) % 32]);
-      mbar_arrive_expect_tx(bar, (two ? 2u : 1u) * kPageSlots * HD);
-      tma_load_2d_s(dst, m, bar, 0, (pg.x * p.Hkv + h) * kPageSlots, pol);
-      if (two) tma_load_2d_s(dst + kPageSlots * HD, m, bar, 0, (pg.y * p.Hkv + h) * kPageSlots, pol);
-    };
-    // K and V each as soon as their stage is free (K's is when the scores are
-    // in TMEM, V's when its products are)
-    while (vi < nt) {
-      // the chunk before is kept, for V: it follows K by no more than the K
-      // stages and the 3 tiles between the scores and the products
-      if (ki < nt && ki % 8 == 0 && ki != chunk) {
-        chunk = ki;
-        __syncwarp();
-        if (lane < 16) {
-          sm.pages[(2 * ki + lane) % 32] = next;
-          next = page_at(2 * ki + 16 + lane);
-        }
-        __syncwarp();
+    Ring r;
+    bool ok = true;
+    int i = 0, issued = 0;
+    while (i < nt && ok) {
+      __syncwarp();
+      if (lane < 16) {
+        pages[lane] = next;
+        next = page_at(2 * i + 16 + lane);
       }
-      int did = 0, go = 1;
+      __syncwarp();
+      const int end = min(i + 8, nt);
       if (lane == 0) {
-        if (ki < nt && (ki < NK || mbar_test(&sm.empty_k[kr.s], kr.par ^ 1u))) {
-          load(&maps.k, ring_k + kr.s * S::kTileB, &sm.full_k[kr.s], ki);
-          kr.next(NK);
-          did = 1;
+        for (int k = 0; i + k < end; ++k) {
+          if (i + k >= stages && !mbar_wait(&empty[r.s], r.par ^ 1u, &sm.abort)) {
+            ok = false;
+            break;
+          }
+          const bool two = entries - 2 * (i + k) > 1;  // a page past the end is not read
+          const int2 pg = *reinterpret_cast<const int2*>(&pages[2 * k]);
+          const uint32_t dst = ring + r.s * S::kTileB;
+          mbar_arrive_expect_tx(&full[r.s], (two ? 2u : 1u) * kPageSlots * HD);
+          tma_load_2d_s(dst, map, &full[r.s], 0, (pg.x * p.Hkv + h) * kPageSlots, pol);
+          if (two) tma_load_2d_s(dst + kPageSlots * HD, map, &full[r.s], 0, (pg.y * p.Hkv + h) * kPageSlots, pol);
+          r.next(stages);
+          ++issued;
         }
-        if (vi < ki + did && (vi < NV || mbar_test(&sm.empty_v[vr.s], vr.par ^ 1u))) {
-          load(&maps.v, ring_v + vr.s * S::kTileB, &sm.full_v[vr.s], vi);
-          vr.next(NV);
-          did |= 2;
-        }
-        if (did)
-          idle.reset();
-        else
-          go = idle.more(&sm.abort);
       }
-      did = __shfl_sync(0xffffffffu, did, 0);
-      ki += did & 1;
-      vi += did >> 1;
-      if (!__shfl_sync(0xffffffffu, go, 0)) break;
+      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+      i = end;
     }
-    if (lane == 0) {
-      if (sm.abort) {  // loads in flight land before the CTA leaves (bounded as every wait)
-        int none = 0;
-        for (int i = max(0, ki - NK); i < ki; ++i)
-          mbar_wait(&sm.full_k[i % NK], static_cast<uint32_t>((i / NK) & 1), &none);
-        for (int i = max(0, vi - NV); i < vi; ++i)
-          mbar_wait(&sm.full_v[i % NV], static_cast<uint32_t>((i / NV) & 1), &none);
-      }
+    if (lane == 0 && sm.abort) {  // loads in flight land before the CTA leaves (bounded as every wait)
+      int none = 0;
+      for (int k = max(0, issued - stages); k < issued; ++k)
+        mbar_wait(&full[k % stages], static_cast<uint32_t>((k / stages) & 1), &none);
     }
     __syncwarp();
-  } else if (warp >= 5) {
-    // -------------------------------- MMA issuers: scores (5), products (6)
+  } else if (warp >= kIssueS) {
+    // ------------------------------------- MMA issuers: scores, products
     // A thread issues one MMA per ~90 cycles whatever its N, so the two
     // products of a tile come from two threads.
     if (lane == 0) {
-      const bool scores = warp == 5;
+      const bool scores = warp == kIssueS;
       const int stages = scores ? NK : NV;
       Ring ring;
       bool ok = true;
@@ -992,7 +951,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   if (tid == 0 && sm.abort) set_status(p.status, SPEC_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == 6) {
+  if (warp == kIssueO) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
