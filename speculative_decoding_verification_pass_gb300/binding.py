@@ -202,8 +202,13 @@ class ModelConfig:
         return self.d_model // self.n_heads
 
     def c(self) -> spec_model_config:
-        return spec_model_config(self.n_layers, self.d_model, self.n_heads, self.n_kv_heads,
-                                 self.d_ffn, self.vocab, self.rms_eps, self.rope_theta)
+        """The C struct (made once: the fields do not change)."""
+        s = self.__dict__.get("_c")
+        if s is None:
+            s = spec_model_config(self.n_layers, self.d_model, self.n_heads, self.n_kv_heads,
+                                  self.d_ffn, self.vocab, self.rms_eps, self.rope_theta)
+            object.__setattr__(self, "_c", s)
+        return s
 
 
 LLAMA_8B = ModelConfig(32, 4096, 32, 8, 14336, 128256)
@@ -413,8 +418,12 @@ class KV8Cache:
                               self.v_scale.data_ptr(), self.len.data_ptr(), self.table.data_ptr(),
                               self.batch, self.n_pages, self.max_pages)
 
-    def _device(self, *tensors) -> int:
-        """The cache's device, on which the call's tensors lie too."""
+    def _device(self, cfg, *tensors) -> int:
+        """The cache's device, on which the call's tensors (a workspace last) lie too; cfg its own shape."""
+        if cfg is not self.cfg and cfg != self.cfg:
+            raise ValueError(f"the cache was made for {self.cfg}, the call is for {cfg}")
+        if tensors[-1].nbytes < 4:
+            raise ValueError("expected a workspace of 4 bytes or more")
         dev = self.len.get_device()
         for t in tensors:
             if t is not None and t.get_device() != dev:
@@ -490,7 +499,7 @@ def spec_kv8_append(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, k, 
     m, width = kv.batch * n, cfg.d_model
     kv_width = width // cfg.n_heads * cfg.n_kv_heads
     dtype = torch.float32 if q.dtype == torch.float32 else torch.bfloat16
-    dev = kv._device(q, k, v, rope.table, q_out, ws, depth)
+    dev = kv._device(cfg, q, k, v, rope.table, q_out, depth, ws)
     q_ld, k_ld, v_ld = (_rows(q, m, width, dtype, "q"), _rows(k, m, kv_width, dtype, "k"),
                         _rows(v, m, kv_width, dtype, "v"))
     with _on(dev):
@@ -505,7 +514,7 @@ def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, 
                        scale: float = 0.0, stream=None):
     """Attention of n new tokens per sequence (q, out bf16 rows) over `layer`'s pages."""
     m, width = kv.batch * n, cfg.d_model
-    dev = kv._device(q, out, ws, anc)
+    dev = kv._device(cfg, q, out, anc, ws)
     q_ld, o_ld = _rows(q, m, width, torch.bfloat16, "q"), _rows(out, m, width, torch.bfloat16, "out")
     with _on(dev):
         _check(lib().spec_kv8_attention(
@@ -515,14 +524,14 @@ def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, 
 
 def spec_kv8_advance(kv: "KV8Cache", n: int, ws, stream=None):
     """len += n after the layers of a pass."""
-    dev = kv._device(ws)
+    dev = kv._device(kv.cfg, ws)
     with _on(dev):
         _check(lib().spec_kv8_advance(kv.c(), n, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_advance")
 
 
 def spec_kv8_truncate(kv: "KV8Cache", n_accepted, gamma: int, ws, stream=None):
     """Rollback: len -= gamma - n_accepted."""
-    dev = kv._device(n_accepted, ws)
+    dev = kv._device(kv.cfg, n_accepted, ws)
     with _on(dev):
         _check(lib().spec_kv8_truncate(kv.c(), _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), gamma,
                                        ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_truncate")
@@ -530,7 +539,7 @@ def spec_kv8_truncate(kv: "KV8Cache", n_accepted, gamma: int, ws, stream=None):
 
 def spec_kv8_tree_commit(cfg: ModelConfig, kv: "KV8Cache", path, n_accepted, n_nodes: int, ws, stream=None):
     """Move the accepted path's rows together in every layer and set the lengths."""
-    dev = kv._device(path, n_accepted, ws)
+    dev = kv._device(cfg, path, n_accepted, ws)
     with _on(dev):
         _check(lib().spec_kv8_tree_commit(
             cfg.c(), kv.c(), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
@@ -545,7 +554,7 @@ def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
 def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cache", logits, ws, anc=None,
                             depth=None, stream=None):
     """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
-    dev = kv._device(tokens, logits, ws, anc, depth)
+    dev = kv._device(kv.cfg, tokens, logits, anc, depth, ws)
     with _on(dev):
         _check(lib().spec_verify_forward_kv8(
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),

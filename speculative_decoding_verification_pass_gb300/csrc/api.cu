@@ -1416,11 +1416,14 @@ namespace {
 
 constexpr int kKv8MaxSlots = 1 << 20;
 
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
+
 // Shape and cache checks shared by the entry points of the 8-bit cache.
 int kv8_checks(const spec_model_config* c, const spec_kv8_cache* kv) {
   if (!kv || !kv->len || !kv->table) return SPEC_EINVAL;
   if (kv->batch < 0 || kv->n_pages <= 0 || kv->max_pages <= 0) return SPEC_EINVAL;
   if (kv->batch > 65535 || kv->max_pages > kKv8MaxSlots / SPEC_PAGE_SLOTS) return SPEC_ESIZE;
+  if (!aligned4(kv->len) || !aligned4(kv->table)) return SPEC_EINVAL;
   if (!c) return SPEC_OK;
   if (!cfg_ok(c) || c->n_layers == 0) return SPEC_EINVAL;
   if (!kv->k || !kv->v || !kv->k_scale || !kv->v_scale) return SPEC_EINVAL;
@@ -1429,6 +1432,9 @@ int kv8_checks(const spec_model_config* c, const spec_kv8_cache* kv) {
     if (reinterpret_cast<uintptr_t>(a) % 16) return SPEC_EINVAL;
   // a layer's row coordinates are 32-bit
   if (static_cast<long long>(kv->n_pages) * c->n_kv_heads * SPEC_PAGE_SLOTS >= (1ll << 31)) return SPEC_ESIZE;
+  // the launches' grids: KV heads in y, (sequence, KV head) in x, layers in y
+  if (c->n_kv_heads > 65535 || c->n_layers > 65535 || static_cast<long long>(kv->batch) * c->n_kv_heads >= (1ll << 31))
+    return SPEC_ESIZE;
   return SPEC_OK;
 }
 
@@ -1474,7 +1480,8 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
   if (!rows_ok(d_q, q_ld, static_cast<int64_t>(cfg->n_heads) * hd, elem) ||
       !rows_ok(d_k, k_ld, static_cast<int64_t>(cfg->n_kv_heads) * hd, elem) ||
       !rows_ok(d_v, v_ld, static_cast<int64_t>(cfg->n_kv_heads) * hd, elem) ||
-      reinterpret_cast<uintptr_t>(d_q_out) % 16 || reinterpret_cast<uintptr_t>(d_table) % 8)
+      reinterpret_cast<uintptr_t>(d_q_out) % 16 || reinterpret_cast<uintptr_t>(d_table) % 8 || !aligned4(d_depth) ||
+      !aligned4(d_ws))
     return SPEC_EINVAL;
   if (n > kMaxN) return SPEC_ESIZE;
   if (kv->batch == 0) return SPEC_OK;
@@ -1520,7 +1527,8 @@ int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, i
   const int64_t width = static_cast<int64_t>(cfg->n_heads) * hd;
   if (layer < 0 || layer >= cfg->n_layers || n < 1) return SPEC_EINVAL;
   if (!rows_ok(d_q, q_ld, width, 2) || !rows_ok(d_o, o_ld, width, 2)) return SPEC_EINVAL;
-  if (!(scale >= 0.f) || std::isinf(scale)) return SPEC_EINVAL;
+  if (!(scale >= 0.f) || std::isinf(scale) || reinterpret_cast<uintptr_t>(d_anc) % 8 || !aligned4(d_ws))
+    return SPEC_EINVAL;
   if (n > (d_anc ? kTreeMaxNodes : kMaxN)) return SPEC_ESIZE;
   if (kv->batch == 0) return SPEC_OK;
   const size_t rows = static_cast<size_t>(kv->n_pages) * cfg->n_kv_heads * SPEC_PAGE_SLOTS * layer;
@@ -1552,7 +1560,7 @@ int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, i
 }
 
 int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) {
-  if (!d_ws || n < 1) return SPEC_EINVAL;
+  if (!d_ws || n < 1 || !aligned4(d_ws)) return SPEC_EINVAL;
   if (const int r = kv8_checks(nullptr, kv)) return r;
   if (n > kMaxN) return SPEC_ESIZE;
   if (kv->batch == 0) return SPEC_OK;
@@ -1563,6 +1571,7 @@ int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) 
 
 int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws, void* stream) {
   if (const int r = kv8_checks(nullptr, kv)) return r;
+  if (!aligned4(d_n_accepted) || !aligned4(d_ws)) return SPEC_EINVAL;
   spec_kv_cache view{};
   view.len = kv->len;
   view.batch = kv->batch;
@@ -1572,8 +1581,9 @@ int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int
 int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv, const int32_t* d_path,
                          const int32_t* d_n_accepted, int n_nodes, void* d_ws, void* stream) {
   if (!cfg || !d_path || !d_n_accepted || !d_ws || n_nodes < 1) return SPEC_EINVAL;
+  if (!aligned4(d_path) || !aligned4(d_n_accepted) || !aligned4(d_ws)) return SPEC_EINVAL;
   if (const int r = kv8_checks(cfg, kv)) return r;
-  if (n_nodes > kTreeMaxNodes || cfg->n_layers > 65535) return SPEC_ESIZE;
+  if (n_nodes > kTreeMaxNodes) return SPEC_ESIZE;
   if (kv->batch == 0) return SPEC_OK;
   Kv8CommitParams p{};
   p.kc = static_cast<uint8_t*>(kv->k);
@@ -1607,6 +1617,7 @@ int spec_verify_forward_kv8(const spec_model* m, const int32_t* d_tokens, const 
                             const int32_t* d_depth, int batch, int n, const spec_kv8_cache* kv, float* d_logits,
                             void* d_ws, size_t ws_bytes, void* stream) {
   if (!m || !d_ws || n < 1 || (d_anc == nullptr) != (d_depth == nullptr)) return SPEC_EINVAL;
+  if (reinterpret_cast<uintptr_t>(d_anc) % 8 || !aligned4(d_depth)) return SPEC_EINVAL;
   if (m->cfg.n_layers == 0) return SPEC_ENOTSUP;
   if (const int r = kv8_checks(&m->cfg, kv)) return r;
   if (batch < 0 || kv->batch != batch) return SPEC_EINVAL;

@@ -149,10 +149,9 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   u /= p.Hkv;
   const int blk_i = static_cast<int>(u % p.nb), b = static_cast<int>(u / p.nb);
   const int L = p.base[b];
-  int32_t bad = kv8_fit(L, p.n, p.table, p.max_pages, p.n_pages, b);
   if (p.seq_ok && !p.seq_ok[b]) return;  // flagged when the pass began
-  if (bad) {
-    if (lane == 0) set_status(p.status, bad);
+  if (L < 0 || L > p.max_pages * kPageSlots - p.n) {
+    if (lane == 0) set_status(p.status, SPEC_DEV_KV_OVERFLOW);
     return;
   }
   const int slot0 = (L / kKv8Block + blk_i) * kKv8Block;  // the block's first slot
@@ -160,7 +159,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   const void* src = which ? p.v : p.k;
   const long long ld = which ? p.v_ld : p.k_ld;
   const Pair4 at = which ? pair4(li, 0, 1) : pr;
-  float x[IT][4];
+  float x[IT][4];  // (on their way before the pages are looked at)
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
     const int j = slot0 + i * RPW + sub - L;  // the row's token
@@ -171,6 +170,15 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
       x[i][0] = a.x, x[i][1] = a.y, x[i][2] = c.x, x[i][3] = c.y;
     }
   }
+  int page;
+  if (const int32_t bad = kv8_fit_warp(L, p.n, p.table, p.max_pages, p.n_pages, b, slot0, &page)) {
+    if (lane == 0) set_status(p.status, bad);
+    return;
+  }
+  const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
+  float* sp = (which ? p.vs : p.ks) + map.scale(page, h, slot0);
+  const int kept = max(0, L - slot0);  // rows the block holds from before
+  const float s_held = kept ? *sp : 0.f;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
@@ -189,17 +197,10 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
     }
   }
   amax = warp_max(amax);
-  const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
-  const int page = map.page(b, slot0);
   uint8_t* codes = (which ? p.vc : p.kc) + map.row(page, h, slot0);
-  float* sp = (which ? p.vs : p.ks) + map.scale(page, h, slot0);
-  const int kept = max(0, L - slot0);  // rows the block holds from before
-  float s = kv8_scale(amax);
-  float s_old = s;
-  if (kept) {
-    s_old = *sp;
-    s = fmaxf(s, s_old);
-  }
+  const float s_new = kv8_scale(amax);
+  const float s = kept ? fmaxf(s_new, s_held) : s_new;
+  const float s_old = kept ? s_held : s;
   const float inv = pow2_inv(s), ratio = s_old * inv;
   __syncwarp();  // every lane has read the scale before lane 0 replaces it
 #pragma unroll
@@ -224,115 +225,136 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
 
 // ------------------------------------------------------------------ commit
 // Moves the accepted path's rows L0 + path[d - 1] -> L0 + d (d = 1 .. m) of one
-// (layer, sequence, KV head), keys and values.  A destination block's scale is
-// the largest of those its rows come with: the rows moved in, and its own if
-// it keeps rows (slots up to the root, L0).  Every row is read before any is
-// written: rows and scales go through registers and shared memory.
-constexpr int kMoveThreads = 128;
+// (sequence, KV head), keys and values, in up to kMoveLayers layers.  A
+// destination block's scale is the largest of those its rows come with: the
+// rows moved in, and its own if it keeps rows (slots up to the root, L0).
+// Every row of a layer is read before any is written: rows and scales go
+// through registers and shared memory.  What bounds it is the chain of round
+// trips (length, path, page, row); a path of a few rows leaves a thread one
+// 16-byte word a layer, so a CTA takes as many layers at once as its registers
+// hold (one layer a CTA, 4096 CTAs: 16.4 us at 16 sequences and 32 layers).
+constexpr int kMoveThreads = 256;
+constexpr int kMoveLayers = 8;
+constexpr int kMoveWords = 8;                                                 // 16-byte words per thread
 constexpr int kMoveBlocks = (kTreeMaxNodes + 2 * kKv8Block - 2) / kKv8Block;  // blocks n slots can touch
 
-// 0 when the path of sequence b can be committed, else the status bit.
+// 0 when the path of sequence b can be committed, else the status bit (the
+// same for every lane of the warp).
 SPEC_DEVINL int32_t kv8_path_bad(const Kv8CommitParams& p, int b, int len, int m) {
+  static_assert(kTreeMaxNodes <= 64, "two nodes a lane");
   if (m < 0 || m >= p.n) return SPEC_DEV_BAD_TREE;
   const int32_t* path = p.path + static_cast<long long>(b) * p.n;
-  int prev = 0;
-  for (int d = 0; d < m; ++d) {
-    const int s = __ldg(path + d);
-    if (s <= prev || s >= p.n) return SPEC_DEV_BAD_TREE;
-    prev = s;
+  const int lane = threadIdx.x & 31;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int d = lane + 32 * k;
+    if (d < m) {
+      const int s = __ldg(path + d);
+      bad |= s <= (d ? __ldg(path + d - 1) : 0) || s >= p.n;
+    }
   }
+  if (__any_sync(0xffffffffu, bad)) return SPEC_DEV_BAD_TREE;
   if (len < p.n) return SPEC_DEV_KV_OVERFLOW;
-  return kv8_fit(len - p.n, p.n, p.table, p.max_pages, p.n_pages, b);
+  int page;
+  return kv8_fit_warp(len - p.n, p.n, p.table, p.max_pages, p.n_pages, b, len - p.n, &page);
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kMoveThreads) kv8_commit_kernel(const Kv8CommitParams p) {
-  constexpr int VEC = HD / 16;                                             // 16-byte words per row
-  constexpr int PER = 2 * (kTreeMaxNodes - 1) * VEC / kMoveThreads + 1;   // words per thread
-  __shared__ float s_src[2][kTreeMaxNodes], s_dst[2][kMoveBlocks], s_own[2];
+  constexpr int VEC = HD / 16;  // 16-byte words per row
+  static_assert(2 * (kTreeMaxNodes - 1) * VEC <= kMoveWords * kMoveThreads, "a layer fits the registers");
+  __shared__ float s_src[kMoveLayers][2][kTreeMaxNodes], s_dst[kMoveLayers][2][kMoveBlocks], s_own[kMoveLayers][2];
   grid_dep_wait();
   grid_dep_launch();
-  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv, layer = blockIdx.y;
+  const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int tid = threadIdx.x;
   const int len = p.len[b], m = __ldg(p.n_acc + b);
   if (m <= 0 || kv8_path_bad(p, b, len, m)) return;  // the length update reports it
   const int L0 = len - p.n;
   const int32_t* path = p.path + static_cast<long long>(b) * p.n;
   const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
-  const long long lrow = static_cast<long long>(layer) * p.n_pages * p.Hkv * kPageSlots * HD;
-  const long long lsc = static_cast<long long>(layer) * p.n_pages * p.Hkv * kKv8Sub;
-  uint8_t* const codes[2] = {p.kc + lrow, p.vc + lrow};
-  float* const scales[2] = {p.ks + lsc, p.vs + lsc};
-  const int per_side = m * VEC;
-  uint4 w[PER];
+  const long long layer_rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
+  const auto codes = [&](int side, int layer) { return (side ? p.vc : p.kc) + layer * layer_rows * HD; };
+  const auto scales = [&](int side, int layer) { return (side ? p.vs : p.ks) + layer * (layer_rows / kKv8Block); };
+  const int per_side = m * VEC, per_layer = 2 * per_side;
+  const int blk0 = L0 / kKv8Block, nblk = (L0 + m) / kKv8Block - blk0 + 1;
+  const int last = min(p.L, static_cast<int>(blockIdx.y + 1) * kMoveLayers);
+  const int at_once = min(kMoveLayers, kMoveWords * kMoveThreads / per_layer);
+  for (int layer0 = blockIdx.y * kMoveLayers; layer0 < last; layer0 += at_once) {
+    const int nl = min(at_once, last - layer0);
+    uint4 w[kMoveWords];
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int e = tid + k * kMoveThreads;
-    if (e < 2 * per_side) {
-      const int side = e >= per_side, rem = e - side * per_side;
-      const int src = L0 + __ldg(path + rem / VEC);
-      w[k] = reinterpret_cast<const uint4*>(codes[side] + map.row(map.page(b, src), h, src))[rem % VEC];
+    for (int k = 0; k < kMoveWords; ++k) {
+      const int e = tid + k * kMoveThreads;
+      if (e < nl * per_layer) {
+        const int l = e / per_layer, f = e - l * per_layer, side = f >= per_side, rem = f - side * per_side;
+        const int src = L0 + __ldg(path + rem / VEC);
+        w[k] = reinterpret_cast<const uint4*>(codes(side, layer0 + l) + map.row(map.page(b, src), h, src))[rem % VEC];
+      }
     }
-  }
-  for (int e = tid; e < 2 * m; e += kMoveThreads) {
-    const int side = e >= m, d = e - side * m;
-    const int src = L0 + __ldg(path + d);
-    s_src[side][d] = scales[side][map.scale(map.page(b, src), h, src)];
-  }
-  if (tid < 2) s_own[tid] = scales[tid][map.scale(map.page(b, L0), h, L0)];
-  __syncthreads();
-  const int blk0 = L0 / kKv8Block;
-  const int nblk = (L0 + m) / kKv8Block - blk0 + 1;
-  for (int e = tid; e < 2 * nblk; e += kMoveThreads) {
-    const int side = e >= nblk, i = e - side * nblk;
-    const int d0 = max(1, (blk0 + i) * kKv8Block - L0), d1 = min(m, (blk0 + i + 1) * kKv8Block - 1 - L0);
-    float s = i == 0 ? s_own[side] : 0.f;  // the root's block keeps rows
-    for (int d = d0; d <= d1; ++d) s = fmaxf(s, s_src[side][d - 1]);
-    s_dst[side][i] = s;
-    if (d0 <= d1) {
-      const int t = (blk0 + i) * kKv8Block;
-      scales[side][map.scale(map.page(b, t), h, t)] = s;
+    for (int e = tid; e < nl * 2 * m; e += kMoveThreads) {
+      const int l = e / (2 * m), f = e - l * 2 * m, side = f >= m, d = f - side * m;
+      const int src = L0 + __ldg(path + d);
+      s_src[l][side][d] = scales(side, layer0 + l)[map.scale(map.page(b, src), h, src)];
     }
-  }
-  __syncthreads();
+    if (tid < 2 * nl) s_own[tid / 2][tid % 2] = scales(tid % 2, layer0 + tid / 2)[map.scale(map.page(b, L0), h, L0)];
+    __syncthreads();
+    for (int e = tid; e < nl * 2 * nblk; e += kMoveThreads) {
+      const int l = e / (2 * nblk), f = e - l * 2 * nblk, side = f >= nblk, i = f - side * nblk;
+      const int d0 = max(1, (blk0 + i) * kKv8Block - L0), d1 = min(m, (blk0 + i + 1) * kKv8Block - 1 - L0);
+      float s = i == 0 ? s_own[l][side] : 0.f;  // the root's block keeps rows
+      for (int d = d0; d <= d1; ++d) s = fmaxf(s, s_src[l][side][d - 1]);
+      s_dst[l][side][i] = s;
+      if (d0 <= d1) {
+        const int t = (blk0 + i) * kKv8Block;
+        scales(side, layer0 + l)[map.scale(map.page(b, t), h, t)] = s;
+      }
+    }
+    __syncthreads();
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int e = tid + k * kMoveThreads;
-    if (e >= 2 * per_side) continue;
-    const int side = e >= per_side, rem = e - side * per_side, d = rem / VEC + 1;
-    const float ratio = s_src[side][d - 1] * pow2_inv(s_dst[side][(L0 + d) / kKv8Block - blk0]);
-    uint4 v = w[k];
-    if (ratio < 1.f)
-      v = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
-                     kv8_rescale4(v.w, ratio));
-    reinterpret_cast<uint4*>(codes[side] + map.row(map.page(b, L0 + d), h, L0 + d))[rem % VEC] = v;
-  }
-  // rows that the root's block holds, if its scale has grown
-  const int t0 = blk0 * kKv8Block, kept = L0 - t0 + 1;
-  for (int e = tid; e < 2 * kept * VEC; e += kMoveThreads) {
-    const int side = e >= kept * VEC, rem = e - side * kept * VEC;
-    const float ratio = s_own[side] * pow2_inv(s_dst[side][0]);
-    if (ratio >= 1.f) continue;
-    const int t = t0 + rem / VEC;
-    uint4* a = reinterpret_cast<uint4*>(codes[side] + map.row(map.page(b, t), h, t)) + rem % VEC;
-    const uint4 v = *a;
-    *a = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
-                    kv8_rescale4(v.w, ratio));
+    for (int k = 0; k < kMoveWords; ++k) {
+      const int e = tid + k * kMoveThreads;
+      if (e >= nl * per_layer) continue;
+      const int l = e / per_layer, f = e - l * per_layer, side = f >= per_side, rem = f - side * per_side;
+      const int d = rem / VEC + 1;
+      const float ratio = s_src[l][side][d - 1] * pow2_inv(s_dst[l][side][(L0 + d) / kKv8Block - blk0]);
+      uint4 v = w[k];
+      if (ratio < 1.f)
+        v = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
+                       kv8_rescale4(v.w, ratio));
+      reinterpret_cast<uint4*>(codes(side, layer0 + l) + map.row(map.page(b, L0 + d), h, L0 + d))[rem % VEC] = v;
+    }
+    // rows that the root's block holds, if its scale has grown
+    const int t0 = blk0 * kKv8Block, kept = L0 - t0 + 1;
+    for (int e = tid; e < nl * 2 * kept * VEC; e += kMoveThreads) {
+      const int l = e / (2 * kept * VEC), f = e - l * 2 * kept * VEC, side = f >= kept * VEC, rem = f - side * kept * VEC;
+      const float ratio = s_own[l][side] * pow2_inv(s_dst[l][side][0]);
+      if (ratio >= 1.f) continue;
+      const int t = t0 + rem / VEC;
+      uint4* a = reinterpret_cast<uint4*>(codes(side, layer0 + l) + map.row(map.page(b, t), h, t)) + rem % VEC;
+      const uint4 v = *a;
+      *a = make_uint4(kv8_rescale4(v.x, ratio), kv8_rescale4(v.y, ratio), kv8_rescale4(v.z, ratio),
+                      kv8_rescale4(v.w, ratio));
+    }
+    __syncthreads();  // the scales in shared memory are the next layers'
   }
 }
 
-// len = L0 + 1 + m, after the copies (a launch of its own: they read len).
+// len = L0 + 1 + m, after the copies (a launch of its own: they read len); a
+// warp per sequence.
 __global__ void kv8_commit_len_kernel(const Kv8CommitParams p) {
   grid_dep_wait();
   grid_dep_launch();
-  const int b = blockIdx.x * blockDim.x + threadIdx.x;
+  const int b = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32;
   if (b >= p.B) return;
   const int len = p.len[b], m = p.n_acc[b];
-  if (const int32_t bad = kv8_path_bad(p, b, len, m)) {
+  const int32_t bad = kv8_path_bad(p, b, len, m);
+  if (threadIdx.x % 32) return;
+  if (bad)
     set_status(p.status, bad);
-    return;
-  }
-  p.len[b] = len - p.n + 1 + m;
+  else
+    p.len[b] = len - p.n + 1 + m;
 }
 
 // len += n for every sequence whose slots and pages (all of [0, len + n)) are
@@ -387,10 +409,10 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
 cudaError_t launch_kv8_commit(const Kv8CommitParams& p, cudaStream_t stream) {
   if (p.n > 1) {
     const cudaError_t e = launch_dep(p.hd == 128 ? kv8_commit_kernel<128> : kv8_commit_kernel<64>,
-                                     dim3(p.B * p.Hkv, p.L), kMoveThreads, stream, p);
+                                     dim3(p.B * p.Hkv, (p.L + kMoveLayers - 1) / kMoveLayers), kMoveThreads, stream, p);
     if (e != cudaSuccess) return e;
   }
-  return launch_dep(kv8_commit_len_kernel, dim3((p.B + 127) / 128), 128, stream, p);
+  return launch_dep(kv8_commit_len_kernel, dim3((p.B + 3) / 4), 128, stream, p);
 }
 
 cudaError_t launch_kv8_advance(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,

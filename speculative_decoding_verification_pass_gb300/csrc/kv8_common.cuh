@@ -75,15 +75,18 @@ struct Kv8Map {
   }
 };
 
-// 0 when slots [L, L + n) of sequence b lie within the capacity and on pages
-// of the pool, else the status bit.  Only
-// the pages written are looked at.
-SPEC_DEVINL int32_t kv8_fit(int L, int n, const int32_t* table, int max_pages, int n_pages, int b) {
+// 0 when slots [L, L + n) of sequence b (n <= 128) lie within the capacity and
+// on pages of the pool, else the status bit.  Only those pages are looked at, a
+// lane each; every lane of the warp calls it and gets the answer, and in *page
+// the page of slot t (one of the slots, or of the block that slot L is in).
+SPEC_DEVINL int32_t kv8_fit_warp(int L, int n, const int32_t* table, int max_pages, int n_pages, int b, int t,
+                                 int* page) {
+  *page = 0;
   if (L < 0 || L > max_pages * kPageSlots - n) return SPEC_DEV_KV_OVERFLOW;
-  for (int j = L / kPageSlots; j <= (L + n - 1) / kPageSlots; ++j) {
-    const int pg = __ldg(table + static_cast<long long>(b) * max_pages + j);
-    if (pg < 0 || pg >= n_pages) return SPEC_DEV_BAD_PAGE;
-  }
+  const int p0 = L / kPageSlots, np = (L + n - 1) / kPageSlots - p0 + 1, lane = threadIdx.x & 31;
+  const int pg = lane < np ? __ldg(table + static_cast<long long>(b) * max_pages + p0 + lane) : 0;
+  if (__any_sync(0xffffffffu, pg < 0 || pg >= n_pages)) return SPEC_DEV_BAD_PAGE;
+  *page = __shfl_sync(0xffffffffu, pg, t / kPageSlots - p0);
   return 0;
 }
 
