@@ -595,6 +595,197 @@ def test_other_stream_and_graph():
     assert _status(ws) == (sb.SPEC_OK, 0)
 
 
+def _fill(kv, seed):
+    """Codes that are numbers and scales near those of unit rows in every page."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    for x, s in ((kv.k, kv.k_scale), (kv.v, kv.v_scale)):
+        bits = x.view(torch.uint8)
+        bits.random_(0, 256, generator=g)
+        bits[(bits & 0x7F) == 0x7F] = 0x31
+        s.copy_(torch.exp2(torch.randint(-9, -6, s.shape, generator=g, device="cuda").float()))
+
+
+@pytest.mark.parametrize("B,top,n", [(100, 300, 2), (40, 1500, 5), (13, 4000, 3), (2, 3000, 5), (96, 40, 1)])
+def test_attention_of_many_sequences(B, top, n):
+    """Batches on either side of the ordering by length, with lengths far apart: every sequence gets what
+    it gets alone, but for the order in which its tiles are summed."""
+    cfg = _cfg("64x16/2")
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, top, B)
+    lens[:: 7] //= 50
+    lens[0], lens[-1] = 0, top
+    pages = [(int(x) + n + 63) // 64 for x in lens]
+    kv = sb.KV8Cache(cfg, B, sum(pages), max(pages))
+    for b in rng.permutation(B):
+        kv.reserve(int(b), int(lens[b]) + n)
+    kv.sync()
+    _fill(kv, B)
+    kv.len.copy_(_dev(lens.astype(np.int32)))
+    q = _q(B * n, cfg.d_model, 61)
+    ws = sb.workspace(256)
+    out = torch.empty_like(q)
+    sb.spec_kv8_attention(cfg, kv, 0, n, q, out, ws)
+    one = sb.KV8Cache(cfg, 1, kv.n_pages, kv.max_pages)
+    one.k, one.v, one.k_scale, one.v_scale = kv.k, kv.v, kv.k_scale, kv.v_scale
+    for b in range(B):
+        one.table.copy_(kv.table[b:b + 1])
+        one.len.fill_(int(lens[b]))
+        want = torch.empty(n, cfg.d_model, dtype=torch.bfloat16, device="cuda")
+        sb.spec_kv8_attention(cfg, one, 0, n, q[b * n:(b + 1) * n], want, ws)
+        got = out[b * n:(b + 1) * n]
+        # each side rounds once (half a step each: a whole one between them), its weights 2^-11 of the values
+        lim = 2.0 ** -7 * want.float().abs() + 2.0 ** -9 * want.float().abs().max()
+        assert ((got.float() - want.float()).abs() <= lim).all(), (b, int(lens[b]))
+    assert _status(ws) == (sb.SPEC_OK, 0)
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond 2^32 bytes of one layer: the same rows there and at the start of a small pool."""
+    cfg, n, L = _cfg("128x8/8", 2), 5, 300
+    many = 70000  # x 8 heads x 64 x 128 bytes = 4.6 GB a layer and side, the second layer past 2^32 from its start
+    H, hd, Hkv = cfg.n_heads, cfg.head_dim, cfg.n_kv_heads
+    small = sb.KV8Cache(cfg, 1, 8, 6)
+    big = sb.KV8Cache(cfg, 1, many, 6)
+    _fill(small, 3)
+    ids = torch.tensor([[5, 1, 7, 0, 2, 3]], dtype=torch.int32)
+    far = ids + many - 8
+    small.table.copy_(ids)
+    big.table.copy_(far)
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x, y = getattr(small, name), getattr(big, name)
+        y.view(torch.uint8)[:, many - 8:] = x.view(torch.uint8)
+    R, ws = sb.RopeTable(hd, THETA), sb.workspace(256)
+    q, k, v = (_q(n, h * hd, 70 + i) for i, h in enumerate((H, Hkv, Hkv)))
+    res = []
+    for kv in (small, big):
+        kv.len.fill_(L)
+        for layer in range(2):
+            q_out, o = torch.empty_like(q), torch.empty_like(q)
+            sb.spec_kv8_append(cfg, kv, layer, n, q, k, v, R, q_out, ws)
+            sb.spec_kv8_attention(cfg, kv, layer, n, q_out, o, ws)
+            res.append(o)
+        sb.spec_kv8_advance(kv, n, ws)
+        path = torch.tensor([[2, 4, -1, -1, -1]], dtype=torch.int32, device="cuda")
+        sb.spec_kv8_tree_commit(cfg, kv, path, torch.tensor([2], dtype=torch.int32, device="cuda"), n, ws)
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    assert torch.equal(res[0], res[2]) and torch.equal(res[1], res[3]) and not torch.equal(res[0], res[1])
+    for name in ("k", "v", "k_scale", "v_scale"):
+        x, y = getattr(small, name).view(torch.uint8), getattr(big, name).view(torch.uint8)
+        assert torch.equal(x, y[:, many - 8:])
+        assert not y[0, :64].any() if name in "kv" else True
+
+
+def test_two_streams_at_once():
+    """Two caches worked on by two streams at the same time, one workspace each."""
+    cfg, B = _cfg("128x4/1"), 3
+    R = sb.RopeTable(cfg.head_dim, THETA)
+
+    def cache():
+        kv = sb.KV8Cache(cfg, B, 2 * B, 2)
+        for b in range(B):
+            kv.reserve(b, 128)
+        kv.sync()
+        return kv
+
+    steps = [_steps(cfg, B, s) for s in (81, 82)]
+    want = [_round_trip(cfg, cache(), st, R, sb.workspace(256)) for st in steps]
+    kvs, wss = [cache() for _ in range(2)], [sb.workspace(256) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for i in range(len(steps[0])):
+        for k in range(2):
+            got[k] += _round_trip(cfg, kvs[k], [steps[k][i]], R, wss[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for a, b in zip(want[0] + want[1], got[0] + got[1]):
+        assert torch.equal(a, b)
+    for ws in wss:
+        assert _status(ws) == (sb.SPEC_OK, 0)
+
+
+def test_tree_round_against_the_oracle():
+    """Append of a tree at its depths, its attention, the commit, and the next chain round."""
+    cfg, n, lens = _cfg("64x4/2"), 11, (13, 60, 0)
+    hd, H, Hkv, B = cfg.head_dim, cfg.n_heads, cfg.n_kv_heads, 3
+    P = Pair(cfg, lens, n + 8, 27)
+    R, ws = sb.RopeTable(hd, THETA), sb.workspace(256)
+    masks, depth = zip(*(sb.spec_tree_masks(wl.random_tree(90 + b, n)) for b in range(B)))
+    anc = _dev(np.array(masks, np.uint64).astype(np.int64))
+    dep = _dev(np.array(depth, np.int32))
+    g = torch.Generator().manual_seed(91)
+    q, k, v = (torch.randn(B * n, h * hd, generator=g) for h in (H, Hkv, Hkv))
+    q_out = torch.empty(B * n, H * hd, dtype=torch.bfloat16, device="cuda")
+    o = torch.empty_like(q_out)
+    sb.spec_kv8_append(cfg, P.kv, 0, n, q.cuda(), k.cuda(), v.cuda(), R, q_out, ws, depth=dep)
+    sb.spec_kv8_attention(cfg, P.kv, 0, n, q_out, o, ws, anc=anc)
+    freq = O8.frequencies(hd, THETA)
+    for b, L in enumerate(lens):
+        for j in range(n):
+            m = b * n + j
+            want = O8.rotate(q[m].double().numpy().reshape(H, hd), L + depth[b][j], freq, False)
+            got = q_out[m].double().cpu().numpy().reshape(H, hd)
+            assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want) + 2.0 ** -18).all()
+        for name, x in (("k", k), ("v", v)):  # from here on the rows that the device holds
+            new = x[b * n:(b + 1) * n].double().numpy().reshape(n, Hkv, hd)
+            want = P.rows[0, b, name]
+            want.append(L, new)
+            code, scale = P.got(0, b, name)
+            if name == "v":
+                np.testing.assert_array_equal(code[:, :L + n], want.code[:, :L + n])
+                np.testing.assert_array_equal(scale[:, : (L + n + 15) // 16], want.scale[:, : (L + n + 15) // 16])
+            want.code, want.scale = code, scale
+    see = [np.array([[(m >> i) & 1 for i in range(n)] for m in masks[b]], bool) for b in range(B)]
+    _check_attention(cfg, P, n, q_out, o, see, hd ** -0.5)
+    sb.spec_kv8_advance(P.kv, n, ws)
+    path = np.full((B, n), -1, np.int32)
+    paths = []
+    for b in range(B):  # root-to-node path of the last node
+        m = masks[b][n - 1]
+        paths.append([i for i in range(1, n) if (m >> i) & 1])
+        path[b, :len(paths[b])] = paths[b]
+    sb.spec_kv8_tree_commit(cfg, P.kv, _dev(path), _dev(np.array([len(p) for p in paths], np.int32)), n, ws)
+    for b, L in enumerate(lens):
+        for name in "kv":
+            P.rows[0, b, name].commit(L, paths[b])
+            code, scale = P.got(0, b, name)
+            np.testing.assert_array_equal(code, P.rows[0, b, name].code)
+            np.testing.assert_array_equal(scale, P.rows[0, b, name].scale)
+    P.lens = [L + 1 + len(p) for L, p in zip(lens, paths)]
+    assert P.kv.len.cpu().tolist() == P.lens
+    q2 = _q(B * 4, H * hd, 92)
+    out, _ = _run_attention(cfg, P, 4, q2, ws=ws)
+    _check_attention(cfg, P, 4, q2, out, [_chain(4)] * B, hd ** -0.5)
+    assert _status(ws) == (sb.SPEC_OK, 0)
+
+
+def test_refused_caches():
+    cfg = _cfg("64x4/2")
+    kv = sb.KV8Cache(cfg, 2, 4, 2)
+    for name, bad in (("k", kv.k[:, :3]), ("k", kv.k.view(torch.uint8)), ("k_scale", kv.k_scale.double()),
+                      ("len", kv.len.long()), ("table", kv.table.t()), ("len", kv.len.cpu())):
+        with pytest.raises(ValueError):
+            setattr(kv, name, bad)
+    ws = sb.workspace(256)
+    q = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError):  # the cache of another shape
+        sb.spec_kv8_attention(_cfg("64x4/2", 2), kv, 0, 2, q, q.clone(), ws)
+    with pytest.raises(ValueError):
+        sb.spec_kv8_attention(cfg, kv, 0, 2, q, q.clone(), ws[:0])
+    with pytest.raises(sb.SpecError) as e:
+        sb.spec_kv8_attention(cfg, kv, 1, 2, q, q.clone(), ws)
+    assert e.value.status == sb.SPEC_EINVAL
+
+
+def test_attention_in_place():
+    """The output may be the queries' own rows."""
+    cfg, n, lens = _cfg("128x4/1"), 9, (700, 3)
+    P = Pair(cfg, lens, n, 28)
+    q = _q(len(lens) * n, cfg.d_model, 36)
+    want, ws = _run_attention(cfg, P, n, q)
+    sb.spec_kv8_attention(cfg, P.kv, 0, n, q, q, ws)
+    assert torch.equal(q, want)
+
+
 # ------------------------------------------------------------------ forward
 class Kv8State(OM.KVState):
     """The oracle's cache with rows held in 8 bits (keep() rounds the new rows in place)."""
@@ -689,4 +880,51 @@ def test_forward_tree_equals_chain_and_commits():
     sb.spec_verify_forward_kv8(m.handle, nxt, B, 3, kvc, zd, ws)
     assert close(zt, zd)
     assert _status(ws) == (sb.SPEC_OK, 0)
+    m.close()
+
+
+def test_forward_of_a_large_batch_and_refusals():
+    """More than 128 token rows: each sequence as in a batch of its own; and what the pass refuses."""
+    shape = (2, 256, 4, 2, 256, 1000)
+    cfg, B, n, seed = sb.ModelConfig(*shape), 40, 5, 46
+    m = sb.Model(cfg, seed)
+    ws = sb.workspace(sb.spec_kv8_workspace_bytes(cfg, B, 12))
+    lens = np.random.default_rng(4).integers(1, 12, B)
+    toks = wl.tokens(seed, B, 12, cfg.vocab)
+    new = wl.tokens(seed + 1, B, n, cfg.vocab)
+
+    def run(rows):
+        kv = sb.KV8Cache(cfg, len(rows), len(rows), 1)
+        for i in range(len(rows)):
+            kv.reserve(i, 64)
+        kv.sync()
+        z = torch.empty(len(rows), 12, cfg.vocab, device="cuda")
+        sb.spec_verify_forward_kv8(m.handle, _dev(toks[rows]), len(rows), 12, kv, z, ws)
+        kv.len.copy_(_dev(lens[rows].astype(np.int32)))  # sequences of different lengths
+        z = torch.empty(len(rows), n, cfg.vocab, device="cuda")
+        sb.spec_verify_forward_kv8(m.handle, _dev(new[rows]), len(rows), n, kv, z, ws)
+        return z, kv
+
+    z, kv = run(np.arange(B))
+    assert kv.len.cpu().tolist() == (lens + n).tolist()
+    for b in (0, 7, 39):
+        want, _ = run(np.array([b]))
+        assert ((z[b] - want[0]).abs() <= 1e-2 * (1 + want[0].abs())).all()
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    # a sequence without room is flagged and keeps its length and rows
+    kv.len[3] = 62
+    before = kv.k.view(torch.uint8)[:, int(kv.table[3, 0])].clone()
+    sb.spec_verify_forward_kv8(m.handle, _dev(new), B, n, kv, z, ws)
+    assert _status(ws) == (sb.SPEC_EDEVICE, sb.DEV_KV_OVERFLOW)
+    assert int(kv.len[3]) == 62 and torch.equal(kv.k.view(torch.uint8)[:, int(kv.table[3, 0])], before)
+    for kw, status in ((dict(ws=ws[:4096]), sb.SPEC_ESIZE), (dict(n=13), sb.SPEC_ESIZE)):
+        k = dict(dict(n=n, ws=ws), **kw)
+        t = torch.zeros(B, k["n"], dtype=torch.int32, device="cuda")
+        with pytest.raises(sb.SpecError) as e:
+            sb.spec_verify_forward_kv8(m.handle, t, B, k["n"], kv, torch.empty(B, k["n"], cfg.vocab, device="cuda"), k["ws"])
+        assert e.value.status == status
+    with pytest.raises(sb.SpecError) as e:  # a tree's masks without its depths
+        sb.spec_verify_forward_kv8(m.handle, _dev(new), B, n, kv, z, ws,
+                                   anc=torch.zeros(B, n, dtype=torch.int64, device="cuda"))
+    assert e.value.status == sb.SPEC_EINVAL
     m.close()

@@ -94,7 +94,7 @@ def test_refusals(lib):
     assert L.spec_kv8_advance(_cache(lib), 5, ok, None) == lib.SPEC_OK
     bad_caches = [(_cache(lib, len=0), E), (_cache(lib, table=0), E), (_cache(lib, batch=-1), E),
                   (_cache(lib, n_pages=0), E), (_cache(lib, max_pages=0), E), (_cache(lib, batch=65536), S),
-                  (_cache(lib, max_pages=16385), S)]
+                  (_cache(lib, max_pages=16385), S), (_cache(lib, len=4098), E), (_cache(lib, table=4097), E)]
     for kv, want in bad_caches:
         assert append(kv=kv) == attend(kv=kv) == commit(kv=kv) == want
         assert L.spec_kv8_advance(kv, 5, ok, None) == want
@@ -123,6 +123,10 @@ def test_refusals(lib):
     for kw in (dict(cfg=None), dict(path=None), dict(m=None), dict(ws=None), dict(n=0)):
         assert commit(**kw) == E, kw
     assert commit(n=65) == S
+    assert commit(path=P(4098)) == commit(m=P(4097)) == commit(ws=P(4099)) == E
+    assert attend(anc=P(4100)) == attend(ws=P(4097)) == append(ws=P(4098)) == E
+    big = ctypes.byref(lib.ModelConfig(70000, 256, 4, 2, 256, 1000).c())  # layers past a launch's grid
+    assert append(cfg=big) == attend(cfg=big) == commit(cfg=big) == S
     assert L.spec_kv8_advance(_cache(lib), 0, ok, None) == E
     assert L.spec_kv8_advance(_cache(lib), 129, ok, None) == S
     assert L.spec_rope_table(ctypes.byref(rope), None, None) == E
