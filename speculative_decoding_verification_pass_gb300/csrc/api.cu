@@ -863,6 +863,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
       Kv8AttnParams t{};
       t.q = q;
       t.o = o;
+      t.o_lo = o_lo;
       t.q_ld = t.o_ld = qd;
       t.kc = a.kc;
       t.vc = a.vc;
@@ -969,7 +970,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
       p.hb_lo = hb_lo;
       p.g_next = reinterpret_cast<const float*>(B + L.g_mlp[l]);
       p.ssq_out = ssq;
-      int r = run_gemm(cx, &m->tm_o[l], o, k8 ? nullptr : o_lo, M, d, qd, p);
+      int r = run_gemm(cx, &m->tm_o[l], o, o_lo, M, d, qd, p);
       if (r) return r;
     }
     {  // gate/up + SwiGLU

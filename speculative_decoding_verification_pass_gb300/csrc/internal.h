@@ -320,6 +320,7 @@ cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream);
 struct Kv8AttnParams {
   const uint16_t* q;          // [B*n] rows of H*hd bf16, q_ld apart
   uint16_t* o;
+  uint16_t* o_lo;             // bf16 residual of o in the same places, or nullptr
   long long q_ld, o_ld;
   const uint8_t *kc, *vc;     // this layer's codes
   const float *ks, *vs;       // this layer's scales

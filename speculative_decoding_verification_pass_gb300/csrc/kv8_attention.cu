@@ -122,6 +122,12 @@ SPEC_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
   return d;
 }
+// Two fp32 values to bf16 (`a` low; infinities and NaN kept).
+SPEC_DEVINL uint32_t bf16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
 // fp16 pairs: two fp32 rounded, product, a b + c, to e4m3 and back (`a` low).
 SPEC_DEVINL uint32_t f16x2(float a, float b) {
   uint32_t r;
@@ -321,7 +327,9 @@ struct AttMaps {
   CUtensorMap k, v;
 };
 
-template <int HD, int RT>
+// kLo: the bf16 residual of o is written too (a kernel of its own: as a branch,
+// its code cost batch 64 5%).
+template <int HD, int RT, bool kLo>
 __global__ void __launch_bounds__(kAttThreads, 2)
     kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int lc, const int NK, const int NV,
                          const int share) {
@@ -890,10 +898,21 @@ __global__ void __launch_bounds__(kAttThreads, 2)
           const longlong2 at = *reinterpret_cast<const longlong2*>(&sm.out[r]);
           // (a factor of zero is a row that sees nothing, whatever its sum holds)
           const float x = f.x == 0.f ? 0.f : acc[r] * f.x, y = f.y == 0.f ? 0.f : acc[r + 1] * f.y;
-          uint32_t u;
-          asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(y), "f"(x));
+          const uint32_t u = bf16x2(x, y);
           if (at.x >= 0) o[at.x] = static_cast<uint16_t>(u);
           if (at.y >= 0) o[at.y] = static_cast<uint16_t>(u >> 16);
+          acc[r] = x - bf16lo(u);
+          acc[r + 1] = y - bf16hi(u);
+        }
+        if constexpr (kLo) {
+          o = p.o_lo + tid;
+#pragma unroll
+          for (int r = 0; r < RT; r += 2) {
+            const longlong2 at = *reinterpret_cast<const longlong2*>(&sm.out[r]);
+            const uint32_t u = bf16x2(acc[r], acc[r + 1]);
+            if (at.x >= 0) o[at.x] = static_cast<uint16_t>(u);
+            if (at.y >= 0) o[at.y] = static_cast<uint16_t>(u >> 16);
+          }
         }
       }
     }
@@ -942,10 +961,11 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       o.y = zero ? 0.f : o.y * inv;
       o.z = zero ? 0.f : o.z * inv;
       o.w = zero ? 0.f : o.w * inv;
-      uint2 u;
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.x) : "f"(o.y), "f"(o.x));
-      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u.y) : "f"(o.w), "f"(o.z));
+      const uint2 u = make_uint2(bf16x2(o.x, o.y), bf16x2(o.z, o.w));
       *reinterpret_cast<uint2*>(p.o + sm.out[r] + d) = u;
+      if constexpr (kLo)
+        *reinterpret_cast<uint2*>(p.o_lo + sm.out[r] + d) = make_uint2(
+            bf16x2(o.x - bf16lo(u.x), o.y - bf16hi(u.x)), bf16x2(o.z - bf16lo(u.y), o.w - bf16hi(u.y)));
     }
     __syncwarp();
     cluster_sync_all();  // peers' shared memory stays until every CTA has read it
@@ -1008,7 +1028,7 @@ cudaLaunchConfig_t att_config(dim3 grid, uint32_t smem, cudaStream_t stream, cud
   return cfg;
 }
 
-template <int HD, int RT>
+template <int HD, int RT, bool kLo>
 cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   using S = AttSmem<HD, RT>;
   static PerDevice<AttSetup> setup;
@@ -1019,7 +1039,7 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
             int dev = 0;
             if ((r.err = cudaGetDevice(&dev)) != cudaSuccess) return r;
             if ((r.err = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return r;
-            const auto fn = kv8_attention_kernel<HD, RT>;
+            const auto fn = kv8_attention_kernel<HD, RT, kLo>;
             if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                               kSmemCta)) != cudaSuccess)
               return r;
@@ -1056,10 +1076,10 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
   const cudaLaunchConfig_t cfg = att_config(dim3(rtiles << lc, p.Hkv, p.B), S::bytes(nk, nv), stream, attr, 1 << lc);
-  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT>, maps, p, lc, nk, nv, 2 * s.sms);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo>, maps, p, lc, nk, nv, 2 * s.sms);
 }
 
-template <int HD>
+template <int HD, bool kLo>
 cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
   // the row tile that leaves the fewest rows empty, the larger of equal ones
   const int R = p.n * p.G;
@@ -1067,17 +1087,18 @@ cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
   for (int rt = 24; rt >= 8; rt -= 8)
     if ((R + rt - 1) / rt * rt < (R + best - 1) / best * best) best = rt;
   switch (best) {
-    case 8: return launch_tile<HD, 8>(p, stream);
-    case 16: return launch_tile<HD, 16>(p, stream);
-    case 24: return launch_tile<HD, 24>(p, stream);
-    default: return launch_tile<HD, 32>(p, stream);
+    case 8: return launch_tile<HD, 8, kLo>(p, stream);
+    case 16: return launch_tile<HD, 16, kLo>(p, stream);
+    case 24: return launch_tile<HD, 24, kLo>(p, stream);
+    default: return launch_tile<HD, 32, kLo>(p, stream);
   }
 }
 
 }  // namespace
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream) {
-  return p.hd == 128 ? launch_rows<128>(p, stream) : launch_rows<64>(p, stream);
+  if (p.o_lo) return p.hd == 128 ? launch_rows<128, true>(p, stream) : launch_rows<64, true>(p, stream);
+  return p.hd == 128 ? launch_rows<128, false>(p, stream) : launch_rows<64, false>(p, stream);
 }
 
 }  // namespace spec
