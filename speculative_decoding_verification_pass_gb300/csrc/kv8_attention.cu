@@ -35,6 +35,7 @@
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <climits>
 
 #include "internal.h"
 #include "kv8_common.cuh"
@@ -384,12 +385,12 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   const int slots = lc ? share / (p.Hkv * (gridDim.x >> lc)) : 0;  // CTAs of the GPU per sequence, KV head and row tile
   int b = blockIdx.z;
   if (p.B > 1 && p.B <= kSortSeqs) {
-    if (tid < kSortSeqs) sm.len[tid] = tid < p.B ? p.base[tid] : -1;
+    if (tid < kSortSeqs) sm.len[tid] = tid < p.B ? p.base[tid] : INT_MIN;  // (no length, after all others)
     __syncthreads();
     if (tid < p.B) {
       const int mine = sm.len[tid];
       int before = 0, total = 0;
-      for (int j = 0; j < p.B; j += 4) {  // (the rows past B count as empty)
+      for (int j = 0; j < p.B; j += 4) {
         const int4 v = *reinterpret_cast<const int4*>(&sm.len[j]);
         const int o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll

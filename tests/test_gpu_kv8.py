@@ -12,6 +12,10 @@ Tolerances, from the formats:
   row's largest (its last piece's subnormal step); a score by 2^-17 of
   sum |q| |k|, which moves a weight and the normaliser by that much each.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -24,6 +28,7 @@ from speculative_decoding_verification_pass_gb300 import workloads as wl
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 THETA = 500000.0
 HEADS = {"64x4/2": (64, 4, 2), "128x4/1": (128, 4, 1), "128x8/8": (128, 8, 8), "64x16/2": (64, 16, 2),
          "128x6/2": (128, 6, 2)}
@@ -471,6 +476,80 @@ def test_sequences_that_do_not_fit():
     sb.spec_kv8_truncate(kv, torch.tensor([0, 2, 1, 3], dtype=torch.int32, device="cuda"), 2, ws)
     assert _status(ws) == (sb.SPEC_EDEVICE, sb.DEV_BAD_NACC)
     assert kv.len.cpu().tolist() == [5, 2, 9, 5]
+
+
+def test_lengths_that_are_none():
+    """Lengths below zero and past the capacity, some equal, in a batch that is put in order of length: those
+    rows are zero, the other sequences are served."""
+    cfg, n = _cfg("128x4/1"), 2
+    lens = [5, -7, 1 << 30, 64, -(1 << 31), -7, (1 << 31) - 1, 0, -1, 126]
+    kv = sb.KV8Cache(cfg, len(lens), 2 * len(lens), 2)
+    for b in range(len(lens)):
+        kv.reserve(b, 128)
+    kv.sync()
+    _fill(kv, 5)
+    kv.len.copy_(torch.tensor(lens, dtype=torch.int32))
+    q = _q(len(lens) * n, cfg.d_model, 37)
+    ws = sb.workspace(256)
+    out = torch.full_like(q, 3.0)
+    sb.spec_kv8_attention(cfg, kv, 0, n, q, out, ws)
+    assert _status(ws) == (sb.SPEC_EDEVICE, sb.DEV_KV_OVERFLOW)
+    one = sb.KV8Cache(cfg, 1, kv.n_pages, 2)
+    one.k, one.v, one.k_scale, one.v_scale = kv.k, kv.v, kv.k_scale, kv.v_scale
+    for b, L in enumerate(lens):
+        got = out[b * n:(b + 1) * n]
+        if not 0 <= L <= 128 - n:
+            assert (got == 0).all()
+            continue
+        one.table.copy_(kv.table[b:b + 1])
+        one.len.fill_(L)
+        want = torch.empty_like(got)
+        sb.spec_kv8_attention(cfg, one, 0, n, q[b * n:(b + 1) * n], want, ws)
+        assert torch.equal(got, want)
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    before = kv.k.view(torch.uint8).clone()
+    R, q_out = sb.RopeTable(cfg.head_dim, THETA), torch.empty_like(q)
+    k = _q(len(lens) * n, cfg.head_dim, 38)
+    sb.spec_kv8_append(cfg, kv, 0, n, q, k, k, R, q_out, ws)
+    sb.spec_kv8_advance(kv, n, ws)
+    assert _status(ws) == (sb.SPEC_EDEVICE, sb.DEV_KV_OVERFLOW)
+    fits = [0 <= L <= 128 - n for L in lens]
+    assert kv.len.cpu().tolist() == [L + n if f else L for L, f in zip(lens, fits)]
+    for b in range(len(lens)):
+        same = torch.equal(kv.k.view(torch.uint8)[0, kv.table[b].long()], before[0, kv.table[b].long()])
+        assert same != fits[b]
+
+
+def test_first_calls_inside_a_capture():
+    """The set-up that a first call makes (attributes, cluster sizes) is allowed while a stream captures."""
+    code = """
+import sys
+sys.path.insert(0, %r)
+import torch
+from speculative_decoding_verification_pass_gb300 import binding as sb
+cfg = sb.ModelConfig(1, 512, 4, 1, 128, 1000)
+kv = sb.KV8Cache(cfg, 1, 40, 40)
+kv.reserve(0, 2560)
+kv.sync()
+kv.len.fill_(2000)
+R, ws = sb.RopeTable(128, 1e4), sb.workspace(256)
+q = torch.ones(3, 512, device='cuda', dtype=torch.bfloat16)
+k = torch.ones(3, 128, device='cuda', dtype=torch.bfloat16)
+q_out, o = torch.empty_like(q), torch.zeros_like(q)
+path, m = torch.tensor([[1, 2, -1]], dtype=torch.int32, device='cuda'), torch.tensor([2], dtype=torch.int32, device='cuda')
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    sb.spec_kv8_append(cfg, kv, 0, 3, q, k, k, R, q_out, ws)
+    sb.spec_kv8_attention(cfg, kv, 0, 3, q_out, o, ws)
+    sb.spec_kv8_advance(kv, 3, ws)
+    sb.spec_kv8_tree_commit(cfg, kv, path, m, 3, ws)
+g.replay()
+torch.cuda.synchronize()
+assert sb.spec_device_status(ws) == (sb.SPEC_OK, 0) and kv.len.tolist() == [2003] and (o > 0).all()
+print("captured")
+""" % ROOT
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
 def test_refused_tensors():
