@@ -31,6 +31,10 @@ __global__ void kv8_rope_kernel(float2* dst, int rd, double theta, double factor
 }
 
 // ------------------------------------------------------------------ append
+// Every input may come from the launch before, which this one overlaps up to
+// its wait, so none is read through the read-only path (that is for data that
+// nothing writes while the kernel runs; the frequencies are such).
+//
 // One warp per unit.  A q unit is one token and a few of its heads; a k or v
 // unit is one block of 16 slots of one (sequence, KV head), so that the
 // warp alone sees every row that the block's scale depends on:
@@ -44,8 +48,8 @@ constexpr int kAppThreads = 128;
 constexpr int kAppHeads = 4;  // head rows per lane of a q unit
 
 SPEC_DEVINL float2 load2(const void* p, long long i, int f32) {
-  if (f32) return __ldg(reinterpret_cast<const float2*>(static_cast<const float*>(p) + i));
-  const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i));
+  if (f32) return *reinterpret_cast<const float2*>(static_cast<const float*>(p) + i);
+  const uint32_t w = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(p) + i);
   return make_float2(bf16lo(w), bf16hi(w));
 }
 
@@ -127,7 +131,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
         x[k][0] = a.x, x[k][1] = a.y, x[k][2] = c.x, x[k][3] = c.y;
       }
     }
-    const int pos = p.base[b] + (p.depth ? __ldg(p.depth + m) : m - b * p.n);
+    const int pos = p.base[b] + (p.depth ? p.depth[m] : m - b * p.n);
     float cs[2], sn[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k) kv8_sincos(pos, fr[k], &sn[k], &cs[k]);
@@ -184,7 +188,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   for (int i = 0; i < IT; ++i) {
     const int j = slot0 + i * RPW + sub - L;
     if (at.rot && j >= 0 && j < p.n) {
-      const int pos = L + (p.depth ? __ldg(p.depth + b * p.n + j) : j);
+      const int pos = L + (p.depth ? p.depth[b * p.n + j] : j);
       float cs[2], sn[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) kv8_sincos(pos, fr[k], &sn[k], &cs[k]);
@@ -250,8 +254,8 @@ SPEC_DEVINL int32_t kv8_path_bad(const Kv8CommitParams& p, int b, int len, int m
   for (int k = 0; k < 2; ++k) {
     const int d = lane + 32 * k;
     if (d < m) {
-      const int s = __ldg(path + d);
-      bad |= s <= (d ? __ldg(path + d - 1) : 0) || s >= p.n;
+      const int s = path[d];
+      bad |= s <= (d ? path[d - 1] : 0) || s >= p.n;
     }
   }
   if (__any_sync(0xffffffffu, bad)) return SPEC_DEV_BAD_TREE;
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_commit_kernel(const Kv8Commi
   grid_dep_launch();
   const int b = blockIdx.x / p.Hkv, h = blockIdx.x % p.Hkv;
   const int tid = threadIdx.x;
-  const int len = p.len[b], m = __ldg(p.n_acc + b);
+  const int len = p.len[b], m = p.n_acc[b];
   if (m <= 0 || kv8_path_bad(p, b, len, m)) return;  // the length update reports it
   const int L0 = len - p.n;
   const int32_t* path = p.path + static_cast<long long>(b) * p.n;
@@ -289,13 +293,13 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_commit_kernel(const Kv8Commi
       const int e = tid + k * kMoveThreads;
       if (e < nl * per_layer) {
         const int l = e / per_layer, f = e - l * per_layer, side = f >= per_side, rem = f - side * per_side;
-        const int src = L0 + __ldg(path + rem / VEC);
+        const int src = L0 + path[rem / VEC];
         w[k] = reinterpret_cast<const uint4*>(codes(side, layer0 + l) + map.row(map.page(b, src), h, src))[rem % VEC];
       }
     }
     for (int e = tid; e < nl * 2 * m; e += kMoveThreads) {
       const int l = e / (2 * m), f = e - l * 2 * m, side = f >= m, d = f - side * m;
-      const int src = L0 + __ldg(path + d);
+      const int src = L0 + path[d];
       s_src[l][side][d] = scales(side, layer0 + l)[map.scale(map.page(b, src), h, src)];
     }
     if (tid < 2 * nl) s_own[tid / 2][tid % 2] = scales(tid % 2, layer0 + tid / 2)[map.scale(map.page(b, L0), h, L0)];

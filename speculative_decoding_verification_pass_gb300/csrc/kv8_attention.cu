@@ -29,9 +29,28 @@
 // need not be its maximum: the pieces hold weights up to 448, so M is set to put
 // the maximum of the first tile at 2^2 and raised only when a weight would pass
 // 2^8.75 (one barrier per tile asks whether any does).  Until then O^T adds
-// up in TMEM and no thread reads it.  Warp 4 issues the TMA loads, warp 5 the
-// MMAs; S and P are double-buffered, so the scores of tile i + 1 and the
-// products of tile i - 1 run beside the softmax of tile i.
+// up in TMEM and no thread reads it.  Warps 0 - 3 are the softmax's; warp 4
+// issues the TMA loads of K, warp 5 those of V, warp 6 the score MMAs and warp 7
+// the products: one thread for both of either kind had less time a tile than its
+// waits and issues took.  S and P are double-buffered, so the scores of tile
+// i + 1 and the products of tile i - 1 run beside the softmax of tile i.
+//
+// Why two CTAs an SM (113 KB and 128 registers a thread each): a tile is one
+// chain of score, weights and product, and another CTA's chain fills its gaps;
+// two groups of softmax threads in one CTA took the same time.
+//
+// What bounds it, with what it measured (152 SMs; 32 query heads on 8 KV heads,
+// head dim 128 and 5 tokens a sequence unless it says otherwise; device time of
+// a launch inside a graph):
+//   64 sequences, 309 MB of cache: 51 us, 6.0 TB/s; in its loop it runs at the
+//     copy bandwidth, the rest is the second wave's prologue and the tail
+//   16 sequences, 77 MB: 23.5 us, 3.3 TB/s; ~7 us of setup and end, and tiles
+//     that do not divide evenly over the SMs
+//   1 sequence of 131000 slots, 1 token: 51 us, 5.3 TB/s; a cluster of 16 per KV
+//     head lies two CTAs to an SM, so 114 of the SMs take part at the most
+//   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
+//   4 sequences x 128 tokens at 512 slots: 31.7 us; softmax threads, whose
+//     conversions to e4m3 run at a quarter rate
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   }
   const int32_t* table = p.table + static_cast<long long>(b) * p.max_pages;
   const auto page_of = [&](int t) {  // the page of slot t, clamped into the pool
-    const int pg = __ldg(table + min(t / kPageSlots, p.max_pages - 1));
+    const int pg = table[min(t / kPageSlots, p.max_pages - 1)];
     if (pg < 0 || pg >= p.n_pages) {
       if (t < T) set_status(p.status, SPEC_DEV_BAD_PAGE);
       return pg < 0 ? 0 : p.n_pages - 1;
@@ -577,8 +596,9 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     __syncwarp();
   } else if (warp >= kIssueS) {
     // ------------------------------------- MMA issuers: scores, products
-    // A thread issues one MMA per ~90 cycles whatever its N, so the two
-    // products of a tile come from two threads.
+    // An MMA of N columns holds the pipe for 32 + N / 4 cycles (M = 128, K =
+    // 32), and its thread for 57 to 92 at any N, so the two products of a tile
+    // come from two threads.
     if (lane == 0) {
       const bool scores = warp == kIssueS;
       const int stages = scores ? NK : NV;
@@ -627,7 +647,6 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // A wait that gives up sets the abort flag; the threads leave the loop
     // together at its barrier.
     const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
     const int sub = (tid % kPageSlots) / kKv8Block;
     const auto scale_at = [&](int pg) { return (static_cast<long long>(pg) * p.Hkv + h) * kKv8Sub + sub; };
     const auto seen = [&](int t) {  // bit r: row rbase + r sees slot t
@@ -646,7 +665,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     };
     // the pages that the new slots lie on, looked at in the end
     const int new_pages = over ? 0 : (T - 1) / kPageSlots - L / kPageSlots + 1;
-    const int new_page = tid < new_pages ? __ldg(table + L / kPageSlots + tid) : 0;
+    const int new_page = tid < new_pages ? table[L / kPageSlots + tid] : 0;
     // rows r .. r + 7 of O, the pieces put together
     const auto o_rows = [&](int r, float (&o)[8]) {
       uint32_t w[3][8];
@@ -664,9 +683,9 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // this thread's scales, one tile ahead, and its page, two ahead (the TMA
     // warp flags ids outside the pool; here they are clamped)
     const int last_page = p.max_pages - 1;
-    const auto page_id = [&](int i) { return __ldg(table + min(((i0 + i) * kTile + tid) / kPageSlots, last_page)); };
+    const auto page_id = [&](int i) { return table[min(((i0 + i) * kTile + tid) / kPageSlots, last_page)]; };
     const auto scale_of = [&](const float* sc, int pg) {
-      return __ldg(sc + scale_at(min(max(pg, 0), p.n_pages - 1)));
+      return sc[scale_at(min(max(pg, 0), p.n_pages - 1))];
     };
     int pg1 = nt > 0 ? page_id(0) : 0;
     float ks_n = nt > 0 ? scale_of(p.ks, pg1) : 1.f, vs_n = nt > 0 ? scale_of(p.vs, pg1) : 1.f;

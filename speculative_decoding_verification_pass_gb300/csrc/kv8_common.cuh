@@ -64,7 +64,7 @@ struct Kv8Map {
   int max_pages, n_pages, Hkv, hd;
   // the page holding slot t of sequence b, clamped into the pool
   SPEC_DEVINL int page(int b, int t) const {
-    const int pg = __ldg(table + static_cast<long long>(b) * max_pages + t / kPageSlots);
+    const int pg = table[static_cast<long long>(b) * max_pages + t / kPageSlots];
     return pg < 0 ? 0 : (pg >= n_pages ? n_pages - 1 : pg);
   }
   SPEC_DEVINL long long row(int page, int h, int t) const {
@@ -84,7 +84,7 @@ SPEC_DEVINL int32_t kv8_fit_warp(int L, int n, const int32_t* table, int max_pag
   *page = 0;
   if (L < 0 || L > max_pages * kPageSlots - n) return SPEC_DEV_KV_OVERFLOW;
   const int p0 = L / kPageSlots, np = (L + n - 1) / kPageSlots - p0 + 1, lane = threadIdx.x & 31;
-  const int pg = lane < np ? __ldg(table + static_cast<long long>(b) * max_pages + p0 + lane) : 0;
+  const int pg = lane < np ? table[static_cast<long long>(b) * max_pages + p0 + lane] : 0;
   if (__any_sync(0xffffffffu, pg < 0 || pg >= n_pages)) return SPEC_DEV_BAD_PAGE;
   *page = __shfl_sync(0xffffffffu, pg, t / kPageSlots - p0);
   return 0;
