@@ -376,7 +376,8 @@ int spec_page_pool_free_pages(const spec_page_pool* pool);
  *   k_scale, v_scale  fp32 [n_layers][n_pages][n_kv_heads][64 / SPEC_KV8_BLOCK]
  *                     (spec_kv8_scale_bytes each), 16-byte aligned: one power
  *                     of two in [2^-40, 2^40] per block of SPEC_KV8_BLOCK slots
- *                     and KV head.
+ *                     and KV head;
+ *   len, table        as there, 4-byte aligned.
  * The scale of a block is the smallest such power s with |x| <= 448 s for the
  * finite values of its rows (2^-40 where all are zero); larger values and
  * infinities are held as +-448 s, NaN as NaN.  The scales of blocks that hold
@@ -385,7 +386,8 @@ int spec_page_pool_free_pages(const spec_page_pool* pool);
  * workspace of this library as d_ws (its status word is used) and works on
  * the current device; `cfg` gives the layer count and the head shape.
  * Two sequences may share pages that neither appends to (a common prefix); a
- * page that receives rows belongs to one sequence alone.
+ * page that receives rows belongs to one sequence alone.  Pointers that are not
+ * aligned as their element (uint64 8 bytes, other 4) are SPEC_EINVAL.
  *
  * One pass: for each layer spec_kv8_append then spec_kv8_attention, both at
  * the lengths before the pass; then spec_kv8_advance, the accept, and
@@ -436,8 +438,10 @@ int spec_rope_table(const spec_rope_config* rope, float* d_table, void* stream);
  *             of one projection's output, say); base and row distance
  *             16-byte aligned.
  *   d_depth   int32 [batch][n] position offsets (a draft tree's depths), or
- *             NULL: token j is at position len[b] + j.
- *   d_q_out   bf16 [batch*n][n_heads*head_dim]: q rotated, rounded once.
+ *             NULL: token j is at position len[b] + j.  Positions lie within
+ *             +-2^24.
+ *   d_q_out   bf16 [batch*n][n_heads*head_dim]: q rotated, rounded once;
+ *             16-byte aligned; may be d_q's own rows (bf16, side by side).
  * Token j's rows go to slot len[b] + j; len is not changed.  A block that
  * already holds rows keeps the larger of its scale and the one its new rows
  * need; when it grows, the rows held are re-rounded at it.  A sequence whose
@@ -454,13 +458,16 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  * one layer: o = softmax(scale * q k^T) v per head, query heads sharing KV
  * heads in order (n_heads / n_kv_heads each).
  *   d_q    bf16 rows (spec_kv8_append's d_q_out), q_ld elements apart;
- *   d_o    bf16 rows, o_ld elements apart; both 16-byte aligned;
+ *   d_o    bf16 rows, o_ld elements apart; bases and row distances of both
+ *          16-byte aligned; d_o may be d_q's own rows (o_ld = q_ld);
  *   d_anc  uint64 [batch][n] ancestor masks (spec_tree_masks; n <= 64), or
  *          NULL: token j sees the cached slots and new slots 0 .. j.
  *   scale  > 0, or 0 for 1/sqrt(head_dim).
- * Scores, softmax and sums are in fp32 or finer; q as given, each weight
- * p within 2^-11 of its value.  A row that sees no slot (a mask without its own bit, an
- * empty cache) is zero.  Slots at or past len[b] + n and slots a row does not
+ * Scores, softmax and sums are in fp32.  q is as given but for elements 2^-18
+ * below its row's largest; a weight p is within 2^-11 of its value or, where
+ * p x v_scale is small, within 2^-20 of the largest such product in the row.
+ * A score past fp32's range makes its row NaN.  A row that sees no slot (a mask
+ * with no bit of an empty cache) is zero.  Slots at or past len[b] + n and slots a row does not
  * see have no influence, whatever they hold; a NaN code that it sees makes
  * the row's affected outputs NaN, an infinite or NaN q its whole row.  A
  * sequence that does not fit (as in spec_kv8_append) gets zero rows and a

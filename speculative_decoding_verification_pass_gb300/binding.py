@@ -555,6 +555,8 @@ def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cac
                             depth=None, stream=None):
     """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
     dev = kv._device(kv.cfg, tokens, logits, anc, depth, ws)
+    if logits.dtype != torch.float32 or logits.numel() != batch * n * kv.cfg.vocab:
+        raise ValueError(f"logits: expected a {(batch, n, kv.cfg.vocab)} {torch.float32} tensor")
     with _on(dev):
         _check(lib().spec_verify_forward_kv8(
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),

@@ -49,8 +49,8 @@
 //   1 sequence of 131000 slots, 1 token: 51 us, 5.3 TB/s; a cluster of 16 per KV
 //     head lies two CTAs to an SM, so 114 of the SMs take part at the most
 //   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
-//   4 sequences x 128 tokens at 512 slots: 31.7 us; softmax threads, whose
-//     conversions to e4m3 run at a quarter rate
+//   1 sequence x 128 tokens at 4000 slots: 31.5 us (4.2 us of bf16 products);
+//     the softmax threads' chain, with conversions to e4m3 at a quarter rate
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -64,11 +64,14 @@ namespace {
 
 constexpr int kTile = 128;                  // keys per tile
 constexpr int kSoft = 128;                  // softmax threads
-constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O issuing warps
-constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;  // (warps)
+constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O issuing warps:
+constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 constexpr int kMaxCluster = 16;
-constexpr int kSortSeqs = 96;               // sequences that are put in order of length (a multiple of 4)
+// Sequences that are put in order of length, a thread each among the first 96 (a
+// multiple of 4); of more, the waves are many enough that their order counts
+// for little, and each CTA would pay for the search.
+constexpr int kSortSeqs = 96;
 constexpr int kMinTiles = 2;                // tiles of a CTA at least, where they are shared
 constexpr int kSmemCta = 227 * 1024;        // dynamic shared memory of a CTA alone on its SM,
 constexpr int kSmemHalf = 113 * 1024;       // ... and of two (1 KB of each CTA's share is the system's)
@@ -86,7 +89,8 @@ SPEC_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
 SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr)
       : "memory");
 }
@@ -319,12 +323,12 @@ struct AttSmem {
     uint64_t full_k[kMaxStages], full_v[kMaxStages], empty_k[kMaxStages], empty_v[kMaxStages];
     uint64_t s_full[2], s_free[2], p_full[2], o_full[2], drain[2];
     uint64_t anc[RT];
-    alignas(16) float red[4][RT];  // per-warp maxima (sums at the end); this and the next two are read as float4
-    float mneg[4][RT];         // each warp's copy of -M
-    float cq[RT];              // score factor of a row: 2^k scale log2(e)
-    alignas(16) float stat[2][RT];   // this CTA's M and sum per row
-    alignas(16) long long out[RT];         // where the row's output starts, -1: no such row
-    union {                    // before the loop, and from it on
+    alignas(16) float red[4][RT];   // per-warp maxima (sums at the end); this and the next two are read as float4
+    float mneg[4][RT];              // each warp's copy of -M
+    float cq[RT];                   // score factor of a row: 2^k scale log2(e)
+    alignas(16) float stat[2][RT];  // this CTA's M and sum per row
+    alignas(16) long long out[RT];  // where the row's output starts, -1: no such row
+    union {                         // before the loop, and from it on
       alignas(16) int len[kSortSeqs];
       uint32_t nan[RT][HD / 32];  // outputs that a NaN value code reaches
     };
@@ -351,8 +355,8 @@ struct AttMaps {
 // its code cost batch 64 5%).
 template <int HD, int RT, bool kLo>
 __global__ void __launch_bounds__(kAttThreads, 2)
-    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int lc, const int NK, const int NV,
-                         const int share) {
+    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int lc, const int NK,
+                         const int NV, const int share) {
   using S = AttSmem<HD, RT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_u32(smem_raw);  // swizzled tiles lie on their own span's boundaries
@@ -941,7 +945,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   __syncwarp();
   if (C > 1) {
     const int rows = min(RT, R - rbase);
-  // ---- merge: the cluster's CTAs share the (row, 4 dimensions) items
+    // ---- merge: the cluster's CTAs share the (row, 4 dimensions) items
     __syncwarp();
     cluster_sync_all();
     const uint32_t stat = smem_u32(&sm.stat[0][0]);

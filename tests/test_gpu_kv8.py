@@ -865,6 +865,42 @@ def test_attention_in_place():
     assert torch.equal(q, want)
 
 
+@pytest.mark.parametrize("rope", ["half", "inter-part-scaled"])
+def test_append_in_place(rope):
+    """The rotated queries may take the queries' own rows."""
+    cfg, n, lens = _cfg("128x4/1"), 9, (700, 3)
+    g = torch.Generator().manual_seed(51)
+    q, k, v = (torch.randn(len(lens) * n, w, generator=g).to(torch.bfloat16).cuda()
+               for w in (cfg.d_model, cfg.head_dim, cfg.head_dim))
+    how = ROPES[rope]
+    R = sb.RopeTable(64 if how.get("part") else 128, THETA, how["inter"], how.get("factor", 1.0))
+    want, ws = torch.empty_like(q), sb.workspace(256)
+    a, b = Pair(cfg, lens, n, 52), Pair(cfg, lens, n, 52)
+    sb.spec_kv8_append(cfg, a.kv, 0, n, q, k, v, R, want, ws)
+    sb.spec_kv8_append(cfg, b.kv, 0, n, q, k, v, R, q, ws)
+    assert torch.equal(q, want) and torch.equal(a.kv.k.view(torch.uint8), b.kv.k.view(torch.uint8))
+    assert _status(ws) == (sb.SPEC_OK, 0)
+
+
+def test_advance_looks_at_every_page():
+    """Lengths move on by themselves: a page id out of the pool anywhere below the new length, a length that
+    does not fit, or none of these, in one batch."""
+    cfg = _cfg("64x4/2")
+    kv, ws = sb.KV8Cache(cfg, 6, 4, 300), sb.workspace(256)
+    lens = [0, 19136, 19195, -1, 6000, 2 ** 31 - 1]  # the third fits to the last slot
+    table = torch.zeros(6, 300, dtype=torch.int32)
+    table[0, 1:] = -1  # not looked at
+    table[4, 70] = 4  # one past the pool, in the third group of pages
+    kv.table.copy_(table)
+    kv.len.copy_(torch.tensor(lens, dtype=torch.int32))
+    sb.spec_kv8_advance(kv, 5, ws)
+    assert kv.len.cpu().tolist() == [5, 19141, 19200, -1, 6000, 2 ** 31 - 1]
+    assert _status(ws) == (sb.SPEC_EDEVICE, sb.DEV_BAD_PAGE | sb.DEV_KV_OVERFLOW)
+    kv.len.copy_(torch.tensor([60, 19196, 1, 1, 4475, 1], dtype=torch.int32))
+    sb.spec_kv8_advance(kv, 5, ws)  # the first's second page is none now; 4480 slots end before page 70
+    assert kv.len.cpu().tolist() == [60, 19196, 6, 6, 4480, 6]
+
+
 # ------------------------------------------------------------------ forward
 class Kv8State(OM.KVState):
     """The oracle's cache with rows held in 8 bits (keep() rounds the new rows in place)."""
@@ -1002,6 +1038,9 @@ def test_forward_of_a_large_batch_and_refusals():
         with pytest.raises(sb.SpecError) as e:
             sb.spec_verify_forward_kv8(m.handle, t, B, k["n"], kv, torch.empty(B, k["n"], cfg.vocab, device="cuda"), k["ws"])
         assert e.value.status == status
+    for bad in (z[:, :4], z.half(), z[:39]):  # logits of another size or type
+        with pytest.raises(ValueError):
+            sb.spec_verify_forward_kv8(m.handle, _dev(new), B, n, kv, bad, ws)
     with pytest.raises(sb.SpecError) as e:  # a tree's masks without its depths
         sb.spec_verify_forward_kv8(m.handle, _dev(new), B, n, kv, z, ws,
                                    anc=torch.zeros(B, n, dtype=torch.int64, device="cuda"))
