@@ -333,6 +333,7 @@ struct Kv8AttnParams {
   float scale_log2;           // log2(e) * the score scale
 };
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream);
+cudaError_t launch_kv8_attention_wide(const Kv8AttnParams& p, cudaStream_t stream);  // (of many query rows)
 
 struct Kv8CommitParams {
   uint8_t *kc, *vc;           // all layers

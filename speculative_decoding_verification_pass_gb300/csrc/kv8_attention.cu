@@ -51,49 +51,27 @@
 //   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
 //   1 sequence x 128 tokens at 4000 slots: 31.5 us (4.2 us of bf16 products);
 //     the softmax threads' chain, with conversions to e4m3 at a quarter rate
-#include <cudaTypedefs.h>
-
-#include <algorithm>
-#include <climits>
-
-#include "internal.h"
-#include "kv8_common.cuh"
+#include "kv8_attn.cuh"
 
 namespace spec {
 namespace {
 
-constexpr int kTile = 128;                  // keys per tile
 constexpr int kSoft = 128;                  // softmax threads
 constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O issuing warps:
 constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
-constexpr int kMaxCluster = 16;
-// Sequences that are put in order of length, a thread each among the first 96 (a
-// multiple of 4); of more, the waves are many enough that their order counts
-// for little, and each CTA would pay for the search.
-constexpr int kSortSeqs = 96;
-constexpr int kMinTiles = 2;                // tiles of a CTA at least, where they are shared
-constexpr int kSmemCta = 227 * 1024;        // dynamic shared memory of a CTA alone on its SM,
-constexpr int kSmemHalf = 113 * 1024;       // ... and of two (1 KB of each CTA's share is the system's)
+// The kernel for many query rows takes over where a KV head has more than 64 of
+// them and the calls' (128 rows x 128 keys) at full capacity are 640 or more:
+// below, its longer prologue and merge cost more than its cheaper tiles save.
+// Measured, this kernel / that one in us (32 heads on 8, head dim 128, 4000 slots
+// but where it says): 1 x 32 tokens (264) 15.2 / 16.1, 1 x 64 (528) 18.7 / 20.8,
+// 1 x 96 (792) 29.6 / 21.0, 1 x 128 (1056) 31.5 / 24.5, 16 x 32 (4224) 75 / 54,
+// 4 x 64 at 700 (448) 13.6 / 16.9, 4 x 128 at 700 (896) 25.7 / 19.3; 64 rows a
+// head: 16 x 16 tokens 44.7 / 52.7, 64 x 16 141 / 160.
+constexpr int kWideRows = 64, kWideWork = 640;
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
 constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
-constexpr float kNoRef = -3.402823466e38f;  // M of a row that has seen no slot: any score passes it
 
-SPEC_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-SPEC_DEVINL void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
 // N columns of the thread's lane at each of two places, ready for use.
 template <int N>
 SPEC_DEVINL void tmem_ld2(uint32_t ta, uint32_t tb, uint32_t (&a)[N], uint32_t (&b)[N]) {
@@ -108,56 +86,12 @@ SPEC_DEVINL void tmem_ld2(uint32_t ta, uint32_t tb, uint32_t (&a)[N], uint32_t (
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]));  // no use moves above the wait
 }
-SPEC_DEVINL void tmem_st_x8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-SPEC_DEVINL void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 SPEC_DEVINL void tmem_ld_wait(uint32_t (&a)[8], uint32_t (&b)[8], uint32_t (&c)[8]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
   for (int i = 0; i < 8; ++i) asm volatile("" : "+r"(a[i]), "+r"(b[i]), "+r"(c[i]));
 }
 
-// Two fp32 operations in one instruction.
-SPEC_DEVINL float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.ftz.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-SPEC_DEVINL float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "mul.rn.ftz.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-SPEC_DEVINL float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.ftz.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-// Two fp32 values to bf16 (`a` low; infinities and NaN kept).
-SPEC_DEVINL uint32_t bf16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-// fp16 pairs: two fp32 rounded, product, a b + c, to e4m3 and back (`a` low).
-SPEC_DEVINL uint32_t f16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 SPEC_DEVINL uint32_t f16x2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -173,88 +107,10 @@ SPEC_DEVINL uint32_t f16x2_to_e4m3x2(uint32_t a) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
 }
-SPEC_DEVINL uint32_t e4m3x2_to_f16x2(uint32_t a) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(a)));
-  return r;
-}
-
-// D[tmem] (+)= A[smem] * B[smem] of e4m3 operands, issued by one thread.
-SPEC_DEVINL void umma_e4m3(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// Instruction descriptor of kind::f8f6f4, e4m3 x e4m3 -> fp32, M x N; tra / trb:
-// operand stored MN-major.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool tra, bool trb) {
-  return (1u << 4) | (tra ? 1u << 15 : 0u) | (trb ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) |
-         (static_cast<uint32_t>(M >> 4) << 24);
-}
-// Shared-memory descriptor of rows of ROWB bytes (128, 64 or 32) with the swizzle
-// of that span: 8-row groups ROWB * 8 apart (stride offset); lbo: distance
-// between two spans along an MN-major operand's own dimension.
-template <int ROWB>
-SPEC_DEVINL uint64_t sdesc_rows(uint32_t saddr, uint32_t lbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((ROWB * 8) >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(ROWB == 128 ? 2 : (ROWB == 64 ? 4 : 6)) << 61;
-  return d;
-}
-// Byte offset of 16-byte chunk c of row i in such rows.
-template <int ROWB>
-SPEC_DEVINL uint32_t swz_off(int i, int c) {
-  if constexpr (ROWB == 128) return static_cast<uint32_t>(i * 128 + ((c ^ (i & 7)) << 4));
-  if constexpr (ROWB == 64) return static_cast<uint32_t>(i * 64 + ((c ^ ((i >> 1) & 3)) << 4));
-  return static_cast<uint32_t>(i * 32 + ((c ^ ((i >> 2) & 1)) << 4));
-}
 // ... and of chunk c of key i's row of P, which is cut into spans of 32 bytes
 // ([128 keys][32 bytes] each): three pieces of 24 rows then take 96 bytes a key
 // where a 128-byte span would take 128.
 SPEC_DEVINL uint32_t p_off(int i, int c) { return (c >> 1) * (kTile * kPSpan) + swz_off<kPSpan>(i, c & 1); }
-
-SPEC_DEVINL void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
-SPEC_DEVINL void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-SPEC_DEVINL void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-SPEC_DEVINL uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
-SPEC_DEVINL float peer_f32(uint32_t a) {
-  float v;
-  asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
-  return v;
-}
-SPEC_DEVINL float4 peer_f32x4(uint32_t a) {
-  float4 v;
-  asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-  return v;
-}
-
-// A place in the ring: stage and the parity of the fill being awaited there
-// (counted along: a division by a stage count known only at run time costs the
-// one issuing thread ~100 cycles).
-struct Ring {
-  int s = 0;
-  uint32_t par = 0;
-  SPEC_DEVINL void next(int stages) {
-    if (++s == stages) {
-      s = 0;
-      par ^= 1u;
-    }
-  }
-};
 
 // Named barrier that also tells every thread whether any of them raised v.
 SPEC_DEVINL bool named_bar_any(int id, int nthreads, bool v) {
@@ -355,7 +211,7 @@ struct AttMaps {
 // its code cost batch 64 5%).
 template <int HD, int RT, bool kLo>
 __global__ void __launch_bounds__(kAttThreads, 2)
-    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int lc, const int NK,
+    kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int csize, const int NK,
                          const int NV, const int share) {
   using S = AttSmem<HD, RT>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -363,7 +219,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   const uint32_t ring_k = base + S::kK, ring_v = ring_k + NK * S::kTileB;
   auto& sm = *reinterpret_cast<typename S::Misc*>(smem_raw + (ring_v + NV * S::kTileB - smem_u32(smem_raw)));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = blockIdx.x & ((1 << lc) - 1), rtile = blockIdx.x >> lc, h = blockIdx.y;
+  const int rank = blockIdx.x % csize, rtile = blockIdx.x / csize, h = blockIdx.y;
   const int G = p.G, R = p.n * G, rbase = rtile * RT;
 
   if (tid == 0) {
@@ -398,39 +254,12 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   const uint32_t tmem = sm.tmem;
   grid_dep_wait();
 
-  // Which sequence, and how many of the cluster's CTAs share its tiles.  With
-  // the lengths at hand (up to kSortSeqs), the longest sequences go first
-  // (blocks start in index order: block z takes the sequence with z longer
-  // ones), and every CTA gets about the share of all tiles that fills the GPU
-  // once; the CTAs that a short sequence does not need leave.
+  // Which sequence, and how many of the cluster's CTAs share its tiles (the CTAs
+  // that a short sequence does not need leave).
   const int cap = p.max_pages * kPageSlots;
-  const auto tiles_of = [&](int len) { return len < 0 || len > cap - p.n ? 0 : (len + p.n + kTile - 1) / kTile; };
-  const int slots = lc ? share / (p.Hkv * (gridDim.x >> lc)) : 0;  // CTAs of the GPU per sequence, KV head and row tile
-  int b = blockIdx.z;
-  if (p.B > 1 && p.B <= kSortSeqs) {
-    if (tid < kSortSeqs) sm.len[tid] = tid < p.B ? p.base[tid] : INT_MIN;  // (no length, after all others)
-    __syncthreads();
-    if (tid < p.B) {
-      const int mine = sm.len[tid];
-      int before = 0, total = 0;
-      for (int j = 0; j < p.B; j += 4) {
-        const int4 v = *reinterpret_cast<const int4*>(&sm.len[j]);
-        const int o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) before += o[k] > mine || (o[k] == mine && j + k < tid);
-        if (lc)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) total += tiles_of(o[k]);
-      }
-      if (before == static_cast<int>(blockIdx.z)) {
-        sm.seq = tid;
-        sm.seq_len = mine;
-        if (lc) sm.unit = max(kMinTiles, (total + slots - 1) / max(slots, 1));
-      }
-    }
-    __syncthreads();
-    b = sm.seq;
-  }
+  const int slots = csize > 1 ? share / (p.Hkv * (gridDim.x / csize)) : 0;  // CTAs of the GPU per KV head and row tile
+  const AttPick pick = att_pick(p, csize > 1, slots, sm);
+  const int b = pick.b;
   // ---- the query rows: row r = token r / G, head h * G + r % G (loads on their
   // way before the length is known)
   constexpr int TPR = RT <= 16 && HD == 128 ? 8 : 4;  // threads per query row
@@ -454,15 +283,15 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     }
   }
 
-  const bool sorted = p.B > 1 && p.B <= kSortSeqs;
+  const bool sorted = pick.sorted;
   const int L = sorted ? sm.seq_len : p.base[b];
   const bool over = L < 0 || L > cap - p.n;
   const int T = over ? 0 : L + p.n;  // slots [0, T)
   const int tiles = (T + kTile - 1) / kTile;
   int C = 1, i0 = 0, nt = tiles;  // CTAs that share the tiles; this one's
-  if (lc) {
+  if (csize > 1) {
     const int unit = sorted ? sm.unit : max(kMinTiles, p.B > 1 ? 0 : (tiles + slots - 1) / max(slots, 1));
-    C = min(1 << lc, max(1, (tiles + unit - 1) / unit));
+    C = min(csize, max(1, (tiles + unit - 1) / unit));
     if (rank >= C) {  // (its peers' barriers go on without it)
       if (warp == kIssueO) tmem_dealloc(tmem, S::kTmemCols);
       return;
@@ -549,55 +378,12 @@ __global__ void __launch_bounds__(kAttThreads, 2)
 
   if (warp == kLoadK || warp == kLoadV) {
     // ------------------------------------------- TMA: the tiles of K, or of V
-    // Page ids come 16 at a time (8 tiles), the next 16 on their way: a
-    // lookup per page in line with the loads took ~500 cycles each.
     const bool is_k = warp == kLoadK;
-    const CUtensorMap* map = is_k ? &maps.k : &maps.v;
-    uint64_t* const full = is_k ? sm.full_k : sm.full_v;
-    uint64_t* const empty = is_k ? sm.empty_k : sm.empty_v;
-    int* const pages = sm.pages[is_k ? 0 : 1];
-    const uint32_t ring = is_k ? ring_k : ring_v;
-    const int stages = is_k ? NK : NV;
-    const uint64_t pol = l2_policy_evict_first();
     const int entries = (T + kPageSlots - 1) / kPageSlots - 2 * i0;  // pages from this CTA's first slot on
     const auto page_at = [&](int e) { return e < entries ? page_of(i0 * kTile + e * kPageSlots) : 0; };
-    int next = nt > 0 && lane < 16 ? page_at(lane) : 0;
-    Ring r;
-    bool ok = true;
-    int i = 0, issued = 0;
-    while (i < nt && ok) {
-      __syncwarp();
-      if (lane < 16) {
-        pages[lane] = next;
-        next = page_at(2 * i + 16 + lane);
-      }
-      __syncwarp();
-      const int end = min(i + 8, nt);
-      if (lane == 0) {
-        for (int k = 0; i + k < end; ++k) {
-          if (i + k >= stages && !mbar_wait(&empty[r.s], r.par ^ 1u, &sm.abort)) {
-            ok = false;
-            break;
-          }
-          const bool two = entries - 2 * (i + k) > 1;  // a page past the end is not read
-          const int2 pg = *reinterpret_cast<const int2*>(&pages[2 * k]);
-          const uint32_t dst = ring + r.s * S::kTileB;
-          mbar_arrive_expect_tx(&full[r.s], (two ? 2u : 1u) * kPageSlots * HD);
-          tma_load_2d_s(dst, map, &full[r.s], 0, (pg.x * p.Hkv + h) * kPageSlots, pol);
-          if (two) tma_load_2d_s(dst + kPageSlots * HD, map, &full[r.s], 0, (pg.y * p.Hkv + h) * kPageSlots, pol);
-          r.next(stages);
-          ++issued;
-        }
-      }
-      ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-      i = end;
-    }
-    if (lane == 0 && sm.abort) {  // loads in flight land before the CTA leaves (bounded as every wait)
-      int none = 0;
-      for (int k = max(0, issued - stages); k < issued; ++k)
-        mbar_wait(&full[k % stages], static_cast<uint32_t>((k / stages) & 1), &none);
-    }
-    __syncwarp();
+    att_load_tiles<HD>(is_k ? &maps.k : &maps.v, is_k ? sm.full_k : sm.full_v, is_k ? sm.empty_k : sm.empty_v,
+                       sm.pages[is_k ? 0 : 1], is_k ? ring_k : ring_v, is_k ? NK : NV, nt, entries, p.Hkv, h,
+                       &sm.abort, page_at);
   } else if (warp >= kIssueS) {
     // ------------------------------------- MMA issuers: scores, products
     // An MMA of N columns holds the pipe for 32 + N / 4 cycles (M = 128, K =
@@ -1003,104 +789,24 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   }
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
-// One layer's codes as [rows][hd] bytes, boxes of one page of one head (64 rows).
-bool page_map(CUtensorMap* m, const void* codes, long long rows, int hd) {
-  const auto fn = tmap_encoder();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {static_cast<cuuint64_t>(hd), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(hd)};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(hd), kPageSlots};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(codes), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, hd == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-struct AttSetup {
-  cudaError_t err;
-  int max_cluster;  // largest cluster size that can be placed
-  int sms;
-};
-
-cudaLaunchConfig_t att_config(dim3 grid, uint32_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2], int C) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(kAttThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cfg;
-}
-
 template <int HD, int RT, bool kLo>
 cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   using S = AttSmem<HD, RT>;
   static PerDevice<AttSetup> setup;
   AttSetup s{};
-  if (!setup.get(
-          [] {
-            AttSetup r{cudaSuccess, 1, 0};
-            int dev = 0;
-            if ((r.err = cudaGetDevice(&dev)) != cudaSuccess) return r;
-            if ((r.err = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return r;
-            const auto fn = kv8_attention_kernel<HD, RT, kLo>;
-            if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                              kSmemCta)) != cudaSuccess)
-              return r;
-            if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
-              return r;
-            for (int c = kMaxCluster; c > 1; c /= 2) {
-              cudaLaunchAttribute attr[2];
-              cudaLaunchConfig_t cfg = att_config(dim3(c), kSmemHalf, nullptr, attr, c);
-              cfg.numAttrs = 1;
-              int n = 0;
-              if (cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n > 0) {
-                r.max_cluster = c;
-                break;
-              }
-            }
-            return r;
-          },
-          &s))
+  if (!setup.get([] { return att_setup(kv8_attention_kernel<HD, RT, kLo>, kAttThreads, kSmemHalf); }, &s))
     return cudaErrorInvalidDevice;
   if (s.err != cudaSuccess) return s.err;
   const int R = p.n * p.G, rtiles = (R + RT - 1) / RT;
-  // Clusters of up to 16 CTAs per row tile, as many CTAs as the GPU holds (two
-  // per SM), each of two tiles at least at full capacity.  (More, the surplus
-  // leaving at once, costs more than the even shares give: batch 16 29 us
-  // against 21.)
-  const long long groups = static_cast<long long>(p.B) * p.Hkv * rtiles;
-  const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
-  int lc = 0;
-  while ((2 << lc) <= s.max_cluster && (2 << lc) * kMinTiles <= tiles && (groups << (lc + 1)) <= 2ll * s.sms) ++lc;
+  const int c = att_cluster(p, rtiles, s, 2);
   const int fit = static_cast<int>((kSmemHalf - S::bytes(0, 0)) / S::kTileB);
   const int nv = std::min((fit + 1) / 2, S::kMaxStages), nk = std::min(fit / 2, S::kMaxStages);
   AttMaps maps;
   const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = att_config(dim3(rtiles << lc, p.Hkv, p.B), S::bytes(nk, nv), stream, attr, 1 << lc);
-  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo>, maps, p, lc, nk, nv, 2 * s.sms);
+  const cudaLaunchConfig_t cfg = att_config(dim3(rtiles * c, p.Hkv, p.B), kAttThreads, S::bytes(nk, nv), stream, attr, c);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo>, maps, p, c, nk, nv, 2 * s.sms);
 }
 
 template <int HD, bool kLo>
@@ -1121,6 +827,9 @@ cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_kv8_attention(const Kv8AttnParams& p, cudaStream_t stream) {
+  const long long R = static_cast<long long>(p.n) * p.G;
+  const long long tiles = (static_cast<long long>(p.max_pages) * kPageSlots + kTile - 1) / kTile;
+  if (R > kWideRows && (R + 127) / 128 * p.Hkv * p.B * tiles >= kWideWork) return launch_kv8_attention_wide(p, stream);
   if (p.o_lo) return p.hd == 128 ? launch_rows<128, true>(p, stream) : launch_rows<64, true>(p, stream);
   return p.hd == 128 ? launch_rows<128, false>(p, stream) : launch_rows<64, false>(p, stream);
 }

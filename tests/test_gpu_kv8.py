@@ -54,13 +54,13 @@ def _dev(a):
 class Pair:
     """A device cache with shuffled pages and the oracle's rows of the same contents."""
 
-    def __init__(self, cfg, lens, room, seed, layers=1):
+    def __init__(self, cfg, lens, room, seed, layers=1, columns=0):
         self.cfg, self.lens, self.B = cfg, list(lens), len(lens)
         rng = np.random.default_rng(seed)
         need = [(x + room + 63) // 64 for x in lens]
-        self.kv = sb.KV8Cache(cfg, self.B, sum(need) + 2, max(need) + 1)
+        self.kv = sb.KV8Cache(cfg, self.B, sum(need) + 2, max(max(need) + 1, columns))
         ids = rng.permutation(sum(need) + 2)
-        table = np.full((self.B, max(need) + 1), -1, np.int32)
+        table = np.full((self.B, self.kv.max_pages), -1, np.int32)
         at = 0
         for b in range(self.B):
             table[b, :need[b]] = ids[at:at + need[b]]
@@ -899,6 +899,193 @@ def test_advance_looks_at_every_page():
     kv.len.copy_(torch.tensor([60, 19196, 1, 1, 4475, 1], dtype=torch.int32))
     sb.spec_kv8_advance(kv, 5, ws)  # the first's second page is none now; 4480 slots end before page 70
     assert kv.len.cpu().tolist() == [60, 19196, 6, 6, 4480, 6]
+
+
+# Large capacities (a table of WIDE columns) take calls of more than 64 rows a KV head to the kernel for many rows.
+WIDE = 1400
+
+
+@pytest.mark.parametrize("heads,lens,n", [
+    ("128x4/1", (0, 77, 300, 1, 640), 128),
+    ("128x4/1", (0, 3, 59, 123, 124, 250, 700), 17),
+    ("128x8/8", (130, 0), 65),
+    ("64x4/2", (5, 190, 62), 33),
+    ("64x16/2", (2000, 17), 9),
+    ("64x16/2", (255, 0, 128), 100),
+    ("128x6/2", (300, 1), 43),
+    ("128x4/1", (5000,), 40),
+])
+def test_attention_many_rows(heads, lens, n):
+    cfg = _cfg(heads)
+    P = Pair(cfg, lens, n + 40, 71, columns=WIDE)
+    _stale(P, n)
+    q = _q(len(lens) * n, cfg.d_model, 72)
+    out, ws = _run_attention(cfg, P, n, q)
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    _check_attention(cfg, P, n, q, out, [_chain(n)] * len(lens), cfg.head_dim ** -0.5)
+
+
+@pytest.mark.parametrize("heads,lens,n", [("128x4/1", (0, 100, 250), 17), ("64x4/2", (0, 125, 500), 64),
+                                          ("64x16/2", (60, 1), 63), ("128x4/1", (1, 130), 64)])
+def test_attention_many_rows_tree(heads, lens, n):
+    cfg = _cfg(heads)
+    P = Pair(cfg, lens, n + 40, 73, columns=WIDE)
+    _stale(P, n)
+    q = _q(len(lens) * n, cfg.d_model, 74)
+    see, anc = [], []
+    for b in range(len(lens)):
+        masks, _ = sb.spec_tree_masks(wl.random_tree(80 + b, n))
+        masks[0] = 0
+        masks[n - 1] &= ~(1 << (n - 1))
+        see.append(np.array([[(m >> i) & 1 for i in range(n)] for m in masks], bool))
+        anc.append([m | (1 << n) if n < 63 else m for m in masks])
+    out, ws = _run_attention(cfg, P, n, q, anc=_dev(np.array(anc, np.uint64).astype(np.int64)))
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    _check_attention(cfg, P, n, q, out, see, cfg.head_dim ** -0.5)
+    for b, L in enumerate(lens):
+        if L == 0:
+            assert (out[b * n] == 0).all()
+
+
+def test_attention_many_rows_scale_strides_and_sharp_rows():
+    """Also rows that start at scores far below the later ones, so that what is summed is scaled on the way."""
+    cfg, n, lens = _cfg("128x4/1"), 30, (900, 70)
+    P = Pair(cfg, lens, n, 75, columns=WIDE)
+    P.scales["k"][0, P.table[0, 9:]] *= 8  # the later keys are the larger ones
+    P.put_bits("k")
+    for b in range(2):
+        P.rows[0, b, "k"] = P._oracle_rows(0, b, "k", cfg.n_kv_heads, cfg.head_dim)
+    wide = _q(len(lens) * n, cfg.d_model + 64, 76, size=8.0)
+    q = wide[:, 64:]
+    ow = torch.full((len(lens) * n, cfg.d_model + 8), 3.0, dtype=torch.bfloat16, device="cuda")
+    ws = sb.workspace(256)
+    sb.spec_kv8_attention(cfg, P.kv, 0, n, q, ow[:, :cfg.d_model], ws, scale=0.5)
+    assert (ow[:, cfg.d_model:] == 3.0).all()
+    _check_attention(cfg, P, n, q, ow[:, :cfg.d_model], [_chain(n)] * 2, 0.5)
+    # in place: the output may be the queries' own rows
+    q = q.contiguous()
+    sb.spec_kv8_attention(cfg, P.kv, 0, n, q, q, ws, scale=0.5)
+    assert torch.equal(q, ow[:, :cfg.d_model])
+
+
+@pytest.mark.parametrize("name,top", [("v", 2.0 ** 30), ("v", 0.0), ("k", 0.0)])
+def test_attention_many_rows_uneven_scales(name, top):
+    cfg, n, lens = _cfg("128x4/1"), 20, (300, 40)
+    P = Pair(cfg, lens, n, 77, columns=WIDE)
+    pg = P.table[0, 2]
+    if top:
+        P.scales[name][0, pg] *= top
+    else:
+        P.bits[name][0, pg] = 0
+        P.scales[name][0, pg] = 2.0 ** -40
+    P.put_bits(name)
+    for b in range(2):
+        for nm in "kv":
+            P.rows[0, b, nm] = P._oracle_rows(0, b, nm, cfg.n_kv_heads, cfg.head_dim)
+    q = _q(len(lens) * n, cfg.d_model, 78)
+    out, _ = _run_attention(cfg, P, n, q)
+    _check_attention(cfg, P, n, q, out, [_chain(n)] * 2, cfg.head_dim ** -0.5)
+
+
+@pytest.mark.parametrize("heads", ["128x4/1", "64x4/2"])
+def test_attention_many_rows_not_numbers(heads):
+    """As in test_attention_not_numbers; and sequences that do not fit get zero rows."""
+    cfg, n, lens = _cfg(heads), 40, (70, 200)
+    H, hd, Hkv = cfg.n_heads, cfg.head_dim, cfg.n_kv_heads
+    G = H // Hkv
+    q = _q(len(lens) * n, H * hd, 79)
+    ref, _ = _run_attention(cfg, Pair(cfg, lens, n + 30, 80, columns=WIDE), n, q)
+    want = ref.view(len(lens), n, H, hd)
+    last = slice((Hkv - 1) * G, H)
+    for name, b, slot, dim in (("v", 0, 70 + 3, 9), ("v", 1, 200 + 3, hd - 1), ("k", 0, 70 + 3, 1), ("v", 1, 20, 3),
+                               ("k", 1, 199, 0), ("v", 1, 239, 33)):
+        P = Pair(cfg, lens, n + 30, 80, columns=WIDE)
+        P.bits[name][0, P.table[b, slot // 64], Hkv - 1, slot % 64, dim] = 0xFF
+        P.put_bits(name)
+        out, _ = _run_attention(cfg, P, n, q)
+        out = out.view(len(lens), n, H, hd)
+        hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+        j0 = max(0, slot - lens[b])
+        if name == "v":
+            hit[b, j0:, last, dim] = True
+        else:
+            hit[b, j0:, last, :] = True
+        assert torch.equal(torch.isnan(out), hit), (name, b, slot)
+        assert torch.equal(out[~hit], want[~hit])
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        q2 = q.clone()
+        q2[n + 2, hd + 5] = bad
+        out, _ = _run_attention(cfg, Pair(cfg, lens, n + 30, 80, columns=WIDE), n, q2)
+        out = out.view(len(lens), n, H, hd)
+        assert torch.isnan(out[1, 2, 1]).all()
+        keep = torch.ones(out.shape[:3], dtype=torch.bool)
+        keep[1, 2, 1] = False
+        assert torch.equal(out[keep.cuda()], want[keep.cuda()])
+    P = Pair(cfg, lens, n + 30, 80, columns=WIDE)
+    for at, bit in ((-1, sb.DEV_KV_OVERFLOW), (64 * WIDE - n + 1, sb.DEV_KV_OVERFLOW), (400, sb.DEV_BAD_PAGE)):
+        P.kv.len[1] = at  # slots 400 .. 439 lie on no page
+        out, ws = _run_attention(cfg, P, n, q)
+        assert _status(ws) == (sb.SPEC_EDEVICE, bit)
+        assert torch.equal(out[:n], ref[:n]) and (out[n:] == 0).all()
+
+
+def test_attention_many_rows_streams_and_graph():
+    """Two calls at once on two streams, of few and of many rows, and a captured one replayed: the same bits."""
+    cfg, lens, n = _cfg("64x4/2"), (900, 300, 1500), 128
+    P = Pair(cfg, lens, n, 81, columns=WIDE)
+    q = _q(len(lens) * n, cfg.d_model, 82)
+    want, ws = _run_attention(cfg, P, n, q)
+    few, wsf = _run_attention(cfg, P, 5, q[:15])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    outs = [torch.empty_like(want) for _ in range(2)] + [torch.empty_like(few)]
+    for _ in range(20):
+        for s, o in zip(streams, outs):
+            sb.spec_kv8_attention(cfg, P.kv, 0, o.shape[0] // 3, q[:o.shape[0]], o, wsf, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], want) and torch.equal(outs[1], want) and torch.equal(outs[2], few)
+    graph, out = torch.cuda.CUDAGraph(), torch.empty_like(want)
+    with torch.cuda.graph(graph):
+        for _ in range(3):
+            sb.spec_kv8_attention(cfg, P.kv, 0, n, q, out, ws)
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert _status(ws) == (sb.SPEC_OK, 0) and _status(wsf) == (sb.SPEC_OK, 0)
+
+
+def test_attention_many_rows_of_many_sequences():
+    """Batches on either side of the ordering by length: every sequence as alone, but for the order of its sums."""
+    cfg, n = _cfg("64x16/2"), 10
+    for B, top in ((100, 300), (13, 3000)):
+        rng = np.random.default_rng(B)
+        lens = rng.integers(0, top, B)
+        lens[0], lens[-1] = 0, top
+        pages = [(int(x) + n + 63) // 64 for x in lens]
+        kv = sb.KV8Cache(cfg, B, sum(pages), WIDE)
+        for b in range(B):
+            kv.reserve(b, int(lens[b]) + n)
+        kv.sync()
+        _fill(kv, B)
+        kv.len.copy_(_dev(lens.astype(np.int32)))
+        q, ws = _q(B * n, cfg.d_model, 83), sb.workspace(256)
+        out = torch.empty_like(q)
+        sb.spec_kv8_attention(cfg, kv, 0, n, q, out, ws)
+        one = sb.KV8Cache(cfg, 1, kv.n_pages, WIDE)
+        one.k, one.v, one.k_scale, one.v_scale = kv.k, kv.v, kv.k_scale, kv.v_scale
+        for b in range(B):
+            one.table.copy_(kv.table[b:b + 1])
+            one.len.fill_(int(lens[b]))
+            want = torch.empty(n, cfg.d_model, dtype=torch.bfloat16, device="cuda")
+            sb.spec_kv8_attention(cfg, one, 0, n, q[b * n:(b + 1) * n], want, ws)
+            got = out[b * n:(b + 1) * n]
+            # each side rounds once (half a step each: a whole one between them), its weights 2^-11 of the values
+            lim = 2.0 ** -7 * want.float().abs() + 2.0 ** -9 * want.float().abs().max()
+            assert ((got.float() - want.float()).abs() <= lim).all(), (b, int(lens[b]))
+        assert _status(ws) == (sb.SPEC_OK, 0)
 
 
 # ------------------------------------------------------------------ forward
