@@ -25,6 +25,7 @@ namespace {
 constexpr int kRows = 128;                // query rows of a tile
 constexpr int kGroups = 2;                // softmax groups of four warps, a thread per row: even and odd tiles
 constexpr int kSoftW = kGroups * kRows;   // softmax threads
+constexpr int kHalf = kTile / 2;          // keys of a group's score buffer (it has two)
 constexpr int kWiden = 128;               // threads that widen the values
 constexpr int kWLoadK = 12, kWIssue = 13; // (warps; an issuer for each group)
 constexpr int kWideThreads = 32 * (kWIssue + kGroups);
@@ -88,7 +89,8 @@ struct WideSmem {
   static constexpr uint32_t kMisc = kV + 2 * kVB;
   struct Misc {
     uint64_t full_k[kStages], empty_k[kStages];
-    uint64_t c_full[kGroups], v_full[kGroups], s_full[kGroups], p_full[kGroups], o_full[kGroups], drain[kGroups], second;
+    uint64_t c_full[kGroups], v_full[kGroups], drain[kGroups], second;
+    uint64_t s_full[kGroups][2], p_full[kGroups][2], o_full[kGroups][2];  // of a tile's halves
     alignas(16) float2 scale[kGroups][kTile / kKv8Block];  // of a tile's blocks: of the keys, log2 of that of the values
     uint64_t anc[kRows];
     float cq[kRows];               // score factor of a row: 2^k scale log2(e)
@@ -132,10 +134,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     for (int g = 0; g < kGroups; ++g) {
       mbar_init(&sm.c_full[g], 1);
       mbar_init(&sm.v_full[g], kWiden);
-      mbar_init(&sm.s_full[g], 1);
-      mbar_init(&sm.p_full[g], kRows);
-      mbar_init(&sm.o_full[g], 1);
       mbar_init(&sm.drain[g], 1);
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(&sm.s_full[g][u], 1);
+        mbar_init(&sm.p_full[g][u], kRows);
+        mbar_init(&sm.o_full[g][u], 1);
+      }
     }
     mbar_init(&sm.second, 1);
     fence_mbar_init();
@@ -268,31 +272,40 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       // The second group starts behind the first: its MMAs run beside the other's
       // softmax, and the other way round.
       if (g && nt > 1) ok = mbar_wait(&sm.second, 0, &sm.abort);
-      for (int i = g, j = 0; i < nt && ok; i += kGroups, ++j) {  // tile i, the group's j'th
-        // the scores take the place of the weights that the last products read
-        ok = (j == 0 || mbar_wait(&sm.o_full[g], static_cast<uint32_t>((j - 1) & 1), &sm.abort)) &&
-             mbar_wait(&sm.full_k[i % S::kStages], static_cast<uint32_t>((i / S::kStages) & 1), &sm.abort);
-        if (!ok) break;
+      // Scores of half u of the group's j'th tile; they take the place of the
+      // weights of the half before the last, whose products must be done.
+      const auto issue_scores = [&](int j, int u) {
+        const int i = kGroups * j + g;
+        ok = (j == 0 || mbar_wait(&sm.o_full[g][u], static_cast<uint32_t>((j - 1) & 1), &sm.abort)) &&
+             (u || mbar_wait(&sm.full_k[i % S::kStages], static_cast<uint32_t>((i / S::kStages) & 1), &sm.abort));
+        if (!ok) return;
         tc_fence_after();
-        const uint64_t bk = bk0 + static_cast<uint32_t>(i % S::kStages) * (S::kTileB >> 4);
+        const uint64_t bk = bk0 + static_cast<uint32_t>(i % S::kStages * S::kTileB + u * kHalf * HD >> 4);
 #pragma unroll
         for (int kk = 0; kk < HD / 32; ++kk)
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece)
-            umma_e4m3(ts, aq + piece * (kRows * HD >> 4) + kk * 2, bk + kk * 2, idesc_e4m3(kRows, kTile, false, false),
-                      kk + piece > 0 ? 1u : 0u);
-        umma_commit(&sm.s_full[g]);
-        umma_commit(&sm.empty_k[i % S::kStages]);
-        ok = mbar_wait(&sm.v_full[g], static_cast<uint32_t>(j & 1), &sm.abort) &&
-             mbar_wait(&sm.p_full[g], static_cast<uint32_t>(j & 1), &sm.abort);
+            umma_e4m3(ts + u * kHalf, aq + piece * (kRows * HD >> 4) + kk * 2, bk + kk * 2,
+                      idesc_e4m3(kRows, kHalf, false, false), kk + piece > 0 ? 1u : 0u);
+        umma_commit(&sm.s_full[g][u]);
+        if (u) umma_commit(&sm.empty_k[i % S::kStages]);
+      };
+      const int ntg = (nt + 1 - g) / 2;
+      if (ntg && ok) issue_scores(0, 0);
+      for (int t = 0; t < 2 * ntg && ok; ++t) {
+        const int j = t >> 1, u = t & 1;
+        if (t + 1 < 2 * ntg) issue_scores((t + 1) >> 1, (t + 1) & 1);
         if (!ok) break;
-        if (i == 0) mbar_arrive(&sm.second);
+        ok = mbar_wait(&sm.v_full[g], static_cast<uint32_t>(j & 1), &sm.abort) &&
+             mbar_wait(&sm.p_full[g][u], static_cast<uint32_t>(j & 1), &sm.abort);
+        if (!ok) break;
+        if (g == 0 && t == 0) mbar_arrive(&sm.second);
         tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)  // (the same descriptor bits name fp16 in this kind)
-          umma_f16_ts(to, ts + kk * 8, bv + kk * (16 * 128 >> 4), idesc_e4m3(kRows, HD, false, true),
-                      j + kk > 0 ? 1u : 0u);
-        umma_commit(&sm.o_full[g]);
+        for (int kk = 0; kk < kHalf / 16; ++kk)  // (the same descriptor bits name fp16 in this kind)
+          umma_f16_ts(to, ts + u * kHalf + kk * 8, bv + (u * kHalf + kk * 16) * (128 >> 4),
+                      idesc_e4m3(kRows, HD, false, true), t + kk > 0 ? 1u : 0u);
+        umma_commit(&sm.o_full[g][u]);
       }
       if (!ok) {  // MMAs in flight end before TMEM and shared memory go
         int none = 0;
@@ -342,7 +355,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     }
     for (int i = 0; i < nt; ++i) {
       // the group's last products have read its tile and scales (and its softmax, before them)
-      const bool ok = i < 2 || mbar_wait(&sm.o_full[i & 1], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
+      const bool ok = i < 2 || mbar_wait(&sm.o_full[i & 1][1], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
       if (__any_sync(0xffffffffu, !ok)) break;
       if (w < 32) {
         if (scales)
@@ -428,12 +441,13 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       return off < 64 ? static_cast<uint32_t>(am >> off) & 0xFFFFu : 0u;
     };
     bool stopped = false;
-    for (int i = 0; i < ntg; ++i) {
-      const int t0 = (i0 + kGroups * i + g) * kTile;
-      const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
-      const bool ok = mbar_wait(&sm.c_full[g], static_cast<uint32_t>(i & 1), &sm.abort) &&
-                      mbar_wait(&sm.s_full[g], static_cast<uint32_t>(i & 1), &sm.abort);
-      const float2* const scale = sm.scale[g];
+    for (int i = 0; i < 2 * ntg; ++i) {  // half u of the group's j'th tile
+      const int j = i >> 1, u = i & 1;
+      const int t0 = (i0 + kGroups * j + g) * kTile + u * kHalf;
+      const bool masked = t0 + kHalf > L;  // it holds slots that some row does not see
+      const uint32_t tsu = ts + u * kHalf;
+      const bool ok = mbar_wait(&sm.c_full[g], static_cast<uint32_t>(j & 1), &sm.abort) &&
+                      mbar_wait(&sm.s_full[g][u], static_cast<uint32_t>(j & 1), &sm.abort);
       if (__any_sync(0xffffffffu, !ok)) {
         stopped = true;
         break;
@@ -441,55 +455,49 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       tc_fence_after();
       // (never zero: a masked score of -inf stays that)
       const auto factor = [&](float ks) { return fmaxf(ks * cq, 1.17549435e-38f); };
-      // Columns 0 - 63, which P will take, stay in u; 64 - 127 come through v, one
-      // half of them twice (the row's 128 scores at once would take 160 registers).
-      uint32_t u0[32], u1[32], v[32];
-      tmem_ld_x32(ts + 64, v);
-      tmem_ld_x32(ts, u0);
-      tmem_ld_x32(ts + 32, u1);
-      ld_wait(v);
-      ld_pin(u0);
-      ld_pin(u1);
-      float top = -INFINITY;
-      const auto mask = [&](int c0, uint32_t (&x)[32]) {  // masked scores of columns c0 .. c0 + 31 go to -inf
-#pragma unroll
-        for (int k = 0; k < 32; k += 16) {
-          const uint32_t vis = seen16(t0 + c0 + k);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) x[k + j] = (vis >> j) & 1u ? x[k + j] : 0xFF800000u;
-        }
-      };
-      // The largest exponent of those columns.  (Four chains: with one or two
-      // warps a scheduler, a chain's latency is what a row costs.)
-      const auto largest = [&](int c0, const uint32_t (&x)[32]) {
-        const float4 sc = *reinterpret_cast<const float4*>(scale + c0 / 16);
-        float m[4] = {-3.402823466e38f, -3.402823466e38f, -3.402823466e38f, -3.402823466e38f};
-#pragma unroll
-        for (int j = 0; j < 8; j += 2)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            m[k] = max3(m[k], __uint_as_float(x[8 * k + j]), __uint_as_float(x[8 * k + j + 1]));
-        top = max3(top, fmaf(fmaxf(m[0], m[1]), factor(sc.x), sc.y), fmaf(fmaxf(m[2], m[3]), factor(sc.z), sc.w));
-      };
+      const float4* const scale = reinterpret_cast<const float4*>(sm.scale[g] + u * (kHalf / kKv8Block));
+      uint32_t x[2][32];
+      tmem_ld_x32(tsu, x[0]);
+      tmem_ld_x32(tsu + 32, x[1]);
+      ld_wait(x[0]);
+      ld_pin(x[1]);
       if (masked) {
-        mask(0, u0);
-        mask(32, u1);
-        mask(64, v);
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int q = 0; q < 32; q += 16) {
+            const uint32_t vis = seen16(t0 + 32 * k + q);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[k][q + e] = (vis >> e) & 1u ? x[k][q + e] : 0xFF800000u;
+          }
       }
-      largest(64, v);
-      tmem_ld_x32(ts + 96, v);
-      largest(0, u0);
-      largest(32, u1);
-      ld_wait(v);
-      if (masked) mask(96, v);
-      largest(96, v);
-      // ---- raise M (at i = 0: set it); O and l shrink with it.  The products so
-      // far are in O: the scores were issued after them.
+      // ---- the row's largest exponent.  (Eight chains: with two warps a scheduler,
+      // a chain's latency is what a row costs.)
+      float top = -INFINITY;
+      {
+        float m[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m[k] = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < 8; e += 2)
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            m[k] = max3(m[k], __uint_as_float(x[k / 4][k % 4 * 8 + e]), __uint_as_float(x[k / 4][k % 4 * 8 + e + 1]));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float4 sc = scale[k];
+          top = max3(top, fmaf(fmaxf(m[4 * k], m[4 * k + 1]), factor(sc.x), sc.y),
+                     fmaf(fmaxf(m[4 * k + 2], m[4 * k + 3]), factor(sc.z), sc.w));
+        }
+      }
+      // ---- raise M (at first: set it); O and l shrink with it
       if (__any_sync(0xffffffffu, i == 0 || top - M > kWTop)) {
         const float mn = fmaxf(M, top - kWStart), alpha = exp2f(M - mn);
         M = mn;
         l *= alpha;
-        if (i) {
+        if (i) {  // the products so far must be in O
+          mbar_wait(&sm.o_full[g][u ^ 1], static_cast<uint32_t>(((i - 1) >> 1) & 1), &sm.abort);
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < HD; c += 16) {
             uint32_t o[16];
@@ -499,7 +507,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             for (int q = 0; q < 16; q += 8) {
               uint32_t z[8];
 #pragma unroll
-              for (int j = 0; j < 8; ++j) z[j] = __float_as_uint(__uint_as_float(o[q + j]) * alpha);
+              for (int e = 0; e < 8; ++e) z[e] = __float_as_uint(__uint_as_float(o[q + e]) * alpha);
               tmem_st_x8(to + c + q, z);
             }
           }
@@ -507,40 +515,33 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         }
       }
       // ---- weights, their sums, and P over the scores
-      const auto weights = [&](int c0, const uint32_t (&x)[32]) {
-        const float4 sc = *reinterpret_cast<const float4*>(scale + c0 / 16);
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        const float4 sc = scale[h2];
         const float a[2] = {factor(sc.x), factor(sc.z)}, lv[2] = {sc.y, sc.w};
         float2 sum[2][2];
         uint32_t w[2][8];
 #pragma unroll
-        for (int j = 0; j < 16; j += 2) {
+        for (int e = 0; e < 16; e += 2) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 y =
-                fma2(make_float2(__uint_as_float(x[k * 16 + j]), __uint_as_float(x[k * 16 + j + 1])),
-                     make_float2(a[k], a[k]), make_float2(lv[k] - M, lv[k] - M));
-            const float2 e = make_float2(exp2f(y.x), exp2f(y.y));
-            sum[k][j / 2 % 2] = j < 4 ? e : add2(sum[k][j / 2 % 2], e);
-            w[k][j / 2] = f16x2(e.x, e.y);
+            const float2 y = fma2(make_float2(__uint_as_float(x[h2][k * 16 + e]), __uint_as_float(x[h2][k * 16 + e + 1])),
+                                  make_float2(a[k], a[k]), make_float2(lv[k] - M, lv[k] - M));
+            const float2 p2 = make_float2(exp2f(y.x), exp2f(y.y));
+            sum[k][e / 2 % 2] = e < 4 ? p2 : add2(sum[k][e / 2 % 2], p2);
+            w[k][e / 2] = f16x2(p2.x, p2.y);
           }
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           const float2 t = add2(sum[k][0], sum[k][1]);
           l = fmaf(t.x + t.y, __uint_as_float(static_cast<uint32_t>(127 - static_cast<int>(lv[k])) << 23), l);
-          tmem_st_x8(ts + c0 / 2 + k * 8, w[k]);
+          tmem_st_x8(tsu + h2 * 16 + k * 8, w[k]);
         }
-      };
-      weights(0, u0);
-      tmem_ld_x32(ts + 64, u0);
-      weights(32, u1);
-      weights(96, v);
-      ld_wait(u0);
-      if (masked) mask(64, u0);
-      weights(64, u0);
+      }
       tmem_st_wait();
       tc_fence_before();
-      mbar_arrive(&sm.p_full[g]);
+      mbar_arrive(&sm.p_full[g][u]);
     }
     grid_dep_launch();
     // the pages that the new slots lie on
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
       if (unfit) set_status(p.status, over ? SPEC_DEV_KV_OVERFLOW : SPEC_DEV_BAD_PAGE);
     }
     if (ntg && !stopped) {
-      mbar_wait(&sm.o_full[g], static_cast<uint32_t>((ntg - 1) & 1), &sm.abort);
+      mbar_wait(&sm.o_full[g][1], static_cast<uint32_t>((ntg - 1) & 1), &sm.abort);
       mbar_wait(&sm.v_full[g], static_cast<uint32_t>((ntg - 1) & 1), &sm.abort);  // (sm.nan)
       tc_fence_after();
     }
