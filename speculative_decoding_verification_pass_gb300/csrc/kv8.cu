@@ -339,7 +339,8 @@ __global__ void __launch_bounds__(kMoveThreads) kv8_commit_kernel(const Kv8Commi
     // rows that the root's block holds, if its scale has grown
     const int t0 = blk0 * kKv8Block, kept = L0 - t0 + 1;
     for (int e = tid; e < nl * 2 * kept * VEC; e += kMoveThreads) {
-      const int l = e / (2 * kept * VEC), f = e - l * 2 * kept * VEC, side = f >= kept * VEC, rem = f - side * kept * VEC;
+      const int l = e / (2 * kept * VEC), f = e - l * 2 * kept * VEC;
+      const int side = f >= kept * VEC, rem = f - side * kept * VEC;
       const float ratio = s_own[l][side] * pow2_inv(s_dst[l][side][0]);
       if (ratio >= 1.f) continue;
       const int t = t0 + rem / VEC;

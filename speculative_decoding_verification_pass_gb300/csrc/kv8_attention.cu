@@ -1,4 +1,5 @@
-// Attention of n new positions over the 8-bit paged KV cache.
+// Attention of n new positions over the 8-bit paged KV cache (kv8_attention_wide.cu
+// takes the calls with many query rows).
 //   s_j = scale * q . (ks_j k_j),  o = sum_j p_j vs_j v_j / sum_j p_j,
 //   p_j = exp(s_j - max s) over the slots that the row's token may see
 // (the cached ones, and of the new ones its own and earlier, or those of its
@@ -49,8 +50,8 @@
 //   1 sequence of 131000 slots, 1 token: 51 us, 5.3 TB/s; a cluster of 16 per KV
 //     head lies two CTAs to an SM, so 114 of the SMs take part at the most
 //   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
-//   1 sequence x 128 tokens at 4000 slots: 31.5 us (4.2 us of bf16 products);
-//     the softmax threads' chain, with conversions to e4m3 at a quarter rate
+//   1 sequence x 32 tokens at 4000 slots: 15.3 us; the softmax threads' chain,
+//     with conversions to e4m3 at a quarter rate (for more rows: the other kernel)
 #include "kv8_attn.cuh"
 
 namespace spec {
@@ -61,14 +62,15 @@ constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O 
 constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 // The kernel for many query rows takes over where a KV head has more than 64 of
-// them and the calls' (128 rows x 128 keys) at full capacity are 640 or more:
+// them and the call's (128 rows x 128 keys) at full capacity are 448 or more:
 // below, its longer prologue and merge cost more than its cheaper tiles save.
 // Measured, this kernel / that one in us (32 heads on 8, head dim 128, 4000 slots
-// but where it says): 1 x 32 tokens (264) 15.2 / 16.1, 1 x 64 (528) 18.7 / 20.8,
-// 1 x 96 (792) 29.6 / 21.0, 1 x 128 (1056) 31.5 / 24.5, 16 x 32 (4224) 75 / 54,
-// 4 x 64 at 700 (448) 13.6 / 16.9, 4 x 128 at 700 (896) 25.7 / 19.3; 64 rows a
-// head: 16 x 16 tokens 44.7 / 52.7, 64 x 16 141 / 160.
-constexpr int kWideRows = 64, kWideWork = 640;
+// but where it says): 1 x 32 tokens (256) 15.3 / 15.1, 1 x 64 (512) 18.7 / 18.1,
+// 1 x 96 (792) 29.6 / 19.2, 1 x 128 (1056) 31.5 / 22.1, 16 x 32 (4096) 75 / 51,
+// 4 x 64 at 700 (384) 13.6 / 15.4, 4 x 128 at 700 (896) 25.7 / 16.7, head dim 64
+// 4 x 32 at 1900 (480) 15.5 / 12.1; 64 rows a head: 16 x 16 tokens 45 / 50,
+// 64 x 16 141 / 149.
+constexpr int kWideRows = 64, kWideWork = 448;
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
 constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
 
@@ -805,7 +807,8 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg = att_config(dim3(rtiles * c, p.Hkv, p.B), kAttThreads, S::bytes(nk, nv), stream, attr, c);
+  const cudaLaunchConfig_t cfg =
+      att_config(dim3(rtiles * c, p.Hkv, p.B), kAttThreads, S::bytes(nk, nv), stream, attr, c);
   return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo>, maps, p, c, nk, nv, 2 * s.sms);
 }
 

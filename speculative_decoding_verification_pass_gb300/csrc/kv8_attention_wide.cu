@@ -1,36 +1,50 @@
 // Attention over the 8-bit paged KV cache for many query rows (prefill chunks,
-// large trees): the same formulas as the kernel for few rows, but a row tile is
-// 128 query rows, one per softmax thread.
-//   S [128 rows][128 keys]  = (Q hi + Q lo) x K^T     kind::f8f6f4, K as stored
-//   O [128 rows][hd dims]  += P x V                   kind::f16, P from TMEM
-// With few rows a weight can afford its three e4m3 pieces, since the tile of
-// values is what costs; with many the pieces are what costs, and it is cheaper to
-// widen the values once per tile, e4m3 to fp16 (exact), for all 128 rows: four
-// warps do that, straight from global memory into a swizzled tile, and a weight
-// is one fp16 (11 bits, as the three pieces hold).
+// large trees): the same formulas as the kernel for few rows, but a tile is
+// 128 query rows x 128 keys with a row per softmax thread.
+//   S [128 rows][64 keys]   = (Q hi + Q lo) x K^T   kind::f8f6f4, K as stored
+//   O [128 rows][hd dims]  += P x V                 kind::f16, P from TMEM
+// With few rows a weight can afford three e4m3 pieces, since there the tile of
+// values is what costs.  With many the pieces cost, and it is cheaper to widen
+// the values once a tile, e4m3 to fp16 (exact), for all 128 rows: four warps do
+// that, straight from global memory into a swizzled tile.  A weight is then one
+// fp16, with the 11 bits that the three pieces hold.
 //   p'_j = 2^(s_j + log2 vs_j - M),  l = sum over blocks of (sum of p'_j) / vs
-// A block's 16 keys are 16 neighbouring columns, so its key scale and value scale
-// enter as the two constants of one multiply-add per score.  M is a row's own
-// (thread-local) and raised only when a weight would pass 2^15, its warp then
-// scaling its rows of O; P takes the place of the scores it came from.
+// A block's 16 keys are 16 neighbouring columns, so its two scales enter as the
+// two constants of one multiply-add per score.  M is a row's own (one thread
+// knows it) and is raised only when a weight would pass 2^15; the row's warp then
+// scales its rows of O.  P takes the place of the scores it came from.
 //
-// A CTA is one chain (scores, softmax, products), ~1.2 us a tile; two CTAs an SM
-// fill each other's gaps (256 TMEM columns and 113 KB each).  The runs of a row
-// tile over the keys are a cluster that merges through distributed shared memory.
+// A CTA has an SM to itself.  Two softmax groups of four warps take the even and
+// the odd tiles of its run over the keys, each with an M, l and O of its own and
+// a warp that issues its MMAs, half a turn apart; a group has two score buffers of
+// half a tile, so the tensor cores work on the next half during its softmax.
+// (Two CTAs an SM of one group each: 2700 cycles a tile and SM, 128-register
+// threads could not be had; two groups with a row tile each, of 256 rows: 3000,
+// and twice the prologue and merge; so: 2400.)  At the end the groups' sums are put
+// together in shared memory, and those of the cluster's CTAs, whose runs share a
+// row tile, through distributed shared memory.
+//
+// What bounds it: the latency of a group's chain (scores, TMEM load, largest,
+// weights, TMEM store, products); of the SM's cycles the tensor pipe is busy 41%,
+// the issue slots 38%, and nothing else more.  32 heads on 8, head dim 128: 128
+// tokens at 4000 slots 21.9 us (4.3 us of products at the measured bf16 rate), of
+// which ~10 are prologue, merge and a launch; at 131000 slots 322 us, 0.43 of that
+// rate; four sequences of 128 at 700 16.7 us; head dim 64 at 1900 19.3 us.
 #include "kv8_attn.cuh"
 
 namespace spec {
 namespace {
 
-constexpr int kRows = 128;                // query rows of a tile
-constexpr int kGroups = 2;                // softmax groups of four warps, a thread per row: even and odd tiles
-constexpr int kSoftW = kGroups * kRows;   // softmax threads
-constexpr int kHalf = kTile / 2;          // keys of a group's score buffer (it has two)
-constexpr int kWiden = 128;               // threads that widen the values
-constexpr int kWLoadK = 12, kWIssue = 13; // (warps; an issuer for each group)
+constexpr int kRows = 128;               // query rows of a tile
+constexpr int kGroups = 2;               // softmax groups of four warps, a thread per row: even and odd tiles
+constexpr int kSoftW = kGroups * kRows;  // softmax threads
+constexpr int kHalf = kTile / 2;         // keys of a score buffer (a group has two)
+constexpr int kWiden = 128;              // threads that widen the values
+constexpr int kWLoadK = 12;              // the warp that loads K,
+constexpr int kWIssue = 13;              // ... and the first of the issuing ones
 constexpr int kWideThreads = 32 * (kWIssue + kGroups);
-constexpr float kWTop = 15.f;            // a weight stays below 2^15: fp16's largest is 2^16
-constexpr float kWStart = 4.f;           // exponent of a row's maximum where M is set
+constexpr float kWTop = 15.f;   // a weight stays below 2^15: fp16's largest is 2^16
+constexpr float kWStart = 4.f;  // exponent of a row's maximum where M is set
 
 // D[tmem] (+)= A[tmem] * B[smem] of fp16 operands, issued by one thread.
 SPEC_DEVINL void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
@@ -64,7 +78,7 @@ SPEC_DEVINL void ld_wait(uint32_t (&a)[N]) {
 }
 SPEC_DEVINL float2 peer_f32x2(uint32_t a) {
   float2 v;
-  asm("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
   return v;
 }
 SPEC_DEVINL uint32_t max_u16x2(uint32_t a, uint32_t b) {
@@ -80,23 +94,24 @@ SPEC_DEVINL float max3(float a, float b, float c) {
 
 template <int HD>
 struct WideSmem {
-  static constexpr int kStages = 4;                         // of K
+  static constexpr int kStages = 4;  // of K
   static constexpr uint32_t kTileB = kTile * HD;
-  static constexpr uint32_t kQ = 0;                         // [hi | lo][rows][HD] e4m3
+  static constexpr uint32_t kQ = 0;  // [hi | lo][rows][HD] e4m3
   static constexpr uint32_t kK = kQ + 2 * kRows * HD;
-  static constexpr uint32_t kVB = 2 * kTileB;               // a value tile: [HD / 64][keys][64] fp16
-  static constexpr uint32_t kV = kK + kStages * kTileB;     // two of them
+  static constexpr uint32_t kVB = 2 * kTileB;            // a group's value tile: [HD / 64][keys][64] fp16
+  static constexpr uint32_t kV = kK + kStages * kTileB;
   static constexpr uint32_t kMisc = kV + 2 * kVB;
   struct Misc {
     uint64_t full_k[kStages], empty_k[kStages];
     uint64_t c_full[kGroups], v_full[kGroups], drain[kGroups], second;
     uint64_t s_full[kGroups][2], p_full[kGroups][2], o_full[kGroups][2];  // of a tile's halves
-    alignas(16) float2 scale[kGroups][kTile / kKv8Block];  // of a tile's blocks: of the keys, log2 of that of the values
+    // of a tile's blocks: the keys' scale, log2 of the values'
+    alignas(16) float2 scale[kGroups][kTile / kKv8Block];
     uint64_t anc[kRows];
-    float cq[kRows];               // score factor of a row: 2^k scale log2(e)
-    float2 part[kGroups][kRows];   // a group's M and sum per row,
+    float cq[kRows];                // score factor of a row: 2^k scale log2(e)
+    float2 part[kGroups][kRows];    // a group's M and sum per row,
     alignas(8) float2 stat[kRows];  // ... and the CTA's
-    uint32_t nan[kRows][HD / 32];  // outputs that a NaN value code reaches
+    uint32_t nan[kRows][HD / 32];   // outputs that a NaN value code reaches
     alignas(16) int len[kSortSeqs];
     uint32_t tmem;
     alignas(8) int pages[16];
@@ -110,7 +125,8 @@ struct WideSmem {
   // needs less than 67 KB.
   static constexpr uint32_t kBytes = std::max<uint32_t>(kMisc + sizeof(Misc), 160 * 1024);
   static_assert(kW + kMaxCluster * kRows * 4 <= kMisc, "they lie within the tiles");
-  static_assert(kBytes <= kSmemCta && kMisc % 16 == 0 && kV % 1024 == 0, "");
+  static_assert(kBytes <= kSmemCta && kMisc % 16 == 0, "");
+  static_assert(kK % 1024 == 0 && kV % 1024 == 0, "swizzled tiles lie on their own span's boundaries");
   static constexpr uint32_t kTmemCols = 512;  // a group's S (then P) 128 each, O HD each
 };
 
@@ -332,7 +348,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
           const int row = r0 + k * RV;
           x[k] = make_uint4(0, 0, 0, 0);  // past the end: zero
           if (t0 + row < T)
-            x[k] = __ldcs(reinterpret_cast<const uint4*>(vc + ((page * p.Hkv + h) * kPageSlots + row % kPageSlots) * HD));
+            x[k] = __ldcs(
+                reinterpret_cast<const uint4*>(vc + ((page * p.Hkv + h) * kPageSlots + row % kPageSlots) * HD));
         }
       }
     };
@@ -525,8 +542,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         for (int e = 0; e < 16; e += 2) {
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            const float2 y = fma2(make_float2(__uint_as_float(x[h2][k * 16 + e]), __uint_as_float(x[h2][k * 16 + e + 1])),
-                                  make_float2(a[k], a[k]), make_float2(lv[k] - M, lv[k] - M));
+            const float2 s2 = make_float2(__uint_as_float(x[h2][k * 16 + e]), __uint_as_float(x[h2][k * 16 + e + 1]));
+            const float2 y = fma2(s2, make_float2(a[k], a[k]), make_float2(lv[k] - M, lv[k] - M));
             const float2 p2 = make_float2(exp2f(y.x), exp2f(y.y));
             sum[k][e / 2 % 2] = e < 4 ? p2 : add2(sum[k][e / 2 % 2], p2);
             w[k][e / 2] = f16x2(p2.x, p2.y);

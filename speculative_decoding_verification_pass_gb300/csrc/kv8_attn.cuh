@@ -139,12 +139,14 @@ SPEC_DEVINL uint32_t peer_addr(uint32_t saddr, uint32_t rank) {
 }
 SPEC_DEVINL float peer_f32(uint32_t a) {
   float v;
-  asm("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a));
   return v;
 }
 SPEC_DEVINL float4 peer_f32x4(uint32_t a) {
   float4 v;
-  asm("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a));
   return v;
 }
 
@@ -281,11 +283,12 @@ bool page_map(CUtensorMap* m, const void* codes, long long rows, int hd) {
 
 struct AttSetup {
   cudaError_t err;
-  int active[kMaxCluster + 1];  // clusters of each size that can run at once
+  int active[kMaxCluster + 1];  // clusters of each size that can run at once, a CTA an SM
   int sms;
 };
 
-cudaLaunchConfig_t att_config(dim3 grid, int threads, uint32_t smem, cudaStream_t stream, cudaLaunchAttribute (&attr)[2], int C) {
+cudaLaunchConfig_t att_config(dim3 grid, int threads, uint32_t smem, cudaStream_t stream,
+                              cudaLaunchAttribute (&attr)[2], int C) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -303,14 +306,16 @@ cudaLaunchConfig_t att_config(dim3 grid, int threads, uint32_t smem, cudaStream_
 }
 
 // Set up once per device: shared-memory limit, cluster permission, how many
-// clusters of CTAs of `smem` bytes fit.
+// clusters of CTAs of `smem` bytes fit (the query places one CTA on an SM even
+// where two fit; twice as many clusters were seen to run then).
 template <class F>
 AttSetup att_setup(F fn, int threads, int smem) {
   AttSetup r{cudaSuccess, {}, 0};
   int dev = 0;
   if ((r.err = cudaGetDevice(&dev)) != cudaSuccess) return r;
   if ((r.err = cudaDeviceGetAttribute(&r.sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return r;
-  if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCta)) != cudaSuccess) return r;
+  if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCta)) != cudaSuccess)
+    return r;
   if ((r.err = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return r;
   for (int c = 1; c <= kMaxCluster; ++c) {
     cudaLaunchAttribute attr[2];
