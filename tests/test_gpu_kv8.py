@@ -1185,6 +1185,28 @@ def test_forward_tree_equals_chain_and_commits():
     m.close()
 
 
+def test_forward_of_many_rows():
+    """A prefill pass on caches of a small and of a large capacity, whose attention takes different kernels: the
+    same logits but for rounding (a layer's codes may differ where a value lies on a border)."""
+    cfg, B, n, seed = sb.ModelConfig(2, 256, 4, 2, 256, 1000), 2, 64, 47
+    m = sb.Model(cfg, seed)
+    ws = sb.workspace(sb.spec_kv8_workspace_bytes(cfg, B, n))
+    toks = _dev(wl.tokens(seed, B, n, cfg.vocab))
+    out = []
+    for pages in (3, WIDE):
+        kv = sb.KV8Cache(cfg, B, 3 * B, pages)
+        for b in range(B):
+            kv.reserve(b, 3 * 64)
+        kv.sync()
+        z = torch.empty(2, B, n, cfg.vocab, device="cuda")
+        for k in range(2):
+            sb.spec_verify_forward_kv8(m.handle, toks, B, n, kv, z[k], ws)
+        assert _status(ws) == (sb.SPEC_OK, 0) and kv.len.cpu().tolist() == [2 * n] * B
+        out.append(z)
+    assert ((out[0] - out[1]).abs() <= 1e-2 * (1 + out[0].abs())).all()
+    m.close()
+
+
 def test_forward_of_a_large_batch_and_refusals():
     """More than 128 token rows: each sequence as in a batch of its own; and what the pass refuses."""
     shape = (2, 256, 4, 2, 256, 1000)
