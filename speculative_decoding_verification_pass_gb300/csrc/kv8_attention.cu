@@ -542,7 +542,10 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         // Value rows that not every query row sees: zero past the end (pages
         // hold anything there), and NaN codes of new slots taken out (a weight
         // of 0 would not clear them) and noted for the rows that see them.
+        // (The products of tile i - 2 are waited for first: the stage's last fill is
+        // then a past one, else this fill's parity would also name the one before.)
         const uint32_t vt = ring_v + vring.s * S::kTileB;
+        if (i >= 2) mbar_wait(&sm.o_full[buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
         mbar_wait(&sm.full_v[vring.s], vring.par, &sm.abort);
         const uint32_t row0 = max(L - t0, 0), row1 = min(T - t0, kTile);
         for (uint32_t a = vt + row1 * HD + tid * 16; a < vt + kTile * HD; a += kSoft * 16) st_shared_v4(a, 0, 0, 0, 0);
