@@ -37,8 +37,12 @@
 // i + 1 and the products of tile i - 1 run beside the softmax of tile i.
 //
 // Why two CTAs an SM (113 KB and 128 registers a thread each): a tile is one
-// chain of score, weights and product, and another CTA's chain fills its gaps;
-// two groups of softmax threads in one CTA took the same time.
+// chain of score, weights and product, and another CTA's chain fills its gaps.
+// Where the clusters are too few for that (one KV head's tiles are shared by 16
+// CTAs at the most), a CTA has an SM to itself and two groups of softmax warps (NG
+// = 2), one for the even and one for the odd tiles of its run, each with its own
+// M, sums, O and issuing warps; their sums are put together at the end.  (Groups
+// that share a tile, half the rows each, took the time of one.)
 //
 // What bounds it, with what it measured (152 SMs; 32 query heads on 8 KV heads,
 // head dim 128 and 5 tokens a sequence unless it says otherwise; device time of
@@ -47,8 +51,9 @@
 //     copy bandwidth, the rest is the second wave's prologue and the tail
 //   16 sequences, 77 MB: 23.5 us, 3.3 TB/s; ~7 us of setup and end, and tiles
 //     that do not divide evenly over the SMs
-//   1 sequence of 131000 slots, 1 token: 51 us, 5.3 TB/s; a cluster of 16 per KV
-//     head lies two CTAs to an SM, so 114 of the SMs take part at the most
+//   1 sequence of 131000 slots: 1 token 44.6 us, 6.0 TB/s, 5 tokens 57 us; 12 CTAs
+//     for each of the 8 KV heads, so 96 of the SMs take part (a cluster lies
+//     within a group of SMs, and 8 of 16 do not fit at once)
 //   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
 //   1 sequence x 32 tokens at 4000 slots: 15.3 us; the softmax threads' chain,
 //     with conversions to e4m3 at a quarter rate (for more rows: the other kernel)
@@ -57,9 +62,13 @@
 namespace spec {
 namespace {
 
-constexpr int kSoft = 128;                  // softmax threads
-constexpr int kAttThreads = kSoft + 128;    // + K and V loading warps, S and O issuing warps:
-constexpr int kLoadK = 4, kLoadV = 5, kIssueS = 6, kIssueO = 7;
+constexpr int kSoft = 128;                  // threads of a softmax group
+// The warps of a CTA with NG groups: those of the groups, K and V loader, and S
+// and O issuer of each group.
+template <int NG>
+struct Warps {
+  static constexpr int kLoadK = 4 * NG, kLoadV = kLoadK + 1, kIssue = kLoadK + 2, kAll = kIssue + 2 * NG;
+};
 constexpr int kPSpan = 32;                  // bytes of a key's row in one span of P
 // The kernel for many query rows takes over where a KV head has more than 64 of
 // them and the call's (128 rows x 128 keys) at full capacity are 448 or more:
@@ -168,23 +177,24 @@ SPEC_DEVINL float warp_rows_reduce(const float (&v)[RT], float none, Op op) {
   return op(keep, __shfl_xor_sync(0xffffffffu, send, 8));
 }
 
-template <int HD, int RT>
+template <int HD, int RT, int NG>
 struct AttSmem {
-  static constexpr int kMaxStages = 5;  // of K, and of V
+  static constexpr int kMaxStages = NG > 1 ? 6 : 5;  // of K, and of V
   static constexpr uint32_t kTileB = kTile * HD;  // bytes of a K or V tile
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kP = kQ + 2 * RT * HD;
   static constexpr uint32_t kPB = (3 * RT + kPSpan - 1) / kPSpan * (kTile * kPSpan);  // bytes of one P buffer
-  static constexpr uint32_t kK = kP + 2 * kPB;
+  static constexpr uint32_t kK = kP + 2 * NG * kPB;
   // then nk K tiles, nv V tiles and Misc
   struct Misc {
     uint64_t full_k[kMaxStages], full_v[kMaxStages], empty_k[kMaxStages], empty_v[kMaxStages];
-    uint64_t s_full[2], s_free[2], p_full[2], o_full[2], drain[2];
+    uint64_t s_full[2 * NG], s_free[2 * NG], p_full[2 * NG], o_full[2 * NG], drain[2 * NG];
     uint64_t anc[RT];
-    alignas(16) float red[4][RT];   // per-warp maxima (sums at the end); this and the next two are read as float4
-    float mneg[4][RT];              // each warp's copy of -M
+    alignas(16) float red[4 * NG][RT];   // per-warp maxima (sums at the end); this and the next two are read as float4
+    float mneg[4 * NG][RT];              // each warp's copy of -M
     float cq[RT];                   // score factor of a row: 2^k scale log2(e)
     alignas(16) float stat[2][RT];  // this CTA's M and sum per row
+    float part[NG][2][RT];          // ... a group's, and then the factor of its O
     alignas(16) long long out[RT];  // where the row's output starts, -1: no such row
     union {                         // before the loop, and from it on
       alignas(16) int len[kSortSeqs];
@@ -201,8 +211,9 @@ struct AttSmem {
   static_assert(RT * HD * 4 <= 4 * kTileB, "the partial sums lie over a ring of two stages or more");
   static constexpr uint32_t bytes(int nk, int nv) { return kK + (nk + nv) * kTileB + sizeof(Misc); }
   static constexpr int kNO = (3 * RT + 15) / 16 * 16;              // O columns (M = 128 takes multiples of 16)
-  static constexpr uint32_t kTmemCols = RT >= 24 ? 256 : (RT == 16 ? 128 : 64);
-  static_assert(4 * RT + kNO <= static_cast<int>(kTmemCols), "two S buffers and O");
+  static constexpr int kGroupCols = 4 * RT + kNO;  // a group's two S buffers and O
+  static constexpr uint32_t kTmemCols = NG * (RT >= 24 ? 256 : (RT == 16 ? 128 : 64));
+  static_assert(NG * kGroupCols <= static_cast<int>(kTmemCols), "the groups' columns");
 };
 
 struct AttMaps {
@@ -211,11 +222,12 @@ struct AttMaps {
 
 // kLo: the bf16 residual of o is written too (a kernel of its own: as a branch,
 // its code cost batch 64 5%).
-template <int HD, int RT, bool kLo>
-__global__ void __launch_bounds__(kAttThreads, 2)
+template <int HD, int RT, bool kLo, int NG>
+__global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
     kv8_attention_kernel(const __grid_constant__ AttMaps maps, const Kv8AttnParams p, const int csize, const int NK,
                          const int NV, const int share) {
-  using S = AttSmem<HD, RT>;
+  using S = AttSmem<HD, RT, NG>;
+  using W = Warps<NG>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t base = smem_u32(smem_raw);  // swizzled tiles lie on their own span's boundaries
   const uint32_t ring_k = base + S::kK, ring_v = ring_k + NK * S::kTileB;
@@ -231,7 +243,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       mbar_init(&sm.empty_k[i], 1);
       mbar_init(&sm.empty_v[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 2 * NG; ++i) {
       mbar_init(&sm.s_full[i], 1);
       mbar_init(&sm.s_free[i], kSoft);
       mbar_init(&sm.p_full[i], kSoft);
@@ -242,11 +254,11 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     sm.abort = 0;
     sm.any_nan = 0;
   }
-  if (tid == 32 * kLoadK) {
+  if (tid == 32 * W::kLoadK) {
     prefetch_tmap(&maps.k);
     prefetch_tmap(&maps.v);
   }
-  if (warp == kIssueO) {
+  if (warp == W::kAll - 1) {
     tmem_alloc(&sm.tmem, S::kTmemCols);
     tmem_relinquish();
     tc_fence_before();
@@ -295,7 +307,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     const int unit = sorted ? sm.unit : max(kMinTiles, p.B > 1 ? 0 : (tiles + slots - 1) / max(slots, 1));
     C = min(csize, max(1, (tiles + unit - 1) / unit));
     if (rank >= C) {  // (its peers' barriers go on without it)
-      if (warp == kIssueO) tmem_dealloc(tmem, S::kTmemCols);
+      if (warp == W::kAll - 1) tmem_dealloc(tmem, S::kTmemCols);
       return;
     }
     i0 = tiles * rank / C;  // (tiles * C <= 2^13 * 2^4)
@@ -362,7 +374,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     }
     if (qpart == 0) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) sm.mneg[c][qr] = -kNoRef;
+      for (int c = 0; c < 4 * NG; ++c) sm.mneg[c][qr] = -kNoRef;
       sm.cq[qr] = odd ? __uint_as_float(0x7FC00000u)
                       : p.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 + k2) << 23);
       sm.out[qr] = out_at;
@@ -373,64 +385,71 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     fence_async_smem();
   }
   // q and the row arrays are ready (the loading warps need neither)
-  if (warp != kLoadK && warp != kLoadV) named_bar(3, kSoft + 64);
+  if (warp != W::kLoadK && warp != W::kLoadV) named_bar(3, NG * (kSoft + 64));
   tc_fence_after();
 
   float mrun = kNoRef;  // lane r: row r's reference M
 
-  if (warp == kLoadK || warp == kLoadV) {
+  if (warp == W::kLoadK || warp == W::kLoadV) {
     // ------------------------------------------- TMA: the tiles of K, or of V
-    const bool is_k = warp == kLoadK;
+    const bool is_k = warp == W::kLoadK;
     const int entries = (T + kPageSlots - 1) / kPageSlots - 2 * i0;  // pages from this CTA's first slot on
     const auto page_at = [&](int e) { return e < entries ? page_of(i0 * kTile + e * kPageSlots) : 0; };
     att_load_tiles<HD>(is_k ? &maps.k : &maps.v, is_k ? sm.full_k : sm.full_v, is_k ? sm.empty_k : sm.empty_v,
                        sm.pages[is_k ? 0 : 1], is_k ? ring_k : ring_v, is_k ? NK : NV, nt, entries, p.Hkv, h,
                        &sm.abort, page_at);
-  } else if (warp >= kIssueS) {
+  } else if (warp >= W::kIssue) {
     // ------------------------------------- MMA issuers: scores, products
     // An MMA of N columns holds the pipe for 32 + N / 4 cycles (M = 128, K =
     // 32), and its thread for 57 to 92 at any N, so the two products of a tile
     // come from two threads.
     if (lane == 0) {
-      const bool scores = warp == kIssueS;
+      const int g = (warp - W::kIssue) / 2;  // of group g: its j'th tile is the CTA's NG j + g
+      const bool scores = (warp - W::kIssue) % 2 == 0;
       const int stages = scores ? NK : NV;
+      const uint32_t tg = tmem + g * S::kGroupCols;
       Ring ring;
+      if (g) ring.next(stages);
       bool ok = true;
       const uint64_t a0 = scores ? sdesc_rows<HD>(ring_k, 16) : sdesc_rows<HD>(ring_v, 0);
-      const uint64_t b0 = scores ? sdesc_rows<HD>(base + S::kQ, 16) : sdesc_rows<kPSpan>(base + S::kP, kTile * kPSpan);
-      for (int i = 0; i < nt; ++i) {
+      const uint64_t b0 = scores ? sdesc_rows<HD>(base + S::kQ, 16)
+                                 : sdesc_rows<kPSpan>(base + S::kP + g * 2 * S::kPB, kTile * kPSpan);
+      const int ntg = (nt + NG - 1 - g) / NG;
+      for (int j = 0; j < ntg; ++j) {
+        const int buf = j & 1, at = 2 * g + buf;
         const uint64_t a = a0 + static_cast<uint32_t>(ring.s) * (S::kTileB >> 4);
         if (scores) {
-          ok = (i < 2 || mbar_wait(&sm.s_free[i & 1], static_cast<uint32_t>((i / 2 - 1) & 1), &sm.abort)) &&
+          ok = (j < 2 || mbar_wait(&sm.s_free[at], static_cast<uint32_t>((j / 2 - 1) & 1), &sm.abort)) &&
                mbar_wait(&sm.full_k[ring.s], ring.par, &sm.abort);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
           for (int kk = 0; kk < HD / 32; ++kk)
-            umma_e4m3(tmem + (i & 1) * 2 * RT, a + kk * 2, b0 + kk * 2, idesc_e4m3(kTile, 2 * RT, false, false),
+            umma_e4m3(tg + buf * 2 * RT, a + kk * 2, b0 + kk * 2, idesc_e4m3(kTile, 2 * RT, false, false),
                       kk > 0 ? 1u : 0u);
-          umma_commit(&sm.s_full[i & 1]);
+          umma_commit(&sm.s_full[at]);
           umma_commit(&sm.empty_k[ring.s]);
         } else {
           ok = mbar_wait(&sm.full_v[ring.s], ring.par, &sm.abort) &&
-               mbar_wait(&sm.p_full[i & 1], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
+               mbar_wait(&sm.p_full[at], static_cast<uint32_t>((j >> 1) & 1), &sm.abort);
           if (!ok) break;
           tc_fence_after();
-          const uint64_t bp = b0 + static_cast<uint32_t>(i & 1) * (S::kPB >> 4);
+          const uint64_t bp = b0 + static_cast<uint32_t>(buf) * (S::kPB >> 4);
 #pragma unroll
           for (int kk = 0; kk < kTile / 32; ++kk)
             // head dim 64: the 128 rows of the A operand are the 64 dimensions twice
-            umma_e4m3(tmem + 4 * RT, a + kk * (32 * HD >> 4), bp + kk * (32 * kPSpan >> 4),
-                      idesc_e4m3(kTile, S::kNO, true, true), i > 0 || kk > 0 ? 1u : 0u);
-          umma_commit(&sm.o_full[i & 1]);
+            umma_e4m3(tg + 4 * RT, a + kk * (32 * HD >> 4), bp + kk * (32 * kPSpan >> 4),
+                      idesc_e4m3(kTile, S::kNO, true, true), j > 0 || kk > 0 ? 1u : 0u);
+          umma_commit(&sm.o_full[at]);
           umma_commit(&sm.empty_v[ring.s]);
         }
-        ring.next(stages);
+#pragma unroll
+        for (int k = 0; k < NG; ++k) ring.next(stages);
       }
       if (!ok) {  // MMAs in flight end before TMEM and shared memory go
         int none = 0;
-        umma_commit(&sm.drain[scores ? 0 : 1]);
-        mbar_wait(&sm.drain[scores ? 0 : 1], 0, &none);
+        umma_commit(&sm.drain[2 * g + (scores ? 0 : 1)]);
+        mbar_wait(&sm.drain[2 * g + (scores ? 0 : 1)], 0, &none);
       }
     }
     __syncwarp();
@@ -438,8 +457,11 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // ------------------------------------------- softmax and accumulation
     // A wait that gives up sets the abort flag; the threads leave the loop
     // together at its barrier.
-    const uint32_t lane_addr = static_cast<uint32_t>(warp * 32) << 16;
-    const int sub = (tid % kPageSlots) / kKv8Block;
+    const int g = NG > 1 ? warp / 4 : 0, st = tid - g * kSoft;  // group, key (then dimension) of the thread
+    const uint32_t tg = tmem + (static_cast<uint32_t>(warp % 4 * 32) << 16) + g * S::kGroupCols;
+    const int bar = 1 + 3 * g;                // the group's two named barriers, bar and bar + 1
+    const int ntg = (nt + NG - 1 - g) / NG;   // its tiles
+    const int sub = (st % kPageSlots) / kKv8Block;
     const auto scale_at = [&](int pg) { return (static_cast<long long>(pg) * p.Hkv + h) * kKv8Sub + sub; };
     const auto seen = [&](int t) {  // bit r: row rbase + r sees slot t
       if (t < L) return 0xFFFFFFFFu;
@@ -462,7 +484,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     const auto o_rows = [&](int r, float (&o)[8]) {
       uint32_t w[3][8];
 #pragma unroll
-      for (int q = 0; q < 3; ++q) tmem_ld_x8(tmem + lane_addr + (4 + q) * RT + r, w[q]);
+      for (int q = 0; q < 3; ++q) tmem_ld_x8(tg + (4 + q) * RT + r, w[q]);
       tmem_ld_wait(w[0], w[1], w[2]);
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -475,19 +497,20 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // this thread's scales, one tile ahead, and its page, two ahead (the TMA
     // warp flags ids outside the pool; here they are clamped)
     const int last_page = p.max_pages - 1;
-    const auto page_id = [&](int i) { return table[min(((i0 + i) * kTile + tid) / kPageSlots, last_page)]; };
+    const auto page_id = [&](int i) { return table[min(((i0 + NG * i + g) * kTile + st) / kPageSlots, last_page)]; };
     const auto scale_of = [&](const float* sc, int pg) {
       return sc[scale_at(min(max(pg, 0), p.n_pages - 1))];
     };
-    int pg1 = nt > 0 ? page_id(0) : 0;
-    float ks_n = nt > 0 ? scale_of(p.ks, pg1) : 1.f, vs_n = nt > 0 ? scale_of(p.vs, pg1) : 1.f;
-    pg1 = nt > 1 ? page_id(1) : 0;
+    int pg1 = ntg > 0 ? page_id(0) : 0;
+    float ks_n = ntg > 0 ? scale_of(p.ks, pg1) : 1.f, vs_n = ntg > 0 ? scale_of(p.vs, pg1) : 1.f;
+    pg1 = ntg > 1 ? page_id(1) : 0;
     bool stopped = false;
     Ring vring;
-    for (int i = 0; i < nt; ++i, vring.next(NV)) {
-      const int buf = i & 1, t0 = (i0 + i) * kTile, t = t0 + tid;
+    if (g) vring.next(NV);
+    for (int i = 0; i < ntg; ++i) {  // the group's i'th tile
+      const int buf = i & 1, t0 = (i0 + NG * i + g) * kTile, t = t0 + st;
       const float ks = ks_n, vs = vs_n;
-      if (i + 1 < nt) {
+      if (i + 1 < ntg) {
         ks_n = scale_of(p.ks, pg1);
         vs_n = scale_of(p.vs, pg1);
         pg1 = page_id(i + 2);
@@ -497,7 +520,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       const float ivs = none ? 0.f : pow2_inv(vs);
       const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
       const uint32_t vis = masked ? seen(t) : 0xFFFFFFFFu;
-      mbar_wait(&sm.s_full[buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
+      mbar_wait(&sm.s_full[2 * g + buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
       tc_fence_after();
       float s[RT];
       const auto scores = [&] {  // s_j + log2 vs_j of this key for the tile's rows
@@ -506,7 +529,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
 #pragma unroll
         for (int r0 = 0; r0 < RT; r0 += GR) {
           uint32_t hi[GR], lo[GR];
-          tmem_ld2(tmem + lane_addr + buf * 2 * RT + r0, tmem + lane_addr + buf * 2 * RT + RT + r0, hi, lo);
+          tmem_ld2(tg + buf * 2 * RT + r0, tg + buf * 2 * RT + RT + r0, hi, lo);
 #pragma unroll
           for (int r = 0; r < GR; r += 4) {
             const float4 c = *reinterpret_cast<const float4*>(sm.cq + r0 + r);
@@ -545,11 +568,12 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         // (The products of tile i - 2 are waited for first: the stage's last fill is
         // then a past one, else this fill's parity would also name the one before.)
         const uint32_t vt = ring_v + vring.s * S::kTileB;
-        if (i >= 2) mbar_wait(&sm.o_full[buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
+        if (i >= 2)
+          mbar_wait(&sm.o_full[2 * g + buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
         mbar_wait(&sm.full_v[vring.s], vring.par, &sm.abort);
         const uint32_t row0 = max(L - t0, 0), row1 = min(T - t0, kTile);
-        for (uint32_t a = vt + row1 * HD + tid * 16; a < vt + kTile * HD; a += kSoft * 16) st_shared_v4(a, 0, 0, 0, 0);
-        for (uint32_t a = vt + row0 * HD + tid * 16; a < vt + row1 * HD; a += kSoft * 16) {
+        for (uint32_t a = vt + row1 * HD + st * 16; a < vt + kTile * HD; a += kSoft * 16) st_shared_v4(a, 0, 0, 0, 0);
+        for (uint32_t a = vt + row0 * HD + st * 16; a < vt + row1 * HD; a += kSoft * 16) {
           uint32_t w[4];
           asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -578,9 +602,9 @@ __global__ void __launch_bounds__(kAttThreads, 2)
       }
       // ---- does any exponent pass the pieces' range?
       // (the first tile sets M)
-      if (i == 0 || named_bar_any(1, kSoft, exponents() > kTopExp || *static_cast<volatile int*>(&sm.abort) != 0)) {
+      if (i == 0 || named_bar_any(bar, kSoft, exponents() > kTopExp || *static_cast<volatile int*>(&sm.abort) != 0)) {
         // raise M to each row's maximum (at 2^2); what is summed so far shrinks by alpha
-        if (i && named_bar_any(2, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
+        if (i && named_bar_any(bar + 1, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
           stopped = true;
           break;
         }
@@ -588,9 +612,10 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         float alpha = 1.f;  // lane r: row r's
         const float m = warp_rows_reduce(s, -INFINITY, [](float a, float c) { return fmaxf(a, c); });
         if (lane < RT) sm.red[warp][lane] = m;
-        named_bar(1, kSoft);
+        named_bar(bar, kSoft);
         if (lane < RT) {
-          const float mt = fmaxf(fmaxf(sm.red[0][lane], sm.red[1][lane]), fmaxf(sm.red[2][lane], sm.red[3][lane]));
+          const float mt = fmaxf(fmaxf(sm.red[4 * g][lane], sm.red[4 * g + 1][lane]),
+                                 fmaxf(sm.red[4 * g + 2][lane], sm.red[4 * g + 3][lane]));
           const float mn = fmaxf(mrun, mt - kStartExp);
           alpha = exp2f(mrun - mn);
           sm.mneg[warp][lane] = -mn;
@@ -598,7 +623,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         }
         __syncwarp();
         if (i) {  // O and l shrink with it (O's pieces become one)
-          mbar_wait(&sm.o_full[(i - 1) & 1], static_cast<uint32_t>(((i - 1) >> 1) & 1), &sm.abort);
+          mbar_wait(&sm.o_full[2 * g + ((i - 1) & 1)], static_cast<uint32_t>(((i - 1) >> 1) & 1), &sm.abort);
           tc_fence_after();
 #pragma unroll
           for (int r = 0; r < RT; r += 8) {
@@ -612,16 +637,16 @@ __global__ void __launch_bounds__(kAttThreads, 2)
               w[k] = __float_as_uint(o[k] * a);
               z[k] = 0u;
             }
-            tmem_st_x8(tmem + lane_addr + 4 * RT + r, w);
-            tmem_st_x8(tmem + lane_addr + 5 * RT + r, z);
-            tmem_st_x8(tmem + lane_addr + 6 * RT + r, z);
+            tmem_st_x8(tg + 4 * RT + r, w);
+            tmem_st_x8(tg + 5 * RT + r, z);
+            tmem_st_x8(tg + 6 * RT + r, z);
           }
           tmem_st_wait();
         }
         exponents();
       }
       tc_fence_before();
-      mbar_arrive(&sm.s_free[buf]);
+      mbar_arrive(&sm.s_free[2 * g + buf]);
       // ---- weights and their sums; P: this key's row, hi | mid | lo
       uint32_t w[3][RT / 4];
 #pragma unroll
@@ -642,21 +667,23 @@ __global__ void __launch_bounds__(kAttThreads, 2)
         w[2][r / 4] = r % 4 ? w[2][r / 4] | (u2 << 16) : u2;
       }
       // P of tile i - 2 has been read
-      if (i >= 2) mbar_wait(&sm.o_full[buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
-      const uint32_t pbuf = base + S::kP + buf * S::kPB;
+      if (i >= 2) mbar_wait(&sm.o_full[2 * g + buf], static_cast<uint32_t>(((i >> 1) - 1) & 1), &sm.abort);
+      const uint32_t pbuf = base + S::kP + (2 * g + buf) * S::kPB;
       const auto word = [&](int k) { return w[k / (RT / 4)][k % (RT / 4)]; };
 #pragma unroll
       for (int c = 0; c < 3 * RT / 16; ++c)
-        st_shared_v4(pbuf + p_off(tid, c), word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
+        st_shared_v4(pbuf + p_off(st, c), word(4 * c), word(4 * c + 1), word(4 * c + 2), word(4 * c + 3));
       if constexpr (3 * RT % 16 != 0) {
         constexpr int c = 3 * RT / 16;
-        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(pbuf + p_off(tid, c)), "r"(word(4 * c)),
+        asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(pbuf + p_off(st, c)), "r"(word(4 * c)),
                      "r"(word(4 * c + 1))
                      : "memory");
       }
       fence_async_smem();
       tc_fence_before();
-      mbar_arrive(&sm.p_full[buf]);
+      mbar_arrive(&sm.p_full[2 * g + buf]);
+#pragma unroll
+      for (int k = 0; k < NG; ++k) vring.next(NV);
     }
     // the next launch may start now: earlier, its blocks would take the places that
     // free first and lie unevenly over the SMs (batch 16 25.4 us against 23.6)
@@ -664,35 +691,72 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     // ---- this CTA's row sums
     const float ls = warp_rows_reduce(l, 0.f, [](float a, float c) { return a + c; });
     // (and the last maxima have been read)
-    const bool bad_page = named_bar_any(2, kSoft, new_page < 0 || new_page >= p.n_pages);
+    const bool bad_page = named_bar_any(bar + 1, kSoft, new_page < 0 || new_page >= p.n_pages);
     const bool unfit = over || bad_page;  // zero rows
     if (tid == 0) {
       sm.unfit = unfit;
       if (unfit) set_status(p.status, over ? SPEC_DEV_KV_OVERFLOW : SPEC_DEV_BAD_PAGE);
     }
     if (lane < RT) sm.red[warp][lane] = ls;
-    named_bar(1, kSoft);
+    named_bar(bar, kSoft);
+    float lt = 0.f;
+    if (st < RT) {
+      lt = (sm.red[4 * g][st] + sm.red[4 * g + 1][st]) + (sm.red[4 * g + 2][st] + sm.red[4 * g + 3][st]);
+      sm.part[g][0][st] = mrun;
+      sm.part[g][1][st] = lt;
+    }
+    if constexpr (NG > 1) {  // the groups' sums at a common M
+      named_bar(7, NG * kSoft);
+      float mine = 1.f;
+      if (st < RT) {
+        const float m = fmaxf(mrun, sm.part[g ^ 1][0][st]);
+        mine = exp2f(mrun - m);
+        lt = fmaf(mine, lt, exp2f(sm.part[g ^ 1][0][st] - m) * sm.part[g ^ 1][1][st]);
+        mrun = m;
+      }
+      named_bar(7, NG * kSoft);  // (both have read the other's)
+      if (st < RT) sm.part[g][0][st] = mine;
+    }
     if (tid < RT) {
-      const float lt = (sm.red[0][tid] + sm.red[1][tid]) + (sm.red[2][tid] + sm.red[3][tid]);
       sm.stat[0][tid] = C > 1 ? mrun : (lt == 0.f || unfit ? 0.f : 1.f / lt);  // alone: the factor of a row
       sm.stat[1][tid] = lt;
     }
-    if (C == 1) named_bar(1, kSoft);
+    if (C == 1 || NG > 1) named_bar(bar, kSoft);
     // ---- O: dimension tid of every row, to the output, or to shared memory for the merge
-    if (nt && !stopped) {
-      mbar_wait(&sm.o_full[(nt - 1) & 1], static_cast<uint32_t>(((nt - 1) >> 1) & 1), &sm.abort);
+    if (ntg && !stopped) {
+      mbar_wait(&sm.o_full[2 * g + ((ntg - 1) & 1)], static_cast<uint32_t>(((ntg - 1) >> 1) & 1), &sm.abort);
       tc_fence_after();
     }
     float acc[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) acc[r] = 0.f;
-    if (nt) {
+    if (ntg) {
 #pragma unroll
       for (int r = 0; r < RT; r += 8) {
         float o[8];
         o_rows(r, o);
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[r + k] = o[k];
+      }
+    }
+    if constexpr (NG > 1) {  // the second group's O to the first
+      named_bar(7, NG * kSoft);  // (every MMA is done with the tiles that it lies over)
+      const uint32_t mine = base + S::kO + st * 4;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[r] *= sm.part[g][0][r];
+      if (g && st < HD) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + r * HD * 4), "f"(acc[r]) : "memory");
+      }
+      named_bar(7, NG * kSoft);
+      if (!g && st < HD) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          float x;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(x) : "r"(mine + r * HD * 4) : "memory");
+          acc[r] += x;
+        }
       }
     }
     if (sm.any_nan && tid < HD) {
@@ -740,7 +804,7 @@ __global__ void __launch_bounds__(kAttThreads, 2)
     __syncwarp();
     cluster_sync_all();
     const uint32_t stat = smem_u32(&sm.stat[0][0]);
-    for (int e = rank * kAttThreads + tid; e < rows * (HD / 4); e += C * kAttThreads) {
+    for (int e = rank * 32 * W::kAll + tid; e < rows * (HD / 4); e += C * 32 * W::kAll) {
       const int r = e / (HD / 4), d = e % (HD / 4) * 4;
       // every peer's reference, sum and four partial sums, all loads in flight together
       float mc[kMaxCluster], lc[kMaxCluster];
@@ -788,31 +852,45 @@ __global__ void __launch_bounds__(kAttThreads, 2)
   if (tid == 0 && sm.abort) set_status(p.status, SPEC_DEV_TIMEOUT);
   tc_fence_before();
   __syncthreads();
-  if (warp == kIssueO) {
+  if (warp == W::kAll - 1) {
     tc_fence_after();
     tmem_dealloc(tmem, S::kTmemCols);
   }
 }
 
-template <int HD, int RT, bool kLo>
+template <int HD, int RT, bool kLo, int NG>
 cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
-  using S = AttSmem<HD, RT>;
+  using S = AttSmem<HD, RT, NG>;
+  constexpr int kThreads = 32 * Warps<NG>::kAll, kSmem = NG > 1 ? kSmemCta : kSmemHalf;
   static PerDevice<AttSetup> setup;
   AttSetup s{};
-  if (!setup.get([] { return att_setup(kv8_attention_kernel<HD, RT, kLo>, kAttThreads, kSmemHalf); }, &s))
+  if (!setup.get([] { return att_setup(kv8_attention_kernel<HD, RT, kLo, NG>, kThreads, kSmem); }, &s))
     return cudaErrorInvalidDevice;
   if (s.err != cudaSuccess) return s.err;
   const int R = p.n * p.G, rtiles = (R + RT - 1) / RT;
-  const int c = att_cluster(p, rtiles, s, 2);
-  const int fit = static_cast<int>((kSmemHalf - S::bytes(0, 0)) / S::kTileB);
-  const int nv = std::min((fit + 1) / 2, S::kMaxStages), nk = std::min(fit / 2, S::kMaxStages);
+  const int c = att_cluster(p, rtiles, s, 3 - NG);
+  // Two groups a CTA where every CTA has an SM to itself and four tiles or more at
+  // full capacity.  One group / two in us, 8 KV heads: 1 token at 131000 slots 51.4
+  // / 44.6, 5 tokens 75.6 / 57.1, at 16000 16.8 / 15.0; with two tiles a CTA, 5
+  // tokens at 2048 8.4 / 9.1, one KV head at 4000 8.0 / 9.1.
+  if constexpr (NG == 1) {
+    const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
+    if (static_cast<long long>(p.B) * p.Hkv * rtiles * c <= s.sms && tiles >= 4 * c)
+      return launch_tile<HD, RT, kLo, 2>(p, stream);
+  }
+  const int fit = static_cast<int>((kSmem - S::bytes(0, 0)) / S::kTileB);
+  // With two groups the counts are even: a stage then holds tiles of one group
+  // only.  (A group that saw every other fill of a stage could take a past fill,
+  // whose parity is the same, for the one that it waits for.)
+  constexpr int kEven = ~(NG - 1);
+  const int nk = std::min(fit / 2, S::kMaxStages) & kEven, nv = std::min(fit - nk, S::kMaxStages) & kEven;
+  const uint32_t bytes = std::max<uint32_t>(S::bytes(nk, nv), NG > 1 ? kSmemAlone : 0);
   AttMaps maps;
   const long long rows = static_cast<long long>(p.n_pages) * p.Hkv * kPageSlots;
   if (!page_map(&maps.k, p.kc, rows, HD) || !page_map(&maps.v, p.vc, rows, HD)) return cudaErrorInvalidValue;
   cudaLaunchAttribute attr[2];
-  const cudaLaunchConfig_t cfg =
-      att_config(dim3(rtiles * c, p.Hkv, p.B), kAttThreads, S::bytes(nk, nv), stream, attr, c);
-  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo>, maps, p, c, nk, nv, 2 * s.sms);
+  const cudaLaunchConfig_t cfg = att_config(dim3(rtiles * c, p.Hkv, p.B), kThreads, bytes, stream, attr, c);
+  return cudaLaunchKernelEx(&cfg, kv8_attention_kernel<HD, RT, kLo, NG>, maps, p, c, nk, nv, (3 - NG) * s.sms);
 }
 
 template <int HD, bool kLo>
@@ -823,10 +901,10 @@ cudaError_t launch_rows(const Kv8AttnParams& p, cudaStream_t stream) {
   for (int rt = 24; rt >= 8; rt -= 8)
     if ((R + rt - 1) / rt * rt < (R + best - 1) / best * best) best = rt;
   switch (best) {
-    case 8: return launch_tile<HD, 8, kLo>(p, stream);
-    case 16: return launch_tile<HD, 16, kLo>(p, stream);
-    case 24: return launch_tile<HD, 24, kLo>(p, stream);
-    default: return launch_tile<HD, 32, kLo>(p, stream);
+    case 8: return launch_tile<HD, 8, kLo, 1>(p, stream);
+    case 16: return launch_tile<HD, 16, kLo, 1>(p, stream);
+    case 24: return launch_tile<HD, 24, kLo, 1>(p, stream);
+    default: return launch_tile<HD, 32, kLo, 1>(p, stream);
   }
 }
 

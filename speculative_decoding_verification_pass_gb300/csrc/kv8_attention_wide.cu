@@ -120,10 +120,7 @@ struct WideSmem {
   // partial sums [rows][HD] fp32 and after them the merge's weights [cluster][rows],
   // over the tiles once every MMA is done
   static constexpr uint32_t kO = 0, kW = kRows * HD * 4;
-  // A CTA takes all of an SM's TMEM and its cluster waits for it, so it shares its
-  // SM with no CTA that could hold TMEM while waiting for another: none of those
-  // needs less than 67 KB.
-  static constexpr uint32_t kBytes = std::max<uint32_t>(kMisc + sizeof(Misc), 160 * 1024);
+  static constexpr uint32_t kBytes = std::max<uint32_t>(kMisc + sizeof(Misc), kSmemAlone);
   static_assert(kW + kMaxCluster * kRows * 4 <= kMisc, "they lie within the tiles");
   static_assert(kBytes <= kSmemCta && kMisc % 16 == 0, "");
   static_assert(kK % 1024 == 0 && kV % 1024 == 0, "swizzled tiles lie on their own span's boundaries");

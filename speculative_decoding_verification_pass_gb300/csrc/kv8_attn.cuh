@@ -23,6 +23,10 @@ constexpr int kSortSeqs = 96;
 constexpr int kMinTiles = 2;         // tiles of a CTA at least, where they are shared
 constexpr int kSmemCta = 227 * 1024;   // dynamic shared memory of a CTA alone on its SM,
 constexpr int kSmemHalf = 113 * 1024;  // ... and of two (1 KB of each CTA's share is the system's)
+// ... of a CTA that takes an SM's TMEM for itself and whose cluster waits for it: it
+// shares its SM with no CTA that could hold TMEM while waiting for another (none
+// of those needs less than 67 KB)
+constexpr int kSmemAlone = 160 * 1024;
 constexpr float kNoRef = -3.402823466e38f;  // M of a row that has seen no slot: any score passes it
 
 SPEC_DEVINL void tmem_ld_x8(uint32_t taddr, uint32_t* r) {

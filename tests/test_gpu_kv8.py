@@ -906,6 +906,86 @@ WIDE = 1400
 
 
 @pytest.mark.parametrize("heads,lens,n", [
+    ("128x4/1", (40000,), 5),
+    ("128x4/1", (9000, 11), 2),
+    ("64x4/2", (30000,), 7),
+    ("128x8/8", (20000,), 1),
+    ("64x16/2", (5000, 126, 0), 4),
+    ("128x6/2", (3000, 7000), 9),
+    ("128x4/1", (0, 1, 63, 127, 128, 250, 700, 2000), 8),
+    ("64x4/2", (100, 0, 64), 12),
+])
+def test_attention_long_capacity(heads, lens, n):
+    """Few sequences in a large capacity: a CTA has an SM to itself and takes its tiles in two groups; runs of
+    one tile and of many."""
+    cfg = _cfg(heads)
+    P = Pair(cfg, lens, n + 40, 91, columns=WIDE)
+    _stale(P, n)
+    q = _q(len(lens) * n, cfg.d_model, 92)
+    out, ws = _run_attention(cfg, P, n, q)
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    _check_attention(cfg, P, n, q, out, [_chain(n)] * len(lens), cfg.head_dim ** -0.5)
+    for _ in range(10):  # launches that overlap; the same bits
+        again = torch.empty_like(out)
+        sb.spec_kv8_attention(cfg, P.kv, 0, n, q, again, ws)
+        assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("heads,lens,n", [("128x4/1", (0, 100, 2500), 13), ("64x4/2", (0, 1250), 30)])
+def test_attention_long_capacity_tree(heads, lens, n):
+    cfg = _cfg(heads)
+    P = Pair(cfg, lens, n + 40, 93, columns=WIDE)
+    # later keys larger: what is summed is scaled on the way
+    P.scales["k"][0, P.table[-1, 9:][P.table[-1, 9:] >= 0]] *= 8
+    P.put_bits("k")
+    P.rows[0, len(lens) - 1, "k"] = P._oracle_rows(0, len(lens) - 1, "k", cfg.n_kv_heads, cfg.head_dim)
+    _stale(P, n)
+    q = _q(len(lens) * n, cfg.d_model, 94, size=4.0)
+    see, anc = [], []
+    for b in range(len(lens)):
+        masks, _ = sb.spec_tree_masks(wl.random_tree(90 + b, n))
+        masks[0] = 0
+        see.append(np.array([[(m >> i) & 1 for i in range(n)] for m in masks], bool))
+        anc.append(masks)
+    out, ws = _run_attention(cfg, P, n, q, anc=_dev(np.array(anc, np.uint64).astype(np.int64)))
+    assert _status(ws) == (sb.SPEC_OK, 0)
+    _check_attention(cfg, P, n, q, out, see, cfg.head_dim ** -0.5)
+    assert (out[0] == 0).all()
+
+
+@pytest.mark.parametrize("heads", ["128x4/1", "64x4/2"])
+def test_attention_long_capacity_not_numbers(heads):
+    cfg, n, lens = _cfg(heads), 6, (70, 1200)
+    H, hd, Hkv = cfg.n_heads, cfg.head_dim, cfg.n_kv_heads
+    G = H // Hkv
+    q = _q(len(lens) * n, H * hd, 95)
+    ref, _ = _run_attention(cfg, Pair(cfg, lens, n + 30, 96, columns=WIDE), n, q)
+    want = ref.view(len(lens), n, H, hd)
+    last = slice((Hkv - 1) * G, H)
+    for name, b, slot, dim in (("v", 0, 70 + 3, 9), ("v", 1, 1200 + 3, hd - 1), ("k", 0, 70 + 3, 1), ("v", 1, 20, 3),
+                               ("k", 1, 1199, 0)):
+        P = Pair(cfg, lens, n + 30, 96, columns=WIDE)
+        P.bits[name][0, P.table[b, slot // 64], Hkv - 1, slot % 64, dim] = 0xFF
+        P.put_bits(name)
+        out, _ = _run_attention(cfg, P, n, q)
+        out = out.view(len(lens), n, H, hd)
+        hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+        j0 = max(0, slot - lens[b])
+        if name == "v":
+            hit[b, j0:, last, dim] = True
+        else:
+            hit[b, j0:, last, :] = True
+        assert torch.equal(torch.isnan(out), hit), (name, b, slot)
+        assert torch.equal(out[~hit], want[~hit])
+    P = Pair(cfg, lens, n + 30, 96, columns=WIDE)
+    for at, bit in ((-1, sb.DEV_KV_OVERFLOW), (64 * WIDE - n + 1, sb.DEV_KV_OVERFLOW), (1400, sb.DEV_BAD_PAGE)):
+        P.kv.len[1] = at
+        out, ws = _run_attention(cfg, P, n, q)
+        assert _status(ws) == (sb.SPEC_EDEVICE, bit)
+        assert torch.equal(out[:n], ref[:n]) and (out[n:] == 0).all()
+
+
+@pytest.mark.parametrize("heads,lens,n", [
     ("128x4/1", (0, 77, 300, 1, 640), 128),
     ("128x4/1", (0, 3, 59, 123, 124, 250, 700), 17),
     ("128x8/8", (130, 0), 65),
@@ -1185,10 +1265,11 @@ def test_forward_tree_equals_chain_and_commits():
     m.close()
 
 
-def test_forward_of_many_rows():
-    """A prefill pass on caches of a small and of a large capacity, whose attention takes different kernels: the
+@pytest.mark.parametrize("n", [5, 64])
+def test_forward_in_a_large_capacity(n):
+    """A pass on caches of a small and of a large capacity, whose attention takes different kernels: the
     same logits but for rounding (a layer's codes may differ where a value lies on a border)."""
-    cfg, B, n, seed = sb.ModelConfig(2, 256, 4, 2, 256, 1000), 2, 64, 47
+    cfg, B, seed = sb.ModelConfig(2, 256, 4, 2, 256, 1000), 2, 47
     m = sb.Model(cfg, seed)
     ws = sb.workspace(sb.spec_kv8_workspace_bytes(cfg, B, n))
     toks = _dev(wl.tokens(seed, B, n, cfg.vocab))
