@@ -30,10 +30,10 @@
 // need not be its maximum: the pieces hold weights up to 448, so M is set to put
 // the maximum of the first tile at 2^2 and raised only when a weight would pass
 // 2^8.75 (one barrier per tile asks whether any does).  Until then O^T adds
-// up in TMEM and no thread reads it.  Warps 0 - 3 are the softmax's; warp 4
-// issues the TMA loads of K, warp 5 those of V, warp 6 the score MMAs and warp 7
-// the products: one thread for both of either kind had less time a tile than its
-// waits and issues took.  S and P are double-buffered, so the scores of tile
+// up in TMEM and no thread reads it.  After the softmax's four warps one issues the
+// TMA loads of K, one those of V, one the score MMAs and one the products: one
+// thread for both of either kind had less time a tile than its waits and issues
+// took.  S and P are double-buffered, so the scores of tile
 // i + 1 and the products of tile i - 1 run beside the softmax of tile i.
 //
 // Why two CTAs an SM (113 KB and 128 registers a thread each): a tile is one
