@@ -467,12 +467,14 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  * below its row's largest; a weight p is within 2^-11 of its value or, where
  * p x v_scale is small, within 2^-20 of the largest such product in the row.
  * A score past fp32's range makes its row NaN.  A row that sees no slot (a mask
- * with no bit of an empty cache) is zero.  Slots at or past len[b] + n and slots a row does not
- * see have no influence, whatever they hold; a NaN code that it sees makes
- * the row's affected outputs NaN, an infinite or NaN q its whole row.  A
- * sequence that does not fit (as in spec_kv8_append) gets zero rows and a
- * status bit; a page id outside the pool below len[b] sets SPEC_DEV_BAD_PAGE
- * and leaves its rows unspecified. */
+ * with no bit of an empty cache) is zero.  Slots at or past len[b] + n and slots
+ * a row does not see have no influence, whatever they hold; a NaN code that it
+ * sees makes the row's affected outputs NaN, an infinite or NaN q its whole row.
+ * A sequence that does not fit (as in spec_kv8_append) gets zero rows and a
+ * status bit; a page id outside the pool below len[b] sets SPEC_DEV_BAD_PAGE and
+ * leaves its rows unspecified.  The same call gives the same bits; the order of a
+ * row's sums (its last bits) goes by the batch, the lengths and max_pages, by
+ * which the work is split. */
 int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
                        const uint16_t* d_q, int64_t q_ld, const uint64_t* d_anc, float scale,
                        uint16_t* d_o, int64_t o_ld, void* d_ws, void* stream);
