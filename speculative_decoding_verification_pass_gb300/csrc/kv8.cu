@@ -35,9 +35,9 @@ __global__ void kv8_rope_kernel(float2* dst, int rd, double theta, double factor
 // its wait, so none is read through the read-only path (that is for data that
 // nothing writes while the kernel runs; the frequencies are such).
 //
-// One warp per unit.  A q unit is one token and a few of its heads; a k or v
-// unit is one block of 16 slots of one (sequence, KV head), so that the
-// warp alone sees every row that the block's scale depends on:
+// A warp takes one token's q and a few of its heads; a CTA takes one block of 16
+// slots of k or v of one (sequence, KV head), so that it sees every row that the
+// block's scale depends on:
 //   s = max over the block's new rows of the smallest 2^e with |x| <= 448 2^e
 //   (and the scale it has, if it holds rows from before),
 //   code = e4m3(x / s); rows held before are re-rounded when s has grown.
@@ -47,10 +47,14 @@ __global__ void kv8_rope_kernel(float2* dst, int rd, double theta, double factor
 // What bounds it is latency: the launch and one chain of length, page, rows,
 // rotation and store (the bytes of the largest measured call, 8.9 MB, take 1.3
 // us).  So every row of a warp is on its way at once, before the pages are
-// looked at.  Device time inside a graph, 32 query heads on 8 KV heads: 1
-// sequence x 5 tokens of head dim 128 5.1 us, 64 x 5 6.7 us, 4 x 128 tokens of
-// head dim 64 in fp32 5.3 us.
-constexpr int kAppThreads = 128;
+// looked at, and a block's rows are spread over four warps: a warp that took all
+// 16 was a long stretch of code that ran once, and fetching it cost more than
+// the work (1 x 5 tokens 5.2 us, now 2.6; two warps 3.4; eight take 64 x 5 from 6.0
+// to 7.9).  Device time inside a graph, 32 query heads on 8 KV heads: 1 sequence
+// x 5 tokens of head dim 128 2.6 us, 64 x 5 6.0 us, 4 x 128 tokens of head dim 64
+// in fp32 4.7 us.
+constexpr int kAppWarps = 4;
+constexpr int kAppThreads = 32 * kAppWarps;
 constexpr int kAppHeads = 4;  // head rows per lane of a q unit
 
 SPEC_DEVINL float2 load2(const void* p, long long i, int f32) {
@@ -111,18 +115,20 @@ SPEC_DEVINL void rotate4(const Pair4& q, float (&x)[4], const float (&c)[2], con
 
 template <int HD>
 __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8AppendParams p) {
-  constexpr int LPR = HD / 4, RPW = 32 / LPR, IT = kKv8Block / RPW;
+  constexpr int LPR = HD / 4, RPW = 32 / LPR;
+  constexpr int RPC = RPW * kAppWarps, IT = kKv8Block / RPC;  // rows of a CTA at a time
+  __shared__ float s_max[kAppWarps];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, li = lane % LPR, sub = lane / LPR;
-  long long u = static_cast<long long>(blockIdx.x) * (kAppThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, li = lane % LPR;
   const Pair4 pr = pair4(li, p.rd, p.inter);
   float2 fr[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) fr[k] = pr.rot ? __ldg(p.rope + pr.i0 + k) : make_float2(0.f, 0.f);
   const long long kv_units = 2ll * p.B * p.Hkv * p.nb;
-  if (u >= kv_units) {  // ---- q: rotate and round to bf16
-    u -= kv_units;
+  if (blockIdx.x >= kv_units) {  // ---- q: rotate and round to bf16
+    const long long u = (blockIdx.x - kv_units) * kAppWarps + warp;
+    const int sub = lane / LPR;
     const int groups = (p.H + kAppHeads * RPW - 1) / (kAppHeads * RPW);
     const int m = static_cast<int>(u / groups), g = static_cast<int>(u % groups);
     if (m >= p.B * p.n) return;
@@ -153,15 +159,17 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
     return;
   }
   // ---- one block of 16 slots of k (which 0) or v (1)
-  const int which = static_cast<int>(u & 1);
+  int u = blockIdx.x;
+  const int which = u & 1;
   u >>= 1;
-  const int h = static_cast<int>(u % p.Hkv);
+  const int h = u % p.Hkv;
   u /= p.Hkv;
-  const int blk_i = static_cast<int>(u % p.nb), b = static_cast<int>(u / p.nb);
+  const int blk_i = u % p.nb, b = u / p.nb;
+  const int row0 = warp * RPW + lane / LPR;  // the thread's rows: row0 + i RPC
   const int L = p.base[b];
   if (p.seq_ok && !p.seq_ok[b]) return;  // flagged when the pass began
   if (L < 0 || L > p.max_pages * kPageSlots - p.n) {
-    if (lane == 0) set_status(p.status, SPEC_DEV_KV_OVERFLOW);
+    if (threadIdx.x == 0) set_status(p.status, SPEC_DEV_KV_OVERFLOW);
     return;
   }
   const int slot0 = (L / kKv8Block + blk_i) * kKv8Block;  // the block's first slot
@@ -172,7 +180,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   float x[IT][4];  // (on their way before the pages are looked at)
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = slot0 + i * RPW + sub - L;  // the row's token
+    const int j = slot0 + i * RPC + row0 - L;  // the row's token
     x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
     if (j >= 0 && j < p.n) {
       const long long o = (static_cast<long long>(b) * p.n + j) * ld + h * HD;
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   }
   int page;
   if (const int32_t bad = kv8_fit_warp(L, p.n, p.table, p.max_pages, p.n_pages, b, slot0, &page)) {
-    if (lane == 0) set_status(p.status, bad);
+    if (threadIdx.x == 0) set_status(p.status, bad);
     return;
   }
   const Kv8Map map{p.table, p.max_pages, p.n_pages, p.Hkv, HD};
@@ -192,7 +200,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int j = slot0 + i * RPW + sub - L;
+    const int j = slot0 + i * RPC + row0 - L;
     if (at.rot && j >= 0 && j < p.n) {
       const int pos = L + (p.depth ? p.depth[b * p.n + j] : j);
       float cs[2], sn[2];
@@ -207,15 +215,18 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
     }
   }
   amax = warp_max(amax);
+  if (lane == 0) s_max[warp] = amax;
+  __syncthreads();  // (and every thread has read the scale before it is replaced)
+#pragma unroll
+  for (int k = 0; k < kAppWarps; ++k) amax = fmaxf(amax, s_max[k]);
   uint8_t* codes = (which ? p.vc : p.kc) + map.row(page, h, slot0);
   const float s_new = kv8_scale(amax);
   const float s = kept ? fmaxf(s_new, s_held) : s_new;
   const float s_old = kept ? s_held : s;
   const float inv = pow2_inv(s), ratio = s_old * inv;
-  __syncwarp();  // every lane has read the scale before lane 0 replaces it
 #pragma unroll
   for (int i = 0; i < IT; ++i) {
-    const int r = i * RPW + sub, j = slot0 + r - L;
+    const int r = i * RPC + row0, j = slot0 + r - L;
     uint8_t* row = codes + static_cast<long long>(r) * HD;
     if (j >= 0 && j < p.n) {
       const uint32_t w = e4m3x4(x[i][0] * inv, x[i][1] * inv, x[i][2] * inv, x[i][3] * inv);
@@ -230,7 +241,7 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
       *w = kv8_rescale4(*w, ratio);
     }
   }
-  if (lane == 0) *sp = s;
+  if (threadIdx.x == 0) *sp = s;
 }
 
 // ------------------------------------------------------------------ commit
@@ -419,9 +430,8 @@ cudaError_t launch_kv8_rope(float2* dst, int rd, double theta, double factor, do
 
 cudaError_t launch_kv8_append(const Kv8AppendParams& p, cudaStream_t stream) {
   const int rpw = 32 / (p.hd / 4);
-  const long long units = 2ll * p.B * p.Hkv * p.nb +
-                          static_cast<long long>(p.B) * p.n * ((p.H + kAppHeads * rpw - 1) / (kAppHeads * rpw));
-  const long long grid = (units + kAppThreads / 32 - 1) / (kAppThreads / 32);
+  const long long q_units = static_cast<long long>(p.B) * p.n * ((p.H + kAppHeads * rpw - 1) / (kAppHeads * rpw));
+  const long long grid = 2ll * p.B * p.Hkv * p.nb + (q_units + kAppWarps - 1) / kAppWarps;
   if (grid > 0x7FFFFFFFll) return cudaErrorInvalidValue;
   return launch_dep(p.hd == 128 ? kv8_append_kernel<128> : kv8_append_kernel<64>, dim3(static_cast<unsigned>(grid)),
                     kAppThreads, stream, p);
