@@ -252,12 +252,13 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
 // Every row of a layer is read before any is written: rows and scales go
 // through registers and shared memory.  What bounds it is the chain of round
 // trips (length, path, page, row); a path of a few rows leaves a thread one
-// 16-byte word a layer, so a CTA takes as many layers at once as its registers
-// hold (one layer a CTA, 4096 CTAs: 16.4 us at 16 sequences and 32 layers;
-// so, with the length update, 9.0 us, and 6.8 us for one sequence).
+// 16-byte word a layer, so a CTA takes a few layers at once.  With the length
+// update and a copy that puts the lengths back, 1 sequence of 7 nodes / 16 of 33,
+// 32 layers: eight layers of eight words a thread 6.8 / 9.9 us, four of four 6.2 /
+// 9.0, two of eight (128 threads) 6.3 / 11.0; one layer a CTA took 16.4 for the 16.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveLayers = 8;
-constexpr int kMoveWords = 8;                                                 // 16-byte words per thread
+constexpr int kMoveLayers = 4;
+constexpr int kMoveWords = 4;                                                 // 16-byte words per thread
 constexpr int kMoveBlocks = (kTreeMaxNodes + 2 * kKv8Block - 2) / kKv8Block;  // blocks n slots can touch
 
 // 0 when the path of sequence b can be committed, else the status bit (the
