@@ -449,9 +449,10 @@ class RopeTable:
 
 def _rows(t, rows: int, width: int, dtype, what: str) -> int:
     """Elements between the rows of a 2-D tensor of whole rows."""
-    if t.dtype != dtype or t.shape != (rows, width) or t.stride(1) != 1:
+    s = t.stride()
+    if t.dtype != dtype or t.shape != (rows, width) or s[1] != 1:
         raise ValueError(f"{what}: expected a {(rows, width)} {dtype} tensor with unit column stride")
-    return t.stride(0) if rows > 1 else max(t.stride(0), width)
+    return s[0] if rows > 1 else max(s[0], width)
 
 
 def _plain(t, shape, dtype, what: str):
@@ -478,10 +479,12 @@ _HERE = _Here()
 
 def _on(dev: int):
     """Device `dev` as the current one: launches go to the current device."""
-    return _HERE if torch.cuda.current_device() == dev else torch.cuda.device(dev)
+    return _HERE if _current_device() == dev else torch.cuda.device(dev)
 
 
-# the handle of a device's current stream, without a Stream object where torch has that call
+# the current device (CUDA is initialised: the call has tensors on it), and the handle of a device's
+# current stream, without a Stream object, where torch has those calls
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
