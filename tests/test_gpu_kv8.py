@@ -914,6 +914,7 @@ WIDE = 1400
     ("128x6/2", (3000, 7000), 9),
     ("128x4/1", (0, 1, 63, 127, 128, 250, 700, 2000), 8),
     ("64x4/2", (100, 0, 64), 12),
+    ("128x8/8", (60000,), 5),  # runs of 39 tiles
 ])
 def test_attention_long_capacity(heads, lens, n):
     """Few sequences in a large capacity: a CTA has an SM to itself and takes its tiles in two groups; runs of
@@ -994,6 +995,7 @@ def test_attention_long_capacity_not_numbers(heads):
     ("64x16/2", (255, 0, 128), 100),
     ("128x6/2", (300, 1), 43),
     ("128x4/1", (5000,), 40),
+    ("128x8/8", (12000, 3000, 100, 7000), 70),  # runs of 24 tiles: every ring turns over
 ])
 def test_attention_many_rows(heads, lens, n):
     cfg = _cfg(heads)
