@@ -465,7 +465,9 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  *   scale  > 0, or 0 for 1/sqrt(head_dim).
  * Scores, softmax and sums are in fp32.  q is as given but for elements 2^-18
  * below its row's largest; a weight p is within 2^-11 of its value or, where
- * p x v_scale is small, within 2^-20 of the largest such product in the row.
+ * p x v_scale is small, within 2^-19 of the largest such product in the row,
+ * up or down by a pattern of the slot numbers: over a long context such errors
+ * do not add up to more than about the root of their number.
  * A score past fp32's range makes its row NaN.  A row that sees no slot (a mask
  * with no bit of an empty cache) is zero.  Slots at or past len[b] + n and slots
  * a row does not see have no influence, whatever they hold; a NaN code that it
@@ -473,8 +475,8 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  * A sequence that does not fit (as in spec_kv8_append) gets zero rows and a
  * status bit; a page id outside the pool below len[b] sets SPEC_DEV_BAD_PAGE and
  * leaves its rows unspecified.  The same call gives the same bits; the order of a
- * row's sums (its last bits) goes by the batch, the lengths and max_pages, by
- * which the work is split. */
+ * row's sums and the size of its small weights' errors go by the batch, the
+ * lengths and max_pages, by which the work is split. */
 int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
                        const uint16_t* d_q, int64_t q_ld, const uint64_t* d_anc, float scale,
                        uint16_t* d_o, int64_t o_ld, void* d_ws, void* stream);

@@ -11,7 +11,7 @@
 // converted.  The other operand is split into e4m3 pieces that add up to it:
 //   q row = 2^k (hi + lo)            bf16 has 8 significant bits, a piece 4: exact but
 //                                    for elements 2^-18 below the row's largest
-//   p     = hi + 2^-4 mid + 2^-8 lo  an fp16 weight's 11 bits (2^-18 at the least)
+//   p     = hi + 2^-4 mid + 2^-8 lo  an fp16 weight's 11 bits, in steps of 2^-17 at the least
 // and the pieces lie side by side in the N dimension, so a tile of keys or
 // values is read from shared memory once whatever their number.
 //
@@ -30,11 +30,23 @@
 // need not be its maximum: the pieces hold weights up to 448, so M is set to put
 // the maximum of the first tile at 2^2 and raised only when a weight would pass
 // 2^8.75 (one barrier per tile asks whether any does).  Until then O^T adds
-// up in TMEM and no thread reads it.  After the softmax's four warps one issues the
-// TMA loads of K, one those of V, one the score MMAs and one the products: one
-// thread for both of either kind had less time a tile than its waits and issues
-// took.  S and P are double-buffered, so the scores of tile
-// i + 1 and the products of tile i - 1 run beside the softmax of tile i.
+// up in TMEM and no thread reads it.
+//
+// With a row's largest weight at 2^2 the pieces' last step, 2^-17, is 2^-19 of it,
+// and in a long context that many keys may each have less.  Rounded to nearest,
+// weights that are alike would all go the same way, say to zero where together they
+// are half of the row, while the sum of the p_j keeps them.  So a weight is rounded
+// up or down by a fixed pattern of slot numbers (slot_dither), and n errors add up
+// to about sqrt(n) of them.  Measured against rounding to nearest, batch 64 and 16:
+// the pattern (one addition for two weights) 51.7 to 52.4 us and 23.7 to 24.0; a
+// fourth piece 54.0 and 25.5; maxima at 2^4 and M set anew every 16 tiles 54.2 and
+// 24.9.
+//
+// After the softmax's four warps one issues the TMA loads of K, one those of V,
+// one the score MMAs and one the products: one thread for both of either kind had
+// less time a tile than its waits and issues took.  S and P are double-buffered,
+// so the scores of tile i + 1 and the products of tile i - 1 run beside the
+// softmax of tile i.
 //
 // Why two CTAs an SM (113 KB and 128 registers a thread each): a tile is one
 // chain of score, weights and product, and another CTA's chain fills its gaps.
@@ -82,6 +94,7 @@ constexpr int kPSpan = 32;                  // bytes of a key's row in one span 
 constexpr int kWideRows = 64, kWideWork = 448;
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
 constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
+constexpr float kLastStep = 7.62939453125e-06f;  // 2^-17, the last piece's smallest step
 
 // N columns of the thread's lane at each of two places, ready for use.
 template <int N>
@@ -117,6 +130,14 @@ SPEC_DEVINL uint32_t f16x2_to_e4m3x2(uint32_t a) {
   uint16_t r;
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
+}
+// A number in [-1/2, 1/2) made of slot t by two rounds of multiply and xor-shift: in
+// any stretch of slots, and in every k'th of them, as evenly spread as random ones.
+SPEC_DEVINL float slot_dither(int t) {
+  uint32_t h = static_cast<uint32_t>(t) * 0x9E3779B1u;
+  h = (h ^ (h >> 15)) * 0x85EBCA77u;
+  h ^= h >> 13;
+  return static_cast<float>(static_cast<int32_t>(h)) * 2.3283064365386963e-10f;  // 2^-32
 }
 // ... and of chunk c of key i's row of P, which is cut into spans of 32 bytes
 // ([128 keys][32 bytes] each): three pieces of 24 rows then take 96 bytes a key
@@ -648,6 +669,10 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
       tc_fence_before();
       mbar_arrive(&sm.s_free[2 * g + buf]);
       // ---- weights and their sums; P: this key's row, hi | mid | lo
+      // (added before the rounding to fp16, whose smallest step a long context can feel
+      // too; a weight of zero, plus less than half a step, stays zero)
+      const float dither = kLastStep * slot_dither(t);
+      const float2 dither2 = make_float2(dither, dither);
       uint32_t w[3][RT / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
@@ -656,7 +681,8 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
         l[r] = sum.x, l[r + 1] = sum.y;
         // p = hi + mid / 16 + lo / 256, each the nearest e4m3 of what is left
         // times 1, 16 and 256 (fp16 holds every difference exactly)
-        const uint32_t f = f16x2(e.x, e.y);
+        const float2 ed = add2(e, dither2);
+        const uint32_t f = f16x2(ed.x, ed.y);
         const uint32_t u0 = f16x2_to_e4m3x2(f);
         const uint32_t f1 = f16x2_fma(e4m3x2_to_f16x2(u0), 0xBC00BC00u, f);  // - hi
         const uint32_t u1 = f16x2_to_e4m3x2(f16x2_mul(f1, 0x4C004C00u));     // x 16

@@ -1,0 +1,183 @@
+"""Accuracy of the 8-bit cache's attention: limits that a wrong output does not pass.
+
+Every limit is made per row and dimension from the fp64 weights, so it shrinks with the outputs as contexts grow,
+and each case shows that an output of zeros and one with a single tile of keys left out lie beyond it.
+With P_j = p_j vs_j, in units of the row's sum of weights:
+
+* o is bf16: half a step, 2^-8 |o|;
+* a weight is rounded to 11 bits, half a step 2^-11 of itself: 2^-11 sum p |v|;
+* a small weight is rounded up or down by one step of its last piece or, with many query rows, by half of fp16's
+  smallest: where the row's largest P is 2^2 (2^4) or more, a step is 2^-17 (2^-24).  With few rows the slot number
+  decides which way, so that n of them add up like n independent errors of half a step: 6 deviations,
+  6 2^-20 max P sqrt(sum code^2).  With many rows each may go the same way: 2^-29 max P sum |code|.  (The largest P
+  of a weight's own run over the keys is what counts; it is at most the row's.);
+* a score s is off by d: q's elements by 2^-22 of the row's largest (2^-17 for many query rows), its fp32 sum by
+  2^-20 of sum |q k|, its exponent by 2^-21 |s|; that moves a weight and the normaliser by that much each:
+  2 d sum p |v|, and to second order nothing that counts;
+* sums in fp32: an addition may cut off 2^-23 of its sum, one per 32 keys: T / 32 2^-23 sum p |v|.
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from speculative_decoding_verification_pass_gb300 import binding as sb
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+    __graft_entry__.build()
+
+
+class Cache:
+    """A cache of given rows: k, v [pages][Hkv][64][hd] doubles that e4m3 holds, scales [pages][Hkv][4], and each
+    sequence's pages in order (a page may serve several places: attention only reads)."""
+
+    def __init__(self, hd, H, k, v, ks, vs, pages, lens, n, columns=0):
+        P, Hkv = k.shape[:2]
+        self.cfg = sb.ModelConfig(1, hd * H, H, Hkv, 128, 1000)
+        self.k, self.v, self.ks, self.vs = (x.double().cuda() for x in (k, v, ks, vs))
+        self.pages, self.lens, self.n = [torch.as_tensor(p).long().cuda() for p in pages], list(lens), n
+        kv = self.kv = sb.KV8Cache(self.cfg, len(lens), P, max(columns, max(len(p) for p in pages)))
+        for dst, x in ((kv.k, self.k), (kv.v, self.v)):
+            dst[0] = x.float().to(E4M3)
+            assert torch.equal(dst[0].double(), x)
+        kv.k_scale[0], kv.v_scale[0] = self.ks.float(), self.vs.float()
+        for b, p in enumerate(self.pages):
+            kv.table[b, :len(p)] = p.int()
+        kv.len.copy_(torch.tensor(lens, dtype=torch.int32))
+        self.ws = sb.workspace(256)
+
+    def run(self, q, scale=0.0):
+        out = torch.full_like(q, 7.0)
+        sb.spec_kv8_attention(self.cfg, self.kv, 0, self.n, q, out, self.ws, scale=scale)
+        assert sb.spec_device_status(self.ws) == (sb.SPEC_OK, 0)
+        return out
+
+    def rows(self, b, h):
+        """Keys, values, codes of values and their scales of the sequence's slots: [T][hd], ..., [T]."""
+        T, pg = self.lens[b] + self.n, self.pages[b]
+        ks, vs = (s[pg, h].repeat_interleave(16, dim=1).reshape(-1)[:T] for s in (self.ks, self.vs))
+        k, v = (x[pg, h].reshape(-1, x.shape[-1])[:T] for x in (self.k, self.v))
+        return k * ks[:, None], v * vs[:, None], v, vs
+
+
+def _limit(q, K, V, code, vs, seen, scale, q_err):
+    """(o, limit) [rows][hd] of q's rows, which see the first `seen` slots each."""
+    T = len(K)
+    s = (q @ K.T) * scale
+    hide = torch.arange(T, device="cuda")[None] >= seen[:, None]
+    s.masked_fill_(hide, -math.inf)
+    p = torch.softmax(s, dim=1)
+    o, a = p @ V, p @ V.abs()
+    d = scale * (2.0 ** -20 * (q.abs() @ K.abs().T).amax(1) + q_err * q.abs().amax(1) * K.abs().sum(1).max())
+    d += 2.0 ** -21 * s.masked_fill(hide, 0.0).abs().amax(1)
+    lim = 2.0 ** -8 * o.abs() + a * (2.0 ** -11 + 2 * d[:, None] + T / 32 * 2.0 ** -23)
+    top = (p * vs).amax(1, keepdim=True)
+    return o, lim + top * (6 * 2.0 ** -20 * code.norm(dim=0) + 2.0 ** -29 * code.abs().sum(0))
+
+
+def _check(cache, q, out, scale=0.0, q_err=2.0 ** -22, lost=()):
+    """out against the definition in 64 bits; beyond the limits lie zeros and, for each tile of `lost`, the output
+    without it."""
+    cfg, n = cache.cfg, cache.n
+    hd, H, Hkv = cfg.head_dim, cfg.n_heads, cfg.n_kv_heads
+    G, scale = H // Hkv, scale or hd ** -0.5
+    worst = 0.0
+    for b, L in list(enumerate(cache.lens))[::3 if len(cache.lens) > 9 else 1]:
+        for h in range(Hkv):
+            at = (slice(b * n, (b + 1) * n), slice(h * G, (h + 1) * G))
+            qq, got = (x.view(-1, H, hd)[at].reshape(n * G, hd).double() for x in (q, out))
+            seen = torch.arange(L + 1, L + n + 1, device="cuda").repeat_interleave(G)
+            K, V, code, vs = cache.rows(b, h)
+            o, lim = _limit(qq, K, V, code, vs, seen, scale, q_err)
+            assert torch.isfinite(got).all()
+            over = ((got - o).abs() / lim.clamp_min(1e-200)).max().item()
+            worst = max(worst, over)
+            assert over <= 1.0, (b, h, L, over)
+            assert (o.abs() > lim).any(dim=1).all(), (b, h, "zeros would pass")
+            for t in lost:
+                if 128 * t + 128 > L:
+                    continue
+                keep = torch.ones(len(K), dtype=torch.bool, device="cuda")
+                keep[128 * t:128 * t + 128] = False
+                s = (qq @ K.T) * scale
+                s[:, ~keep] = -math.inf
+                s.masked_fill_(torch.arange(len(K), device="cuda")[None] >= seen[:, None], -math.inf)
+                p = torch.softmax(s, dim=1)
+                assert ((p @ V - o).abs() > lim).any(), (b, h, t, "an output without this tile would pass")
+    return worst
+
+
+# ------------------------------------------------------- small weights that count
+def _tail(hd, H, Hkv, T, B, where, nats, n, columns=0):
+    """One key `nats` above all others, which are alike: of B sequences each has it elsewhere.  By dimension (mod 8)
+    the others' values are 1, 1, 0, -1 / 16, 1 in every second slot, 2 in every 16th, 1 and -1 in turn, 0.5 in every
+    third, and its own 0 and then 1."""
+    t = torch.arange(64)
+    by = [1 + 0 * t, 1 + 0 * t, 0 * t, 0 * t - 1 / 16, t % 2, 2 * (t % 16 == 3), 1 - t % 2 * 2, 0.5 * (t % 3 == 1)]
+    k, v = torch.zeros(2, Hkv, 64, hd), torch.stack([x.double() for x in by], dim=1).repeat(2, Hkv, 1, hd // 8)
+    k[1, :, 17, 0] = 1.0
+    v[1, :, 17] = 1.0
+    v[1, :, 17, ::8] = 0.0
+    ones = torch.ones(2, Hkv, 4)
+    pages = []
+    for b in range(B):
+        p = np.zeros((T + n + 63) // 64, np.int64)
+        p[int(where[b % len(where)] * (T // 64 - 1))] = 1
+        pages.append(p)
+    c = Cache(hd, H, k, v, ones, ones, pages, [T - b for b in range(B)], n, columns)
+    q = torch.zeros(B * n, H, hd)
+    for m in range(B * n):
+        for h in range(H):
+            q[m, h, 0] = nats[(m + h) % len(nats)]
+    return c, q.to(torch.bfloat16).view(B * n, H * hd).cuda()
+
+
+@pytest.mark.parametrize("hd,H,Hkv,T,B,n,columns", [
+    (128, 8, 8, 131071, 20, 1, 0),     # a run of a whole context
+    (128, 8, 8, 131000, 1, 1, 0),      # runs of a cluster's CTAs, two groups each
+    (128, 4, 1, (1 << 20) - 2, 1, 2, 0),
+    (64, 16, 2, 33000, 80, 1, 0),
+    (128, 16, 1, 17000, 170, 2, 0),    # 32 rows
+    (128, 12, 1, 9000, 200, 2, 0),     # 24 rows
+    (128, 4, 1, 700, 2, 3, 0),
+    (64, 4, 1, 5000, 3, 2, 0),
+    (128, 8, 8, 16000, 20, 128, 0),    # many query rows
+])
+def test_one_strong_key_over_a_long_tail(hd, H, Hkv, T, B, n, columns):
+    """A tail whose weights are 2^-17 to 2^-23 of the strongest's, but half of the sum by their number."""
+    c, q = _tail(hd, H, Hkv, T, B, (0.0, 0.31, 0.77, 1.0), [8.0, 10.0, 12.0, 13.0, 13.5, 14.0, 16.0], n, columns)
+    out = c.run(q, scale=1.0)
+    _check(c, q, out, scale=1.0, q_err=2.0 ** -17 if n * H // Hkv > 64 else 2.0 ** -22)
+
+
+def test_a_strong_key_after_a_long_weak_run():
+    """The strongest key at the end of runs of growing weights, and of falling ones."""
+    hd, H, Hkv, T, n = 128, 8, 8, 40000, 1
+    for order in (1, -1):
+        steps = 40
+        k, v = torch.zeros(steps, Hkv, 64, hd), torch.zeros(steps, Hkv, 64, hd)
+        for i in range(steps):
+            k[i, :, :, i % 8] = 1.0
+            k[i, :, :, 8 + i // 8] = 1.0
+            v[i, :, :, i] = 1.0
+            v[i, :, :, 127] = 1.0
+        ones = torch.ones(steps, Hkv, 4)
+        per = T // 64 // steps
+        pages = np.repeat(np.arange(steps)[::order], per)
+        pages = [np.concatenate([pages, np.full((T + n + 63) // 64 - len(pages), pages[-1])])] * 20
+        c = Cache(hd, H, k, v, ones, ones, pages, [T] * 20, n)
+        q = torch.zeros(20 * n, H, hd)
+        q[:, :, :8] = torch.arange(8) * 1.5  # score 1.5 i, over 58 nats
+        q[:, :, 8:13] = torch.arange(5) * 12.0
+        for b in range(20):
+            q[b] *= (b % 5 + 1) / 8
+        q = q.to(torch.bfloat16).view(20 * n, H * hd).cuda()
+        _check(c, q, c.run(q, scale=1.0), scale=1.0)
