@@ -463,8 +463,8 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  *   d_anc  uint64 [batch][n] ancestor masks (spec_tree_masks; n <= 64), or
  *          NULL: token j sees the cached slots and new slots 0 .. j.
  *   scale  > 0, or 0 for 1/sqrt(head_dim).
- * Scores, softmax and sums are in fp32.  q is as given but for elements 2^-18
- * below its row's largest; a weight p is within 2^-11 of its value or, where
+ * Scores, softmax and sums are in fp32.  q is as given but for elements below
+ * 2^-13 of its row's largest, which may be off by 2^-21 of it; a weight p is within 2^-11 of its value or, where
  * p x v_scale is small, within 2^-19 of the largest such product in the row,
  * up or down by a pattern of the slot numbers: over a long context such errors
  * do not add up to more than about the root of their number.

@@ -9,8 +9,9 @@
 // cores as it is stored: both products are tcgen05.mma kind::f8f6f4 with e4m3
 // operands and fp32 accumulators in TMEM, so no key or value is ever
 // converted.  The other operand is split into e4m3 pieces that add up to it:
-//   q row = 2^k (hi + lo)            bf16 has 8 significant bits, a piece 4: exact but
-//                                    for elements 2^-18 below the row's largest
+//   q row = 2^k (hi + 2^-5 lo)       bf16 has 8 significant bits, a piece 4: exact for
+//                                    elements down to 2^-14 of the row's largest (at
+//                                    2^7 or more), below off by 2^-22 of it at most
 //   p     = hi + 2^-4 mid + 2^-8 lo  an fp16 weight's 11 bits, in steps of 2^-17 at the least
 // and the pieces lie side by side in the N dimension, so a tile of keys or
 // values is read from shared memory once whatever their number.
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
         const float a = odd ? 0.f : x[16 * c + 2 * k] * down, d = odd ? 0.f : x[16 * c + 2 * k + 1] * down;
         const uint32_t w = e4m3x2(a, d);
         const float2 f = e4m3x2_to_f32(w);
-        const uint32_t u = e4m3x2(a - f.x, d - f.y);
+        const uint32_t u = e4m3x2((a - f.x) * 32.f, (d - f.y) * 32.f);
         if (k & 1) {
           hi[k / 2] |= w << 16;
           lo[k / 2] |= u << 16;
@@ -556,8 +557,9 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
             const float4 c = *reinterpret_cast<const float4*>(sm.cq + r0 + r);
 #pragma unroll
             for (int q = 0; q < 4; q += 2) {
-              const float2 u = add2(make_float2(__uint_as_float(hi[r + q]), __uint_as_float(hi[r + q + 1])),
-                                    make_float2(__uint_as_float(lo[r + q]), __uint_as_float(lo[r + q + 1])));
+              const float2 u = fma2(make_float2(__uint_as_float(lo[r + q]), __uint_as_float(lo[r + q + 1])),
+                                    make_float2(0.03125f, 0.03125f),
+                                    make_float2(__uint_as_float(hi[r + q]), __uint_as_float(hi[r + q + 1])));
               const float2 x = fma2(mul2(u, ks2), q ? make_float2(c.z, c.w) : make_float2(c.x, c.y), lvs2);
               s[r0 + r + q] = x.x;
               s[r0 + r + q + 1] = x.y;

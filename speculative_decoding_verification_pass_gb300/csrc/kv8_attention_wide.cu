@@ -1,7 +1,7 @@
 // Attention over the 8-bit paged KV cache for many query rows (prefill chunks,
 // large trees): the same formulas as the kernel for few rows, but a tile is
 // 128 query rows x 128 keys with a row per softmax thread.
-//   S [128 rows][64 keys]   = (Q hi + Q lo) x K^T   kind::f8f6f4, K as stored
+//   S [128 rows][64 keys]   = (Q hi + Q lo) x K^T   kind::f8f6f4, K as stored, hi e4m3, lo e5m2
 //   O [128 rows][hd dims]  += P x V                 kind::f16, P from TMEM
 // With few rows a weight can afford three e4m3 pieces, since there the tile of
 // values is what costs.  With many the pieces cost, and it is cheaper to widen
@@ -76,6 +76,13 @@ SPEC_DEVINL void ld_wait(uint32_t (&a)[N]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
   ld_pin(a);
 }
+// Two fp32 values to two e5m2 codes (nearest), `a` in the low byte.
+SPEC_DEVINL uint32_t e5m2x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+constexpr uint32_t kIdescE5m2A = 1u << 7;  // instruction descriptor: operand A is e5m2
 SPEC_DEVINL float2 peer_f32x2(uint32_t a) {
   float2 v;
   asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a));
@@ -221,7 +228,10 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     return min(max(pg, 0), p.n_pages - 1);
   };
 
-  // ---- ... as e4m3 pieces, 2^k (hi + lo)
+  // ---- ... as pieces, 2^k (hi + lo).  What hi (4 bits) leaves of an element's 8 bits
+  // is a whole number of its last bit, 8 at most, which lo (3 bits) holds: exact for
+  // elements down to 2^-13 of the row's largest (at 2^7 or more), below off by e5m2's
+  // rounding of 2^-10 (half of hi's smallest step) or less, 2^-21 of the largest.
   if (tid < kSoftW) {
     // the row's largest magnitude, as bf16 bits: those order as integers, with
     // infinities and NaN (which make the row NaN) above all finite values
@@ -249,7 +259,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const float a = bf16lo(v[j]) * down, d = bf16hi(v[j]) * down;
         const uint32_t w = e4m3x2(a, d);
         const float2 f = e4m3x2_to_f32(w);
-        const uint32_t u = e4m3x2(a - f.x, d - f.y);
+        const uint32_t u = e5m2x2(a - f.x, d - f.y);
         hi[j / 2] = j & 1 ? hi[j / 2] | (w << 16) : w;
         lo[j / 2] = j & 1 ? lo[j / 2] | (u << 16) : u;
       }
@@ -299,7 +309,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 #pragma unroll
           for (int piece = 0; piece < 2; ++piece)
             umma_e4m3(ts + u * kHalf, aq + piece * (kRows * HD >> 4) + kk * 2, bk + kk * 2,
-                      idesc_e4m3(kRows, kHalf, false, false), kk + piece > 0 ? 1u : 0u);
+                      idesc_e4m3(kRows, kHalf, false, false) | (piece ? kIdescE5m2A : 0u), kk + piece > 0 ? 1u : 0u);
         umma_commit(&sm.s_full[g][u]);
         if (u) umma_commit(&sm.empty_k[i % S::kStages]);
       };
