@@ -202,11 +202,15 @@ class ModelConfig:
         return self.d_model // self.n_heads
 
     def c(self) -> spec_model_config:
-        """The C struct (made once: the fields do not change)."""
+        """A C struct of its own for each caller, who may change it."""
+        return spec_model_config(self.n_layers, self.d_model, self.n_heads, self.n_kv_heads,
+                                 self.d_ffn, self.vocab, self.rms_eps, self.rope_theta)
+
+    def _kept(self) -> spec_model_config:
+        """The C struct, made once, for calls that only read it and hand it to no one."""
         s = self.__dict__.get("_c")
         if s is None:
-            s = spec_model_config(self.n_layers, self.d_model, self.n_heads, self.n_kv_heads,
-                                  self.d_ffn, self.vocab, self.rms_eps, self.rope_theta)
+            s = self.c()
             object.__setattr__(self, "_c", s)
         return s
 
@@ -507,7 +511,7 @@ def spec_kv8_append(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, k, 
                         _rows(v, m, kv_width, dtype, "v"))
     with _on(dev):
         _check(lib().spec_kv8_append(
-            cfg.c(), kv.c(), layer, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
+            cfg._kept(), kv.c(), layer, n, q.data_ptr(), q_ld, k.data_ptr(), k_ld, v.data_ptr(), v_ld,
             dtype == torch.float32, _plain(depth, (kv.batch, n), torch.int32, "depth"), rope.config,
             rope.table.data_ptr(), _plain(q_out, (m, width), torch.bfloat16, "q_out"), ws.data_ptr(),
             _raw_stream(stream, dev)), "spec_kv8_append")
@@ -521,7 +525,7 @@ def spec_kv8_attention(cfg: ModelConfig, kv: "KV8Cache", layer: int, n: int, q, 
     q_ld, o_ld = _rows(q, m, width, torch.bfloat16, "q"), _rows(out, m, width, torch.bfloat16, "out")
     with _on(dev):
         _check(lib().spec_kv8_attention(
-            cfg.c(), kv.c(), layer, n, q.data_ptr(), q_ld, _plain(anc, (kv.batch, n), torch.int64, "anc"), scale,
+            cfg._kept(), kv.c(), layer, n, q.data_ptr(), q_ld, _plain(anc, (kv.batch, n), torch.int64, "anc"), scale,
             out.data_ptr(), o_ld, ws.data_ptr(), _raw_stream(stream, dev)), "spec_kv8_attention")
 
 
@@ -545,7 +549,7 @@ def spec_kv8_tree_commit(cfg: ModelConfig, kv: "KV8Cache", path, n_accepted, n_n
     dev = kv._device(cfg, path, n_accepted, ws)
     with _on(dev):
         _check(lib().spec_kv8_tree_commit(
-            cfg.c(), kv.c(), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
+            cfg._kept(), kv.c(), _plain(path, (kv.batch, n_nodes), torch.int32, "path"),
             _plain(n_accepted, (kv.batch,), torch.int32, "n_accepted"), n_nodes, ws.data_ptr(),
             _raw_stream(stream, dev)), "spec_kv8_tree_commit")
 

@@ -133,3 +133,15 @@ def test_refusals(lib):
     assert L.spec_rope_table(ctypes.byref(rope), P(4100), None) == E
     assert L.spec_rope_table(None, ok, None) == E
     assert L.spec_verify_forward_kv8(None, ok, None, None, 1, 5, _cache(lib), ok, ok, 1 << 30, None) == E
+
+
+def test_a_changed_struct_is_its_callers_own(lib):
+    """ModelConfig.c() may be edited: neither the config nor a later call sees it."""
+    cfg = lib.ModelConfig(32, 4096, 32, 8, 14336, 128256)
+    want = lib.spec_kv_bytes(cfg, 1, 64), lib.spec_kv8_workspace_bytes(cfg, 1, 5)
+    cfg._kept()
+    mine = cfg.c()
+    mine.n_layers = 2
+    assert cfg.c().n_layers == cfg._kept().n_layers == 32
+    assert (lib.spec_kv_bytes(cfg, 1, 64), lib.spec_kv8_workspace_bytes(cfg, 1, 5)) == want
+    assert lib.lib().spec_kv_bytes(ctypes.byref(mine), 1, 64) == want[0] // 16
