@@ -503,6 +503,8 @@ int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv,
  * spec_verify_forward_paged with spec_kv8_append and spec_kv8_attention in
  * each layer (q rounded once to bf16; the model's own rotary table).
  * Limits as spec_verify_forward but for the capacity, which is the cache's.
+ * The cache's buffers are those of the model's own shape (spec_kv8_bytes of its
+ * config): the call does not see their sizes.
  * Workspace: spec_kv8_workspace_bytes(cfg, batch, n). */
 size_t spec_kv8_workspace_bytes(const spec_model_config* cfg, int batch, int n);
 int spec_verify_forward_kv8(const spec_model* model, const int32_t* d_tokens,

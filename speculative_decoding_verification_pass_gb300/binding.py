@@ -224,15 +224,20 @@ def spec_model_weight_bytes(cfg: ModelConfig) -> int:
     return int(lib().spec_model_weight_bytes(ctypes.byref(cfg.c())))
 
 
+_MODELS: dict = {}  # handle of a live model -> (its config, its weights' device)
+
+
 def spec_model_create(cfg: ModelConfig, seed: int, weights: torch.Tensor, stream=None) -> int:
     h = _P()
     _check(lib().spec_model_create(ctypes.byref(cfg.c()), ctypes.c_uint64(seed), _ptr(weights),
                                    weights.numel() * weights.element_size(), _stream(stream),
                                    ctypes.byref(h)), "spec_model_create")
+    _MODELS[h.value] = cfg, weights.get_device()
     return h.value
 
 
 def spec_model_destroy(handle: int):
+    _MODELS.pop(handle, None)
     _check(lib().spec_model_destroy(handle), "spec_model_destroy")
 
 
@@ -560,10 +565,19 @@ def spec_kv8_workspace_bytes(cfg: ModelConfig, batch: int, n: int) -> int:
 
 def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cache", logits, ws, anc=None,
                             depth=None, stream=None):
-    """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth)."""
+    """The verification forward on the 8-bit cache (a chain, or a tree given by anc and depth).  The cache has the
+    layers and KV heads of the handle's model (spec_model_create's), and lies on its device."""
+    if handle not in _MODELS:
+        raise ValueError("expected the handle of a live model")
+    cfg, model_dev = _MODELS[handle]
+    rows = lambda c: (c.n_layers, c.n_kv_heads, c.head_dim)
+    if rows(cfg) != rows(kv.cfg):
+        raise ValueError(f"the cache was made for {kv.cfg}, the model is {cfg}")
     dev = kv._device(kv.cfg, tokens, logits, anc, depth, ws)
-    if logits.dtype != torch.float32 or logits.numel() != batch * n * kv.cfg.vocab:
-        raise ValueError(f"logits: expected a {(batch, n, kv.cfg.vocab)} {torch.float32} tensor")
+    if dev != model_dev:
+        raise ValueError(f"expected the cache on cuda:{model_dev}, the model's device")
+    if logits.dtype != torch.float32 or logits.numel() != batch * n * cfg.vocab:
+        raise ValueError(f"logits: expected a {(batch, n, cfg.vocab)} {torch.float32} tensor")
     with _on(dev):
         _check(lib().spec_verify_forward_kv8(
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),

@@ -145,3 +145,31 @@ def test_a_changed_struct_is_its_callers_own(lib):
     assert cfg.c().n_layers == cfg._kept().n_layers == 32
     assert (lib.spec_kv_bytes(cfg, 1, 64), lib.spec_kv8_workspace_bytes(cfg, 1, 5)) == want
     assert lib.lib().spec_kv_bytes(ctypes.byref(mine), 1, 64) == want[0] // 16
+
+
+def test_pass_refuses_another_models_cache(lib, monkeypatch):
+    """spec_verify_forward_kv8 compares the cache, the logits and the device with the handle's model before any
+    call of the library (which sees neither buffer's size)."""
+    shape = dict(n_layers=2, d_model=256, n_heads=4, n_kv_heads=2, d_ffn=256, vocab=1000)
+
+    def call(handle=77, model_dev=-1, vocab=1000, **cache):  # tensors of the CPU: device -1
+        kv = object.__new__(lib.KV8Cache)
+        object.__setattr__(kv, "cfg", lib.ModelConfig(**{**shape, **cache}))
+        object.__setattr__(kv, "len", torch.zeros(1, dtype=torch.int32))
+        object.__setattr__(kv, "pool", None)
+        monkeypatch.setitem(lib._MODELS, 77, (lib.ModelConfig(**shape), model_dev))
+        lib.spec_verify_forward_kv8(handle, torch.zeros(1, 3, dtype=torch.int32), 1, 3, kv,
+                                    torch.zeros(1, 3, vocab), torch.zeros(4096, dtype=torch.uint8))
+
+    def never():
+        raise AssertionError("a call of the library")
+
+    monkeypatch.setattr(lib, "lib", never)
+    for kw, match in ((dict(n_layers=1), "cache"), (dict(n_kv_heads=1), "cache"), (dict(n_kv_heads=4), "cache"),
+                      (dict(d_model=512), "cache"), (dict(n_layers=3), "cache"), (dict(vocab=999), "logits"),
+                      (dict(handle=78), "live model"), (dict(handle=None), "live model"),
+                      (dict(model_dev=1), "device")):
+        with pytest.raises(ValueError, match=match):
+            call(**kw)
+    with pytest.raises((AssertionError, RuntimeError)):  # nothing to refuse: on to the library
+        call()
