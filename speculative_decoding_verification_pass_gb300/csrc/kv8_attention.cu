@@ -39,9 +39,12 @@
 // are half of the row, while the sum of the p_j keeps them.  So a weight is rounded
 // up or down by a fixed pattern of slot numbers (slot_dither), and n errors add up
 // to about sqrt(n) of them.  Measured against rounding to nearest, batch 64 and 16:
-// the pattern (one addition for two weights) 51.7 to 52.4 us and 23.7 to 24.0; a
-// fourth piece 54.0 and 25.5; maxima at 2^4 and M set anew every 16 tiles 54.2 and
-// 24.9.
+// the pattern 51.7 to 52.1 us and 23.7 to 23.8; a fourth piece 54.0 and 25.5; maxima
+// at 2^4 and M set anew every 16 tiles 54.2 and 24.9.
+//
+// Why 11 bits: the output is bf16, 8 bits.  An error of 2^-12 of each weight moves it
+// by a small part of its own rounding, which falls the other way in a few percent of
+// the elements.
 //
 // After the softmax's four warps one issues the TMA loads of K, one those of V,
 // one the score MMAs and one the products: one thread for both of either kind had
@@ -95,7 +98,7 @@ constexpr int kPSpan = 32;                  // bytes of a key's row in one span 
 constexpr int kWideRows = 64, kWideWork = 448;
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
 constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
-constexpr float kLastStep = 7.62939453125e-06f;  // 2^-17, the last piece's smallest step
+constexpr float kLift = 4.f;                // exponents are kept this much higher: fp16 then holds small weights too
 
 // N columns of the thread's lane at each of two places, ready for use.
 template <int N>
@@ -132,13 +135,14 @@ SPEC_DEVINL uint32_t f16x2_to_e4m3x2(uint32_t a) {
   asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(a));
   return r;
 }
-// A number in [-1/2, 1/2) made of slot t by two rounds of multiply and xor-shift: in
-// any stretch of slots, and in every k'th of them, as evenly spread as random ones.
-SPEC_DEVINL float slot_dither(int t) {
+// Two fp16 numbers in [-1/2, 1/2) of the last piece's smallest step (2^-9), made of
+// slot t by two rounds of multiply and xor-shift: in any stretch of slots, and in
+// every k'th of them, as evenly spread as random ones.
+SPEC_DEVINL uint32_t slot_dither(int t) {
   uint32_t h = static_cast<uint32_t>(t) * 0x9E3779B1u;
   h = (h ^ (h >> 15)) * 0x85EBCA77u;
-  h ^= h >> 13;
-  return static_cast<float>(static_cast<int32_t>(h)) * 2.3283064365386963e-10f;  // 2^-32
+  h ^= h >> 15;
+  return f16x2_fma((h & 0x03FF03FFu) | 0x3C003C00u, 0x18001800u, 0x9A009A00u);  // ([1, 2) - 1.5) 2^-9
 }
 // ... and of chunk c of key i's row of P, which is cut into spans of 32 bytes
 // ([128 keys][32 bytes] each): three pieces of 24 rows then take 96 bytes a key
@@ -213,7 +217,7 @@ struct AttSmem {
     uint64_t s_full[2 * NG], s_free[2 * NG], p_full[2 * NG], o_full[2 * NG], drain[2 * NG];
     uint64_t anc[RT];
     alignas(16) float red[4 * NG][RT];   // per-warp maxima (sums at the end); this and the next two are read as float4
-    float mneg[4 * NG][RT];              // each warp's copy of -M
+    float mneg[4 * NG][RT];              // each warp's copy of kLift - M
     float cq[RT];                   // score factor of a row: 2^k scale log2(e)
     alignas(16) float stat[2][RT];  // this CTA's M and sum per row
     float part[NG][2][RT];          // ... a group's, and then the factor of its O
@@ -537,9 +541,10 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
         vs_n = scale_of(p.vs, pg1);
         pg1 = page_id(i + 2);
       }
+      const uint32_t dither2 = slot_dither(t);
       const bool none = t >= T;  // past the end: no scale to read
       const float lvs = none ? 0.f : static_cast<float>(static_cast<int>(__float_as_uint(vs) >> 23) - 127);
-      const float ivs = none ? 0.f : pow2_inv(vs);
+      const float ivs = none ? 0.f : pow2_inv(vs) * 0.0625f;  // (of weights that are 2^kLift too large)
       const bool masked = t0 + kTile > L;  // the tile holds slots that some row does not see
       const uint32_t vis = masked ? seen(t) : 0xFFFFFFFFu;
       mbar_wait(&sm.s_full[2 * g + buf], static_cast<uint32_t>((i >> 1) & 1), &sm.abort);
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
           for (int r = 0; r < RT; ++r) s[r] = (vis >> r) & 1u ? s[r] : -INFINITY;
         }
       };
-      const auto exponents = [&] {  // s - M, and the largest of them
+      const auto exponents = [&] {  // s - M + kLift, and the largest of them
         float top = -INFINITY;
 #pragma unroll
         for (int r = 0; r < RT; r += 4) {
@@ -625,7 +630,7 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
       }
       // ---- does any exponent pass the pieces' range?
       // (the first tile sets M)
-      if (i == 0 || named_bar_any(bar, kSoft, exponents() > kTopExp || *static_cast<volatile int*>(&sm.abort) != 0)) {
+      if (i == 0 || named_bar_any(bar, kSoft, exponents() > kTopExp + kLift || *static_cast<volatile int*>(&sm.abort) != 0)) {
         // raise M to each row's maximum (at 2^2); what is summed so far shrinks by alpha
         if (i && named_bar_any(bar + 1, kSoft, *static_cast<volatile int*>(&sm.abort) != 0)) {
           stopped = true;
@@ -641,7 +646,7 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
                                  fmaxf(sm.red[4 * g + 2][lane], sm.red[4 * g + 3][lane]));
           const float mn = fmaxf(mrun, mt - kStartExp);
           alpha = exp2f(mrun - mn);
-          sm.mneg[warp][lane] = -mn;
+          sm.mneg[warp][lane] = kLift - mn;
           mrun = mn;
         }
         __syncwarp();
@@ -671,25 +676,21 @@ __global__ void __launch_bounds__(32 * Warps<NG>::kAll, 3 - NG)
       tc_fence_before();
       mbar_arrive(&sm.s_free[2 * g + buf]);
       // ---- weights and their sums; P: this key's row, hi | mid | lo
-      // (added before the rounding to fp16, whose smallest step a long context can feel
-      // too; a weight of zero, plus less than half a step, stays zero)
-      const float dither = kLastStep * slot_dither(t);
-      const float2 dither2 = make_float2(dither, dither);
       uint32_t w[3][RT / 4];
 #pragma unroll
       for (int r = 0; r < RT; r += 2) {
         const float2 e = make_float2(exp2f(s[r]), exp2f(s[r + 1]));
         const float2 sum = fma2(e, make_float2(ivs, ivs), make_float2(l[r], l[r + 1]));
         l[r] = sum.x, l[r + 1] = sum.y;
-        // p = hi + mid / 16 + lo / 256, each the nearest e4m3 of what is left
-        // times 1, 16 and 256 (fp16 holds every difference exactly)
-        const float2 ed = add2(e, dither2);
-        const uint32_t f = f16x2(ed.x, ed.y);
-        const uint32_t u0 = f16x2_to_e4m3x2(f);
-        const uint32_t f1 = f16x2_fma(e4m3x2_to_f16x2(u0), 0xBC00BC00u, f);  // - hi
-        const uint32_t u1 = f16x2_to_e4m3x2(f16x2_mul(f1, 0x4C004C00u));     // x 16
-        const uint32_t f2 = f16x2_fma(e4m3x2_to_f16x2(u1), 0xAC00AC00u, f1); // - mid / 16
-        const uint32_t u2 = f16x2_to_e4m3x2(f16x2_mul(f2, 0x5C005C00u));     // x 256
+        // p = hi + mid / 16 + lo / 256, each the nearest e4m3 of what is left times 1, 16
+        // and 256 (f is 16 p; fp16 holds every difference exactly), the last with the
+        // slot's number added (zero plus half a step at the most stays zero)
+        const uint32_t f = f16x2(e.x, e.y);
+        const uint32_t u0 = f16x2_to_e4m3x2(f16x2_mul(f, 0x2C002C00u));            // / 16
+        const uint32_t f1 = f16x2_fma(e4m3x2_to_f16x2(u0), 0xCC00CC00u, f);        // - 16 hi
+        const uint32_t u1 = f16x2_to_e4m3x2(f1);
+        const uint32_t f2 = f16x2_fma(e4m3x2_to_f16x2(u1), 0xBC00BC00u, f1);       // - mid
+        const uint32_t u2 = f16x2_to_e4m3x2(f16x2_fma(f2, 0x4C004C00u, dither2));  // x 16
         w[0][r / 4] = r % 4 ? w[0][r / 4] | (u0 << 16) : u0;
         w[1][r / 4] = r % 4 ? w[1][r / 4] | (u1 << 16) : u1;
         w[2][r / 4] = r % 4 ? w[2][r / 4] | (u2 << 16) : u2;
