@@ -378,10 +378,16 @@ int spec_page_pool_free_pages(const spec_page_pool* pool);
  *                     of two in [2^-40, 2^40] per block of SPEC_KV8_BLOCK slots
  *                     and KV head;
  *   len, table        as there, 4-byte aligned.
- * The scale of a block is the smallest such power s with |x| <= 448 s for the
- * finite values of its rows (2^-40 where all are zero); larger values and
- * infinities are held as +-448 s, NaN as NaN.  The scales of blocks that hold
- * no row below len[b] are not read.  Limits: max_pages * 64 <= 2^20 slots, n_pages *
+ * The rows that an append writes to a block need the smallest such power s with
+ * |x| <= 448 s for their finite values (2^-40 where all are zero); larger values
+ * and infinities are held as +-448 s, NaN as NaN.  A block that holds rows
+ * already keeps its scale if that is larger, else its rows are re-rounded at the
+ * new one: values of 2^-6 s and more stay as they are, smaller ones go to steps of
+ * 2^-9 s.  A rollback leaves scales and codes as they are, so the small values of
+ * an accepted token's row may have been rounded for a larger row of a draft that
+ * was rejected: to that extent the cache depends on rejected drafts, which a bf16
+ * cache does not.  The scales of blocks
+ * that hold no row below len[b] are not read.  Limits: max_pages * 64 <= 2^20 slots, n_pages *
  * n_kv_heads * 64 < 2^31, batch <= 65535.  Every call below takes any
  * workspace of this library as d_ws (its status word is used) and works on
  * the current device; `cfg` gives the layer count and the head shape.
@@ -468,7 +474,9 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  * p x v_scale is small, within 2^-19 of the largest such product in the row,
  * up or down by a pattern of the slot numbers: over a long context such errors
  * do not add up to more than about the root of their number.
- * A score past fp32's range makes its row NaN.  A row that sees no slot (a mask
+ * A score above fp32's range makes its row NaN, one below it has no weight; where
+ * scale x the row's largest |q| x a k_scale passes that range by itself, the row
+ * is unspecified.  A row that sees no slot (a mask
  * with no bit of an empty cache) is zero.  Slots at or past len[b] + n and slots
  * a row does not see have no influence, whatever they hold; a NaN code that it
  * sees makes the row's affected outputs NaN, an infinite or NaN q its whole row.
@@ -476,7 +484,9 @@ int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int 
  * status bit; a page id outside the pool below len[b] sets SPEC_DEV_BAD_PAGE and
  * leaves its rows unspecified.  The same call gives the same bits; the order of a
  * row's sums and the size of its small weights' errors go by the batch, the
- * lengths and max_pages, by which the work is split. */
+ * lengths and max_pages, by which the work is split.  (The lengths are on the
+ * device, so kernel and split are chosen for the capacity: a context far below it
+ * can take up to ~1.2 times as long as in a table of its own width.) */
 int spec_kv8_attention(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
                        const uint16_t* d_q, int64_t q_ld, const uint64_t* d_anc, float scale,
                        uint16_t* d_o, int64_t o_ld, void* d_ws, void* stream);
@@ -501,7 +511,8 @@ int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv,
 /* spec_verify_forward on the 8-bit cache (chain: d_anc and d_depth NULL; tree:
  * both, n <= 64 nodes), n new tokens per sequence.  The per-step schedule of
  * spec_verify_forward_paged with spec_kv8_append and spec_kv8_attention in
- * each layer (q rounded once to bf16; the model's own rotary table).
+ * each layer (q rounded once to bf16; the model's own rotary table, half layout
+ * over the whole head: the other forms are for layers put together by hand).
  * Limits as spec_verify_forward but for the capacity, which is the cache's.
  * The cache's buffers are those of the model's own shape (spec_kv8_bytes of its
  * config): the call does not see their sizes.

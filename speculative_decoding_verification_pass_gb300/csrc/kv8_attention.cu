@@ -42,9 +42,9 @@
 // the pattern 51.7 to 52.1 us and 23.7 to 23.8; a fourth piece 54.0 and 25.5; maxima
 // at 2^4 and M set anew every 16 tiles 54.2 and 24.9.
 //
-// Why 11 bits: the output is bf16, 8 bits.  An error of 2^-12 of each weight moves it
-// by a small part of its own rounding, which falls the other way in a few percent of
-// the elements.
+// Why 11 bits: the output is bf16, 8 bits.  Errors of 2^-11 of the weights at the most
+// move it by a small part of its own rounding, which falls the other way in a few
+// percent of the elements; two fp16 values a weight would double the pieces.
 //
 // After the softmax's four warps one issues the TMA loads of K, one those of V,
 // one the score MMAs and one the products: one thread for both of either kind had
@@ -63,14 +63,14 @@
 // What bounds it, with what it measured (152 SMs; 32 query heads on 8 KV heads,
 // head dim 128 and 5 tokens a sequence unless it says otherwise; device time of
 // a launch inside a graph):
-//   64 sequences, 309 MB of cache: 51 us, 6.0 TB/s; in its loop it runs at the
+//   64 sequences, 309 MB of cache: 52 us, 5.9 TB/s; in its loop it runs at the
 //     copy bandwidth, the rest is the second wave's prologue and the tail
-//   16 sequences, 77 MB: 23.5 us, 3.3 TB/s; ~7 us of setup and end, and tiles
+//   16 sequences, 77 MB: 24 us, 3.2 TB/s; ~7 us of setup and end, and tiles
 //     that do not divide evenly over the SMs
 //   1 sequence of 131000 slots: 1 token 44.6 us, 6.0 TB/s, 5 tokens 57 us; 12 CTAs
 //     for each of the 8 KV heads, so 96 of the SMs take part (a cluster lies
 //     within a group of SMs, and 8 of 16 do not fit at once)
-//   1 sequence of 2048: 8.2 us, the latency of one tile, the merge and a launch
+//   1 sequence of 2048: 8.4 us, the latency of one tile, the merge and a launch
 //   1 sequence x 32 tokens at 4000 slots: 15.3 us; the softmax threads' chain,
 //     with conversions to e4m3 at a quarter rate (for more rows: the other kernel)
 #include "kv8_attn.cuh"
@@ -94,7 +94,8 @@ constexpr int kPSpan = 32;                  // bytes of a key's row in one span 
 // 1 x 96 (792) 29.6 / 19.2, 1 x 128 (1056) 31.5 / 22.1, 16 x 32 (4096) 75 / 51,
 // 4 x 64 at 700 (384) 13.6 / 15.4, 4 x 128 at 700 (896) 25.7 / 16.7, head dim 64
 // 4 x 32 at 1900 (480) 15.5 / 12.1; 64 rows a head: 16 x 16 tokens 45 / 50,
-// 64 x 16 141 / 149.
+// 64 x 16 141 / 149.  (Capacity and not length, which the host does not know: the
+// 4 x 64 tokens at 700 slots in a table of 32768 take the other kernel and 15.1 us.)
 constexpr int kWideRows = 64, kWideWork = 448;
 constexpr float kTopExp = 8.75f;            // 2^8.75 < 448: weights that fit e4m3
 constexpr float kStartExp = 2.f;            // exponent of a row's maximum where M is set
@@ -901,7 +902,9 @@ cudaError_t launch_tile(const Kv8AttnParams& p, cudaStream_t stream) {
   // Two groups a CTA where every CTA has an SM to itself and four tiles or more at
   // full capacity.  One group / two in us, 8 KV heads: 1 token at 131000 slots 51.4
   // / 44.6, 5 tokens 75.6 / 57.1, at 16000 16.8 / 15.0; with two tiles a CTA, 5
-  // tokens at 2048 8.4 / 9.1, one KV head at 4000 8.0 / 9.1.
+  // tokens at 2048 8.4 / 9.1, one KV head at 4000 8.0 / 9.1.  Short contexts in wide
+  // tables take the two groups too: 2 x 5 tokens at 300 slots 7.2 us in a table of 320
+  // slots, 8.4 in one of 32768; 1 token at 8000 9.1 and 8.2.
   if constexpr (NG == 1) {
     const int tiles = (p.max_pages * kPageSlots + kTile - 1) / kTile;
     if (static_cast<long long>(p.B) * p.Hkv * rtiles * c <= s.sms && tiles >= 4 * c)

@@ -7,7 +7,8 @@
 // values is what costs.  With many the pieces cost, and it is cheaper to widen
 // the values once a tile, e4m3 to fp16 (exact), for all 128 rows: four warps do
 // that, straight from global memory into a swizzled tile.  A weight is then one
-// fp16, with the 11 bits that the three pieces hold.
+// fp16, with the 11 bits that the three pieces hold (why so few: there), rounded to
+// nearest: where the row's largest is 2^4 or more, the smallest step is 2^-28 of it.
 //   p'_j = 2^(s_j + log2 vs_j - M),  l = sum over blocks of (sum of p'_j) / vs
 // A block's 16 keys are 16 neighbouring columns, so its two scales enter as the
 // two constants of one multiply-add per score.  M is a row's own (one thread

@@ -3,9 +3,10 @@
 //
 // A cached row is code x scale: the codes are e4m3, the scale a power of two
 // shared by a block of kKv8Block slots of one KV head.  A power of two makes
-// code x scale and every change of scale exact but for e4m3 subnormals, so a
-// block can be re-rounded when a later row needs a larger scale without
-// losing bits a second time.
+// code x scale exact, and every change of scale for values that stay normal e4m3
+// numbers, which a larger scale for a later row then leaves as they are; values
+// that become subnormal (below 2^-6 of the new scale) are rounded again at each
+// growth and each move.
 #pragma once
 
 #include "common.cuh"

@@ -1,7 +1,7 @@
 """Accuracy of the 8-bit cache's attention: limits that a wrong output does not pass.
 
-Every limit is made per row and dimension from the fp64 weights, so it shrinks with the outputs as contexts grow,
-and each case shows that an output of zeros and one with a single tile of keys left out lie beyond it.
+Every limit is made per row and dimension from the fp64 weights, so it shrinks with the outputs as contexts grow;
+each case shows that an output of zeros lies beyond it, and those of long contexts an output without one tile of keys.
 With P_j = p_j vs_j, in units of the row's sum of weights:
 
 * o is bf16: half a step, 2^-8 |o|;
@@ -24,8 +24,10 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import kv8 as O8
 from speculative_decoding_verification_pass_gb300 import binding as sb
 from speculative_decoding_verification_pass_gb300 import workloads as wl
+from test_gpu_kv8 import _close_code
 
 pytestmark = pytest.mark.gpu
 
@@ -284,3 +286,60 @@ def test_trees_in_long_contexts(hd, H, Hkv, lens, n, columns):
     _check(c, q, out, lost=(0, 3, -1), see=see)
     for b, L in enumerate(lens):
         assert L or (out[b * n] == 0).all()
+
+
+# ------------------------------------------------------------ rows held while scales grow
+def test_rows_held_while_a_scale_grows():
+    """Rows of one block appended one by one, each larger: codes and scales are the oracle's, and a row is off by
+    its own rounding and at most half of each later scale's smallest step."""
+    hd, H, Hkv = 64, 4, 2
+    cfg = sb.ModelConfig(1, hd * H, H, Hkv, 128, 1000)
+    kv, ws = sb.KV8Cache(cfg, 1, 1, 1), sb.workspace(256)
+    kv.table.zero_()
+    R = sb.RopeTable(hd, 1e4)
+    g = torch.Generator().manual_seed(81)
+    want, slack, rows = O8.Rows(Hkv, 64, hd), np.zeros((Hkv, 64, 1)), []
+    for t in range(20):
+        x = torch.randn(1, Hkv * hd, generator=g) * 2.0 ** (1.5 * (t % 16))
+        q = torch.zeros(1, H * hd)
+        sb.spec_kv8_append(cfg, kv, 0, 1, q.cuda(), torch.zeros(1, Hkv * hd).cuda(), x.cuda(), R,
+                           torch.empty(1, H * hd, dtype=torch.bfloat16, device="cuda"), ws)
+        sb.spec_kv8_advance(kv, 1, ws)
+        rows.append(x.double().numpy().reshape(Hkv, hd))
+        old = want.scale[:, t // 16].copy()
+        want.append(t, rows[-1][None])
+        grown = want.scale[:, t // 16] > old
+        slack[:, t // 16 * 16:t] += np.where(grown, want.scale[:, t // 16] / 1024, 0.0)[:, None, None]
+        code = O8.e4m3_of_byte(kv.v.view(torch.uint8)[0, 0].cpu().numpy())
+        scale = kv.v_scale[0, 0].double().cpu().numpy()
+        blocks = t // 16 + 1
+        np.testing.assert_array_equal(scale[:, :blocks], want.scale[:, :blocks])
+        np.testing.assert_array_equal(code[:, :t + 1], want.code[:, :t + 1])
+        _close_code(code[:, :t + 1], scale, np.stack(rows, axis=1), slack[:, :t + 1])
+    assert sb.spec_device_status(ws) == (sb.SPEC_OK, 0)
+
+
+# ------------------------------------------------------------- scores past fp32's range
+@pytest.mark.parametrize("hd,H,Hkv,n,columns", [(128, 8, 1, 2, 0), (64, 4, 2, 1, 600), (128, 4, 1, 40, 1400)])
+def test_scores_past_the_range(hd, H, Hkv, n, columns):
+    """A score above fp32's range makes the rows that see it NaN; one below it is a key of no weight."""
+    for sign in (1, -1):
+        g = torch.Generator().manual_seed(91)
+        k, v = torch.zeros(4, Hkv, 64, hd), torch.randn(4, Hkv, 64, hd, generator=g).to(E4M3)
+        k[2, :, 21] = 448.0 * sign
+        ks, vs = torch.full((4, Hkv, 4), 2.0 ** 30), torch.ones(4, Hkv, 4)
+        c = Cache(hd, H, k, v, ks, vs, [[0, 1, 2, 3], [3, 0, 1, 1]], [150, 30], n, columns)
+        q = torch.full((2 * n, H * hd), 2.0 ** 90, dtype=torch.bfloat16, device="cuda")
+        out = c.run(q).view(2, n, H, hd).double()
+        if sign > 0:
+            assert torch.isnan(out[0]).all()
+        for b in range(2):
+            if b == 0 and sign > 0:
+                continue
+            for h in range(H):
+                _, V, _, _ = c.rows(b, h // (H // Hkv))
+                for j in range(n):
+                    seen = torch.arange(c.lens[b] + j + 1, device="cuda")
+                    o = V[seen[seen != 2 * 64 + 21] if b == 0 else seen].mean(0)
+                    lim = 2.0 ** -8 * o.abs() + 2.0 ** -10 * V.abs().mean(0)
+                    assert ((out[b, j, h] - o).abs() <= lim).all()
