@@ -1,8 +1,6 @@
 // The C ABI declared in include/spec_verify.h: argument validation, the
 // weight and workspace layouts, TMA descriptors and the launch sequence of
 // one verification pass.  No device memory is allocated here.
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdlib>
@@ -14,6 +12,24 @@
 #include "internal.h"
 
 using namespace spec;
+
+namespace spec {
+
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+}  // namespace spec
 
 namespace {
 
@@ -157,24 +173,10 @@ Layout layout_of(const spec_model_config& c) {
   return L;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  });
-  return fn;
-}
-
 // 2-D bf16 [rows][cols] row-major, box = box_rows x 64 columns, 128-byte swizzle;
 // rows outside the tensor read as zero.
 bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
-  auto fn = encode_fn();
+  auto fn = tmap_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {cols, rows};
   cuuint64_t strides[1] = {cols * 2};
@@ -189,7 +191,7 @@ bool make_tmap(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, u
 // q (or its lo half) as a 3-D tensor [M tokens][H heads][hd]: a box of 64
 // dimensions x G heads x 32 / G tokens is 32 attention rows (token-major).
 bool make_tmap_q(CUtensorMap* m, const void* base, uint64_t M, uint64_t H, uint64_t hd, uint32_t G) {
-  auto fn = encode_fn();
+  auto fn = tmap_encoder();
   if (!fn || G == 0 || 32 % G) return false;
   cuuint64_t dims[3] = {hd, H, M};
   cuuint64_t strides[2] = {hd * 2, H * hd * 2};
@@ -418,7 +420,7 @@ int spec_model_create(const spec_model_config* cfg, uint64_t seed, void* d_weigh
   cudaDeviceProp prop;
   SPEC_CUDA(cudaGetDeviceProperties(&prop, dev));
   if (prop.major != 10 || prop.minor != 3) return SPEC_ENOTSUP;
-  if (!encode_fn()) return SPEC_ENOTSUP;
+  if (!tmap_encoder()) return SPEC_ENOTSUP;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const spec_model_config& c = *cfg;
   auto* m = new spec_model();

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -12,6 +13,9 @@
 #include "spec_verify.h"
 
 namespace spec {
+
+// The driver's cuTensorMapEncodeTiled, looked up once (nullptr if it has none).
+PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder();
 
 // One value per device, made once per device by the first call with that
 // device current.  CUDA keeps function attributes (e.g. the dynamic shared

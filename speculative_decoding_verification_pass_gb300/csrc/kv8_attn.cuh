@@ -3,8 +3,6 @@
 // the host the tensor maps and the launch's clusters.
 #pragma once
 
-#include <cudaTypedefs.h>
-
 #include <algorithm>
 #include <climits>
 
@@ -259,19 +257,6 @@ SPEC_DEVINL void att_load_tiles(const CUtensorMap* map, uint64_t* full, uint64_t
 }
 
 // ------------------------------------------------------------------ host
-PFN_cuTensorMapEncodeTiled_v12000 tmap_encoder() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 // One layer's codes as [rows][hd] bytes, boxes of one page of one head (64 rows).
 bool page_map(CUtensorMap* m, const void* codes, long long rows, int hd) {
   const auto fn = tmap_encoder();
