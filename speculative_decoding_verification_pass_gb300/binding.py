@@ -570,7 +570,7 @@ def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cac
     if handle not in _MODELS:
         raise ValueError("expected the handle of a live model")
     cfg, model_dev = _MODELS[handle]
-    rows = lambda c: (c.n_layers, c.n_kv_heads, c.head_dim)
+    rows = lambda c: (c.n_layers, c.n_kv_heads, c.d_model // max(c.n_heads, 1))
     if rows(cfg) != rows(kv.cfg):
         raise ValueError(f"the cache was made for {kv.cfg}, the model is {cfg}")
     dev = kv._device(kv.cfg, tokens, logits, anc, depth, ws)

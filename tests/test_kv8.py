@@ -173,3 +173,13 @@ def test_pass_refuses_another_models_cache(lib, monkeypatch):
             call(**kw)
     with pytest.raises((AssertionError, RuntimeError)):  # nothing to refuse: on to the library
         call()
+
+
+def test_pass_refuses_a_model_without_layers(lib, monkeypatch):
+    """The handle of an LM head alone has no heads to compare."""
+    kv = object.__new__(lib.KV8Cache)
+    object.__setattr__(kv, "cfg", lib.ModelConfig(2, 256, 4, 2, 256, 1000))
+    object.__setattr__(kv, "pool", None)
+    monkeypatch.setitem(lib._MODELS, 77, (lib.ModelConfig(0, 256, 0, 0, 0, 1000), -1))
+    with pytest.raises(ValueError, match="cache"):
+        lib.spec_verify_forward_kv8(77, None, 1, 3, kv, None, None)
