@@ -379,19 +379,24 @@ class KV8Cache:
     """8-bit paged target cache: k, v e4m3 [layers][n_pages][Hkv][64][hd] with
     power-of-two scales fp32 [layers][n_pages][Hkv][4] (one per 16 slots), len
     int32 [B], the device page table int32 [B][max_pages], and a host page
-    pool as in PagedKVCache."""
+    pool as in PagedKVCache.  Codes and scales that are given are taken as they
+    lie, the others allocated (on the device of k, if that is given)."""
 
-    def __init__(self, cfg: ModelConfig, batch: int, n_pages: int, max_pages: int, device="cuda"):
+    def __init__(self, cfg: ModelConfig, batch: int, n_pages: int, max_pages: int, device="cuda", k=None, v=None,
+                 k_scale=None, v_scale=None):
         self.cfg, self.batch, self.n_pages, self.max_pages = cfg, batch, n_pages, max_pages
+        self.pool = None
         shape = (cfg.n_layers, n_pages, cfg.n_kv_heads, PAGE_SLOTS, cfg.head_dim)
-        self.k = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
-        self.v = torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
-        self.k_scale = torch.ones(shape[:3] + (PAGE_SLOTS // KV8_BLOCK,), dtype=torch.float32, device=device)
-        self.v_scale = torch.ones_like(self.k_scale)
+        device = device if k is None else k.device
+        codes = lambda: torch.zeros(shape, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+        scales = lambda: torch.ones(shape[:3] + (PAGE_SLOTS // KV8_BLOCK,), dtype=torch.float32, device=device)
+        self.k = codes() if k is None else k
+        self.v = codes() if v is None else v
+        self.k_scale = scales() if k_scale is None else k_scale
+        self.v_scale = scales() if v_scale is None else v_scale
         assert self.k.numel() == int(lib().spec_kv8_bytes(ctypes.byref(cfg.c()), n_pages))
         self.len = torch.zeros(batch, dtype=torch.int32, device=device)
         self.table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
-        self.pool = None
         h = ctypes.c_void_p()
         _check(lib().spec_page_pool_create(n_pages, batch, max_pages, ctypes.byref(h)),
                "spec_page_pool_create")

@@ -1338,3 +1338,36 @@ def test_forward_of_a_large_batch_and_refusals():
                                    anc=torch.zeros(B, n, dtype=torch.int64, device="cuda"))
     assert e.value.status == sb.SPEC_EINVAL
     m.close()
+
+
+def test_cache_of_given_buffers():
+    """Codes and scales of the caller's own are the cache's, without a second allocation; others are refused."""
+    cfg = sb.ModelConfig(2, 256, 4, 2, 256, 1000)
+    B, pages = 2, 2000
+    whole = torch.zeros(2, 2, pages, 2, 64, 64, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    scale = torch.ones(2, 2, pages, 2, 4, device="cuda")
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    before = torch.cuda.memory_allocated()
+    given = dict(k=whole[0], v=whole[1], k_scale=scale[0], v_scale=scale[1])
+    kv = sb.KV8Cache(cfg, B, pages, 3, **given)
+    assert torch.cuda.max_memory_allocated() - before < 1 << 16
+    assert all(getattr(kv, name).data_ptr() == t.data_ptr() for name, t in given.items())
+    other = sb.KV8Cache(cfg, B, pages, 3, v=whole[1])
+    assert other.v.data_ptr() == kv.v.data_ptr() and other.k.data_ptr() != kv.k.data_ptr()
+    m = sb.Model(cfg, 48)
+    ws = sb.workspace(sb.spec_kv8_workspace_bytes(cfg, B, 5))
+    toks = _dev(wl.tokens(48, B, 5, cfg.vocab))
+    z = torch.empty(2, B, 5, cfg.vocab, device="cuda")
+    for c, out in ((kv, z[0]), (sb.KV8Cache(cfg, B, pages, 3), z[1])):
+        for b in range(B):
+            c.reserve(b, 64)
+        c.sync()
+        sb.spec_verify_forward_kv8(m.handle, toks, B, 5, c, out, ws)
+    assert _status(ws) == (sb.SPEC_OK, 0) and torch.equal(z[0], z[1])
+    assert (whole.view(torch.uint8) != 0).any()
+    for bad in (dict(k=whole[0, :1]), dict(k=whole[0].view(torch.uint8)), dict(v=whole[1].cpu()),
+                dict(k_scale=scale[0].double()), dict(v_scale=scale[:, 0].transpose(1, 2)), dict(k=whole[:, :, :, 0])):
+        with pytest.raises(ValueError):
+            sb.KV8Cache(cfg, B, pages, 3, **bad)
+    m.close()
