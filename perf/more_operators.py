@@ -199,11 +199,12 @@ def _page_inputs(case, seed):
         r.shuffle(ids)
         held, all_lens, src, dst = [], [], [], []
         for i in range(G):
+            first = len(held)
             held.append(ids[: need[i]])
             ids = ids[need[i]:]
             all_lens.append(lens[i])
             for _ in range(W - 1):
-                src.append(len(held) - 1 - len(held) % W)
+                src.append(first)
                 dst.append(len(held))
                 held.append([])
                 all_lens.append(0)
