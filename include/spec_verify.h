@@ -75,6 +75,9 @@ typedef enum {
 #define SPEC_DEV_BAD_TREE      0x20  /* tree accept / commit: bad parents, path or n_accepted */
 #define SPEC_DEV_EMPTY_MASK    0x40  /* mask_logits: a row's mask allows no token */
 #define SPEC_DEV_BAD_PAGE      0x80  /* paged cache: a page id outside [0, n_pages) */
+#define SPEC_DEV_BAD_PARAM     0x100 /* sampling: a row's parameter outside its range */
+#define SPEC_DEV_BAD_SEQ       0x200 /* page pool: a sequence outside [0, batch), or a fork's order would matter */
+#define SPEC_DEV_NO_PAGES      0x400 /* page pool: a reservation that the free pages did not cover */
 
 /* Text for a spec_status value (static storage). */
 const char* spec_status_string(int status);
@@ -293,6 +296,66 @@ int spec_draft_sample(const float* d_logits, int rows, int vocab, float temperat
  * and is a rejection (SPEC_DEV_Q_ZERO). */
 int spec_mask_logits(float* d_logits, const uint32_t* d_allowed, int rows, int vocab, void* d_ws,
                      void* stream);
+
+/* ----------------------------------------------------- truncated sampling */
+/* Sampling parameters by row, applied in this order, each on what the one
+ * before leaves: temperature T, min-p, top-k, top-p.  With M the row's largest
+ * logit and w(x) = exp((z(x) - M) / T):
+ *   min_p  in [0, 1], 0 = off: keeps p(x) >= min_p * the largest p, that is
+ *          z(x) >= M + T ln min_p;
+ *   top_k  0 = off: keeps every logit not below the k-th largest;
+ *   top_p  in (0, 1], 1 = off: of what these leave, keeps every logit not below
+ *          the one where the descending cumulative weight first reaches top_p
+ *          of their total (spec_accept's rule).
+ * So a row is cut at one logit, ties included.  T = 0 keeps the largest logit's
+ * lowest id alone.  NaN counts as -inf, and a token at -inf is never kept; where
+ * a logit is +inf, only those are.
+ * The arrays (device, one value a set, 4-byte aligned) go before the scalars
+ * where they are given; row r belongs to set r / rows_per_set (1: a set a row;
+ * gamma + 1: a set a sequence of a verification's rows). */
+typedef struct {
+  float temperature;
+  int top_k;
+  float top_p;
+  float min_p;
+  const float* d_temperature;
+  const int32_t* d_top_k;
+  const float* d_top_p;
+  const float* d_min_p;
+  int rows_per_set;
+} spec_sampling;
+
+/* Draw n_draws tokens (1 to 64) from each row: independent draws of one
+ * distribution, such as a draft tree's siblings or parallel continuations.
+ *   d_logits    fp32, or bf16 with is_bf16 != 0, rows ld elements apart (any
+ *               alignment of the element; rows that are 16-byte aligned are read
+ *               faster);
+ *   d_uniforms  fp32 [rows][n_draws] in [0, 1); others are taken as the nearest
+ *               such value, NaN as 0;
+ *   d_tokens    int32 [rows][n_draws]: the smallest id whose cumulative weight, in
+ *               id order, exceeds u * total;
+ *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
+ *               (spec_accept's d_draft_probs).
+ * Weights are summed in fixed point, exactly and in any order: a weight is off by
+ * about 2^-27 of itself and by 2^-36 of the row's largest (2^-34 above 131072 ids), and what
+ * is below that is not drawn; probabilities are off by a few fp32 roundings.  The
+ * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
+ * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and
+ * SPEC_DEV_BAD_PARAM.  Limits: rows <= 65535, vocab <= 262144.  d_ws: any
+ * workspace of this library (its status word is used). */
+int spec_sample(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab, const spec_sampling* sampling,
+                const float* d_uniforms, int n_draws, int32_t* d_tokens, float* d_probs, int64_t probs_ld, void* d_ws,
+                void* stream);
+
+/* The same truncation as -inf in the logits: d_out[r][x] = d_logits[r][x] where x
+ * is kept, else -inf (both of one type; d_out may be d_logits with out_ld = ld).
+ * Applied to the target's rows before spec_accept or spec_tree_accept (with the
+ * same T, and top_p 1), whose drafts were drawn by spec_sample with the same
+ * parameters: the truncation then is the same on both sides.  A row without a
+ * logit above -inf, or with a set out of range, is copied (NaN as -inf) and sets
+ * the status bit as above. */
+int spec_filter_logits(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab,
+                       const spec_sampling* sampling, void* d_out, int64_t out_ld, void* d_ws, void* stream);
 
 /* --------------------------------------------------------------- rollback */
 /* KV rollback after a pass that appended gamma+1 slots ([engine] Rollback
@@ -522,6 +585,86 @@ int spec_verify_forward_kv8(const spec_model* model, const int32_t* d_tokens,
                             const uint64_t* d_anc, const int32_t* d_depth, int batch, int n,
                             const spec_kv8_cache* kv, float* d_logits, void* d_ws,
                             size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------- device page pool */
+/* The page pool of a paged cache (bf16 or 8-bit) on the device, in place of the
+ * host's: sequences can share pages, and rounds run without the host knowing the
+ * lengths.  All arrays are the caller's; table and len are the cache's own:
+ *   table   int32 [batch][max_pages]: a page, -1 (none), or -2 - page: a page that
+ *           is held but not to be written to (see spec_pages_fork);
+ *   len     int32 [batch];
+ *   mapped  int32 [batch]: pages that a sequence holds, a prefix of its row;
+ *   ref     int32 [n_pages]: sequences that hold a page, 0 = free;
+ *   n_free  int32 [1]: free pages.
+ * Limits: batch <= 65535, max_pages * 64 <= 2^20 slots, n_pages * n_kv_heads * 64
+ * < 2^31.  Calls on one pool are made on one stream, or ordered by the caller. */
+typedef struct {
+  int32_t* table;
+  int32_t* len;
+  int32_t* mapped;
+  int32_t* ref;
+  int32_t* n_free;
+  int batch;
+  int n_pages;
+  int max_pages;
+} spec_pages;
+
+/* The pages themselves: k and v of spec_paged_kv_cache (both scales NULL) or
+ * codes and scales of spec_kv8_cache. */
+typedef struct {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int n_pages;
+} spec_page_data;
+
+/* Workspace of the calls below but spec_pages_init and spec_pages_copy (which
+ * takes any workspace of this library); its first word is the status word. */
+size_t spec_pages_workspace_bytes(int batch, int n_pages, int max_pages);
+
+/* Every page free, every sequence empty (len 0). */
+int spec_pages_init(const spec_pages* pages, void* stream);
+
+/* Before a pass of n tokens a sequence (d_n int32 [batch], or NULL: n for each):
+ * a sequence returns its pages past len[b], then takes those that slots [len[b],
+ * len[b] + n) need, the lowest-numbered free ones, by sequence and then by
+ * position.  A partly filled page that others hold is replaced by a copy of its
+ * len[b] % 64 slots; where every holder is about to write to it, the longest of
+ * them (the lowest-numbered of equally long ones) keeps it.  n = 0 only returns
+ * pages (after a rollback).  A sequence that the free pages do not cover keeps
+ * the pages of its length alone, sets SPEC_DEV_NO_PAGES, and is not to be
+ * written to: passes refuse it (SPEC_DEV_BAD_PAGE).  One past the capacity, or
+ * with pages that are not of the pool, is left as it is (SPEC_DEV_KV_OVERFLOW,
+ * SPEC_DEV_BAD_PAGE). */
+int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
+                       const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream);
+
+/* Sequence d_dst[i] becomes a second d_src[i], i < n <= 65535: it returns its pages and
+ * shares the source's up to its length.  Nothing is copied until one of them is
+ * reserved for; a partly filled last page is marked in both rows as not to be
+ * written to until then.  Pairs out of range, to itself, with a destination
+ * given twice or one that is a source too, are left out (SPEC_DEV_BAD_SEQ). */
+int spec_pages_fork(const spec_pages* pages, int n, const int32_t* d_src, const int32_t* d_dst, void* d_ws,
+                    size_t ws_bytes, void* stream);
+
+/* Sequences d_seq[i] return all their pages and have length 0 (one given twice
+ * does so once). */
+int spec_pages_free(const spec_pages* pages, int n, const int32_t* d_seq, void* d_ws, size_t ws_bytes, void* stream);
+
+/* Move the used pages numbered at or above their own number U, in order, to the
+ * free ones below U, in every layer, and rewrite the tables: afterwards pages
+ * [U, n_pages) are free (U = n_pages - n_free). */
+int spec_pages_compact(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, void* d_ws,
+                       size_t ws_bytes, void* stream);
+
+/* Copy whole pages d_src[i] of one cache to pages d_dst[i] of another or of the
+ * same, i < n <= its pages, in every layer: a prefix handed to another pool, say.
+ * Destinations are distinct and no source is one (of the same cache); pairs
+ * outside the caches set SPEC_DEV_BAD_PAGE and are left out.  Counts and tables
+ * are the caller's matter. */
+int spec_pages_copy(const spec_model_config* cfg, const spec_page_data* from, const spec_page_data* to, int n,
+                    const int32_t* d_src, const int32_t* d_dst, void* d_ws, void* stream);
 
 /* ------------------------------------------------------------ draft trees */
 /* Verification of a draft TREE instead of a chain ([aci] Tree-Based Drafting;

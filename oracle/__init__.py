@@ -23,6 +23,9 @@ constrain -- constrained acceptance: one allowed-token mask applied to the
             target and draft logits alike.
 gamma    -- the dynamic speculation-depth controller (rolling acceptance
             window, depth maximising expected tokens per millisecond).
+sample   -- truncated sampling by row: min-p, top-k, top-p, the draws.
+pool     -- the device page pool's books: holders, forks, copies before a
+            write, compaction.
 
 Every function cites the passage it follows.  Parity status per function:
 
@@ -51,4 +54,9 @@ Every function cites the passage it follows.  Parity status per function:
 * constrain.apply_mask         pinned (restricted-softmax closed form,
                                chi-square and acceptance rate with the same
                                mask on both sides, one-sided mask breaks it)
+* sample.*                     pinned (top-p alone equals accept's nucleus;
+                               enumeration of small rows; draws counted over
+                               a grid of uniforms)
+* pool.*                       pinned (contents of the sequences kept through
+                               random calls; counts equal to the tables)
 """

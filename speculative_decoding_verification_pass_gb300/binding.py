@@ -23,6 +23,7 @@ DEV_BAD_TOKEN, DEV_KV_OVERFLOW, DEV_Q_ZERO, DEV_TIMEOUT, DEV_BAD_NACC, DEV_BAD_T
     0x1, 0x2, 0x4, 0x8, 0x10, 0x20)
 DEV_EMPTY_MASK = 0x40
 DEV_BAD_PAGE = 0x80
+DEV_BAD_PARAM, DEV_BAD_SEQ, DEV_NO_PAGES = 0x100, 0x200, 0x400
 
 
 class SpecError(RuntimeError):
@@ -63,6 +64,23 @@ class spec_rope_config(ctypes.Structure):
     _fields_ = [("rotary_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("orig_len", ctypes.c_int),
                 ("theta", ctypes.c_double), ("factor", ctypes.c_double), ("low_freq", ctypes.c_double),
                 ("high_freq", ctypes.c_double)]
+
+
+class spec_sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int), ("top_p", ctypes.c_float),
+                ("min_p", ctypes.c_float), ("d_temperature", ctypes.c_void_p), ("d_top_k", ctypes.c_void_p),
+                ("d_top_p", ctypes.c_void_p), ("d_min_p", ctypes.c_void_p), ("rows_per_set", ctypes.c_int)]
+
+
+class spec_pages(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("mapped", ctypes.c_void_p),
+                ("ref", ctypes.c_void_p), ("n_free", ctypes.c_void_p), ("batch", ctypes.c_int),
+                ("n_pages", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class spec_page_data(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int)]
 
 
 _LIB = None
@@ -114,6 +132,20 @@ _SIGS = {
                                   _I, _P, _P]),
     "spec_kv8_workspace_bytes": (_SZ, [ctypes.POINTER(spec_model_config), _I, _I]),
     "spec_verify_forward_kv8": (_I, [_P, _P, _P, _P, _I, _I, ctypes.POINTER(spec_kv8_cache), _P, _P, _SZ, _P]),
+    "spec_sample": (_I, [_P, ctypes.c_int64, _I, _I, _I, ctypes.POINTER(spec_sampling), _P, _I, _P, _P,
+                         ctypes.c_int64, _P, _P]),
+    "spec_filter_logits": (_I, [_P, ctypes.c_int64, _I, _I, _I, ctypes.POINTER(spec_sampling), _P, ctypes.c_int64,
+                                _P, _P]),
+    "spec_pages_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "spec_pages_init": (_I, [ctypes.POINTER(spec_pages), _P]),
+    "spec_pages_reserve": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_pages),
+                                ctypes.POINTER(spec_page_data), _I, _P, _P, _SZ, _P]),
+    "spec_pages_fork": (_I, [ctypes.POINTER(spec_pages), _I, _P, _P, _P, _SZ, _P]),
+    "spec_pages_free": (_I, [ctypes.POINTER(spec_pages), _I, _P, _P, _SZ, _P]),
+    "spec_pages_compact": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_pages),
+                                ctypes.POINTER(spec_page_data), _P, _SZ, _P]),
+    "spec_pages_copy": (_I, [ctypes.POINTER(spec_model_config), ctypes.POINTER(spec_page_data),
+                             ctypes.POINTER(spec_page_data), _I, _P, _P, _P, _P]),
     "spec_gamma_ctl_create": (_I, [_I, _I, _I, _I, _I, _I, ctypes.c_double, ctypes.c_double,
                                    ctypes.c_double, ctypes.POINTER(_P)]),
     "spec_gamma_ctl_destroy": (_I, [_P]),
@@ -310,13 +342,19 @@ def spec_mask_logits(logits, allowed, rows: int, vocab: int, ws, stream=None):
 class PagedKVCache:
     """Paged target cache: k, v bf16 [layers][n_pages][Hkv][64][hd], len int32
     [B], the device page table int32 [B][max_pages], and a host page pool
-    (free list + host table) that `sync()` copies to the device."""
+    (free list + host table) that `sync()` copies to the device.  k and v that
+    are given are taken as they lie."""
 
-    def __init__(self, cfg: ModelConfig, batch: int, n_pages: int, max_pages: int, device="cuda"):
+    def __init__(self, cfg: ModelConfig, batch: int, n_pages: int, max_pages: int, device="cuda", k=None, v=None):
         self.cfg, self.batch, self.n_pages, self.max_pages = cfg, batch, n_pages, max_pages
+        self.pool = None
         shape = (cfg.n_layers, n_pages, cfg.n_kv_heads, PAGE_SLOTS, cfg.head_dim)
-        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device)
-        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device)
+        device = device if k is None else k.device
+        for name, t in (("k", k), ("v", v)):
+            if t is not None and (_plain(t, shape, torch.bfloat16, name) is None or t.device != torch.device(device)):
+                raise ValueError(f"{name}: expected a tensor on {device}")
+        self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device) if k is None else k
+        self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device) if v is None else v
         assert self.k.numel() * 2 == int(lib().spec_paged_kv_bytes(ctypes.byref(cfg.c()), n_pages))
         self.len = torch.zeros(batch, dtype=torch.int32, device=device)
         self.table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
@@ -588,6 +626,193 @@ def spec_verify_forward_kv8(handle: int, tokens, batch: int, n: int, kv: "KV8Cac
             handle, _plain(tokens, (batch, n), torch.int32, "tokens"), _plain(anc, (batch, n), torch.int64, "anc"),
             _plain(depth, (batch, n), torch.int32, "depth"), batch, n, kv.c(), _ptr(logits), _ptr(ws),
             ws.numel(), _raw_stream(stream, dev)), "spec_verify_forward_kv8")
+
+
+class Sampling:
+    """Temperature, top-k (0 off), top-p (1 off) and min-p (0 off): numbers for every row, or tensors (float32; top_k
+    int32) of one value a set, row r in set r // rows_per_set."""
+
+    def __init__(self, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, rows_per_set: int = 1):
+        if rows_per_set < 1:
+            raise ValueError("rows_per_set: expected 1 or more")
+        self.rows_per_set = rows_per_set
+        self.tensors = []
+        args = []
+        for name, x, off, dtype in (("temperature", temperature, 1.0, torch.float32), ("top_k", top_k, 0, torch.int32),
+                                    ("top_p", top_p, 1.0, torch.float32), ("min_p", min_p, 0.0, torch.float32)):
+            given = isinstance(x, torch.Tensor)
+            if given:
+                if x.dtype != dtype or x.dim() != 1 or not x.is_contiguous() or not x.is_cuda:
+                    raise ValueError(f"{name}: expected a contiguous 1-D {dtype} CUDA tensor")
+                self.tensors.append((name, x))
+            args.append((off, x.data_ptr()) if given else (x, None))
+        (t, dt), (k, dk), (p, dp), (m, dm) = args
+        self.c = spec_sampling(t, k, p, m, dt, dk, dp, dm, rows_per_set)
+
+    def _check(self, rows: int, dev: int):
+        sets = -(-rows // self.rows_per_set)
+        for name, x in self.tensors:
+            if x.numel() < sets or x.get_device() != dev:
+                raise ValueError(f"{name}: expected {sets} values on cuda:{dev}")
+
+
+def _logit_rows(t, what: str) -> tuple[int, int, int]:
+    """(rows, columns, elements between rows) of 2-D bf16 or fp32 rows."""
+    if t.dim() != 2 or t.dtype not in (torch.float32, torch.bfloat16) or not t.is_cuda or (
+            t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what}: expected 2-D float32 or bfloat16 CUDA rows with unit column stride")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if ld < cols:
+        raise ValueError(f"{what}: rows overlap")
+    return rows, cols, ld
+
+
+def _same_device(dev: int, *tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"expected every tensor of the call on cuda:{dev}")
+    if tensors[-1].nbytes < 4:
+        raise ValueError("expected a workspace of 4 bytes or more")
+
+
+def spec_sample(logits, sampling: "Sampling", uniforms, tokens, ws, probs=None, stream=None):
+    """Draw tokens int32 [rows][draws] from the rows of logits with uniforms [rows][draws]; probs: the distributions."""
+    rows, vocab, ld = _logit_rows(logits, "logits")
+    dev = logits.get_device()
+    _same_device(dev, uniforms, tokens, probs, ws)
+    sampling._check(rows, dev)
+    if uniforms.dim() != 2:
+        raise ValueError("uniforms: expected [rows][draws]")
+    draws = uniforms.shape[1]
+    probs_ld = vocab if probs is None else _rows(probs, rows, vocab, torch.float32, "probs")
+    if probs_ld < vocab:
+        raise ValueError("probs: rows overlap")
+    if rows == 0:
+        return
+    with _on(dev):
+        _check(lib().spec_sample(
+            logits.data_ptr(), ld, logits.dtype == torch.bfloat16, rows, vocab, sampling.c,
+            _plain(uniforms, (rows, draws), torch.float32, "uniforms"), draws,
+            _plain(tokens, (rows, draws), torch.int32, "tokens"), None if probs is None else probs.data_ptr(),
+            probs_ld, ws.data_ptr(), _raw_stream(stream, dev)), "spec_sample")
+
+
+def spec_filter_logits(logits, sampling: "Sampling", out, ws, stream=None):
+    """out = logits where the sampling parameters keep a token, else -inf (out may be logits)."""
+    rows, vocab, ld = _logit_rows(logits, "logits")
+    dev = logits.get_device()
+    _same_device(dev, out, ws)
+    sampling._check(rows, dev)
+    out_ld = _rows(out, rows, vocab, logits.dtype, "out")
+    if out_ld < vocab:
+        raise ValueError("out: rows overlap")
+    if rows == 0:
+        return
+    with _on(dev):
+        _check(lib().spec_filter_logits(
+            logits.data_ptr(), ld, logits.dtype == torch.bfloat16, rows, vocab, sampling.c, out.data_ptr(), out_ld,
+            ws.data_ptr(), _raw_stream(stream, dev)), "spec_filter_logits")
+
+
+class Pages:
+    """The device page pool of a PagedKVCache or KV8Cache, in place of its host pool: the cache's table and len, and
+    mapped int32 [B], ref int32 [n_pages], n_free int32 [1].  The books are made empty (spec_pages_init) unless they
+    are given."""
+
+    def __init__(self, kv, mapped=None, ref=None, n_free=None, stream=None):
+        given = [mapped is not None, ref is not None, n_free is not None]
+        if any(given) and not all(given):
+            raise ValueError("expected mapped, ref and n_free together")
+        self.kv = kv
+        dev = kv.len.device
+        ints = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+        self.mapped = ints(kv.batch) if mapped is None else mapped
+        self.ref = ints(kv.n_pages) if ref is None else ref
+        self.n_free = ints(1) if n_free is None else n_free
+        for name, n in (("mapped", kv.batch), ("ref", kv.n_pages), ("n_free", 1)):
+            t = getattr(self, name)
+            if _plain(t, (n,), torch.int32, name) is None or t.device != dev:
+                raise ValueError(f"{name}: expected a tensor on {dev}")
+        if not all(given):
+            d = kv.len.get_device()
+            with _on(d):
+                _check(lib().spec_pages_init(self.c(), _raw_stream(stream, d)), "spec_pages_init")
+
+    def c(self) -> spec_pages:
+        kv = self.kv
+        return spec_pages(_plain(kv.table, (kv.batch, kv.max_pages), torch.int32, "table"),
+                          _plain(kv.len, (kv.batch,), torch.int32, "len"), self.mapped.data_ptr(), self.ref.data_ptr(),
+                          self.n_free.data_ptr(), kv.batch, kv.n_pages, kv.max_pages)
+
+
+def _page_data(kv) -> spec_page_data:
+    scales = (kv.k_scale.data_ptr(), kv.v_scale.data_ptr()) if isinstance(kv, KV8Cache) else (None, None)
+    return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), *scales, kv.n_pages)
+
+
+def _ids(t, what: str):
+    return _plain(t, (t.numel(),), torch.int32, what)
+
+
+def spec_pages_workspace_bytes(batch: int, n_pages: int, max_pages: int) -> int:
+    return int(lib().spec_pages_workspace_bytes(batch, n_pages, max_pages))
+
+
+def spec_pages_reserve(pages: "Pages", n, ws, stream=None):
+    """Pages for n more slots a sequence (a number, or an int32 tensor [B]); shared ones are copied before a write."""
+    kv = pages.kv
+    per = n if isinstance(n, torch.Tensor) else None
+    dev = kv.len.get_device()
+    _same_device(dev, per, ws)
+    with _on(dev):
+        _check(lib().spec_pages_reserve(kv.cfg._kept(), pages.c(), _page_data(kv), 0 if per is not None else n,
+                                        _plain(per, (kv.batch,), torch.int32, "n"), ws.data_ptr(), ws.nbytes,
+                                        _raw_stream(stream, dev)), "spec_pages_reserve")
+
+
+def spec_pages_fork(pages: "Pages", src, dst, ws, stream=None):
+    """Sequences dst[i] become second src[i]s that share their pages."""
+    dev = pages.kv.len.get_device()
+    _same_device(dev, src, dst, ws)
+    if src.numel() != dst.numel():
+        raise ValueError("expected as many sources as destinations")
+    with _on(dev):
+        _check(lib().spec_pages_fork(pages.c(), src.numel(), _ids(src, "src"), _ids(dst, "dst"), ws.data_ptr(),
+                                     ws.nbytes, _raw_stream(stream, dev)), "spec_pages_fork")
+
+
+def spec_pages_free(pages: "Pages", seq, ws, stream=None):
+    """Sequences seq[i] return their pages; their lengths are 0."""
+    dev = pages.kv.len.get_device()
+    _same_device(dev, seq, ws)
+    with _on(dev):
+        _check(lib().spec_pages_free(pages.c(), seq.numel(), _ids(seq, "seq"), ws.data_ptr(), ws.nbytes,
+                                     _raw_stream(stream, dev)), "spec_pages_free")
+
+
+def spec_pages_compact(pages: "Pages", ws, stream=None):
+    """Move the used pages to the lowest numbers and rewrite the tables."""
+    kv = pages.kv
+    dev = kv.len.get_device()
+    _same_device(dev, ws)
+    with _on(dev):
+        _check(lib().spec_pages_compact(kv.cfg._kept(), pages.c(), _page_data(kv), ws.data_ptr(), ws.nbytes,
+                                        _raw_stream(stream, dev)), "spec_pages_compact")
+
+
+def spec_pages_copy(kv, kv_to, src, dst, ws, stream=None):
+    """Copy pages src[i] of one cache to pages dst[i] of another of the same kind and shape (or of itself)."""
+    rows = lambda c: (c.n_layers, c.n_kv_heads, c.head_dim)
+    if type(kv) is not type(kv_to) or rows(kv.cfg) != rows(kv_to.cfg):
+        raise ValueError("expected two caches of one kind and shape")
+    dev = kv.len.get_device()
+    _same_device(dev, kv_to.len, src, dst, ws)
+    if src.numel() != dst.numel():
+        raise ValueError("expected as many sources as destinations")
+    with _on(dev):
+        _check(lib().spec_pages_copy(kv.cfg._kept(), _page_data(kv), _page_data(kv_to), src.numel(), _ids(src, "src"),
+                                     _ids(dst, "dst"), ws.data_ptr(), _raw_stream(stream, dev)), "spec_pages_copy")
 
 
 class GammaController:

@@ -1648,3 +1648,214 @@ int spec_verify_forward_kv8(const spec_model* m, const int32_t* d_tokens, const 
 }
 
 }  // extern "C"
+
+// -------------------------------------------------------- truncated sampling
+namespace {
+
+// Shared by the draw and the filter; r: what the call returns if it is not SPEC_OK.
+int trunc_params(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab, const spec_sampling* s,
+                 void* d_ws, TruncParams* p) {
+  if (!d_logits || !s || !d_ws || rows < 0 || vocab <= 0 || ld < vocab || ld > (1ll << 40)) return SPEC_EINVAL;
+  if (reinterpret_cast<uintptr_t>(d_logits) % (is_bf16 ? 2 : 4) || !aligned4(d_ws)) return SPEC_EINVAL;
+  if (!s->d_temperature && (!(s->temperature >= 0.f) || std::isinf(s->temperature))) return SPEC_EINVAL;
+  if (!s->d_top_k && s->top_k < 0) return SPEC_EINVAL;
+  if (!s->d_top_p && !(s->top_p > 0.f && s->top_p <= 1.f)) return SPEC_EINVAL;
+  if (!s->d_min_p && !(s->min_p >= 0.f && s->min_p <= 1.f)) return SPEC_EINVAL;
+  if (!aligned4(s->d_temperature) || !aligned4(s->d_top_k) || !aligned4(s->d_top_p) || !aligned4(s->d_min_p))
+    return SPEC_EINVAL;
+  if (s->rows_per_set < 1) return SPEC_EINVAL;
+  if (rows > 65535 || vocab > kTruncMaxVocab) return SPEC_ESIZE;
+  *p = TruncParams{};
+  p->z = d_logits;
+  p->ld = ld;
+  p->bf16 = is_bf16 ? 1 : 0;
+  p->rows = rows;
+  p->V = vocab;
+  p->T = s->temperature;
+  p->k = s->top_k;
+  p->top_p = s->top_p;
+  p->min_p = s->min_p;
+  p->d_T = s->d_temperature;
+  p->d_k = s->d_top_k;
+  p->d_p = s->d_top_p;
+  p->d_mp = s->d_min_p;
+  p->rows_per_set = s->rows_per_set;
+  p->status = static_cast<int32_t*>(d_ws);
+  return SPEC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int spec_sample(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab, const spec_sampling* sampling,
+                const float* d_uniforms, int n_draws, int32_t* d_tokens, float* d_probs, int64_t probs_ld, void* d_ws,
+                void* stream) {
+  TruncParams p;
+  if (const int r = trunc_params(d_logits, ld, is_bf16, rows, vocab, sampling, d_ws, &p)) return r;
+  if (!d_tokens || !d_uniforms || n_draws < 1 || !aligned4(d_tokens) || !aligned4(d_uniforms) || !aligned4(d_probs) ||
+      (d_probs && (probs_ld < vocab || probs_ld > (1ll << 40))))
+    return SPEC_EINVAL;
+  if (n_draws > kTruncMaxDraws) return SPEC_ESIZE;
+  if (rows == 0) return SPEC_OK;
+  p.u = d_uniforms;
+  p.draws = n_draws;
+  p.tokens = d_tokens;
+  p.probs = d_probs;
+  p.probs_ld = probs_ld;
+  SPEC_CUDA(launch_trunc(p, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_filter_logits(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab,
+                       const spec_sampling* sampling, void* d_out, int64_t out_ld, void* d_ws, void* stream) {
+  TruncParams p;
+  if (const int r = trunc_params(d_logits, ld, is_bf16, rows, vocab, sampling, d_ws, &p)) return r;
+  if (!d_out || reinterpret_cast<uintptr_t>(d_out) % (is_bf16 ? 2 : 4) || out_ld < vocab || out_ld > (1ll << 40))
+    return SPEC_EINVAL;
+  if (d_out == d_logits && out_ld != ld) return SPEC_EINVAL;
+  if (rows == 0) return SPEC_OK;
+  p.out = d_out;
+  p.out_ld = out_ld;
+  SPEC_CUDA(launch_trunc(p, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+}  // extern "C"
+
+// --------------------------------------------------------- device page pool
+namespace {
+
+int pages_checks(const spec_pages* p) {
+  if (!p || !p->table || !p->len || !p->mapped || !p->ref || !p->n_free) return SPEC_EINVAL;
+  if (p->batch < 0 || p->n_pages <= 0 || p->max_pages <= 0) return SPEC_EINVAL;
+  for (const int32_t* a : {p->table, p->len, p->mapped, p->ref, p->n_free})
+    if (!aligned4(a)) return SPEC_EINVAL;
+  if (p->batch > 65535 || p->max_pages > kKv8MaxSlots / SPEC_PAGE_SLOTS) return SPEC_ESIZE;
+  return SPEC_OK;
+}
+
+int page_data_checks(const spec_model_config* c, const spec_page_data* d) {
+  if (!d || !cfg_ok(c) || c->n_layers == 0 || !d->k || !d->v || d->n_pages <= 0) return SPEC_EINVAL;
+  if ((d->k_scale == nullptr) != (d->v_scale == nullptr)) return SPEC_EINVAL;
+  for (const void* a : {static_cast<const void*>(d->k), static_cast<const void*>(d->v)})
+    if (reinterpret_cast<uintptr_t>(a) % 16) return SPEC_EINVAL;
+  if (!aligned4(d->k_scale) || !aligned4(d->v_scale)) return SPEC_EINVAL;
+  if (static_cast<long long>(d->n_pages) * c->n_kv_heads * SPEC_PAGE_SLOTS >= (1ll << 31) || c->n_layers > 65535)
+    return SPEC_ESIZE;
+  return SPEC_OK;
+}
+
+PagesParams pages_params(const spec_pages* p, void* d_ws) {
+  PagesParams q{};
+  q.table = p->table;
+  q.len = p->len;
+  q.mapped = p->mapped;
+  q.ref = p->ref;
+  q.n_free = p->n_free;
+  q.B = p->batch;
+  q.n_pages = p->n_pages;
+  q.max_pages = p->max_pages;
+  q.status = static_cast<int32_t*>(d_ws);
+  q.scratch = d_ws ? reinterpret_cast<int32_t*>(static_cast<uint8_t*>(d_ws) + kAlign) : nullptr;
+  return q;
+}
+
+PageMoves page_moves(const spec_model_config* c, const spec_page_data* from, const spec_page_data* to, void* d_ws) {
+  PageMoves m{};
+  m.k = static_cast<const uint8_t*>(from->k);
+  m.v = static_cast<const uint8_t*>(from->v);
+  m.ks = from->k_scale;
+  m.vs = from->v_scale;
+  m.to_k = static_cast<uint8_t*>(to->k);
+  m.to_v = static_cast<uint8_t*>(to->v);
+  m.to_ks = to->k_scale;
+  m.to_vs = to->v_scale;
+  m.n_pages = from->n_pages;
+  m.to_n_pages = to->n_pages;
+  m.L = c->n_layers;
+  m.Hkv = c->n_kv_heads;
+  m.row_bytes = c->d_model / c->n_heads * (from->k_scale ? 1 : 2);
+  m.status = static_cast<int32_t*>(d_ws);
+  return m;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_pages_workspace_bytes(int batch, int n_pages, int max_pages) {
+  if (batch < 0 || n_pages <= 0 || max_pages <= 0) return 0;
+  return kAlign + pages_scratch_ints(batch, n_pages) * sizeof(int32_t);
+}
+
+static int pages_ws_checks(const spec_pages* p, const void* d_ws, size_t ws_bytes) {
+  if (const int r = pages_checks(p)) return r;
+  if (!d_ws || !aligned4(d_ws)) return SPEC_EINVAL;
+  return ws_bytes < spec_pages_workspace_bytes(p->batch, p->n_pages, p->max_pages) ? SPEC_ESIZE : SPEC_OK;
+}
+
+int spec_pages_init(const spec_pages* pages, void* stream) {
+  if (const int r = pages_checks(pages)) return r;
+  SPEC_CUDA(launch_pages_init(pages_params(pages, nullptr), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
+                       const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream) {
+  if (const int r = pages_ws_checks(pages, d_ws, ws_bytes)) return r;
+  if (const int r = page_data_checks(cfg, data)) return r;
+  if (data->n_pages != pages->n_pages || n < 0 || !aligned4(d_n)) return SPEC_EINVAL;
+  if (pages->batch == 0) return SPEC_OK;
+  SPEC_CUDA(launch_pages_reserve(pages_params(pages, d_ws), page_moves(cfg, data, data, d_ws), n, d_n,
+                                 device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_pages_fork(const spec_pages* pages, int n, const int32_t* d_src, const int32_t* d_dst, void* d_ws,
+                    size_t ws_bytes, void* stream) {
+  if (const int r = pages_ws_checks(pages, d_ws, ws_bytes)) return r;
+  if (n == 0) return SPEC_OK;
+  if (n < 0 || !d_src || !d_dst || !aligned4(d_src) || !aligned4(d_dst)) return SPEC_EINVAL;
+  if (n > 65535) return SPEC_ESIZE;
+  SPEC_CUDA(launch_pages_fork(pages_params(pages, d_ws), n, d_src, d_dst, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_pages_free(const spec_pages* pages, int n, const int32_t* d_seq, void* d_ws, size_t ws_bytes, void* stream) {
+  if (const int r = pages_ws_checks(pages, d_ws, ws_bytes)) return r;
+  if (n == 0) return SPEC_OK;
+  if (n < 0 || !d_seq || !aligned4(d_seq)) return SPEC_EINVAL;
+  if (n > 65535) return SPEC_ESIZE;
+  SPEC_CUDA(launch_pages_free(pages_params(pages, d_ws), n, d_seq, static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_pages_compact(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, void* d_ws,
+                       size_t ws_bytes, void* stream) {
+  if (const int r = pages_ws_checks(pages, d_ws, ws_bytes)) return r;
+  if (const int r = page_data_checks(cfg, data)) return r;
+  if (data->n_pages != pages->n_pages) return SPEC_EINVAL;
+  SPEC_CUDA(launch_pages_compact(pages_params(pages, d_ws), page_moves(cfg, data, data, d_ws), device_sm_count(),
+                                 static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+int spec_pages_copy(const spec_model_config* cfg, const spec_page_data* from, const spec_page_data* to, int n,
+                    const int32_t* d_src, const int32_t* d_dst, void* d_ws, void* stream) {
+  if (const int r = page_data_checks(cfg, from)) return r;
+  if (const int r = page_data_checks(cfg, to)) return r;
+  if ((from->k_scale == nullptr) != (to->k_scale == nullptr)) return SPEC_EINVAL;
+  if (!d_ws || !aligned4(d_ws)) return SPEC_EINVAL;
+  if (n == 0) return SPEC_OK;
+  if (n < 0 || !d_src || !d_dst || !aligned4(d_src) || !aligned4(d_dst)) return SPEC_EINVAL;
+  if (n > to->n_pages) return SPEC_ESIZE;
+  PageMoves m = page_moves(cfg, from, to, d_ws);
+  m.n = n;
+  m.src = d_src;
+  m.dst = d_dst;
+  SPEC_CUDA(launch_pages_copy(m, device_sm_count(), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
+}
+
+}  // extern "C"

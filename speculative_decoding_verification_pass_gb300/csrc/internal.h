@@ -257,6 +257,59 @@ struct SampleParams {
 };
 cudaError_t launch_sample(const SampleParams& p, cudaStream_t stream);
 
+// ------------------------------------------------------ truncated sampling
+constexpr int kTruncMaxVocab = 1 << 18;
+constexpr int kTruncMaxDraws = 64;
+struct TruncParams {
+  const void* z;          // [rows][V], ld elements apart; bf16 or fp32
+  long long ld;
+  int bf16, rows, V;
+  float T, top_p, min_p;  // of every row, or, where the arrays are there, of the row's set
+  int k;
+  const float *d_T, *d_p, *d_mp;
+  const int32_t* d_k;
+  int rows_per_set;
+  const float* u;         // [rows][draws]
+  int draws;
+  int32_t* tokens;        // [rows][draws]
+  float* probs;           // [rows][V], probs_ld apart, or nullptr
+  long long probs_ld;
+  void* out;              // filtered logits (then there are no draws), or nullptr
+  long long out_ld;
+  int32_t* status;
+};
+cudaError_t launch_trunc(const TruncParams& p, int sms, cudaStream_t stream);
+
+// --------------------------------------------------------- device page pool
+struct PagesParams {
+  int32_t *table, *len, *mapped, *ref, *n_free;
+  int B, n_pages, max_pages;
+  int32_t* status;
+  int32_t* scratch;       // pages_scratch_ints of them
+};
+size_t pages_scratch_ints(int B, int n_pages);
+struct PageMoves {        // pages of one cache (from) to pages of another, or of the same
+  const uint8_t *k, *v;   // [L][n_pages][Hkv][64][row_bytes]
+  const float *ks, *vs;   // [L][n_pages][Hkv][4], or nullptr
+  uint8_t *to_k, *to_v;
+  float *to_ks, *to_vs;
+  int n_pages, to_n_pages;
+  int L, Hkv, row_bytes;
+  const int32_t* count;   // moves, on the device; or nullptr: n of them
+  int n;
+  const int32_t *src, *dst;
+  const int32_t* rows;    // slots of each, or nullptr: whole pages
+  int32_t* status;
+};
+cudaError_t launch_pages_init(const PagesParams& p, cudaStream_t stream);
+cudaError_t launch_pages_reserve(const PagesParams& p, PageMoves m, int n, const int32_t* d_n, int sms,
+                                 cudaStream_t stream);
+cudaError_t launch_pages_fork(const PagesParams& p, int n, const int32_t* src, const int32_t* dst,
+                              cudaStream_t stream);
+cudaError_t launch_pages_free(const PagesParams& p, int n, const int32_t* seq, cudaStream_t stream);
+cudaError_t launch_pages_compact(const PagesParams& p, PageMoves m, int sms, cudaStream_t stream);
+cudaError_t launch_pages_copy(const PageMoves& m, int sms, cudaStream_t stream);
+
 // LM head with explicit stream-K scratch sized for rows <= 16: partials >=
 // max_grid x 2 x 16 x 128 floats, counters >= ceil(vocab/128) ints (zero on
 // entry).  SPEC_ESIZE when the model's vocabulary exceeds max_vocab or the
