@@ -4,8 +4,8 @@ Tokens and kept sets must be the oracle's.  A weight is (1 + t) 2^e with t off
 by at most 2^-24.1 of 1 + t: g, at most 1/2, is rounded by 2^-26 and so 2^g by
 2^-26 ln 2 sqrt 2, the series' last step rounds t by 2^-26, and what goes
 before it adds 2^-27; 1 + t >= 0.707.  In fixed point it is off by half a unit
-more, 2^-36 of the row's largest (2^-34 above 131072 ids).  A border between
-two ids' cumulative masses is then off by at most 2 x 2^-24.1 + V 2^-35 (V 2^-33) of
+more, 2^-36 of the row's largest (2^-33 above 131072 ids).  A border between
+two ids' cumulative masses is then off by at most 2 x 2^-24.1 + V 2^-35 (V 2^-32) of
 the total: a decision that near to one is not compared (it is counted, and
 rare by the sizes below).  Probabilities: 2^-24.1 of the weight and as much of
 the total, and three fp32 roundings (the weight, 1 / total, the product) of
@@ -30,7 +30,7 @@ def _built():
 
 
 def margin(V):
-    return 2 * 2.0 ** -24.1 + V * 2.0 ** (-35 if V <= 131072 else -33)
+    return 2 * 2.0 ** -24.1 + V * 2.0 ** (-35 if V <= 131072 else -32)
 
 
 def _cuda(x, dtype=None):
