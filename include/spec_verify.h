@@ -337,7 +337,7 @@ typedef struct {
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
  *               (spec_accept's d_draft_probs).
  * Weights are summed in fixed point, exactly and in any order: a weight is off by
- * about 2^-27 of itself and by 2^-36 of the row's largest (2^-33 above 131072 ids), and what
+ * about 2^-27 of itself and by 2^-36 of the row's largest, and what
  * is below that is not drawn; probabilities are off by a few fp32 roundings.  The
  * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
  * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and

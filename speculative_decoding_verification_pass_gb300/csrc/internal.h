@@ -277,8 +277,9 @@ struct TruncParams {
   void* out;              // filtered logits (then there are no draws), or nullptr
   long long out_ld;
   int32_t* status;
+  bool resident;          // (set by the launcher) a CTA's logits stay in shared memory
 };
-cudaError_t launch_trunc(const TruncParams& p, int sms, cudaStream_t stream);
+cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream);
 
 // --------------------------------------------------------- device page pool
 struct PagesParams {

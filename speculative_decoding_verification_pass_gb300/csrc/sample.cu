@@ -19,17 +19,18 @@
 // (a plain exp2f((z - M) c) by 2^-20 at z - M = -20 T): few draws lie near enough
 // to a border to differ from the same draws in 64 bits.
 //
-// Layout.  A cluster of up to eight CTAs takes a row; each keeps its part in
-// shared memory, so the row is read once.  The ids that can matter are often
-// few: min-p is a bound by itself, and with top-k up to the number of warps the
-// k-th largest of the warps' maxima is one that at least k logits reach.  Where
-// at most kList ids pass these bounds, they are gathered and one CTA sorts them and
-// decides.  Else the ids are counted in 4096 bins of the distance from M: a bin's
-// weight is its number times the weight at its middle to within 0.32%, so the bins
-// where the nucleus ends are known but for a few; one pass over the weights then
-// gives their total, what lies above those bins, and the few ids in them, among
-// which the threshold is found.  (Should it lie elsewhere, or the ids be too
-// many, histograms of the weights themselves part them, bin by bin.)
+// Layout.  A cluster of one to eight CTAs takes a row, each CTA a part, each warp
+// a part of that.  The row is read from memory once and, by the later passes, from
+// the caches.  The ids that can matter are often few: min-p is a bound by
+// itself, and with top-k up to 128 the k-th largest of the maxima of 128 parts of
+// the row is one that at least k logits reach.  Where at most kList ids pass these
+// bounds, they are gathered and one CTA decides.  Else the ids are counted in 4096
+// bins of the distance from M: a bin's weight is its number times the weight at its
+// middle to within 0.24%, so the bins where the nucleus ends are known but for a few; one
+// pass over the weights then gives their total, what lies above those bins, and
+// the few ids in them, among which the threshold is found.  (Should it lie
+// elsewhere, or the ids be too many, histograms of the weights part them by their
+// bits.)
 #include <algorithm>
 #include <cmath>
 
@@ -47,38 +48,36 @@ constexpr int kMaxC = 8;
 constexpr int kBins = 64;             // of a level
 constexpr int kFine = kBins * kBins;  // of two
 constexpr int kFar = kFine - 6;       // the last that a logit falls in, but for rounding
-constexpr int kList = kT;
-constexpr float kPerBit = kFar / 37.4f;  // fine bins to a halving of the weight: weights end before the bins
-constexpr u64 kMassMask = (1ull << 54) - 1;
-constexpr unsigned kManyIds = 1023;   // counts end there
+constexpr int kPieces = 8;            // of a warp's part, whose weights are kept
+constexpr int kList = 1024;
+constexpr int kHeavyBits = 6;         // ids of more than 2^-6 of the largest weight are few, and weighed one by one
+constexpr float kPerBit = kFar / 28.f;  // fine bins to a halving of the weight: 262144 ids past them weigh 2^-10
+constexpr int kLarge = 5;  // weights above 2^-5 of the largest are few
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds |x| < 2^22 to an integer
 
 struct Shared {
   union {
-    unsigned hist[2][kBins][32];  // a column a lane: no two lanes of a warp meet in a bank
     unsigned fine[kFine];
     struct {
-      u64 x[kList];      // the cluster's list
+      unsigned hist[2][kBins][32];  // a column a lane: no two lanes of a warp meet in a bank
+      u64 bins[kMaxC][kBins];       // every CTA's
+    } h;
+    struct {
+      u64 x[kList];  // the cluster's list
       u64 weight[kList];
       u64 targets[kTruncMaxDraws];
     } l;
   };
-  u64 bins[2][kMaxC][kBins];  // every CTA's bins: weight, and in the upper ten bits the number of ids; two sets in turn
+  u64 list[kList];           // this CTA's gathered ids
   u64 sums[kBins];
-  u64 ex[2][2][kMaxC];   // values exchanged within the cluster, two sets in turn
+  u64 ex[2][4][kMaxC];       // values exchanged within the cluster, two sets in turn
   u64 red[kW];
-  u64 seg[kW];           // weight of each warp's ids
-  u64 list[kList];       // this CTA's gathered ids
-  unsigned wmax[kMaxC * kW];  // the largest of every warp of the cluster (keys)
-  unsigned n, lo, hi;    // ids gathered, the ends of their keys
+  u64 seg[kW * kPieces];     // weights of the pieces
+  unsigned wmax[kMaxC * kW]; // the largest of 128 parts of the row (keys)
+  unsigned n, lo, hi;        // ids gathered, the ends of their keys
   float bound, theta_m, sum_inv;
   double c;
 };
-
-constexpr size_t kSharedBytes = (sizeof(Shared) + 15) / 16 * 16;
-constexpr size_t smem_bytes(int V, int C) {
-  return kSharedBytes + (static_cast<size_t>((V + 3) / 4) + C - 1) / C * sizeof(float4);
-}
 
 // ---------------------------------------------------------------- cluster
 SPEC_DEVINL unsigned cluster_rank() {
@@ -107,8 +106,8 @@ SPEC_DEVINL u64 ld_remote64(uint32_t a) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
-SPEC_DEVINL uint32_t ld_remote32(uint32_t a) {
-  uint32_t v;
+SPEC_DEVINL unsigned ld_remote32(uint32_t a) {
+  unsigned v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
@@ -182,13 +181,6 @@ SPEC_DEVINL u64 mul2(u64 a, u64 b) {
   asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-SPEC_DEVINL u64 add2(u64 a, u64 b) {
-  u64 r;
-  asm("add.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-SPEC_DEVINL u64 neg2(u64 a) { return a ^ 0x8000000080000000ull; }
-
 // 2^31 (2^g - 1) for |g| <= 1/2 (a little over): g times a polynomial that meets
 // (2^g - 1) / g at the six Chebyshev nodes of [-0.502, 0.502], 2^-27.5 of 2^g off
 // at most; its first coefficient in two parts, so that the rounding of what is added
@@ -213,25 +205,24 @@ __device__ __noinline__ void wide_power(float z, float M, double c, int* e, floa
   *t = d < -200.0 ? 0.f : parts(exp2m1_scaled(both(static_cast<float>(d - n)))).x;
 }
 
+__device__ u64 one_weight(float z, float M, float c_hi, float c_lo, float zlow, int n0, bool wide, double c);
+
 struct Weights {
   float M, c_hi, c_lo, zlow;
   int n0;   // M's power, as the rounded sum's bits
-  int off;  // 5 or 2: weights are in units of 2^-(30 + off) of about the largest
   bool wide;
   double c;
 
   // w = 2^e (1 + t 2^-31) of two; -e at least 149 where z is further than that below M
   SPEC_DEVINL void power2(float a, float b, int (&e)[2], float (&t)[2]) const {
-    const u64 x = pair(fmaxf(a, zlow), fmaxf(b, zlow)), c2 = both(c_hi);
-    const u64 p = mul2(x, c2);
-    const u64 nb = add2(p, both(kRound));
-    const u64 rest = fma2(x, both(c_lo), fma2(x, c2, neg2(p)));  // the product's rounding error, and c's
-    const u64 g = add2(add2(p, add2(both(kRound), neg2(nb))), rest);
-    const float2 n = parts(nb), f = parts(exp2m1_scaled(g));
+    const u64 x = pair(fmaxf(a, zlow), fmaxf(b, zlow)), c2 = both(c_hi), round = both(kRound);
+    const u64 nb = fma2(x, c2, round);                   // the whole powers
+    const u64 f = fma2(x, c2, fma2(nb, both(-1.f), round));  // what is left, with the product's rounding error
+    const float2 n = parts(nb), r = parts(exp2m1_scaled(fma2(x, both(c_lo), f)));
     e[0] = __float_as_int(n.x) - n0;
     e[1] = __float_as_int(n.y) - n0;
-    t[0] = f.x;
-    t[1] = f.y;
+    t[0] = r.x;
+    t[1] = r.y;
   }
   SPEC_DEVINL void power4(const float4& z, int (&e)[4], float (&t)[4]) const {
     if (wide) {
@@ -254,29 +245,24 @@ struct Weights {
     t[2] = t1[0];
     t[3] = t1[1];
   }
-  // 2^(30 + off) w, to the nearest, of weights below 2^-off (as most are: larger ones give 0 here, and
-  // all of their weight in large)
+  // 2^35 w, to the nearest, of weights below 2^-5 (as most are: larger ones give 0 here, and all of
+  // their weight in large)
   SPEC_DEVINL unsigned units(int e, float t) const {
     unsigned h;
-    asm("shr.b32 %0, %1, %2;" : "=r"(h) : "r"(mantissa(t)), "r"(-off - e));  // (0 from 32 on, and for less than 0)
+    asm("shr.b32 %0, %1, %2;" : "=r"(h) : "r"(mantissa(t)), "r"(-kLarge - e));  // (0 from 32 on, and for less than 0)
     return (h + 1u) >> 1;
   }
-  SPEC_DEVINL bool is_large(int e) const { return e > -off; }
-  SPEC_DEVINL u64 large(int e, float t) const { return static_cast<u64>(mantissa(t)) << (off + e - 1); }
+  SPEC_DEVINL bool is_large(int e) const { return e > -kLarge; }
+  SPEC_DEVINL u64 large(int e, float t) const { return static_cast<u64>(mantissa(t)) << (kLarge + e - 1); }
   SPEC_DEVINL static unsigned mantissa(float t) { return 0x80000000u + static_cast<unsigned>(__float2int_rn(t)); }
-  SPEC_DEVINL u64 fixed(float z) const {
-    int e[4];
-    float t[4];
-    power4(make_float4(z, z, z, z), e, t);
-    return is_large(e[0]) ? large(e[0], t[0]) : units(e[0], t[0]);
-  }
+  SPEC_DEVINL u64 fixed(float z) const { return one_weight(z, M, c_hi, c_lo, zlow, n0, wide, c); }
   SPEC_DEVINL void fixed4(const float4& z, u64 (&x)[4]) const {
     int e[4];
     float t[4];
     power4(z, e, t);
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[i] = units(e[i], t[i]);
-    if (max(max(e[0], e[1]), max(e[2], e[3])) > -off) {
+    if (max(max(e[0], e[1]), max(e[2], e[3])) > -kLarge) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (is_large(e[i])) x[i] = large(e[i], t[i]);
@@ -286,6 +272,24 @@ struct Weights {
     return e < -125 ? 0.f : fmaf(t, 4.65661287e-10f, 1.f) * __int_as_float((e + 127) << 23) * scale;
   }
 };
+
+// (A function of its own: it stands in many places where little goes through it.)
+__device__ __noinline__ u64 one_weight(float z, float M, float c_hi, float c_lo, float zlow, int n0, bool wide,
+                                       double c) {
+  Weights w;
+  w.M = M;
+  w.c_hi = c_hi;
+  w.c_lo = c_lo;
+  w.zlow = zlow;
+  w.n0 = n0;
+  int e[2];
+  float t[2];
+  if (wide)
+    wide_power(z, M, c, e, t);
+  else
+    w.power2(z, z, e, t);
+  return w.is_large(e[0]) ? w.large(e[0], t[0]) : w.units(e[0], t[0]);
+}
 
 // ------------------------------------------------------------------ kernel
 struct RowSet {
@@ -303,6 +307,7 @@ SPEC_DEVINL RowSet row_set(const TruncParams& p, int row) {
   return r;
 }
 
+// (A NaN stays one: no comparison below lets it through, and fmaxf passes it over.)
 template <bool BF16>
 SPEC_DEVINL void load4(const void* row, int x, int V, bool vec, float (&v)[4]) {
   if (vec && x + 4 <= V) {
@@ -327,9 +332,6 @@ SPEC_DEVINL void load4(const void* row, int x, int V, bool vec, float (&v)[4]) {
         v[e] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(row)[x + e]) : static_cast<const float*>(row)[x + e];
     }
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    v[e] = fmaxf(v[e], -INFINITY);  // (NaN)
 }
 
 template <bool BF16>
@@ -358,27 +360,47 @@ SPEC_DEVINL void store4(void* row, int x, int V, bool vec, const float (&v)[4]) 
 template <bool BF16, bool FILTER>
 struct Row {
   Shared& s;
-  float4* const zs;  // this CTA's ids, in groups of four
+  float4* const zs;  // the CTA's groups in shared memory, or nullptr
   const TruncParams& p;
   const int tid, lane, warp, rank, C;
   int par = 0;
-  int V, g0;   // the first group
-  int i0, i1, wg;  // this warp's groups, within the CTA's, and their number a warp
-  int limb, cnt_at;  // bits of the histogram's low part, and above which it counts ids in the other
+  const char* base;  // the row
+  bool vec;
+  int V, g0, gn;     // the CTA's groups of four ids: the first, and how many
+  int i0, i1;        // the warp's, within the CTA's
+  int iters, sub;    // rounds of the warp, of a piece
   Weights w;
 
   SPEC_DEVINL Row(Shared& s_, float4* zs_, const TruncParams& p_)
       : s(s_), zs(zs_), p(p_), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5),
         rank(static_cast<int>(cluster_rank())), C(static_cast<int>(cluster_size())) {}
 
-  // f(first id, four logits) over the CTA's groups; a warp's are contiguous.
+  SPEC_DEVINL float4 get(int i) const {
+    if (zs) return zs[min(i, i1)];
+    return fetch(i);
+  }
+  SPEC_DEVINL float4 fetch(int i) const {
+    float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    if (i < i1) load4<BF16>(base, 4 * (g0 + i), V, vec, v);
+    return make_float4(v[0], v[1], v[2], v[3]);
+  }
+  // f(first id, four logits) over the CTA's groups (a warp's are contiguous), two loads ahead; after(round) by
+  // whole warps
+  template <class F, class G>
+  SPEC_DEVINL void each(F&& f, G&& after) const {
+    int i = i0 + lane;
+    float4 a = get(i), b = get(i + 32);
+    for (int j = 0; j < iters; ++j, i += 32) {
+      const float4 v = a;
+      a = b;
+      b = get(i + 64);
+      if (i < i1) f(4 * (g0 + i), v);
+      after(j);
+    }
+  }
   template <class F>
   SPEC_DEVINL void each(F&& f) const {
-#pragma unroll 2
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const float4 v = zs[i];
-      f(4 * (g0 + i), v);
-    }
+    each(f, [](int) {});
   }
   // f(first id, z) by single logits
   template <class F>
@@ -391,21 +413,39 @@ struct Row {
     });
   }
 
-  // Two values of every CTA (held by warp 0) to every CTA of the cluster.
-  SPEC_DEVINL const u64 (*exchange(u64 a, u64 b))[kMaxC] {
+  // Up to four values of every CTA (held by warp 0) to every CTA of the cluster.
+  SPEC_DEVINL const u64 (*exchange(u64 a, u64 b = 0, u64 c = 0, u64 d = 0))[kMaxC] {
     par ^= 1;
     if (warp == 0 && lane < C) {
       st_remote(remote(&s.ex[par][0][rank], lane), a);
       st_remote(remote(&s.ex[par][1][rank], lane), b);
+      st_remote(remote(&s.ex[par][2][rank], lane), c);
+      st_remote(remote(&s.ex[par][3][rank], lane), d);
     }
     cluster_barrier();
     return s.ex[par];
   }
   // one of them, of each CTA, added up
   SPEC_DEVINL u64 total_of(const u64* v) const {
+    u64 t = lane < C ? v[lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < kMaxC; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return __shfl_sync(0xffffffffu, t, 0);
+  }
+  // the warps' values in v, added up (a whole warp)
+  SPEC_DEVINL u64 warps_sum(const u64* v) const {
+    u64 t = lane < kW ? v[lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < kW; o <<= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    return __shfl_sync(0xffffffffu, t, 0);
+  }
+
+  // the pieces' weights, added up (a whole warp)
+  SPEC_DEVINL u64 pieces_sum() const {
     u64 t = 0;
-    for (int r = 0; r < C; ++r) t += v[r];
-    return t;
+#pragma unroll
+    for (int i = 0; i < kW * kPieces; i += 32) t += s.seg[i + lane];
+    return warp_sum64(t);
   }
 
   SPEC_DEVINL void list_clear() {
@@ -426,122 +466,150 @@ struct Row {
   SPEC_DEVINL static float value_of(u64 x) { return key_value(static_cast<unsigned>(x >> 32)); }
   SPEC_DEVINL static int id_of(u64 x) { return static_cast<int>(~static_cast<unsigned>(x)); }
 
-  // The cluster's lists (counts[r] entries of CTA r) to this CTA, with their weights (or 1 each).
-  SPEC_DEVINL void pull(const u64* counts, int n, bool mass) {
-    if (tid < n) {
-      int r = 0, at = tid;
+  // The cluster's lists (counts[r] entries of CTA r) to this CTA, with their weights (or 1 each); where its
+  // own start.
+  SPEC_DEVINL int pull(const u64* counts, int n, bool mass) {
+    int own = 0;
+    for (int r = 0; r < rank; ++r) own += static_cast<int>(counts[r]);
+    for (int i = tid; i < n; i += kT) {
+      int r = 0, at = i;
       while (at >= static_cast<int>(counts[r])) at -= static_cast<int>(counts[r++]);
       const u64 x = ld_remote64(remote(&s.list[at], r));
-      s.l.x[tid] = x;
-      s.l.weight[tid] = mass ? w.fixed(value_of(x)) : 1ull;
+      s.l.x[i] = x;
+      s.l.weight[i] = mass ? w.fixed(value_of(x)) : 1ull;
     }
     if (tid == 0) s.hi = 0;
     __syncthreads();
+    return own;
   }
-  // A few threads an entry: f(entry, another, its weight) of all, added up (in each of them).
-  template <class F>
-  SPEC_DEVINL void over_list(int n, int& i, bool& first, u64& sum, F&& f) {
+  // For each entry i of [from, from + some), by a few threads: then(i, the weights of those of the n for which
+  // f(entry, another) holds, added up), by one of them.
+  template <class F, class G>
+  SPEC_DEVINL void over_list(int n, int from, int some, F&& f, G&& then) {
     int lg = 0;
-    while ((kT >> (lg + 1)) >= n && lg < 5) ++lg;
+    while ((kT >> (lg + 1)) >= some && lg < 5) ++lg;
     const int step = 1 << lg, part = tid & (step - 1);
-    i = tid >> lg;
-    first = part == 0;
-    sum = 0;
-    if (i < n) {
-      const u64 x = s.l.x[i];
+    for (int i0 = 0; i0 < some; i0 += kT >> lg) {
+      const int i = from + i0 + (tid >> lg);
+      const bool mine = i < from + some;
+      u64 sum = 0;
+      if (mine) {
+        const u64 x = s.l.x[i];
 #pragma unroll 4
-      for (int j = part; j < n; j += step) sum += f(x, s.l.x[j]) ? s.l.weight[j] : 0ull;
+        for (int j = part; j < n; j += step) sum += f(x, s.l.x[j]) ? s.l.weight[j] : 0ull;
+      }
+      for (int o = 1; o < step; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (mine && part == 0) then(i, sum);
     }
-    for (int o = 1; o < step; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   }
-  // The largest value of the list whose weight and that of larger ones reach the target (false if none's does).
-  SPEC_DEVINL bool reaches(int n, u64 target, float* v) {
-    int i;
-    bool first;
-    u64 sum;
-    over_list(n, i, first, sum, [](u64 x, u64 y) { return (y >> 32) >= (x >> 32); });
-    if (i < n && first && sum >= target) atomicMax(&s.hi, static_cast<unsigned>(s.l.x[i] >> 32));
+  // The key of the largest value of those entries whose weight and that of larger ones reach the target (0 if
+  // none's does).
+  SPEC_DEVINL unsigned reaches(int n, int from, int some, u64 target) {
+    over_list(
+        n, from, some, [](u64 x, u64 y) { return (y >> 32) >= (x >> 32); },
+        [&](int i, u64 sum) {
+          if (sum >= target) atomicMax(&s.hi, static_cast<unsigned>(s.l.x[i] >> 32));
+        });
     __syncthreads();
     const unsigned key = s.hi;
     __syncthreads();  // (it is cleared for the next)
-    if (key) *v = key_value(key);
-    return key != 0;
+    return key;
+  }
+  // The weights of those not below theta (0 for the others), and their sum.
+  SPEC_DEVINL u64 weigh(int n, float theta) {
+    u64 x = 0;
+    for (int i = tid; i < n; i += kT) {
+      const float v = value_of(s.l.x[i]);
+      s.l.weight[i] = v >= theta ? w.fixed(v) : 0ull;
+      x += s.l.weight[i];
+    }
+    x = warp_sum64(x);
+    if (lane == 0) s.red[warp] = x;
+    if (tid == 0) s.hi = 0;
+    __syncthreads();
+    x = warps_sum(s.red);
+    __syncthreads();  // (red is written again)
+    return x;
+  }
+  // The same over the cluster's lists, each CTA its own entries.
+  SPEC_DEVINL bool threshold(const u64* counts, int n, bool mass, u64 target, float* theta) {
+    const int some = static_cast<int>(counts[rank]), own = pull(counts, n, mass);
+    const unsigned key = some ? reaches(n, own, some, target) : 0u;
+    const u64(*ex)[kMaxC] = exchange(key, 0);
+    unsigned top = 0;
+    for (int r = 0; r < C; ++r) top = max(top, static_cast<unsigned>(ex[0][r]));
+    if (top) *theta = key_value(top);
+    return top != 0;
   }
 
-  // What every CTA has in hist to all of them, and there the bin that the target lies in: the bin, the
-  // target less what lies above it, and the ids in it (at most kManyIds).
-  struct Found {
-    int bin;
-    u64 target;
-    int n;
-  };
-  template <bool MASS, class F>
-  SPEC_DEVINL Found find_bin(F&& target_of) {
-    par ^= 1;
+  // What every CTA has in hist to all of them, and there the bin that the target lies in (-1: beyond them
+  // all), and the target less what lies above it.
+  SPEC_DEVINL int find_bin(u64 target, u64* left) {
     __syncthreads();
     static_assert(kT == 8 * kBins && kMaxC == 8, "eight threads a bin");
     const int b = tid >> 3, part = tid & 7;
-    const uint4 lo = *reinterpret_cast<const uint4*>(&s.hist[0][b][4 * part]);
-    u64 x = static_cast<u64>(lo.x) + lo.y + lo.z + lo.w;
-    unsigned n = 0;
-    if (MASS) {
-      const uint4 hi = *reinterpret_cast<const uint4*>(&s.hist[1][b][4 * part]);
-      const unsigned m = (1u << cnt_at) - 1u;
-      x += static_cast<u64>((hi.x & m) + (hi.y & m) + (hi.z & m) + (hi.w & m)) << limb;
-      n = (hi.x >> cnt_at) + (hi.y >> cnt_at) + (hi.z >> cnt_at) + (hi.w >> cnt_at);
-    }
+    const uint4 lo = *reinterpret_cast<const uint4*>(&s.h.hist[0][b][4 * part]);
+    const uint4 hi = *reinterpret_cast<const uint4*>(&s.h.hist[1][b][4 * part]);
+    u64 x = static_cast<u64>(lo.x) + lo.y + lo.z + lo.w + ((static_cast<u64>(hi.x) + hi.y + hi.z + hi.w) << kLimb);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      if (MASS) n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
-    if (!MASS) n = static_cast<unsigned>(x);
-    if (part < C) st_remote(remote(&s.bins[par][rank][b], part), x | static_cast<u64>(min(n, kManyIds)) << 54);
+    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (part < C) st_remote(remote(&s.h.bins[rank][b], part), x);
     cluster_barrier();
-    x = part < C ? s.bins[par][part][b] : 0ull;
-    n = static_cast<unsigned>(x >> 54);
-    x &= kMassMask;
+    x = part < C ? s.h.bins[part][b] : 0ull;
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      n += __shfl_xor_sync(0xffffffffu, n, o);
-    }
-    if (part == 0) s.sums[b] = x | static_cast<u64>(min(n, kManyIds)) << 54;
-    __syncthreads();
-    const u64 p0 = s.sums[2 * lane], p1 = s.sums[2 * lane + 1], m0 = p0 & kMassMask, m1 = p1 & kMassMask;
+    for (int o = 1; o < 8; o <<= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (part == 0) s.sums[b] = x;
+    cluster_barrier();  // (every CTA has read its bins before they are written again)
+    const u64 m0 = s.sums[2 * lane], m1 = s.sums[2 * lane + 1];
     const u64 incl = warp_incl64(m0 + m1, lane), before = incl - m0 - m1;
-    const u64 target = target_of(__shfl_sync(0xffffffffu, incl, 31));
     const unsigned past = __ballot_sync(0xffffffffu, incl >= target);
-    if (!past) return {-1, target, 0};
+    if (!past) return -1;
     const int at = __ffs(past) - 1;
     const bool second = before + m0 < target;
-    Found f;
-    f.bin = __shfl_sync(0xffffffffu, 2 * lane + second, at);
-    f.target = target - __shfl_sync(0xffffffffu, second ? before + m0 : before, at);
-    f.n = static_cast<int>(__shfl_sync(0xffffffffu, static_cast<unsigned>((second ? p1 : p0) >> 54), at));
-    return f;
+    *left = target - __shfl_sync(0xffffffffu, second ? before + m0 : before, at);
+    return __shfl_sync(0xffffffffu, 2 * lane + second, at);
   }
 
   SPEC_DEVINL void hist_clear() {
-    for (int i = tid; i < static_cast<int>(sizeof(s.hist) / 16); i += kT)
-      reinterpret_cast<uint4*>(s.hist)[i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < static_cast<int>(sizeof(s.h.hist) / 16); i += kT)
+      reinterpret_cast<uint4*>(s.h.hist)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
   }
-  // one id of weight x
+  // What a lane adds to a counter fits it: at most 8192 ids, of up to 2^35.5 in weight.
+  static constexpr int kLimb = 19;
   SPEC_DEVINL void hist_add(int b, u64 x) {
-    atomicAdd(&s.hist[0][b][lane], static_cast<unsigned>(x) & ((1u << limb) - 1u));
-    atomicAdd(&s.hist[1][b][lane], static_cast<unsigned>(x >> limb) + (1u << cnt_at));
+    atomicAdd(&s.h.hist[0][b][lane], static_cast<unsigned>(x) & ((1u << kLimb) - 1u));
+    atomicAdd(&s.h.hist[1][b][lane], static_cast<unsigned>(x >> kLimb));
   }
 
+  SPEC_DEVINL static u64 two(float a, float b) {
+    return static_cast<u64>(__float_as_uint(a)) | static_cast<u64>(__float_as_uint(b)) << 32;
+  }
+  SPEC_DEVINL static float low_of(u64 x) { return __uint_as_float(static_cast<unsigned>(x)); }
+  SPEC_DEVINL static float high_of(u64 x) { return __uint_as_float(static_cast<unsigned>(x >> 32)); }
   // Fine bins: distance from M, linear (weights: 109 to a halving; numbers: an eighth of them to the span), by
   // the bits of a sum rounded to a whole number, or, where that is too large, by a difference.
   struct Fine {
-    float M, per, far;
+    float M, per, far, shift;  // (shift: of a bin's middle, in bins)
     int b0;
     bool by_sum;
     SPEC_DEVINL int operator()(float v) const {
       if (by_sum) return b0 - __float_as_int(fmaf(fmaxf(v, far), per, kRound));
       return min(static_cast<int>((M - v) * per), kFar);
+    }
+    // (MASS) the weight in a bin's middle, in 2^-36 of the largest
+    SPEC_DEVINL float middle(int b) const { return exp2f(36.f - (static_cast<float>(b) + shift) * (1.f / kPerBit)); }
+    // The values between which bin b lies, but for rounding (slack: in bins).
+    SPEC_DEVINL float upper(int b, float slack) const {
+      if (b <= 0) return INFINITY;
+      if (!by_sum) return M - __fdividef(static_cast<float>(b) - slack, per);
+      return __fdividef((__int_as_float(b0) - kRound) - static_cast<float>(b) + (0.5f + slack), per);
+    }
+    SPEC_DEVINL float lower(int b, float slack) const {
+      if (b >= kFar - 1) return -INFINITY;
+      if (!by_sum) return M - __fdividef(static_cast<float>(b) + 1.f + slack, per);
+      return __fdividef((__int_as_float(b0) - kRound) - static_cast<float>(b) - (0.5f + slack), per);
     }
   };
   template <bool MASS>
@@ -552,65 +620,112 @@ struct Row {
     f.by_sum = !(MASS && w.wide) && fabsf(w.M) * f.per < 3.2e6f && f.per > 1e-25f;
     f.far = f.by_sum ? w.M - __fdividef(static_cast<float>(kFar), f.per) : 0.f;
     f.b0 = __float_as_int(fmaf(w.M, f.per, kRound));
+    f.shift = f.by_sum ? fmaf(w.M, f.per, kRound - __int_as_float(f.b0)) : 0.5f;
     return f;
   }
 
-  // The fine bins [from, to] between which top_p of the weight of {z >= lower} ends by the ids' numbers in
-  // them, give or take 2^-13 of it; or (MASS false) the one of the k-th.  false: fewer than k.
+  // The fine bins [from, to] in which top_p of the weight of {z >= lower} ends, by the ids' numbers in them; or
+  // (MASS false) the one of the k-th.  false: fewer than k.  A bin of n ids weighs n times its middle's weight
+  // m, but for an error of about 0.0014 m sqrt(n) (ids lie anywhere in it); for the heavy ids, where a single one's
+  // error counts, the difference is added up.  The end is looked for within three times the root of the errors'
+  // squares, what may lie past the bins, and 2^-15 of the whole.
   template <bool MASS>
   SPEC_DEVINL bool count_bins(const Fine& fine, float lower, float top_p, int k, int* from, int* to) {
+    constexpr int kHeavy = static_cast<int>(kHeavyBits * kPerBit);
     __syncthreads();  // (the bins lie where the last list was)
     for (int i = tid; i < kFine / 4; i += kT) reinterpret_cast<uint4*>(s.fine)[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
+    const float heavy = w.M - __fdividef(kHeavyBits + 0.1f, w.c_hi);
+    float extra = 0.f;  // heavy ids' weights less their bins' (in 2^-36)
     each([&](int, const float4& z) {
       const int b[4] = {fine(z.x), fine(z.y), fine(z.z), fine(z.w)};
       const float v[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q)
-        if (v[q] >= lower && v[q] > -INFINITY) atomicAdd(&s.fine[b[q]], 1u);
+        if (v[q] >= lower) atomicAdd(&s.fine[b[q]], 1u);
+      if (MASS && fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w)) >= heavy) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (b[q] < kHeavy && v[q] >= lower) extra += exp2f(36.f - (w.M - v[q]) * w.c_hi) - fine.middle(b[q]);
+      }
     });
     cluster_barrier();
     // each CTA its part of the bins, a thread one to eight in a row
-    const int per = 8 / C, b0 = (rank * kT + tid) * per;
-    u64 v[8], mine = 0;
+    static_assert(kFine == kMaxC * kT, "");
+    const int per = kMaxC / C, b0 = (rank * kT + tid) * per;
+    u64 v[kMaxC], mine = 0, first_bins = 0;  // (the latter: of heavy ids)
+    float err = 0.f, err_heavy = 0.f;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      if (q >= per) break;
+    for (int q = 0; q < kMaxC; ++q) {
+      v[q] = 0;
+      if (q >= per) continue;
       unsigned n = 0;
 #pragma unroll
       for (int r = 0; r < kMaxC; ++r)
         if (r < C) n += ld_remote32(remote(&s.fine[b0 + q], r));
-      v[q] = MASS ? n * static_cast<u64>(__float2ull_rn(exp2f(36.f - static_cast<float>(b0 + q) * (1.f / kPerBit)))) : n;
+      v[q] = n;
+      if (MASS) {
+        const float m = fine.middle(b0 + q), x = static_cast<float>(n) * m;
+        if (b0 + q >= kFar - 1) {  // (anything further from M is counted there)
+          v[q] = 0;
+          err += x * x * 57000.f;  // (their whole weight, squared, over (3 x 0.0014)^2)
+        } else {
+          v[q] = n * static_cast<u64>(m);
+          (b0 + q < kHeavy ? err_heavy : err) += x * m;
+          if (b0 + q < kHeavy) first_bins += v[q];
+        }
+      }
       mine += v[q];
     }
     const u64 incl = warp_incl64(mine, lane);
     if (lane == 31) s.red[warp] = incl;
+    if (MASS) {
+      err = warp_sum(err);
+      err_heavy = warp_sum(err_heavy);
+      extra = warp_sum(extra);
+      first_bins = warp_sum64(first_bins);
+      if (lane == 0) {
+        s.seg[warp] = first_bins;
+        s.seg[kW + warp] = two(err, err_heavy);
+        s.seg[2 * kW + warp] = two(extra, 0.f);
+      }
+    }
     __syncthreads();
-    u64 excl = incl - mine, part = 0;
-#pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      const u64 x = s.red[i];
-      if (i < warp) excl += x;
-      part += x;
+    if (MASS && warp == 0) {
+      first_bins = warps_sum(s.seg);
+      const u64 e = lane < kW ? s.seg[kW + lane] : 0ull;
+      err = warp_sum(low_of(e));
+      err_heavy = warp_sum(high_of(e));
+      extra = warp_sum(lane < kW ? low_of(s.seg[2 * kW + lane]) : 0.f);
     }
-    const u64(*ex)[kMaxC] = exchange(part, 0);
-    u64 all = 0;
-    for (int r = 0; r < C; ++r) {
-      if (r < rank) excl += ex[0][r];
-      all += ex[0][r];
-    }
+    const u64(*ex)[kMaxC] =
+        exchange(warp == 0 ? warps_sum(s.red) : 0ull, two(err, err_heavy), two(extra, 0.f), first_bins);
+    u64 excl = incl - mine;
+    for (int i = 0; i < warp; ++i) excl += s.red[i];
+    for (int r = 0; r < rank; ++r) excl += ex[0][r];
+    const u64 all = total_of(ex[0]);
     u64 first = static_cast<u64>(k), last = first;
     if (MASS) {
-      const u64 t = part_of(all, top_p, true);
-      first = max(t - (t >> 13), static_cast<u64>(1));
-      last = min(t + (t >> 13), all);
+      err = err_heavy = extra = 0.f;
+      for (int r = 0; r < C; ++r) {
+        err += low_of(ex[1][r]);
+        err_heavy += high_of(ex[1][r]);
+        extra += low_of(ex[2][r]);
+      }
+      const long long more = static_cast<long long>(extra);
+      const u64 t = part_of(all + more, top_p, true) - more, off = (all >> 15) + static_cast<u64>(0.0042f * sqrtf(err));
+      first = t > off ? t - off : 1ull;
+      last = min(t + off, all);
+      if (static_cast<long long>(t) <= 0 || first <= total_of(ex[3])) {  // among the heavy ids: they are few
+        const u64 t1 = part_of(all, top_p, true), off1 = off + static_cast<u64>(0.0042f * sqrtf(err + err_heavy));
+        first = t1 > off1 ? t1 - off1 : 1ull;
+        last = min(t1 + off1, all);
+      }
     }
     if (all < first) return false;
     par ^= 1;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < kMaxC; ++q) {
       if (q >= per) break;
       const u64 next = excl + v[q];
       if (excl < first && first <= next)
@@ -625,222 +740,182 @@ struct Row {
     return true;
   }
 
-  // top_p's threshold and, for the draws, seg (this warp's part of what it keeps): false where the bins by
-  // numbers did not hold it, or too many ids.
+  // The largest value v where the weight (MASS; else number) of the logits from v on, of those in [lower,
+  // upper), reaches the target: false if it is less.
+  template <bool MASS>
+  SPEC_DEVINL bool refine(float lower, float upper, u64 target, float* theta) {
+    // keys that are left
+    unsigned klo = max(key_of(lower), key_of(-INFINITY) + 1u),
+             khi = upper == INFINITY ? key_of(INFINITY) : key_of(upper) - 1u;
+    // f(id, z, key) for the logits there
+    auto each_here = [&](auto&& fn) {
+      each1([&](int x, float v) {
+        const unsigned kv = key_of(v);
+        if (kv - klo <= khi - klo) fn(x, v, kv);
+      });
+    };
+    cluster_barrier();  // the bins of other CTAs, written to below, lie where their lists were
+    for (;;) {
+      list_clear();
+      unsigned lo = 0xFFFFFFFFu, hi = 0;
+      each_here([&](int x, float v, unsigned kv) {
+        list_add(v, x);
+        lo = min(lo, kv);
+        hi = max(hi, kv);
+      });
+      lo = __reduce_min_sync(0xffffffffu, lo);
+      hi = __reduce_max_sync(0xffffffffu, hi);
+      if (lane == 0) {
+        atomicMin(&s.lo, lo);
+        atomicMax(&s.hi, hi);
+      }
+      __syncthreads();
+      const u64(*ex)[kMaxC] = exchange((static_cast<u64>(s.lo) << 32) | s.hi, s.n);
+      const int n = static_cast<int>(total_of(ex[1]));
+      klo = 0xFFFFFFFFu;
+      khi = 0;
+      for (int r = 0; r < C; ++r) {
+        klo = min(klo, static_cast<unsigned>(ex[0][r] >> 32));
+        khi = max(khi, static_cast<unsigned>(ex[0][r]));
+      }
+      if (n == 0) return false;
+      if (klo == khi) {  // one value
+        const float v = key_value(klo);
+        if (n * (MASS ? w.fixed(v) : 1ull) < target) return false;
+        *theta = v;
+        return true;
+      }
+      if (n <= kList) return threshold(ex[1], n, MASS, target, theta);
+      // too many: bins of keys between the smallest and the largest
+      int shift = 0;
+      while (((khi - klo) >> shift) >= kBins) ++shift;
+      hist_clear();
+      each_here([&](int, float v, unsigned kv) { hist_add(static_cast<int>((khi - kv) >> shift), MASS ? w.fixed(v) : 1ull); });
+      const int b = find_bin(target, &target);
+      if (b < 0) return false;
+      khi -= static_cast<unsigned>(b) << shift;
+      klo = max(klo, khi - min(khi, (1u << shift) - 1u));
+    }
+  }
+
+  // top_p's threshold of {z >= lower}.  true: seg holds what it keeps of the warps' weights.
   SPEC_DEVINL bool nucleus(float lower, float top_p, float* theta) {
     const Fine fine = fine_bins<true>(0.f);
     int from, to;
     count_bins<true>(fine, lower, top_p, 0, &from, &to);
+    const float high = fine.upper(from, 0.f);  // (the rule below holds for any two values)
+    float low = fmaxf(lower, fine.lower(to, 0.f));
+    low = fminf(low, w.wide ? lower : w.M - __fdividef(6.f, w.c_hi));  // (no large weight lies below it)
+    const float none = w.wide ? -INFINITY : w.M - __fdividef(38.f, w.c_hi);  // no weight from here down
     list_clear();
-    u64 above = 0, rest = 0;
-    each([&](int x, const float4& z) {
-      int e[4];
-      float t[4];
-      w.power4(z, e, t);
-      const float v[4] = {z.x, z.y, z.z, z.w};
-      u64 u[4];
+    u64 above = 0, all = 0;
+    int left = sub, piece = warp * kPieces;
+    each(
+        [&](int x, const float4& z) {
+          const float most = fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w));
+          if (!(most >= none)) return;
+          int e[4];
+          float t[4];
+          w.power4(z, e, t);
+          const float v[4] = {z.x, z.y, z.z, z.w};
+          unsigned u[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) u[q] = w.units(e[q], t[q]);
-      if (max(max(e[0], e[1]), max(e[2], e[3])) > -w.off) {
+          for (int q = 0; q < 4; ++q) u[q] = v[q] >= lower ? w.units(e[q], t[q]) : 0u;
+          all += u[0] + u[1];  // (each below 2^31)
+          all += u[2] + u[3];
+          if (most < low) return;
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (w.is_large(e[q])) u[q] = w.large(e[q], t[q]);
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int b = fine(v[q]);
-        if (v[q] >= lower) {
-          if (b < from)
-            above += u[q];
-          else
-            rest += u[q];
-          if (b >= from && b <= to && v[q] > -INFINITY) list_add(v[q], x + q);
+          for (int q = 0; q < 4; ++q) {
+            u64 x1 = u[q];
+            if (w.is_large(e[q]) && v[q] >= lower) {
+              x1 = w.large(e[q], t[q]);
+              all += x1;
+            }
+            if (v[q] >= high)
+              above += x1;
+            else if (v[q] >= low && v[q] > -INFINITY)
+              list_add(v[q], x + q);
+          }
+        },
+        [&](int j) {
+          if (--left == 0 || j == iters - 1) {
+            above = warp_sum64(above);
+            if (lane == 0) s.seg[piece] = above;
+            ++piece;
+            left = sub;
+            above = 0;
+          }
+        });
+    for (; piece < (warp + 1) * kPieces; ++piece)
+      if (lane == 0) s.seg[piece] = 0;
+    all = warp_sum64(all);
+    if (lane == 0) s.red[warp] = all;
+    __syncthreads();
+    if (warp == 0) {
+      above = pieces_sum();
+      all = warps_sum(s.red);
+    }
+    const u64(*ex)[kMaxC] = exchange(s.n, above, all);
+    const int n = static_cast<int>(total_of(ex[0]));
+    above = total_of(ex[1]);
+    const u64 target = part_of(total_of(ex[2]), top_p, true);
+    if (target > above) {
+      if (n <= kList) {
+        if (threshold(ex[0], n, true, target - above, theta)) {
+          if constexpr (!FILTER) {
+            for (int i = tid; i < static_cast<int>(s.n); i += kT) {  // what this CTA's list keeps, to its pieces' weights
+              const u64 x = s.list[i];
+              const float v = value_of(x);
+              if (v >= *theta) {
+                const int g = (id_of(x) >> 2) - g0, at = g / (32 * iters);
+                atomicAdd(&s.seg[at * kPieces + (g - at * 32 * iters) / (32 * sub)], w.fixed(v));
+              }
+            }
+            __syncthreads();
+          }
+          return true;
         }
+      } else if (refine<true>(low, high, target - above, theta)) {
+        return false;
       }
-    });
-    above = warp_sum64(above);
-    rest = warp_sum64(rest);
-    if (lane == 0) {
-      s.seg[warp] = above;
-      s.red[warp] = rest;
     }
-    __syncthreads();
-    above = rest = 0;
-    for (int i = 0; i < kW; ++i) {
-      above += s.seg[i];
-      rest += s.red[i];
-    }
-    const unsigned mine = min(s.n, kManyIds);
-    const u64(*ex)[kMaxC] = exchange(above, rest | static_cast<u64>(mine) << 54);
-    above = rest = 0;
-    int n = 0;
-    u64* counts = s.sums;
-    for (int r = 0; r < C; ++r) {
-      above += ex[0][r];
-      rest += ex[1][r] & kMassMask;
-      n += static_cast<int>(ex[1][r] >> 54);
-    }
-    if (tid < C) counts[tid] = ex[1][tid] >> 54;
-    const u64 target = part_of(above + rest, top_p, true);
-    if (n == 0 || n > kList || target <= above) return false;
-    __syncthreads();
-    pull(counts, n, true);
-    if (!reaches(n, target - above, theta)) return false;
-    if (!FILTER) {  // what this CTA's part of the list keeps, to its warps' weights
-      if (tid < static_cast<int>(mine)) {
-        const u64 x = s.list[tid];
-        const float v = value_of(x);
-        if (v >= *theta) atomicAdd(&s.seg[((id_of(x) >> 2) - g0) / wg], w.fixed(v));
-      }
-      __syncthreads();
-    }
-    return true;
+    refine<true>(lower, INFINITY, target, theta);
+    return false;
   }
 
-  // The k-th largest of {lower <= z}, -inf if there are fewer: false where too many ids lie near it.
-  SPEC_DEVINL bool kth(float lower, float span, int k, float* theta) {
+  // The k-th largest of {lower <= z}, -inf if there are fewer.
+  SPEC_DEVINL float kth(float lower, float span, int k) {
     const Fine fine = fine_bins<false>(span);
     int from, to;
-    *theta = -INFINITY;
-    if (!count_bins<false>(fine, lower, 0.f, k, &from, &to)) return true;
+    float theta = -INFINITY;
+    if (!count_bins<false>(fine, lower, 0.f, k, &from, &to)) return theta;
+    const float high = fine.upper(from, 0.3f), low = fmaxf(lower, fine.lower(to, 0.3f));
     list_clear();
     unsigned over = 0;
     each([&](int x, const float4& z) {
+      if (fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w)) < low) return;
       const float v[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int b = fine(v[q]);
-        if (b <= from && v[q] >= lower && v[q] > -INFINITY) {
-          if (b < from)
-            ++over;
-          else
-            list_add(v[q], x + q);
-        }
+        if (v[q] >= high)
+          ++over;
+        else if (v[q] >= low && v[q] > -INFINITY)
+          list_add(v[q], x + q);
       }
     });
     over = __reduce_add_sync(0xffffffffu, over);
     if (lane == 0) s.red[warp] = over;
     __syncthreads();
-    u64 above = 0;
-    for (int i = 0; i < kW; ++i) above += s.red[i];
-    const u64(*ex)[kMaxC] = exchange(s.n, above);
+    const u64(*ex)[kMaxC] = exchange(s.n, warp == 0 ? warps_sum(s.red) : 0ull);
     const int n = static_cast<int>(total_of(ex[0]));
-    above = total_of(ex[1]);
-    if (n > kList) return false;
-    pull(ex[0], n, false);
-    return reaches(n, static_cast<u64>(k) - above, theta);
-  }
-
-  // The largest value v with (MASS: weight, else number) of {lower <= z, z >= v}
-  // at least the target: top_p of the whole, or k.  -inf if there is none.
-  template <bool MASS>
-  SPEC_DEVINL float select(float lower, float span, float top_p, int k) {
-    const Fine fine = fine_bins<MASS>(span);
-    __syncthreads();  // (hist lies where the last list was put in order)
-    hist_clear();
-    each([&](int, const float4& z) {
-      const float v[4] = {z.x, z.y, z.z, z.w};
-      const int at[4] = {fine(z.x) / kBins, fine(z.y) / kBins, fine(z.z) / kBins, fine(z.w) / kBins};
-      if (!MASS) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (v[q] >= lower) atomicAdd(&s.hist[0][at[q]][lane], 1u);
-        return;
-      }
-      int e[4];
-      float t[4];
-      w.power4(z, e, t);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (v[q] >= lower) {
-          const unsigned x = w.units(e[q], t[q]);
-          atomicAdd(&s.hist[0][at[q]][lane], x & ((1u << limb) - 1u));
-          atomicAdd(&s.hist[1][at[q]][lane], (x >> limb) + (1u << cnt_at));
-        }
-      if (max(max(e[0], e[1]), max(e[2], e[3])) > -w.off) {
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          if (w.is_large(e[q]) && v[q] >= lower) {
-            const u64 x = w.large(e[q], t[q]);
-            atomicAdd(&s.hist[0][at[q]][lane], static_cast<unsigned>(x) & ((1u << limb) - 1u));
-            atomicAdd(&s.hist[1][at[q]][lane], static_cast<unsigned>(x >> limb));
-          }
-      }
-    });
-    Found f = find_bin<MASS>([&](u64 all) { return MASS ? part_of(all, top_p, true) : static_cast<u64>(k); });
-    if (f.bin < 0) return -INFINITY;  // (fewer than k)
-    unsigned from = f.bin * kBins, width = kBins;  // the fine bins that the threshold lies in
-    unsigned khi = 0xFFFFFFFFu, klo = 1;           // and the keys
-    // f(id, z) for the logits there
-    auto each_here = [&](auto&& fn) {
-      each([&](int x, const float4& z) {
-        const bool h0 = fine(z.x) - from < width, h1 = fine(z.y) - from < width, h2 = fine(z.z) - from < width,
-                   h3 = fine(z.w) - from < width;
-        if (!(h0 || h1 || h2 || h3)) return;
-        const bool h[4] = {h0, h1, h2, h3};
-        const float v[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const unsigned kv = key_of(v[q]);
-          if (h[q] && v[q] >= lower && v[q] > -INFINITY && kv >= klo && kv <= khi) fn(x + q, v[q]);
-        }
-      });
-    };
-    if (f.n > kList) {
-      hist_clear();
-      each_here([&](int, float v) {
-        if (MASS)
-          hist_add(fine(v) - from, w.fixed(v));
-        else
-          atomicAdd(&s.hist[0][fine(v) - from][lane], 1u);
-      });
-      const u64 target = f.target;
-      f = find_bin<MASS>([&](u64) { return target; });
-      from += f.bin;
-      width = 1;
+    const u64 above = total_of(ex[1]), target = static_cast<u64>(k);
+    if (low == lower && above + n < target) return theta;  // fewer than k
+    if (target > above) {
+      if (n <= kList ? threshold(ex[0], n, false, target - above, &theta) : refine<false>(low, high, target - above, &theta))
+        return theta;
     }
-    for (;;) {
-      list_clear();
-      each_here([&](int x, float v) { list_add(v, x); });
-      __syncthreads();
-      const u64(*ex)[kMaxC] = exchange(s.n, 0);
-      const int n = static_cast<int>(total_of(ex[0]));
-      if (n <= kList) {  // (each CTA finds it for itself)
-        pull(ex[0], n, MASS);
-        float v = lower;
-        reaches(n, f.target, &v);
-        return v;
-      }
-      // still too many: bins of keys between the smallest and the largest
-      each_here([&](int, float v) {
-        const unsigned kv = key_of(v);
-        atomicMin(&s.lo, kv);
-        atomicMax(&s.hi, kv);
-      });
-      __syncthreads();
-      ex = exchange(s.lo, s.hi);
-      klo = 0xFFFFFFFFu;
-      khi = 0;
-      for (int r = 0; r < C; ++r) {
-        klo = min(klo, static_cast<unsigned>(ex[0][r]));
-        khi = max(khi, static_cast<unsigned>(ex[1][r]));
-      }
-      if (klo == khi) return key_value(klo);  // one value
-      int shift = 0;
-      while (((khi - klo) >> shift) >= kBins) ++shift;
-      hist_clear();
-      each_here([&](int, float v) {
-        const int b = static_cast<int>((khi - key_of(v)) >> shift);
-        if (MASS)
-          hist_add(b, w.fixed(v));
-        else
-          atomicAdd(&s.hist[0][b][lane], 1u);
-      });
-      const u64 target = f.target;
-      f = find_bin<MASS>([&](u64) { return target; });
-      khi -= static_cast<unsigned>(f.bin) << shift;
-      klo = max(klo, khi - min(khi, (1u << shift) - 1u));
-    }
+    refine<false>(lower, INFINITY, target, &theta);
+    return theta;
   }
 
   // Every output of a row but its draws: value(first id, four logits, out).
@@ -868,7 +943,7 @@ struct Row {
         for (int q = 0; q < 4; ++q) v[q] = v[q] >= theta ? v[q] : -INFINITY;
       });
     } else if (p.probs) {
-      if (tid == 0) s.sum_inv = static_cast<float>(static_cast<double>(1ull << (30 + w.off)) / static_cast<double>(total));
+      if (tid == 0) s.sum_inv = static_cast<float>(static_cast<double>(1ull << 35) / static_cast<double>(total));
       __syncthreads();
       const float inv = s.sum_inv;
       write_row(row, [&](int, const float4& z, float (&v)[4]) {
@@ -886,14 +961,16 @@ struct Row {
   }
   // one id alone (T = 0), or, id -1, a row with nothing to draw
   SPEC_DEVINL void write_single(int row, int only) {
-    if (!FILTER && rank == 0)
-      for (int d = tid; d < p.draws; d += kT) p.tokens[static_cast<long long>(row) * p.draws + d] = only;
+    if constexpr (!FILTER) {
+      if (rank == 0)
+        for (int d = tid; d < p.draws; d += kT) p.tokens[static_cast<long long>(row) * p.draws + d] = only;
+    }
     if (FILTER || p.probs)
       write_row(row, [&](int x, const float4&, float (&v)[4]) {
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (FILTER)
-            v[q] = only < 0 || x + q == only ? v[q] : -INFINITY;
+            v[q] = only < 0 || x + q == only ? fmaxf(v[q], -INFINITY) : -INFINITY;
           else
             v[q] = x + q == only ? 1.f : 0.f;
         }
@@ -909,40 +986,37 @@ struct Row {
     V = p.V;
     const int groups = (V + 3) >> 2, per = (groups + C - 1) / C;
     g0 = rank * per;
-    const int gn = max(0, min(per, groups - g0));
-    wg = (gn + kT - 1) / kT * 32;
-    i0 = min(warp * wg, gn);
-    i1 = min(i0 + wg, gn);
-    // What a lane adds to a bin fits its two counters: 512 ids of up to 2^35.5 (23 bits low; 12.5 + 9 high, and
-    // 10 for their number), or 1024 of up to 2^32.5 (22; 10.5 + 10, and 11)
-    w.off = V <= 131072 ? 5 : 2;
-    limb = V <= 131072 ? 23 : 22;
-    cnt_at = V <= 131072 ? 22 : 21;
-    const char* base = static_cast<const char*>(p.z) + static_cast<long long>(row) * p.ld * (BF16 ? 2 : 4);
-    const bool vec = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7 : 15)) == 0;
+    gn = max(0, min(per, groups - g0));
+    iters = (gn + kT - 1) / kT;
+    sub = max((iters + kPieces - 1) / kPieces, 4);
+    i0 = min(warp * iters * 32, gn);
+    i1 = min(i0 + iters * 32, gn);
+    base = static_cast<const char*>(p.z) + static_cast<long long>(row) * p.ld * (BF16 ? 2 : 4);
+    vec = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7 : 15)) == 0;
     float top = -INFINITY;
     constexpr int kAhead = 8;  // loads on their way at once
     for (int i = i0 + lane; i < i1; i += 32 * kAhead) {
-      float v[kAhead][4];
+      float4 v[kAhead];
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-        if (i + 32 * q < i1) load4<BF16>(base, 4 * (g0 + i + 32 * q), V, vec, v[q]);
+      for (int q = 0; q < kAhead; ++q) v[q] = fetch(i + 32 * q);
 #pragma unroll
-      for (int q = 0; q < kAhead; ++q)
-        if (i + 32 * q < i1) {
-          zs[i + 32 * q] = make_float4(v[q][0], v[q][1], v[q][2], v[q][3]);
-          top = fmaxf(top, fmaxf(fmaxf(v[q][0], v[q][1]), fmaxf(v[q][2], v[q][3])));
-        }
+      for (int q = 0; q < kAhead; ++q) {
+        if (zs && i + 32 * q < i1) zs[i + 32 * q] = v[q];
+        top = fmaxf(top, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
+      }
     }
     const RowSet rs = row_set(p, row);
     const bool bad = !(rs.T >= 0.f) || rs.T > 3.4028234e38f || rs.k < 0 || !(rs.top_p > 0.f && rs.top_p <= 1.f) ||
                      !(rs.min_p >= 0.f && rs.min_p <= 1.f);
     list_clear();
-    // every warp's maximum to every CTA
-    const unsigned kt = __reduce_max_sync(0xffffffffu, key_of(top));
-    if (lane < C) st_remote32(remote(&s.wmax[rank * kW + warp], lane), kt);
+    // the maxima of parts of warps to every CTA
+    // (of 4 C lanes each, so that there are 128 of them)
+    unsigned kt = key_of(top);
+    const int group = 4 * C, in_warp = 32 / group;
+    for (int o = 1; o < group; o <<= 1) kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, o));
+    if (lane % group < C) st_remote32(remote(&s.wmax[(rank * kW + warp) * in_warp + lane / group], lane % group), kt);
     cluster_barrier();
-    const int nw = C * kW;  // (the lists' order of the keys)
+    constexpr int nw = kMaxC * kW;
     unsigned km = 0, kmin = 0xFFFFFFFFu;
     for (int i = lane; i < nw; i += 32) {
       km = max(km, s.wmax[i]);
@@ -974,7 +1048,7 @@ struct Row {
     w.c_lo = __fdiv_rn(fmaf(-c_hi, rs.T, 1.44269502f) + 1.92596303e-8f, rs.T);
     w.wide = !(far < 30000.f) || !(c_hi < 1e30f) || !(c_hi > 1e-25f);
     w.zlow = w.wide ? 0.f : M - __fdividef(150.f, c_hi);
-    w.n0 = __float_as_int(__fadd_rn(__fmul_rn(M, c_hi), kRound));
+    w.n0 = __float_as_int(fmaf(M, c_hi, kRound));
     const bool top_k = rs.k > 0 && rs.k < V, top_p = rs.top_p < 1.f, few_k = top_k && rs.k <= nw;
     float lower = -INFINITY;
     if (rs.min_p > 0.f || w.wide || few_k || M == INFINITY) {
@@ -987,18 +1061,18 @@ struct Row {
       }
       if (tid == 0) s.bound = -INFINITY;
       __syncthreads();
-      // the k-th largest of the warps' maxima: that many logits at least reach it
-      if (few_k) {
-        const int lg = C == 8 ? 2 : C == 4 ? 3 : C == 2 ? 4 : 5;  // kT / nw threads a value
-        const int i = tid >> lg;
+        if (few_k) {
+        constexpr int kPer = kT / nw;  // threads a value
+        const int i = tid / kPer;
         const unsigned mine = s.wmax[i];
         int c = 0;
 #pragma unroll 8
-        for (int j = tid & ((1 << lg) - 1); j < nw; j += 1 << lg) {
+        for (int j = tid % kPer; j < nw; j += kPer) {
           const unsigned y = s.wmax[j];
           c += y > mine || (y == mine && j < i) ? 1 : 0;
         }
-        for (int o = 1; o < 1 << lg; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+#pragma unroll
+        for (int o = 1; o < kPer; o <<= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
         if (c == rs.k - 1) s.bound = key_value(mine);
         __syncthreads();
       }
@@ -1025,64 +1099,36 @@ struct Row {
     if (n <= kList) {  // few: one CTA decides
       if (rank == 0) {
         pull(ex[0], n, false);
-        if (top_k && n > rs.k) reaches(n, rs.k, &theta);
+        if (top_k && n > rs.k) theta = key_value(reaches(n, 0, n, rs.k));
         if (top_p || !FILTER) {
-          u64 x = 0;
-          if (tid < n) {
-            const float v = value_of(s.l.x[tid]);
-            x = v >= theta ? w.fixed(v) : 0ull;
-            s.l.weight[tid] = x;
+          total = weigh(n, theta);
+          if (top_p) {
+            const float v = key_value(reaches(n, 0, n, part_of(total, rs.top_p, true)));
+            if (!FILTER && v > theta) total = weigh(n, v);
+            theta = fmaxf(theta, v);
           }
-          x = warp_sum64(x);
-          if (lane == 0) s.red[warp] = x;
-          if (tid == 0) s.hi = 0;
-          __syncthreads();
-          for (int i = 0; i < kW; ++i) total += s.red[i];
-        }
-        if (top_p) {
-          float v = theta;
-          reaches(n, part_of(total, rs.top_p, true), &v);
-          if (!FILTER && v > theta) {  // weights of what is cut now go
-            u64 x = 0;
-            if (tid < n) {
-              x = value_of(s.l.x[tid]) >= v ? s.l.weight[tid] : 0ull;
-              s.l.weight[tid] = x;
-            }
-            x = warp_sum64(x);
-            if (lane == 0) s.red[warp] = x;
-            __syncthreads();
-            total = 0;
-            for (int i = 0; i < kW; ++i) total += s.red[i];
-          }
-          theta = fmaxf(theta, v);
         }
         if (!FILTER) {
           if (tid < p.draws) s.l.targets[tid] = draw_target(row, tid, total);
           __syncthreads();
-          int i;
-          bool first;
-          u64 sum;  // cumulative weight in the order of ids
-          over_list(n, i, first, sum, [](u64 x, u64 y) { return static_cast<unsigned>(y) >= static_cast<unsigned>(x); });
-          if (i < n && first)
-            for (int d = 0; d < p.draws; ++d)
-              if (s.l.targets[d] < sum && s.l.targets[d] >= sum - s.l.weight[i])
-                p.tokens[static_cast<long long>(row) * p.draws + d] = id_of(s.l.x[i]);
+          over_list(
+              n, 0, n, [](u64 x, u64 y) { return static_cast<unsigned>(y) >= static_cast<unsigned>(x); },
+              [&](int i, u64 sum) {  // cumulative weight in the order of ids
+                for (int d = 0; d < p.draws; ++d)
+                  if (s.l.targets[d] < sum && s.l.targets[d] >= sum - s.l.weight[i])
+                    p.tokens[static_cast<long long>(row) * p.draws + d] = id_of(s.l.x[i]);
+              });
         }
       }
       ex = exchange(key_of(theta), total);  // (and no CTA leaves before its list is read)
       if (FILTER || p.probs) write_kept(row, key_value(static_cast<unsigned>(ex[0][0])), ex[1][0]);
       return;
     }
-    if (top_k) {
-      float v;
-      if (!kth(lower, M - least, rs.k, &v)) v = select<false>(lower, M - least, 0.f, rs.k);
-      theta = fmaxf(theta, v);
-    }
+    if (top_k) theta = fmaxf(theta, kth(lower, M - least, rs.k));
     bool weighed = false;
     if (top_p) {
-      float v;
+      float v = theta;
       weighed = nucleus(theta, rs.top_p, &v);
-      if (!weighed) v = select<true>(theta, 0.f, rs.top_p, 0);
       theta = fmaxf(theta, v);
     }
     if (FILTER) {
@@ -1090,42 +1136,62 @@ struct Row {
       cluster_barrier();  // no CTA leaves before its list is read
       return;
     }
-    // the warps' weights, and the cluster's
-    u64 sum = 0;
+    // the pieces' weights, and the cluster's
     if (!weighed) {
-      each([&](int, const float4& v) {
-        if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < theta) return;
-        u64 x[4];
-        w.fixed4(v, x);
-        sum += (v.x >= theta ? x[0] : 0) + (v.y >= theta ? x[1] : 0) + (v.z >= theta ? x[2] : 0) +
-               (v.w >= theta ? x[3] : 0);
-      });
-      sum = warp_sum64(sum);
-      if (lane == 0) s.seg[warp] = sum;
+      u64 sum = 0;
+      int left = sub, piece = warp * kPieces;
+      each(
+          [&](int, const float4& v) {
+            if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < theta) return;
+            u64 x[4];
+            w.fixed4(v, x);
+            sum += (v.x >= theta ? x[0] : 0) + (v.y >= theta ? x[1] : 0) + (v.z >= theta ? x[2] : 0) +
+                   (v.w >= theta ? x[3] : 0);
+          },
+          [&](int j) {
+            if (--left == 0 || j == iters - 1) {
+              sum = warp_sum64(sum);
+              if (lane == 0) s.seg[piece] = sum;
+              ++piece;
+              left = sub;
+              sum = 0;
+            }
+          });
+      for (; piece < (warp + 1) * kPieces; ++piece)
+        if (lane == 0) s.seg[piece] = 0;
       __syncthreads();
-      sum = 0;
     }
-    for (int i = 0; i < kW; ++i) sum += s.seg[i];
-    ex = exchange(sum, 0);
+    const u64 sum = pieces_sum();
+    ex = exchange(sum);
     u64 before = 0;
-    for (int r = 0; r < C; ++r) {
-      if (r < rank) before += ex[0][r];
-      total += ex[0][r];
-    }
+    for (int r = 0; r < rank; ++r) before += ex[0][r];
+    total = total_of(ex[0]);
     for (int d = warp; d < p.draws; d += kW) {
       u64 x = draw_target(row, d, total);
       if (x < before || x >= before + sum) continue;
       x -= before;
-      // the warp's piece, then 128 ids, the lane and the id whose cumulative weight passes x
+      // the piece, then 128 ids, the lane and the id whose cumulative weight passes x
       int piece = 0;
-      while (piece < kW - 1 && s.seg[piece] <= x) x -= s.seg[piece++];
-      const int j1 = min((piece + 1) * wg, gn);
-      for (int j = piece * wg; j < j1; j += 32) {
-        const float4 v = j + lane < j1 ? zs[j + lane] : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      for (; piece < kW * kPieces; piece += 32) {
+        const u64 c = s.seg[piece + lane], incl = warp_incl64(c, lane);
+        const unsigned past = __ballot_sync(0xffffffffu, incl > x);
+        if (past) {
+          const int at = __ffs(past) - 1;
+          x -= __shfl_sync(0xffffffffu, incl - c, at);
+          piece += at;
+          break;
+        }
+        x -= __shfl_sync(0xffffffffu, incl, 31);
+      }
+      const int j0 = piece / kPieces * 32 * iters + piece % kPieces * 32 * sub,
+                j1 = min(min(j0 + 32 * sub, (piece / kPieces + 1) * 32 * iters), gn);
+      for (int j = j0; j < j1; j += 32) {
+        float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        if (j + lane < j1) load4<BF16>(base, 4 * (g0 + j + lane), V, vec, v);
         u64 f[4];
-        w.fixed4(v, f);
-        const u64 f0 = v.x >= theta ? f[0] : 0, f1 = v.y >= theta ? f[1] : 0, f2 = v.z >= theta ? f[2] : 0,
-                  f3 = v.w >= theta ? f[3] : 0;
+        w.fixed4(make_float4(v[0], v[1], v[2], v[3]), f);
+        const u64 f0 = v[0] >= theta ? f[0] : 0, f1 = v[1] >= theta ? f[1] : 0, f2 = v[2] >= theta ? f[2] : 0,
+                  f3 = v[3] >= theta ? f[3] : 0;
         const u64 t = f0 + f1 + f2 + f3, incl = warp_incl64(t, lane);
         const unsigned past = __ballot_sync(0xffffffffu, incl > x);
         if (past) {
@@ -1148,19 +1214,23 @@ __global__ void __launch_bounds__(kT, 2) trunc_kernel(const TruncParams p) {
   extern __shared__ __align__(16) char smem[];
   grid_dep_wait();
   grid_dep_launch();
-  Row<BF16, FILTER> r(*reinterpret_cast<Shared*>(smem), reinterpret_cast<float4*>(smem + kSharedBytes), p);
+  Row<BF16, FILTER> r(*reinterpret_cast<Shared*>(smem),
+                      p.resident ? reinterpret_cast<float4*>(smem + sizeof(Shared)) : nullptr, p);
   r.run(static_cast<int>(blockIdx.x / static_cast<unsigned>(r.C)));
 }
 
+static_assert(sizeof(Shared) % 16 == 0, "");
+constexpr int kResident = 4096;  // groups of a CTA that stay in shared memory, with room for two CTAs on an SM
+
 template <bool BF16, bool FILTER>
 cudaError_t launch(const TruncParams& p, cudaLaunchConfig_t& cfg) {
-  // the most a CTA of any call takes, asked for once per device
+  // the most a CTA takes, asked for once per device
   static PerDevice<cudaError_t> set;
   cudaError_t e = cudaSuccess;
   if (!set.get(
           [] {
             return cudaFuncSetAttribute(trunc_kernel<BF16, FILTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        static_cast<int>(smem_bytes(kTruncMaxVocab, kMaxC)));
+                                        static_cast<int>(sizeof(Shared) + (kResident + 1) * sizeof(float4)));
           },
           &e))
     return cudaErrorInvalidDevice;
@@ -1170,16 +1240,18 @@ cudaError_t launch(const TruncParams& p, cudaLaunchConfig_t& cfg) {
 
 }  // namespace
 
-cudaError_t launch_trunc(const TruncParams& p, int sms, cudaStream_t stream) {
+cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   const int groups = (p.V + 3) / 4;
-  // as many CTAs as leave two to an SM, or, where SMs are left over, one for every
-  // 512 groups: a row alone takes the less time the more share it
+  // as many CTAs as keep the row in shared memory, two to an SM, or, where SMs are left over, one for
+  // every 512 groups: a row alone takes the less time the more share it
   int C = 1;
-  while (C < kMaxC && (groups > C * kT * 8 || (groups > C * kT && p.rows * C <= sms))) C *= 2;
+  while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
+  const int per = (groups + C - 1) / C;
+  p.resident = per <= kResident;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(p.rows) * C);
   cfg.blockDim = dim3(kT);
-  cfg.dynamicSmemBytes = smem_bytes(p.V, C);
+  cfg.dynamicSmemBytes = sizeof(Shared) + (p.resident ? (per + 1) * sizeof(float4) : 0);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
