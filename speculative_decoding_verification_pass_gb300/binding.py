@@ -725,6 +725,7 @@ class Pages:
         if any(given) and not all(given):
             raise ValueError("expected mapped, ref and n_free together")
         self.kv = kv
+        self._table, self._len = (kv.batch, kv.max_pages), (kv.batch,)
         dev = kv.len.device
         ints = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
         self.mapped = ints(kv.batch) if mapped is None else mapped
@@ -741,18 +742,36 @@ class Pages:
 
     def c(self) -> spec_pages:
         kv = self.kv
-        return spec_pages(_plain(kv.table, (kv.batch, kv.max_pages), torch.int32, "table"),
-                          _plain(kv.len, (kv.batch,), torch.int32, "len"), self.mapped.data_ptr(), self.ref.data_ptr(),
+        table, length = kv.table, kv.len
+        if table.dtype is not torch.int32 or table.shape != self._table or not table.is_contiguous():
+            raise ValueError(f"table: expected a contiguous {self._table} {torch.int32} tensor")
+        if length.dtype is not torch.int32 or length.shape != self._len or not length.is_contiguous():
+            raise ValueError(f"len: expected a contiguous {self._len} {torch.int32} tensor")
+        return spec_pages(table.data_ptr(), length.data_ptr(), self.mapped.data_ptr(), self.ref.data_ptr(),
                           self.n_free.data_ptr(), kv.batch, kv.n_pages, kv.max_pages)
+
+    def _device(self, ws) -> int:
+        """The books' device, on which the cache's buffers and the workspace lie too."""
+        kv = self.kv
+        dev = self.ref.get_device()
+        if (kv.table.get_device() != dev or kv.len.get_device() != dev or kv.k.get_device() != dev
+                or ws.get_device() != dev):
+            raise ValueError(f"expected every tensor of the call on cuda:{dev}")
+        return dev
 
 
 def _page_data(kv) -> spec_page_data:
-    scales = (kv.k_scale.data_ptr(), kv.v_scale.data_ptr()) if isinstance(kv, KV8Cache) else (None, None)
-    return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), *scales, kv.n_pages)
+    if type(kv) is KV8Cache:
+        return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), kv.k_scale.data_ptr(), kv.v_scale.data_ptr(),
+                              kv.n_pages)
+    return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), None, None, kv.n_pages)
 
 
-def _ids(t, what: str):
-    return _plain(t, (t.numel(),), torch.int32, what)
+def _ids(t, n: int, dev: int, what: str) -> int:
+    """Address of n int32 numbers, one after another, on device dev."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{what}: expected {n} contiguous {torch.int32} numbers on cuda:{dev}")
+    return t.data_ptr()
 
 
 def spec_pages_workspace_bytes(batch: int, n_pages: int, max_pages: int) -> int:
@@ -761,41 +780,34 @@ def spec_pages_workspace_bytes(batch: int, n_pages: int, max_pages: int) -> int:
 
 def spec_pages_reserve(pages: "Pages", n, ws, stream=None):
     """Pages for n more slots a sequence (a number, or an int32 tensor [B]); shared ones are copied before a write."""
-    kv = pages.kv
-    per = n if isinstance(n, torch.Tensor) else None
-    dev = kv.len.get_device()
-    _same_device(dev, per, ws)
+    kv, dev = pages.kv, pages._device(ws)
+    per = None
+    if isinstance(n, torch.Tensor):
+        n, per = 0, _ids(n, kv.batch, dev, "n")
     with _on(dev):
-        _check(lib().spec_pages_reserve(kv.cfg._kept(), pages.c(), _page_data(kv), 0 if per is not None else n,
-                                        _plain(per, (kv.batch,), torch.int32, "n"), ws.data_ptr(), ws.nbytes,
+        _check(lib().spec_pages_reserve(kv.cfg._kept(), pages.c(), _page_data(kv), n, per, ws.data_ptr(), ws.nbytes,
                                         _raw_stream(stream, dev)), "spec_pages_reserve")
 
 
 def spec_pages_fork(pages: "Pages", src, dst, ws, stream=None):
     """Sequences dst[i] become second src[i]s that share their pages."""
-    dev = pages.kv.len.get_device()
-    _same_device(dev, src, dst, ws)
-    if src.numel() != dst.numel():
-        raise ValueError("expected as many sources as destinations")
+    dev, n = pages._device(ws), src.numel()
     with _on(dev):
-        _check(lib().spec_pages_fork(pages.c(), src.numel(), _ids(src, "src"), _ids(dst, "dst"), ws.data_ptr(),
+        _check(lib().spec_pages_fork(pages.c(), n, _ids(src, n, dev, "src"), _ids(dst, n, dev, "dst"), ws.data_ptr(),
                                      ws.nbytes, _raw_stream(stream, dev)), "spec_pages_fork")
 
 
 def spec_pages_free(pages: "Pages", seq, ws, stream=None):
     """Sequences seq[i] return their pages; their lengths are 0."""
-    dev = pages.kv.len.get_device()
-    _same_device(dev, seq, ws)
+    dev, n = pages._device(ws), seq.numel()
     with _on(dev):
-        _check(lib().spec_pages_free(pages.c(), seq.numel(), _ids(seq, "seq"), ws.data_ptr(), ws.nbytes,
+        _check(lib().spec_pages_free(pages.c(), n, _ids(seq, n, dev, "seq"), ws.data_ptr(), ws.nbytes,
                                      _raw_stream(stream, dev)), "spec_pages_free")
 
 
 def spec_pages_compact(pages: "Pages", ws, stream=None):
     """Move the used pages to the lowest numbers and rewrite the tables."""
-    kv = pages.kv
-    dev = kv.len.get_device()
-    _same_device(dev, ws)
+    kv, dev = pages.kv, pages._device(ws)
     with _on(dev):
         _check(lib().spec_pages_compact(kv.cfg._kept(), pages.c(), _page_data(kv), ws.data_ptr(), ws.nbytes,
                                         _raw_stream(stream, dev)), "spec_pages_compact")
@@ -803,16 +815,17 @@ def spec_pages_compact(pages: "Pages", ws, stream=None):
 
 def spec_pages_copy(kv, kv_to, src, dst, ws, stream=None):
     """Copy pages src[i] of one cache to pages dst[i] of another of the same kind and shape (or of itself)."""
-    rows = lambda c: (c.n_layers, c.n_kv_heads, c.head_dim)
-    if type(kv) is not type(kv_to) or rows(kv.cfg) != rows(kv_to.cfg):
+    a, b = kv.cfg, kv_to.cfg
+    if type(kv) is not type(kv_to) or a is not b and (a.n_layers, a.n_kv_heads, a.head_dim) != (
+            b.n_layers, b.n_kv_heads, b.head_dim):
         raise ValueError("expected two caches of one kind and shape")
-    dev = kv.len.get_device()
-    _same_device(dev, kv_to.len, src, dst, ws)
-    if src.numel() != dst.numel():
-        raise ValueError("expected as many sources as destinations")
+    dev, n = kv.k.get_device(), src.numel()
+    if kv_to.k.get_device() != dev or ws.get_device() != dev or ws.nbytes < 4:
+        raise ValueError(f"expected every tensor of the call on cuda:{dev}, and a workspace of 4 bytes or more")
     with _on(dev):
-        _check(lib().spec_pages_copy(kv.cfg._kept(), _page_data(kv), _page_data(kv_to), src.numel(), _ids(src, "src"),
-                                     _ids(dst, "dst"), ws.data_ptr(), _raw_stream(stream, dev)), "spec_pages_copy")
+        _check(lib().spec_pages_copy(a._kept(), _page_data(kv), _page_data(kv_to), n, _ids(src, n, dev, "src"),
+                                     _ids(dst, n, dev, "dst"), ws.data_ptr(), _raw_stream(stream, dev)),
+               "spec_pages_copy")
 
 
 class GammaController:
