@@ -307,8 +307,8 @@ int spec_mask_logits(float* d_logits, const uint32_t* d_allowed, int rows, int v
  *   top_p  in (0, 1], 1 = off: of what these leave, keeps every logit not below
  *          the one where the descending cumulative weight first reaches top_p
  *          of their total (spec_accept's rule).
- * So a row is cut at one logit, ties included.  T = 0 keeps the largest logit's
- * lowest id alone.  NaN counts as -inf, and a token at -inf is never kept; where
+ * So a row is cut at one logit, ties included.  T = 0 (or below 2^-126) keeps the
+ * largest logit's lowest id alone.  NaN counts as -inf, and a token at -inf is never kept; where
  * a logit is +inf, only those are.
  * The arrays (device, one value a set, 4-byte aligned) go before the scalars
  * where they are given; row r belongs to set r / rows_per_set (1: a set a row;
@@ -337,7 +337,7 @@ typedef struct {
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
  *               (spec_accept's d_draft_probs).
  * Weights are summed in fixed point, exactly and in any order: a weight is off by
- * about 2^-27 of itself and by 2^-36 of the row's largest, and what
+ * about 2^-26 of itself and by 2^-36 of the row's largest, and what
  * is below that is not drawn; probabilities are off by a few fp32 roundings.  The
  * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
  * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and

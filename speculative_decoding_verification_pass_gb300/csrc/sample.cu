@@ -15,7 +15,7 @@
 // (2^-35 of about the largest): sums are exact and the same in any order.  What
 // is left is a weight's own error.  z c (c = log2(e) / T in two parts) is taken
 // with its rounding error by an fma, whole powers leave exactly, and 2^g - 1 is
-// added to 1 as an integer, so that a weight is off by about 2^-27 of itself
+// added to 1 as an integer, so that a weight is off by about 2^-26 of itself
 // (a plain exp2f((z - M) c) by 2^-20 at z - M = -20 T): few draws lie near enough
 // to a border to differ from the same draws in 64 bits.
 //
@@ -181,6 +181,7 @@ SPEC_DEVINL u64 mul2(u64 a, u64 b) {
   asm("mul.rn.ftz.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+
 // 2^31 (2^g - 1) for |g| <= 1/2 (a little over): g times a polynomial that meets
 // (2^g - 1) / g at the six Chebyshev nodes of [-0.502, 0.502], 2^-27.5 of 2^g off
 // at most; its first coefficient in two parts, so that the rounding of what is added
@@ -588,7 +589,7 @@ struct Row {
   }
   SPEC_DEVINL static float low_of(u64 x) { return __uint_as_float(static_cast<unsigned>(x)); }
   SPEC_DEVINL static float high_of(u64 x) { return __uint_as_float(static_cast<unsigned>(x >> 32)); }
-  // Fine bins: distance from M, linear (weights: 109 to a halving; numbers: an eighth of them to the span), by
+  // Fine bins: distance from M, linear (weights: 146 to a halving; numbers: an eighth of them to the span), by
   // the bits of a sum rounded to a whole number, or, where that is too large, by a difference.
   struct Fine {
     float M, per, far, shift;  // (shift: of a bin's middle, in bins)
@@ -643,7 +644,7 @@ struct Row {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         if (v[q] >= lower) atomicAdd(&s.fine[b[q]], 1u);
-      if (MASS && fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w)) >= heavy) {
+      if (MASS && fine.by_sum && fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w)) >= heavy) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           if (b[q] < kHeavy && v[q] >= lower) extra += exp2f(36.f - (w.M - v[q]) * w.c_hi) - fine.middle(b[q]);
@@ -716,7 +717,8 @@ struct Row {
       const u64 t = part_of(all + more, top_p, true) - more, off = (all >> 15) + static_cast<u64>(0.0042f * sqrtf(err));
       first = t > off ? t - off : 1ull;
       last = min(t + off, all);
-      if (static_cast<long long>(t) <= 0 || first <= total_of(ex[3])) {  // among the heavy ids: they are few
+      // among the heavy ids (which are few), or where those were not weighed
+      if (!fine.by_sum || static_cast<long long>(t) <= 0 || first <= total_of(ex[3])) {
         const u64 t1 = part_of(all, top_p, true), off1 = off + static_cast<u64>(0.0042f * sqrtf(err + err_heavy));
         first = t1 > off1 ? t1 - off1 : 1ull;
         last = min(t1 + off1, all);
@@ -744,9 +746,9 @@ struct Row {
   // upper), reaches the target: false if it is less.
   template <bool MASS>
   SPEC_DEVINL bool refine(float lower, float upper, u64 target, float* theta) {
-    // keys that are left
-    unsigned klo = max(key_of(lower), key_of(-INFINITY) + 1u),
-             khi = upper == INFINITY ? key_of(INFINITY) : key_of(upper) - 1u;
+    // keys that are left (0 and -0 are equal, and so on the same side of a bound)
+    auto end = [](float v) { return key_of(v == 0.f ? -0.f : v); };
+    unsigned klo = max(end(lower), end(-INFINITY) + 1u), khi = upper == INFINITY ? end(INFINITY) : end(upper) - 1u;
     // f(id, z, key) for the logits there
     auto each_here = [&](auto&& fn) {
       each1([&](int x, float v) {
@@ -798,14 +800,14 @@ struct Row {
     }
   }
 
-  // top_p's threshold of {z >= lower}.  true: seg holds what it keeps of the warps' weights.
+  // top_p's threshold of {z >= lower}.  true: seg holds what it keeps of the pieces' weights.
   SPEC_DEVINL bool nucleus(float lower, float top_p, float* theta) {
     const Fine fine = fine_bins<true>(0.f);
-    int from, to;
+    int from = 0, to = kFine;
     count_bins<true>(fine, lower, top_p, 0, &from, &to);
-    const float high = fine.upper(from, 0.f);  // (the rule below holds for any two values)
-    float low = fmaxf(lower, fine.lower(to, 0.f));
-    low = fminf(low, w.wide ? lower : w.M - __fdividef(6.f, w.c_hi));  // (no large weight lies below it)
+    // (what follows holds for any two values: should the threshold not lie between them, it is found by itself)
+    const float high = fine.upper(from, 0.f), low = fmaxf(lower, fine.lower(to, 0.f));
+    const float light = fminf(low, w.wide ? lower : w.M - __fdividef(kLarge + 1.f, w.c_hi));  // no large weight below
     const float none = w.wide ? -INFINITY : w.M - __fdividef(38.f, w.c_hi);  // no weight from here down
     list_clear();
     u64 above = 0, all = 0;
@@ -823,7 +825,7 @@ struct Row {
           for (int q = 0; q < 4; ++q) u[q] = v[q] >= lower ? w.units(e[q], t[q]) : 0u;
           all += u[0] + u[1];  // (each below 2^31)
           all += u[2] + u[3];
-          if (most < low) return;
+          if (most < light) return;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             u64 x1 = u[q];
@@ -1009,8 +1011,7 @@ struct Row {
     const bool bad = !(rs.T >= 0.f) || rs.T > 3.4028234e38f || rs.k < 0 || !(rs.top_p > 0.f && rs.top_p <= 1.f) ||
                      !(rs.min_p >= 0.f && rs.min_p <= 1.f);
     list_clear();
-    // the maxima of parts of warps to every CTA
-    // (of 4 C lanes each, so that there are 128 of them)
+    // the maxima of parts of warps (of 4 C lanes each: 128 of them) to every CTA
     unsigned kt = key_of(top);
     const int group = 4 * C, in_warp = 32 / group;
     for (int o = 1; o < group; o <<= 1) kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, o));
@@ -1061,7 +1062,8 @@ struct Row {
       }
       if (tid == 0) s.bound = -INFINITY;
       __syncthreads();
-        if (few_k) {
+      // the k-th largest of those maxima: that many logits at least reach it
+      if (few_k) {
         constexpr int kPer = kT / nw;  // threads a value
         const int i = tid / kPer;
         const unsigned mine = s.wmax[i];

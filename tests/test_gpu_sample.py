@@ -189,6 +189,38 @@ def test_nucleus_deep_in_the_tail():
     check(z, [(0.9, 0, p, 2.0 ** -60) for _, _, p, _ in par], draws=3, seed=10)
 
 
+@pytest.mark.parametrize("top_p", [0.01, 0.05, 0.3, 0.999, 0.99999])
+def test_nuclei_of_every_size(top_p):
+    """From among the heaviest ids of flat rows to nearly all ids; temperatures that leave one id and nearly equal
+    ones."""
+    V = 128256
+    z = _peaked(17, 8, V)
+    check(z, [(T, 0, top_p, 0.0) for T in (0.05, 0.3, 0.7, 1.0, 1.5, 2.5, 8.0, 50.0)], draws=2, seed=11)
+
+
+def test_zeros_of_both_signs_at_the_threshold():
+    """0 and -0 are equal: neither is cut without the other, nor counted without it."""
+    V = 30000
+    g = wl.rng(7, 44)
+    z = np.where(g.random((6, V)) < 0.5, np.float32(0.0), np.float32(-0.0)).astype(np.float32)
+    z[:, ::3] = (-0.001 * g.random((6, len(z[0, ::3])))).astype(np.float32)
+    z[:, 1::300] = 0.25
+    par = [(1.0, 5000, 1.0, 0.0), (1.0, 0, 0.2, 0.0), (1.0, 5000, 0.6, 0.0), (1.0, 101, 0.9, 0.0), (1.0, 0, 0.5, 0.7),
+           (1e-30, 0, 0.5, 0.0)]
+    check(z, par, draws=2, seed=12)
+
+
+def test_infinities_in_long_rows():
+    """More infinite logits than a list holds."""
+    V = 50000
+    z = _peaked(18, 4, V)
+    z[0, ::9] = np.inf
+    z[1, ::2] = np.inf
+    z[2, 5] = np.inf
+    z[3, ::2] = np.nan
+    check(z, [(1.0, 0, 0.9, 0.0), (0.7, 3000, 0.5, 0.1), (1.0, 0, 1.0, 0.0), (1.0, 0, 0.9, 0.0)], draws=4, seed=13)
+
+
 def test_masked_rows():
     """-inf, the type's lowest value and NaN in masked places, rows with one id, with none, and with infinities."""
     V = 3000
