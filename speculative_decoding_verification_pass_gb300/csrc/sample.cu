@@ -23,7 +23,7 @@
 // a part of that.  The row is read from memory once and, by the later passes, from
 // the caches.  The ids that can matter are often few: min-p is a bound by
 // itself, and with top-k up to 128 the k-th largest of the maxima of 128 parts of
-// the row is one that at least k logits reach.  Where at most kList ids pass these
+// the row is one that at least k logits reach.  Where at most 256 ids pass these
 // bounds, they are gathered and one CTA decides.  Else the ids are counted in 4096
 // bins of the distance from M: a bin's weight is its number times the weight at its
 // middle to within 0.24%, so the bins where the nucleus ends are known but for a few; one
@@ -50,6 +50,7 @@ constexpr int kFine = kBins * kBins;  // of two
 constexpr int kFar = kFine - 6;       // the last that a logit falls in, but for rounding
 constexpr int kPieces = 8;            // of a warp's part, whose weights are kept
 constexpr int kList = 1024;
+constexpr int kFew = 256;              // candidates that one CTA decides about (by comparing each with each)
 constexpr int kHeavyBits = 6;         // ids of more than 2^-6 of the largest weight are few, and weighed one by one
 constexpr float kPerBit = kFar / 28.f;  // fine bins to a halving of the weight: 262144 ids past them weigh 2^-10
 constexpr int kLarge = 5;  // weights above 2^-5 of the largest are few
@@ -460,7 +461,7 @@ struct Row {
   // (the order of the list is of no account: what reads it puts it in order first)
   SPEC_DEVINL void list_add(float v, int id) {
     const unsigned at = atomicAdd(&s.n, 1u);
-    if (at < kList) s.list[at] = entry(key_of(v), id);
+    if (at < kList) s.list[at] = entry(key_of(v == 0.f ? 0.f : v), id);  // (-0 as 0)
   }
   // larger first, the lower id of equal ones
   SPEC_DEVINL static u64 entry(unsigned key, int id) { return (static_cast<u64>(key) << 32) | ~static_cast<unsigned>(id); }
@@ -516,21 +517,76 @@ struct Row {
     __syncthreads();  // (it is cleared for the next)
     return key;
   }
-  // The weights of those not below theta (0 for the others), and their sum.
-  SPEC_DEVINL u64 weigh(int n, float theta) {
-    u64 x = 0;
-    for (int i = tid; i < n; i += kT) {
-      const float v = value_of(s.l.x[i]);
-      s.l.weight[i] = v >= theta ? w.fixed(v) : 0ull;
-      x += s.l.weight[i];
-    }
-    x = warp_sum64(x);
-    if (lane == 0) s.red[warp] = x;
-    if (tid == 0) s.hi = 0;
+  // The largest of the threads' values, in every thread (set: 0 or 1 in turn).
+  SPEC_DEVINL u64 block_max(u64 v, int set) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = max(v, static_cast<u64>(__shfl_xor_sync(0xffffffffu, v, o)));
+    u64* const red = set ? s.seg : s.red;
+    if (lane == 0) red[warp] = v;
     __syncthreads();
-    x = warps_sum(s.red);
-    __syncthreads();  // (red is written again)
-    return x;
+    v = lane < kW ? red[lane] : 0ull;
+#pragma unroll
+    for (int o = 1; o < kW; o <<= 1) v = max(v, static_cast<u64>(__shfl_xor_sync(0xffffffffu, v, o)));
+    return __shfl_sync(0xffffffffu, v, 0);
+  }
+  // A row whose n <= kFew candidates this CTA has pulled, with their weights: the threshold, the weight of what is
+  // kept, and the draws.  Of each candidate: how many are larger, and the weight of the larger ones and of those
+  // not smaller.  top-k keeps it if fewer than k are larger; top-p, if the larger ones' weight falls short of its
+  // part of what top-k keeps, which is the most that ones not smaller than one of those weigh.
+  SPEC_DEVINL u64 decide(int row, int n, int k, float top_p, float* theta) {
+    int lg = 0;
+    while ((kT >> (lg + 1)) >= n && lg < 5) ++lg;
+    const int step = 1 << lg, part = tid & (step - 1), i = tid >> lg;
+    const bool mine = i < n;
+    u64 larger = 0, reached = 0;
+    int rank_of = 0;
+    const u64 x = mine ? s.l.x[i] : ~0ull;
+    const unsigned key = static_cast<unsigned>(x >> 32);
+    if (mine) {
+#pragma unroll 4
+      for (int j = part; j < n; j += step) {
+        const unsigned other = static_cast<unsigned>(s.l.x[j] >> 32);
+        const u64 y = s.l.weight[j];
+        if (other > key) {
+          larger += y;
+          ++rank_of;
+        }
+        if (other >= key) reached += y;
+      }
+    }
+    for (int o = 1; o < step; o <<= 1) {
+      larger += __shfl_xor_sync(0xffffffffu, larger, o);
+      reached += __shfl_xor_sync(0xffffffffu, reached, o);
+      rank_of += __shfl_xor_sync(0xffffffffu, rank_of, o);
+    }
+    bool keep = mine && rank_of < k;
+    u64 total = block_max(keep ? reached : 0ull, 0);
+    if (top_p < 1.f) {
+      keep = keep && larger < part_of(total, top_p, true);
+      total = block_max(keep ? reached : 0ull, 1);
+    }
+    if (keep && part == 0 && reached == total) atomicMax(&s.hi, ~key);  // (the smallest: some may weigh nothing)
+    if (FILTER) {
+      __syncthreads();
+      *theta = key_value(~s.hi);
+      return total;
+    }
+    if (mine && part == 0 && !keep) s.l.weight[i] = 0;
+    if (tid < p.draws) s.l.targets[tid] = draw_target(row, tid, total);
+    __syncthreads();
+    *theta = key_value(~s.hi);
+    u64 sum = 0;  // cumulative weight in the order of ids
+    if (mine) {
+#pragma unroll 4
+      for (int j = part; j < n; j += step)
+        sum += static_cast<unsigned>(s.l.x[j]) >= static_cast<unsigned>(x) ? s.l.weight[j] : 0ull;
+    }
+    for (int o = 1; o < step; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (keep && part == 0)
+      for (int d = 0; d < p.draws; ++d)
+        if (s.l.targets[d] < sum && s.l.targets[d] >= sum - s.l.weight[i])
+          p.tokens[static_cast<long long>(row) * p.draws + d] = id_of(x);
+    return total;
   }
   // The same over the cluster's lists, each CTA its own entries.
   SPEC_DEVINL bool threshold(const u64* counts, int n, bool mass, u64 target, float* theta) {
@@ -995,6 +1051,7 @@ struct Row {
     i1 = min(i0 + iters * 32, gn);
     base = static_cast<const char*>(p.z) + static_cast<long long>(row) * p.ld * (BF16 ? 2 : 4);
     vec = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7 : 15)) == 0;
+    const RowSet rs = row_set(p, row);
     float top = -INFINITY;
     constexpr int kAhead = 8;  // loads on their way at once
     for (int i = i0 + lane; i < i1; i += 32 * kAhead) {
@@ -1007,7 +1064,6 @@ struct Row {
         top = fmaxf(top, fmaxf(fmaxf(v[q].x, v[q].y), fmaxf(v[q].z, v[q].w)));
       }
     }
-    const RowSet rs = row_set(p, row);
     const bool bad = !(rs.T >= 0.f) || rs.T > 3.4028234e38f || rs.k < 0 || !(rs.top_p > 0.f && rs.top_p <= 1.f) ||
                      !(rs.min_p >= 0.f && rs.min_p <= 1.f);
     list_clear();
@@ -1082,11 +1138,11 @@ struct Row {
       lower = fmaxf(s.theta_m, s.bound);
     }
     const u64(*ex)[kMaxC];
-    int n = kList + 1;
-    if (lower > -INFINITY || V <= kList) {
+    int n = kFew + 1;
+    if ((lower > -INFINITY || V <= kFew) && !(FILTER && !top_k && !top_p)) {
       each([&](int x, const float4& v) {
         if (fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)) < lower) return;
-        if (*const_cast<volatile unsigned*>(&s.n) > kList) return;  // too many already
+        if (*const_cast<volatile unsigned*>(&s.n) > kFew) return;  // too many already
         if (v.x >= lower && v.x > -INFINITY) list_add(v.x, x);
         if (v.y >= lower && v.y > -INFINITY) list_add(v.y, x + 1);
         if (v.z >= lower && v.z > -INFINITY) list_add(v.z, x + 2);
@@ -1098,32 +1154,14 @@ struct Row {
     }
     float theta = lower;
     u64 total = 0;
-    if (n <= kList) {  // few: one CTA decides
-      if (rank == 0) {
-        pull(ex[0], n, false);
-        if (top_k && n > rs.k) theta = key_value(reaches(n, 0, n, rs.k));
-        if (top_p || !FILTER) {
-          total = weigh(n, theta);
-          if (top_p) {
-            const float v = key_value(reaches(n, 0, n, part_of(total, rs.top_p, true)));
-            if (!FILTER && v > theta) total = weigh(n, v);
-            theta = fmaxf(theta, v);
-          }
-        }
-        if (!FILTER) {
-          if (tid < p.draws) s.l.targets[tid] = draw_target(row, tid, total);
-          __syncthreads();
-          over_list(
-              n, 0, n, [](u64 x, u64 y) { return static_cast<unsigned>(y) >= static_cast<unsigned>(x); },
-              [&](int i, u64 sum) {  // cumulative weight in the order of ids
-                for (int d = 0; d < p.draws; ++d)
-                  if (s.l.targets[d] < sum && s.l.targets[d] >= sum - s.l.weight[i])
-                    p.tokens[static_cast<long long>(row) * p.draws + d] = id_of(s.l.x[i]);
-              });
-        }
-      }
-      ex = exchange(key_of(theta), total);  // (and no CTA leaves before its list is read)
-      if (FILTER || p.probs) write_kept(row, key_value(static_cast<unsigned>(ex[0][0])), ex[1][0]);
+    if (n <= kFew) {  // few: one CTA decides
+      if (rank == 0) pull(ex[0], n, true);
+      const bool alone = !FILTER && !p.probs;
+      if (alone) cluster_barrier();  // no CTA leaves before its list is read
+      if (rank == 0) total = decide(row, n, top_k ? rs.k : kT, rs.top_p, &theta);
+      if (alone) return;
+      ex = exchange(key_of(theta), total);
+      write_kept(row, key_value(static_cast<unsigned>(ex[0][0])), ex[1][0]);
       return;
     }
     if (top_k) theta = fmaxf(theta, kth(lower, M - least, rs.k));
@@ -1135,7 +1173,7 @@ struct Row {
     }
     if (FILTER) {
       write_kept(row, theta, 0);
-      cluster_barrier();  // no CTA leaves before its list is read
+      if (top_k || top_p) cluster_barrier();  // no CTA leaves before its list is read
       return;
     }
     // the pieces' weights, and the cluster's
