@@ -1282,10 +1282,14 @@ cudaError_t launch(const TruncParams& p, cudaLaunchConfig_t& cfg) {
 
 cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   const int groups = (p.V + 3) / 4;
-  // as many CTAs as keep the row in shared memory, two to an SM, or, where SMs are left over, one for
-  // every 512 groups: a row alone takes the less time the more share it
+  // As many CTAs as keep the row in shared memory, two to an SM, or, where SMs are left over, one for
+  // every 512 groups: a row alone takes the less time the more share it.  Of so many rows that their CTAs
+  // take turns, fewer, down to four turns and a half: what a cluster's CTAs wait for one another costs more
+  // then than reading the row again from the caches (320 rows of 128256, top-p / mixed parameters: eight
+  // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181; 64 rows: eight 47 us, four 62).
   int C = 1;
   while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
+  while (C > 1 && p.rows * C > 9 * sms) C /= 2;
   const int per = (groups + C - 1) / C;
   p.resident = per <= kResident;
   cudaLaunchConfig_t cfg = {};
