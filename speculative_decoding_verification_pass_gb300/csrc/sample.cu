@@ -370,6 +370,8 @@ struct Row {
   bool vec;
   int V, g0, gn;     // the CTA's groups of four ids: the first, and how many
   int i0, i1;        // the warp's, within the CTA's
+  const float4* src; // where groups below full are to be had as they are
+  int full;
   int iters, sub;    // rounds of the warp, of a piece
   Weights w;
 
@@ -377,9 +379,14 @@ struct Row {
       : s(s_), zs(zs_), p(p_), tid(threadIdx.x), lane(threadIdx.x & 31), warp(threadIdx.x >> 5),
         rank(static_cast<int>(cluster_rank())), C(static_cast<int>(cluster_size())) {}
 
+  // (of a group past the warp's: anything)
   SPEC_DEVINL float4 get(int i) const {
-    if (zs) return zs[min(i, i1)];
-    return fetch(i);
+    float4 v;
+    if (i < full)
+      v = src[i];
+    else
+      v = fetch(i);
+    return v;
   }
   SPEC_DEVINL float4 fetch(int i) const {
     float v[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
@@ -1051,6 +1058,8 @@ struct Row {
     i1 = min(i0 + iters * 32, gn);
     base = static_cast<const char*>(p.z) + static_cast<long long>(row) * p.ld * (BF16 ? 2 : 4);
     vec = (reinterpret_cast<uintptr_t>(base) & (BF16 ? 7 : 15)) == 0;
+    src = zs ? zs : reinterpret_cast<const float4*>(base) + g0;
+    full = zs ? i1 : !BF16 && vec ? min(i1, (V >> 2) - g0) : 0;
     const RowSet rs = row_set(p, row);
     float top = -INFINITY;
     constexpr int kAhead = 8;  // loads on their way at once
@@ -1285,8 +1294,9 @@ cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   // As many CTAs as keep the row in shared memory, two to an SM, or, where SMs are left over, one for
   // every 512 groups: a row alone takes the less time the more share it.  Of so many rows that their CTAs
   // take turns, fewer, down to four turns and a half: what a cluster's CTAs wait for one another costs more
-  // then than reading the row again from the caches (320 rows of 128256, top-p / mixed parameters: eight
-  // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181; 64 rows: eight 47 us, four 62).
+  // then than reading the row again from the caches.  320 rows of 128256, top-p / mixed parameters: eight
+  // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181, by loads slower than these, which take
+  // 192 / 110 with four; 64 rows: eight 47 us, four 62.
   int C = 1;
   while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
   while (C > 1 && p.rows * C > 9 * sms) C /= 2;
