@@ -335,7 +335,7 @@ typedef struct {
  *   d_tokens    int32 [rows][n_draws]: the smallest id whose cumulative weight, in
  *               id order, exceeds u * total;
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
- *               (spec_accept's d_draft_probs).
+ *               (spec_accept's d_draft_probs); never over the logits.
  * Weights are summed in fixed point, exactly and in any order: a weight is off by
  * about 2^-26 of itself and by 2^-36 of the row's largest, and what
  * is below that is not drawn; probabilities are off by a few fp32 roundings.  The

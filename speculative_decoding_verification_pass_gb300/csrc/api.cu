@@ -1694,7 +1694,7 @@ int spec_sample(const void* d_logits, int64_t ld, int is_bf16, int rows, int voc
   TruncParams p;
   if (const int r = trunc_params(d_logits, ld, is_bf16, rows, vocab, sampling, d_ws, &p)) return r;
   if (!d_tokens || !d_uniforms || n_draws < 1 || !aligned4(d_tokens) || !aligned4(d_uniforms) || !aligned4(d_probs) ||
-      (d_probs && (probs_ld < vocab || probs_ld > (1ll << 40))))
+      (d_probs && (probs_ld < vocab || probs_ld > (1ll << 40))) || d_probs == d_logits)
     return SPEC_EINVAL;
   if (n_draws > kTruncMaxDraws) return SPEC_ESIZE;
   if (rows == 0) return SPEC_OK;

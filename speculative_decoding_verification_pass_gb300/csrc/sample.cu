@@ -94,6 +94,9 @@ SPEC_DEVINL unsigned cluster_size() {
 SPEC_DEVINL void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// The cluster's first barrier in two halves: no CTA writes to another's shared memory before that has started.
+SPEC_DEVINL void cluster_started() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+SPEC_DEVINL void cluster_all_started() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 SPEC_DEVINL uint32_t remote(const void* p, unsigned rank) {
   uint32_t r;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
@@ -1080,6 +1083,7 @@ struct Row {
     unsigned kt = key_of(top);
     const int group = 4 * C, in_warp = 32 / group;
     for (int o = 1; o < group; o <<= 1) kt = max(kt, __shfl_xor_sync(0xffffffffu, kt, o));
+    cluster_all_started();
     if (lane % group < C) st_remote32(remote(&s.wmax[(rank * kW + warp) * in_warp + lane / group], lane % group), kt);
     cluster_barrier();
     constexpr int nw = kMaxC * kW;
@@ -1261,6 +1265,7 @@ struct Row {
 template <bool BF16, bool FILTER>
 __global__ void __launch_bounds__(kT, 2) trunc_kernel(const TruncParams p) {
   extern __shared__ __align__(16) char smem[];
+  cluster_started();
   grid_dep_wait();
   grid_dep_launch();
   Row<BF16, FILTER> r(*reinterpret_cast<Shared*>(smem),

@@ -98,3 +98,11 @@ def test_python_refusals(lib):
     with pytest.raises(ValueError):
         lib.spec_sample(torch.zeros(2, 8), lib.Sampling(), torch.zeros(2, 1), torch.zeros(2, 1, dtype=torch.int32),
                         torch.zeros(256, dtype=torch.uint8))
+
+
+def test_probs_over_the_logits_are_refused(lib):
+    fake = ctypes.c_void_p(4096)
+    s = ctypes.byref(lib.spec_sampling(1.0, 0, 1.0, 0.0, None, None, None, None, 1))
+    other = ctypes.c_void_p(8192)
+    assert lib.lib().spec_sample(fake, 10, 0, 0, 10, s, other, 1, other, fake, 10, other, None) == lib.SPEC_EINVAL
+    assert lib.lib().spec_sample(fake, 10, 0, 0, 10, s, other, 1, other, other, 10, other, None) == lib.SPEC_OK
