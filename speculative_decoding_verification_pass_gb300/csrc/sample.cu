@@ -713,7 +713,8 @@ struct Row {
       if (MASS && fine.by_sum && fmaxf(fmaxf(z.x, z.y), fmaxf(z.z, z.w)) >= heavy) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if (b[q] < kHeavy && v[q] >= lower) extra += exp2f(36.f - (w.M - v[q]) * w.c_hi) - fine.middle(b[q]);
+          if (b[q] < kHeavy && v[q] >= lower)
+            extra = fmaf(fine.middle(b[q]), fmaf(v[q] - w.M, fine.per, static_cast<float>(b[q]) + fine.shift), extra);
       }
     });
     cluster_barrier();
@@ -747,6 +748,7 @@ struct Row {
     const u64 incl = warp_incl64(mine, lane);
     if (lane == 31) s.red[warp] = incl;
     if (MASS) {
+      extra *= 0.693147181f / kPerBit;  // (2^d - 1 of less than half a bin)
       err = warp_sum(err);
       err_heavy = warp_sum(err_heavy);
       extra = warp_sum(extra);
@@ -873,10 +875,12 @@ struct Row {
     count_bins<true>(fine, lower, top_p, 0, &from, &to);
     // (what follows holds for any two values: should the threshold not lie between them, it is found by itself)
     const float high = fine.upper(from, 0.f), low = fmaxf(lower, fine.lower(to, 0.f));
-    const float light = fminf(low, w.wide ? lower : w.M - __fdividef(kLarge + 1.f, w.c_hi));  // no large weight below
+    const float large = w.wide ? lower : w.M - __fdividef(kLarge + 1.f, w.c_hi);  // no large weight below
+    const float least = fminf(low, large);
     const float none = w.wide ? -INFINITY : w.M - __fdividef(38.f, w.c_hi);  // no weight from here down
     list_clear();
     u64 above = 0, all = 0;
+    const bool some = lower > -INFINITY || w.wide;  // (else a NaN's power is 0, as -inf's)
     int left = sub, piece = warp * kPieces;
     each(
         [&](int x, const float4& z) {
@@ -888,22 +892,36 @@ struct Row {
           const float v[4] = {z.x, z.y, z.z, z.w};
           unsigned u[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) u[q] = v[q] >= lower ? w.units(e[q], t[q]) : 0u;
+          for (int q = 0; q < 4; ++q) u[q] = w.units(e[q], t[q]);
+          if (some) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) u[q] = v[q] >= lower ? u[q] : 0u;
+          }
           all += u[0] + u[1];  // (each below 2^31)
           all += u[2] + u[3];
-          if (most < light) return;
+          if (most < least) return;
+          bool between = false;
+          unsigned o[4];
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            u64 x1 = u[q];
-            if (w.is_large(e[q]) && v[q] >= lower) {
-              x1 = w.large(e[q], t[q]);
-              all += x1;
-            }
-            if (v[q] >= high)
-              above += x1;
-            else if (v[q] >= low && v[q] > -INFINITY)
-              list_add(v[q], x + q);
+            o[q] = v[q] >= high ? u[q] : 0u;
+            between = between || (v[q] < high && v[q] >= low);
           }
+          above += o[0] + o[1];
+          above += o[2] + o[3];
+          if (between) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (v[q] < high && v[q] >= low && v[q] > -INFINITY) list_add(v[q], x + q);
+          }
+          if (most < large) return;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (w.is_large(e[q]) && v[q] >= lower) {
+              const u64 x1 = w.large(e[q], t[q]);
+              all += x1;
+              if (v[q] >= high) above += x1;
+            }
         },
         [&](int j) {
           if (--left == 0 || j == iters - 1) {
@@ -1301,7 +1319,7 @@ cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   // take turns, fewer, down to four turns and a half: what a cluster's CTAs wait for one another costs more
   // then than reading the row again from the caches.  320 rows of 128256, top-p / mixed parameters: eight
   // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181, by loads slower than these, which take
-  // 192 / 110 with four; 64 rows: eight 47 us, four 62.
+  // 179 / 109 with four; 64 rows: eight 47 us, four 62.
   int C = 1;
   while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
   while (C > 1 && p.rows * C > 9 * sms) C /= 2;

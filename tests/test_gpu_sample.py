@@ -246,6 +246,18 @@ def test_masked_rows():
     check(z, par, bf16=True, status=sb.DEV_EMPTY_MASK, seed=5)
 
 
+def test_masked_places_of_rows_far_from_zero():
+    """Logits so large that their powers are taken in 64 bits: NaN and -inf there have no weight either."""
+    g = np.random.default_rng(44)
+    V = 5003
+    z = (2.0 * g.standard_normal((8, V)) + np.array([4e4, -4e4, 3e5, 0.0])[np.arange(8) % 4, None])
+    z[:, ::7] = np.nan
+    z[:, 3::11] = -np.inf
+    par = [(1.0, 0, 0.9, 0.0)] * 4 + [(0.7, 0, 1.0, 0.0), (0.7, 1000, 0.8, 0.0), (1.0, 0, 0.95, 1e-4), (0.9, 900, 1.0, 0.0)]
+    check(z, par, seed=45)
+    check(z[:1].repeat(2, 0), [(1.0, 0, 0.9, 0.0), (1.0, 0, 0.5, 0.0)], pad=1, seed=46)
+
+
 def test_scales_of_temperature_and_logits():
     """Temperatures and offsets past where whole powers leave in 32 bits, far apart logits, tiny differences."""
     V = 2500
