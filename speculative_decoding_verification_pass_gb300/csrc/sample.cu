@@ -110,10 +110,21 @@ SPEC_DEVINL u64 ld_remote64(uint32_t a) {
   asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(a) : "memory");
   return v;
 }
-SPEC_DEVINL unsigned ld_remote32(uint32_t a) {
-  unsigned v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+// N words in a row, of an address that is a multiple of as many (or of four)
+template <int N>
+SPEC_DEVINL void ld_remote_n(uint32_t a, unsigned (&v)[N]) {
+  if constexpr (N == 1) {
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v[0]) : "r"(a) : "memory");
+  } else if constexpr (N == 2) {
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v[0]), "=r"(v[1]) : "r"(a) : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 4)
+      asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v[i]), "=r"(v[i + 1]), "=r"(v[i + 2]), "=r"(v[i + 3])
+                   : "r"(a + 4 * i)
+                   : "memory");
+  }
 }
 SPEC_DEVINL void st_remote32(uint32_t a, unsigned v) {
   asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
@@ -691,6 +702,21 @@ struct Row {
     return f;
   }
 
+  // All CTAs' ids in this thread's bins (every load on its way before the first is waited for).
+  template <int CTAS>
+  SPEC_DEVINL void counts_of(int b0, unsigned (&count)[kMaxC]) const {
+    constexpr int kPer = kMaxC / CTAS;
+    unsigned x[CTAS][kPer];
+#pragma unroll
+    for (int r = 0; r < CTAS; ++r) ld_remote_n<kPer>(remote(&s.fine[b0], r), x[r]);
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      count[q] = 0;
+#pragma unroll
+      for (int r = 0; r < CTAS; ++r) count[q] += x[r][q];
+    }
+  }
+
   // The fine bins [from, to] in which top_p of the weight of {z >= lower} ends, by the ids' numbers in them; or
   // (MASS false) the one of the k-th.  false: fewer than k.  A bin of n ids weighs n times its middle's weight
   // m, but for an error of about 0.0014 m sqrt(n) (ids lie anywhere in it); for the heavy ids, where a single one's
@@ -721,16 +747,22 @@ struct Row {
     // each CTA its part of the bins, a thread one to eight in a row
     static_assert(kFine == kMaxC * kT, "");
     const int per = kMaxC / C, b0 = (rank * kT + tid) * per;
+    unsigned count[kMaxC];
+    if (per == 1)
+      counts_of<8>(b0, count);
+    else if (per == 2)
+      counts_of<4>(b0, count);
+    else if (per == 4)
+      counts_of<2>(b0, count);
+    else
+      counts_of<1>(b0, count);
     u64 v[kMaxC], mine = 0, first_bins = 0;  // (the latter: of heavy ids)
     float err = 0.f, err_heavy = 0.f;
 #pragma unroll
     for (int q = 0; q < kMaxC; ++q) {
       v[q] = 0;
       if (q >= per) continue;
-      unsigned n = 0;
-#pragma unroll
-      for (int r = 0; r < kMaxC; ++r)
-        if (r < C) n += ld_remote32(remote(&s.fine[b0 + q], r));
+      const unsigned n = count[q];
       v[q] = n;
       if (MASS) {
         const float m = fine.middle(b0 + q), x = static_cast<float>(n) * m;
@@ -1319,7 +1351,7 @@ cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   // take turns, fewer, down to four turns and a half: what a cluster's CTAs wait for one another costs more
   // then than reading the row again from the caches.  320 rows of 128256, top-p / mixed parameters: eight
   // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181, by loads slower than these, which take
-  // 179 / 109 with four; 64 rows: eight 47 us, four 62.
+  // 177 / 107 with four; 64 rows: eight 47 us, four 62.
   int C = 1;
   while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
   while (C > 1 && p.rows * C > 9 * sms) C /= 2;
