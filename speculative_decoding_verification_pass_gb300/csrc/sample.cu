@@ -213,12 +213,13 @@ SPEC_DEVINL u64 exp2m1_scaled(u64 g) {
 }
 
 // Where z c is too large for whole powers to leave it exactly in 32 bits: 64.
-// (Few values of such a row are near enough to M to have a weight.)
-__device__ __noinline__ void wide_power(float z, float M, double c, int* e, float* t) {
+// (Few values of such a row are near enough to M to have a weight.)  e, and t's bits: by address, they would
+// lie in memory for every row (320 rows top-p 177 us, mixed filter 107; so 167 and 105).
+__device__ __noinline__ int2 wide_power(float z, float M, double c) {
   const double d = z == M ? 0.0 : (static_cast<double>(z) - static_cast<double>(M)) * c;
   const double n = d < -200.0 ? -200.0 : rint(d);
-  *e = static_cast<int>(n);
-  *t = d < -200.0 ? 0.f : parts(exp2m1_scaled(both(static_cast<float>(d - n)))).x;
+  const float t = d < -200.0 ? 0.f : parts(exp2m1_scaled(both(static_cast<float>(d - n)))).x;
+  return make_int2(static_cast<int>(n), __float_as_int(t));
 }
 
 __device__ u64 one_weight(float z, float M, float c_hi, float c_lo, float zlow, int n0, bool wide, double c);
@@ -242,10 +243,13 @@ struct Weights {
   }
   SPEC_DEVINL void power4(const float4& z, int (&e)[4], float (&t)[4]) const {
     if (wide) {
-      wide_power(z.x, M, c, e, t);
-      wide_power(z.y, M, c, e + 1, t + 1);
-      wide_power(z.z, M, c, e + 2, t + 2);
-      wide_power(z.w, M, c, e + 3, t + 3);
+      const float v[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int2 x = wide_power(v[i], M, c);
+        e[i] = x.x;
+        t[i] = __int_as_float(x.y);
+      }
       return;
     }
     int e0[2], e1[2];
@@ -300,9 +304,11 @@ __device__ __noinline__ u64 one_weight(float z, float M, float c_hi, float c_lo,
   w.n0 = n0;
   int e[2];
   float t[2];
-  if (wide)
-    wide_power(z, M, c, e, t);
-  else
+  if (wide) {
+    const int2 a = wide_power(z, M, c);
+    e[0] = a.x;
+    t[0] = __int_as_float(a.y);
+  } else
     w.power2(z, z, e, t);
   return w.is_large(e[0]) ? w.large(e[0], t[0]) : w.units(e[0], t[0]);
 }
@@ -826,16 +832,19 @@ struct Row {
     }
     if (all < first) return false;
     par ^= 1;
+    int first_bin = -1, last_bin = -1;
 #pragma unroll
     for (int q = 0; q < kMaxC; ++q) {
-      if (q >= per) break;
+      if (q >= per) continue;
       const u64 next = excl + v[q];
-      if (excl < first && first <= next)
-        for (int r = 0; r < C; ++r) st_remote(remote(&s.ex[par][0][0], r), b0 + q);
-      if (excl < last && last <= next)
-        for (int r = 0; r < C; ++r) st_remote(remote(&s.ex[par][1][0], r), b0 + q);
+      if (excl < first && first <= next) first_bin = b0 + q;
+      if (excl < last && last <= next) last_bin = b0 + q;
       excl = next;
     }
+    if (first_bin >= 0)
+      for (int r = 0; r < C; ++r) st_remote(remote(&s.ex[par][0][0], r), first_bin);
+    if (last_bin >= 0)
+      for (int r = 0; r < C; ++r) st_remote(remote(&s.ex[par][1][0], r), last_bin);
     cluster_barrier();
     *from = static_cast<int>(s.ex[par][0][0]);
     *to = static_cast<int>(s.ex[par][1][0]);
@@ -1348,13 +1357,17 @@ cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   const int groups = (p.V + 3) / 4;
   // As many CTAs as keep the row in shared memory, two to an SM, or, where SMs are left over, one for
   // every 512 groups: a row alone takes the less time the more share it.  Of so many rows that their CTAs
-  // take turns, fewer, down to four turns and a half: what a cluster's CTAs wait for one another costs more
-  // then than reading the row again from the caches.  320 rows of 128256, top-p / mixed parameters: eight
-  // CTAs 260 / 129 us, four 206 / 118, two 185 / 134, one 238 / 181, by loads slower than these, which take
-  // 177 / 107 with four; 64 rows: eight 47 us, four 62.
+  // take turns, fewer: what a cluster's CTAs wait for one another costs more then than reading the row
+  // again from the caches, and the more so the longer a row's chain of passes (a filter's is shorter).
+  // Rows of 128256, us with eight / four / two CTAs a row:
+  //                            38 rows           64                152               320
+  //   draws, top-p alone       43 / 38 / 43      56 / 43 / 50      115 / 85 / 68     232 / 168 / 144
+  //   draws, mixed, probs      31 / 38 / 52      43 / 40 / 53      91 / 83 / 85      163 / 129 / 136
+  //   filter, mixed            24 / 32 / 46      30 / 34 / 46      69 / 64 / 71      125 / 104 / 119
   int C = 1;
   while (C < kMaxC && (groups > C * kResident || (groups > C * 512 && p.rows * C <= sms))) C *= 2;
-  while (C > 1 && p.rows * C > 9 * sms) C /= 2;
+  if (C == 8 && p.rows * 8 > (p.out ? 4 : 2) * sms) C = 4;
+  if (C == 4 && p.rows * 4 > 3 * sms && !p.out) C = 2;
   const int per = (groups + C - 1) / C;
   p.resident = per <= kResident;
   cudaLaunchConfig_t cfg = {};
