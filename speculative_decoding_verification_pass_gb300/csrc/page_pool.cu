@@ -10,7 +10,9 @@
 // One CTA keeps the books of a call: its phases depend on one another through
 // counts over all sequences, each phase is short, and a barrier within a CTA
 // costs far less than one across the GPU.  What reads and writes the cache (the
-// copies) is a kernel of its own over all SMs.
+// copies) is a kernel of its own over all SMs.  Of 4 / 64
+// sequences, on the device: free and fork 4.1 / 9.4 us, the books of a reservation 3.1 /
+// 5.6 us: chains of counts, lengths, entries and barriers.
 #include <algorithm>
 
 #include "common.cuh"
@@ -432,7 +434,11 @@ struct Retable {
 
 // ------------------------------------------------------------------- moves
 // A warp moves 16 slots of one KV head, k or v, of one layer at a time (1 to 4
-// KB, all of it in flight before the first store), and a lane their scale.
+// KB, all of it in flight before the first store), and a lane their scale.  Bound
+// by memory: 200 pages of an 8B-shaped bf16 cache (3.36 GB moved) 498 us, 6.73 TB/s,
+// the rate of a plain copy; 1200 pages half used, 8-bit, 300 moved (2.52 GB) 412 us
+// with the books, 6.1 TB/s.  Few pages: 16 slots a warp spread 4 pages of a 1B-shaped
+// cache over 4096 warps, 2.9 us.
 constexpr int kCopyThreads = 256;
 constexpr int kCopyWords = 8;  // 16-byte words a lane: 16 slots of at most 256 bytes
 
