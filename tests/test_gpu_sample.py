@@ -142,6 +142,14 @@ def test_batches(rows):
     check(_peaked(rows, rows, V), sets, seed=rows, draws=2, rows_per_set=5)
 
 
+@pytest.mark.parametrize("rows,V,bf16", [(60, 131077, False), (100, 40001, True), (170, 50257, False),
+                                         (170, 32768, True), (90, 262144, False)])
+def test_batches_of_long_rows(rows, V, bf16):
+    """Rows that share the SMs by two, four and eight CTAs, kept on chip and read again."""
+    sets = [ALL[(i * 5) % len(ALL)] for i in range(rows)]
+    check(_peaked(rows, rows, V), sets, bf16=bf16, seed=rows, draws=2)
+
+
 @pytest.mark.parametrize("draws", [1, 2, 17, 64])
 def test_many_draws(draws):
     check(_peaked(draws, 6, 50257), ALL[:6], draws=draws, seed=draws)
