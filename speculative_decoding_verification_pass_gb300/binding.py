@@ -761,7 +761,7 @@ class Pages:
 
 
 def _page_data(kv) -> spec_page_data:
-    if type(kv) is KV8Cache:
+    if isinstance(kv, KV8Cache):
         return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), kv.k_scale.data_ptr(), kv.v_scale.data_ptr(),
                               kv.n_pages)
     return spec_page_data(kv.k.data_ptr(), kv.v.data_ptr(), None, None, kv.n_pages)
@@ -816,7 +816,7 @@ def spec_pages_compact(pages: "Pages", ws, stream=None):
 def spec_pages_copy(kv, kv_to, src, dst, ws, stream=None):
     """Copy pages src[i] of one cache to pages dst[i] of another of the same kind and shape (or of itself)."""
     a, b = kv.cfg, kv_to.cfg
-    if type(kv) is not type(kv_to) or a is not b and (a.n_layers, a.n_kv_heads, a.head_dim) != (
+    if isinstance(kv, KV8Cache) != isinstance(kv_to, KV8Cache) or a is not b and (a.n_layers, a.n_kv_heads, a.head_dim) != (
             b.n_layers, b.n_kv_heads, b.head_dim):
         raise ValueError("expected two caches of one kind and shape")
     dev, n = kv.k.get_device(), src.numel()
