@@ -349,7 +349,7 @@ class PagedKVCache:
         self.cfg, self.batch, self.n_pages, self.max_pages = cfg, batch, n_pages, max_pages
         self.pool = None
         shape = (cfg.n_layers, n_pages, cfg.n_kv_heads, PAGE_SLOTS, cfg.head_dim)
-        device = device if k is None else k.device
+        device = next((t.device for t in (k, v) if t is not None), device)
         for name, t in (("k", k), ("v", v)):
             if t is not None and (_plain(t, shape, torch.bfloat16, name) is None or t.device != torch.device(device)):
                 raise ValueError(f"{name}: expected a tensor on {device}")

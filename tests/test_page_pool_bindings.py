@@ -2,6 +2,7 @@
 import types
 
 import pytest
+import torch
 
 from speculative_decoding_verification_pass_gb300 import binding as sb
 
@@ -63,3 +64,17 @@ def test_a_derived_cache_is_of_its_base_kind(a, b):
     ids = types.SimpleNamespace(numel=lambda: 1)
     with pytest.raises(ValueError, match="cuda:0"):
         sb.spec_pages_copy(_bare(a), _bare(b), ids, ids, ws)
+
+
+def _rows(cfg, pages, dtype=torch.bfloat16):
+    return torch.zeros(cfg.n_layers, pages, cfg.n_kv_heads, 64, cfg.head_dim, dtype=dtype)
+
+
+def test_a_cache_is_made_around_v_alone():
+    """The other buffers go to the device of the one given."""
+    cfg = sb.ModelConfig(2, 256, 4, 2, 256, 1000)
+    v = _rows(cfg, 3)
+    kv = sb.PagedKVCache(cfg, 2, 3, 4, v=v)
+    assert kv.v is v and kv.k.shape == v.shape and kv.k.device == kv.len.device == v.device
+    with pytest.raises(ValueError):
+        sb.PagedKVCache(cfg, 2, 4, 4, v=v)
