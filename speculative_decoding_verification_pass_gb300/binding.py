@@ -350,9 +350,6 @@ class PagedKVCache:
         self.pool = None
         shape = (cfg.n_layers, n_pages, cfg.n_kv_heads, PAGE_SLOTS, cfg.head_dim)
         device = next((t.device for t in (k, v) if t is not None), device)
-        for name, t in (("k", k), ("v", v)):
-            if t is not None and (_plain(t, shape, torch.bfloat16, name) is None or t.device != torch.device(device)):
-                raise ValueError(f"{name}: expected a tensor on {device}")
         self.k = torch.zeros(shape, dtype=torch.bfloat16, device=device) if k is None else k
         self.v = torch.zeros(shape, dtype=torch.bfloat16, device=device) if v is None else v
         assert self.k.numel() * 2 == int(lib().spec_paged_kv_bytes(ctypes.byref(cfg.c()), n_pages))
@@ -366,6 +363,19 @@ class PagedKVCache:
     @property
     def capacity(self) -> int:
         return self.max_pages * PAGE_SLOTS
+
+    def __setattr__(self, name, value):
+        """A buffer is looked at when it is put in place, not at every call."""
+        if isinstance(value, torch.Tensor):
+            rows = ((self.cfg.n_layers, self.n_pages, self.cfg.n_kv_heads, PAGE_SLOTS, self.cfg.head_dim),
+                    torch.bfloat16)
+            shape, dtype = {"k": rows, "v": rows, "len": ((self.batch,), torch.int32),
+                            "table": ((self.batch, self.max_pages), torch.int32)}.get(name, (value.shape, value.dtype))
+            _plain(value, shape, dtype, name)
+            first = self.__dict__.get("k", value)
+            if value.device != first.device:
+                raise ValueError(f"{name}: expected a tensor on {first.device}")
+        object.__setattr__(self, name, value)
 
     def c(self) -> spec_paged_kv_cache:
         return spec_paged_kv_cache(self.k.data_ptr(), self.v.data_ptr(), self.len.data_ptr(),
@@ -727,18 +737,25 @@ class Pages:
         self.kv = kv
         self._table, self._len = (kv.batch, kv.max_pages), (kv.batch,)
         dev = kv.len.device
+        if not kv.len.is_cuda:
+            raise ValueError("expected a cache on a CUDA device")
         ints = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
         self.mapped = ints(kv.batch) if mapped is None else mapped
         self.ref = ints(kv.n_pages) if ref is None else ref
         self.n_free = ints(1) if n_free is None else n_free
-        for name, n in (("mapped", kv.batch), ("ref", kv.n_pages), ("n_free", 1)):
-            t = getattr(self, name)
-            if _plain(t, (n,), torch.int32, name) is None or t.device != dev:
-                raise ValueError(f"{name}: expected a tensor on {dev}")
         if not all(given):
             d = kv.len.get_device()
             with _on(d):
                 _check(lib().spec_pages_init(self.c(), _raw_stream(stream, d)), "spec_pages_init")
+
+    def __setattr__(self, name, value):
+        """The books are looked at when they are put in place, not at every call."""
+        if isinstance(value, torch.Tensor):
+            kv = self.kv
+            n = {"mapped": kv.batch, "ref": kv.n_pages, "n_free": 1}.get(name)
+            if n is not None and (_plain(value, (n,), torch.int32, name) is None or value.device != kv.len.device):
+                raise ValueError(f"{name}: expected a tensor on {kv.len.device}")
+        object.__setattr__(self, name, value)
 
     def c(self) -> spec_pages:
         kv = self.kv

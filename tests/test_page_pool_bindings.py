@@ -78,3 +78,34 @@ def test_a_cache_is_made_around_v_alone():
     assert kv.v is v and kv.k.shape == v.shape and kv.k.device == kv.len.device == v.device
     with pytest.raises(ValueError):
         sb.PagedKVCache(cfg, 2, 4, 4, v=v)
+
+
+def test_buffers_put_in_place_later_are_looked_at():
+    """Kernels go by the cache's sizes: a buffer of others is refused when it is put there."""
+    cfg = sb.ModelConfig(2, 256, 4, 2, 256, 1000)
+    kv = sb.PagedKVCache(cfg, 2, 5, 4, device="cpu")
+    k, table, length = kv.k, kv.table, kv.len
+    ints = lambda *n: torch.zeros(n, dtype=torch.int32)
+    for name, bad in (("k", _rows(cfg, 4)), ("v", _rows(cfg, 5, torch.float16)), ("v", _rows(cfg, 10)[:, ::2]),
+                      ("v", torch.empty(kv.v.shape, dtype=torch.bfloat16, device="meta")), ("table", ints(2, 3)),
+                      ("table", ints(2, 4).long()), ("table", ints(4, 2).t()), ("len", ints(3)),
+                      ("len", ints(2).float())):
+        with pytest.raises(ValueError, match=name):
+            setattr(kv, name, bad)
+    assert kv.k is k and kv.table is table and kv.len is length
+    good = _rows(cfg, 5)
+    kv.v, kv.table, kv.len = good, ints(2, 4), ints(4)[:2]
+    assert kv.v is good
+    with pytest.raises(ValueError, match="CUDA"):  # the books are kept by kernels
+        sb.Pages(kv, mapped=ints(2), ref=ints(5), n_free=ints(1))
+
+
+def test_books_put_in_place_later_are_looked_at():
+    p = object.__new__(sb.Pages)
+    p.__dict__.update(kv=types.SimpleNamespace(batch=2, n_pages=5, len=torch.zeros(2, dtype=torch.int32)))
+    ints = lambda n: torch.zeros(n, dtype=torch.int32)
+    for name, n in (("mapped", 2), ("ref", 5), ("n_free", 1)):
+        for bad in (ints(n + 1), ints(n).long(), ints(2 * n)[::2] if n > 1 else ints(0), ints(n).to("meta")):
+            with pytest.raises(ValueError, match=name):
+                setattr(p, name, bad)
+        setattr(p, name, ints(n))
