@@ -62,7 +62,9 @@ SPEC_DEVINL int32_t seq_fit(int L, int n, int cap, const int32_t* table, int max
   if (table) {
     const int np = (L + n + kPageSlots - 1) / kPageSlots;
     for (int j = 0; j < np; ++j) {
-      const int pg = __ldg(table + static_cast<long long>(b) * max_pages + j);
+      // (not by the read-only path: the launch before, which the pass's first kernel overlaps up to its
+      // wait, may be one that writes the table, a compaction say)
+      const int pg = table[static_cast<long long>(b) * max_pages + j];
       if (pg < 0 || pg >= n_pages) return SPEC_DEV_BAD_PAGE;
     }
   }
