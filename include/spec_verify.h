@@ -407,7 +407,8 @@ int spec_verify_forward_paged(const spec_model* model, const int32_t* d_tokens, 
                               size_t ws_bytes, void* stream);
 
 /* Rollback of a paged cache on the device: len[b] -= gamma - n_accepted[b]
- * (as spec_kv_truncate).  The pages wholly past the new length are then
+ * (as spec_kv_truncate; a sequence that sat the pass out, see spec_pages_reserve,
+ * is left with SPEC_DEV_BAD_PAGE).  The pages wholly past the new length are then
  * returned by the host page pool (spec_page_pool_release). */
 int spec_paged_kv_truncate(const spec_paged_kv_cache* kv, const int32_t* d_n_accepted, int gamma,
                            void* d_ws, void* stream);
@@ -590,14 +591,17 @@ int spec_verify_forward_kv8(const spec_model* model, const int32_t* d_tokens,
 /* The page pool of a paged cache (bf16 or 8-bit) on the device, in place of the
  * host's: sequences can share pages, and rounds run without the host knowing the
  * lengths.  All arrays are the caller's; table and len are the cache's own:
- *   table   int32 [batch][max_pages]: a page, -1 (none), or -2 - page: a page that
- *           is held but not to be written to (see spec_pages_fork);
+ *   table   int32 [batch][max_pages]: a page, -1 (none), or a page that is held but
+ *           not to be written to: -2 - page (see spec_pages_fork), or
+ *           -2 - SPEC_PAGES_OUT - page as a sequence's last page, where the sequence
+ *           sits passes out (see spec_pages_reserve);
  *   len     int32 [batch];
  *   mapped  int32 [batch]: pages that a sequence holds, a prefix of its row;
  *   ref     int32 [n_pages]: sequences that hold a page, 0 = free;
  *   n_free  int32 [1]: free pages.
  * Limits: batch <= 65535, max_pages * 64 <= 2^20 slots, n_pages * n_kv_heads * 64
  * < 2^31.  Calls on one pool are made on one stream, or ordered by the caller. */
+#define SPEC_PAGES_OUT 0x4000000
 typedef struct {
   int32_t* table;
   int32_t* len;
@@ -631,19 +635,27 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * len[b] + n) need, the lowest-numbered free ones, by sequence and then by
  * position.  A partly filled page that others hold is replaced by a copy of its
  * len[b] % 64 slots; where every holder is about to write to it, the longest of
- * them (the lowest-numbered of equally long ones) keeps it.  n = 0 only returns
- * pages (after a rollback).  A sequence that the free pages do not cover keeps
- * the pages of its length alone, sets SPEC_DEV_NO_PAGES, and is not to be
- * written to: passes refuse it (SPEC_DEV_BAD_PAGE).  One past the capacity, or
- * with pages that are not of the pool, is left as it is (SPEC_DEV_KV_OVERFLOW,
- * SPEC_DEV_BAD_PAGE). */
+ * them (the lowest-numbered of equally long ones) keeps it.  n = 0 without d_n
+ * only returns pages (after a rollback).
+ * A sequence that the free pages do not cover keeps the pages of its length alone
+ * and sets SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or
+ * whose d_n is negative, keeps what it holds and sets SPEC_DEV_KV_OVERFLOW; one
+ * whose d_n is 0 returns pages.  These sit the pass out: their last page is
+ * marked in the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages has
+ * nothing to mark), passes refuse them (SPEC_DEV_BAD_PAGE), nothing is written to
+ * their pages, and spec_paged_kv_truncate, spec_kv8_truncate and
+ * spec_kv8_tree_commit leave their lengths and rows (SPEC_DEV_BAD_PAGE).  So a
+ * round may go on behind a short pool: what the pass and the acceptance put out
+ * for a marked sequence is of no account, and the next reservation tries it again
+ * at the length that it had.  A sequence with pages that are not of the pool is left
+ * as it is (SPEC_DEV_BAD_PAGE). */
 int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
                        const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream);
 
 /* Sequence d_dst[i] becomes a second d_src[i], i < n <= 65535: it returns its pages and
  * shares the source's up to its length.  Nothing is copied until one of them is
  * reserved for; a partly filled last page is marked in both rows as not to be
- * written to until then.  Pairs out of range, to itself, with a destination
+ * written to until then (a source that sits passes out: its second does too).  Pairs out of range, to itself, with a destination
  * given twice or one that is a source too, are left out (SPEC_DEV_BAD_SEQ). */
 int spec_pages_fork(const spec_pages* pages, int n, const int32_t* d_src, const int32_t* d_dst, void* d_ws,
                     size_t ws_bytes, void* stream);

@@ -8,11 +8,13 @@ The pages describe a block table whose rollback returns pages to a free list
 pages are taken lowest number first, by sequence and then by position; a page
 held by several sequences is counted, and copied before one of them writes to
 it, unless every holder is about to, when the longest (then the lowest-numbered)
-keeps it.
+keeps it.  A sequence that a reservation gives no slots sits the pass out: its
+last page is marked until a reservation serves it.
 """
 from __future__ import annotations
 
 SLOTS = 64
+OUT = 1 << 26
 
 
 def pages_for(slots: int) -> int:
@@ -25,6 +27,7 @@ class Pool:
         self.held = [[] for _ in range(batch)]   # pages in position order
         self.len = [0] * batch
         self.guard = [False] * batch             # its partly filled page is not to be written to
+        self.out = [set() for _ in range(batch)]  # entries that say that it sits passes out
 
     def ref(self) -> list:
         r = [0] * self.n_pages
@@ -35,20 +38,32 @@ class Pool:
 
     def table(self) -> list:
         out = []
-        for row, g, length in zip(self.held, self.guard, self.len):
+        for row, g, marks, length in zip(self.held, self.guard, self.out, self.len):
             e = list(row)
             if g:
                 e[length // SLOTS] = -2 - e[length // SLOTS]
+            for i in marks:
+                e[i] = -2 - OUT - e[i]
             out.append(e + [-1] * (self.max_pages - len(e)))
         return out
 
+    def sit_out(self, b):
+        last = pages_for(self.len[b]) - 1
+        if last >= 0:
+            self.guard[b] = False
+            self.out[b].add(last)
+
     def reserve(self, n) -> tuple[list, list]:
-        """(moves (source, destination, slots), sequences that got nothing)."""
+        """(moves (source, destination, slots), sequences that the free pages did not cover)."""
+        by_seq = not isinstance(n, int)
         n = [n] * self.batch if isinstance(n, int) else list(n)
         ok = [self.len[b] + n[b] <= self.max_pages * SLOTS for b in range(self.batch)]
         for b in range(self.batch):
             if ok[b]:
                 self.held[b] = self.held[b][:pages_for(self.len[b])]
+                self.out[b] = {i for i in self.out[b] if i < len(self.held[b])}
+            elif self.len[b] <= self.max_pages * SLOTS:
+                self.sit_out(b)
         ref = self.ref()
         writers = {}
         for b in range(self.batch):
@@ -68,15 +83,19 @@ class Pool:
             taken += c
             if c and taken > len(free):
                 short.append(b)
-                self.guard[b] = self.guard[b] or copy
+                self.sit_out(b)
+                continue
+            if n[b] == 0:
+                if by_seq:
+                    self.sit_out(b)
                 continue
             got = free[taken - c:taken]
             if copy:
                 q = got.pop(0)
                 moves.append((row[-1], q, L % SLOTS))
                 row[-1] = q
-            if partial:
-                self.guard[b] = False
+            self.guard[b] = False
+            self.out[b].discard(len(row) - 1)
             row += got
         return moves, short
 
@@ -91,7 +110,8 @@ class Pool:
                 continue
             self.held[b] = self.held[a][:pages_for(self.len[a])]
             self.len[b] = self.len[a]
-            self.guard[b] = self.len[a] % SLOTS > 0
+            self.out[b] = self.out[a] & {len(self.held[b]) - 1}
+            self.guard[b] = self.len[a] % SLOTS > 0 and not self.out[b]
             if self.guard[b]:
                 self.guard[a] = True
         return bad
@@ -99,7 +119,7 @@ class Pool:
     def free(self, seqs):
         for b in seqs:
             if 0 <= b < self.batch:
-                self.held[b], self.len[b], self.guard[b] = [], 0, False
+                self.held[b], self.len[b], self.guard[b], self.out[b] = [], 0, False, set()
 
     def compact(self) -> list:
         ref = self.ref()

@@ -24,6 +24,7 @@ DEV_BAD_TOKEN, DEV_KV_OVERFLOW, DEV_Q_ZERO, DEV_TIMEOUT, DEV_BAD_NACC, DEV_BAD_T
 DEV_EMPTY_MASK = 0x40
 DEV_BAD_PAGE = 0x80
 DEV_BAD_PARAM, DEV_BAD_SEQ, DEV_NO_PAGES = 0x100, 0x200, 0x400
+PAGES_OUT = 0x4000000
 
 
 class SpecError(RuntimeError):
@@ -767,6 +768,12 @@ class Pages:
         return spec_pages(table.data_ptr(), length.data_ptr(), self.mapped.data_ptr(), self.ref.data_ptr(),
                           self.n_free.data_ptr(), kv.batch, kv.n_pages, kv.max_pages)
 
+    def waiting(self) -> torch.Tensor:
+        """bool [B], on the device: sequences that sit the pass out after the last reservation (not enough pages, no
+        room, or no slots asked for), or hold no page at all."""
+        last = self.kv.table.gather(1, (self.mapped - 1).clamp_(0, self.kv.max_pages - 1).long()[:, None])[:, 0]
+        return (self.mapped <= 0) | (last <= -2 - PAGES_OUT)
+
     def _device(self, ws) -> int:
         """The books' device, on which the cache's buffers and the workspace lie too."""
         kv = self.kv
@@ -796,7 +803,8 @@ def spec_pages_workspace_bytes(batch: int, n_pages: int, max_pages: int) -> int:
 
 
 def spec_pages_reserve(pages: "Pages", n, ws, stream=None):
-    """Pages for n more slots a sequence (a number, or an int32 tensor [B]); shared ones are copied before a write."""
+    """Pages for n more slots a sequence (a number, or an int32 tensor [B]); shared ones are copied before a write.
+    Sequences that get none sit the pass out (Pages.waiting)."""
     kv, dev = pages.kv, pages._device(ws)
     per = None
     if isinstance(n, torch.Tensor):

@@ -1624,8 +1624,10 @@ __global__ void tree_len_kernel(int32_t* len, const int32_t* path, const int32_t
   len[b] = l - n + 1 + m;
 }
 
+// (table: of a paged cache, or nullptr.  A sequence that sat the pass out was not advanced by it: nothing of it is
+// dropped.)
 __global__ void truncate_kernel(int32_t* len, const int32_t* n_acc, int B, int gamma,
-                                int32_t* status) {
+                                const int32_t* table, int max_pages, int32_t* status) {
   grid_dep_wait();
   grid_dep_launch();
   const int b = blockIdx.x * blockDim.x + threadIdx.x;
@@ -1635,12 +1637,17 @@ __global__ void truncate_kernel(int32_t* len, const int32_t* n_acc, int B, int g
     set_status(status, SPEC_DEV_BAD_NACC);
     return;
   }
-  const int drop = gamma - n;
-  if (len[b] < drop) {
+  const int drop = gamma - n, l = len[b];
+  if (table && l > 0 && l <= max_pages * kPageSlots &&
+      sits_out(table[static_cast<long long>(b) * max_pages + (l - 1) / kPageSlots])) {
+    set_status(status, SPEC_DEV_BAD_PAGE);
+    return;
+  }
+  if (l < drop) {
     set_status(status, SPEC_DEV_KV_OVERFLOW);
     return;
   }
-  len[b] -= drop;
+  len[b] = l - drop;
 }
 
 cudaError_t launch_pdl(const void* fn, dim3 grid, dim3 block, void** args, cudaStream_t stream,
@@ -1757,10 +1764,10 @@ cudaError_t launch_sample(const SampleParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, int32_t* status,
-                            cudaStream_t stream, bool pdl) {
+cudaError_t launch_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, const int32_t* table,
+                            int max_pages, int32_t* status, cudaStream_t stream, bool pdl) {
   if (B == 0) return cudaSuccess;
-  void* args[] = {&len, const_cast<int32_t**>(&n_acc), &B, &gamma, &status};
+  void* args[] = {&len, const_cast<int32_t**>(&n_acc), &B, &gamma, const_cast<int32_t**>(&table), &max_pages, &status};
   return launch_pdl(reinterpret_cast<const void*>(truncate_kernel), dim3((B + 127) / 128),
                     dim3(128), args, stream, pdl);
 }

@@ -1048,15 +1048,6 @@ int spec_verify_forward_paged(const spec_model* m, const int32_t* d_tokens, int 
                              stream, pg);
 }
 
-int spec_paged_kv_truncate(const spec_paged_kv_cache* kv, const int32_t* d_n_accepted, int gamma,
-                           void* d_ws, void* stream) {
-  spec_kv_cache view{};
-  PageDesc pg;
-  const int r = paged_view(kv, &view, &pg);
-  if (r) return r;
-  return spec_kv_truncate(&view, d_n_accepted, gamma, d_ws, stream);
-}
-
 int spec_tree_masks(const int32_t* parents, int n_nodes, uint64_t* out_anc, int32_t* out_depth) {
   if (!parents || !out_anc || !out_depth || n_nodes < 1) return SPEC_EINVAL;
   if (n_nodes > kTreeMaxNodes) return SPEC_ESIZE;
@@ -1279,13 +1270,27 @@ int spec_draft_sample(const float* d_logits, int rows, int vocab, float temperat
   return SPEC_OK;
 }
 
-int spec_kv_truncate(const spec_kv_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws,
-                     void* stream) {
-  if (!kv || !kv->len || !d_n_accepted || !d_ws) return SPEC_EINVAL;
-  if (gamma < 0 || kv->batch < 0) return SPEC_EINVAL;
-  SPEC_CUDA(launch_truncate(kv->len, d_n_accepted, kv->batch, gamma, static_cast<int32_t*>(d_ws),
+static int truncate_impl(int32_t* len, int batch, const int32_t* table, int max_pages, const int32_t* d_n_accepted,
+                         int gamma, void* d_ws, void* stream) {
+  if (!len || !d_n_accepted || !d_ws) return SPEC_EINVAL;
+  if (gamma < 0 || batch < 0) return SPEC_EINVAL;
+  SPEC_CUDA(launch_truncate(len, d_n_accepted, batch, gamma, table, max_pages, static_cast<int32_t*>(d_ws),
                             static_cast<cudaStream_t>(stream), true));
   return SPEC_OK;
+}
+
+int spec_kv_truncate(const spec_kv_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws,
+                     void* stream) {
+  if (!kv) return SPEC_EINVAL;
+  return truncate_impl(kv->len, kv->batch, nullptr, 0, d_n_accepted, gamma, d_ws, stream);
+}
+
+int spec_paged_kv_truncate(const spec_paged_kv_cache* kv, const int32_t* d_n_accepted, int gamma,
+                           void* d_ws, void* stream) {
+  spec_kv_cache view{};
+  PageDesc pg;
+  if (const int r = paged_view(kv, &view, &pg)) return r;
+  return truncate_impl(kv->len, kv->batch, kv->table, kv->max_pages, d_n_accepted, gamma, d_ws, stream);
 }
 
 int spec_mask_logits(float* d_logits, const uint32_t* d_allowed, int rows, int vocab, void* d_ws,
@@ -1575,10 +1580,7 @@ int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) 
 int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws, void* stream) {
   if (const int r = kv8_checks(nullptr, kv)) return r;
   if (!aligned4(d_n_accepted) || !aligned4(d_ws)) return SPEC_EINVAL;
-  spec_kv_cache view{};
-  view.len = kv->len;
-  view.batch = kv->batch;
-  return spec_kv_truncate(&view, d_n_accepted, gamma, d_ws, stream);
+  return truncate_impl(kv->len, kv->batch, kv->table, kv->max_pages, d_n_accepted, gamma, d_ws, stream);
 }
 
 int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv, const int32_t* d_path,
@@ -1731,7 +1733,8 @@ int pages_checks(const spec_pages* p) {
   if (p->batch < 0 || p->n_pages <= 0 || p->max_pages <= 0) return SPEC_EINVAL;
   for (const int32_t* a : {p->table, p->len, p->mapped, p->ref, p->n_free})
     if (!aligned4(a)) return SPEC_EINVAL;
-  if (p->batch > 65535 || p->max_pages > kKv8MaxSlots / SPEC_PAGE_SLOTS) return SPEC_ESIZE;
+  if (p->batch > 65535 || p->max_pages > kKv8MaxSlots / SPEC_PAGE_SLOTS || p->n_pages >= SPEC_PAGES_OUT / 2)
+    return SPEC_ESIZE;
   return SPEC_OK;
 }
 

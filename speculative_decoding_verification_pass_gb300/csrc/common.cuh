@@ -53,6 +53,14 @@ SPEC_DEVINL uint32_t ld_acquire(const unsigned* p) {
 // a page id outside [0, n_pages) is clamped, the pass flags it beforehand).
 constexpr int kPageSlots = SPEC_PAGE_SLOTS;
 
+// Entries of a page table (the device pool's): a page, -1, or a page that is held but not to be written to,
+// as -2 - page (shared by a fork) or -2 - SPEC_PAGES_OUT - page (the sequence sits passes out).  Passes refuse
+// both as pages outside the pool.
+SPEC_DEVINL int guarded(int page) { return -2 - page; }
+SPEC_DEVINL int sat_out(int page) { return -2 - SPEC_PAGES_OUT - page; }
+SPEC_DEVINL bool sits_out(int e) { return e <= -2 - SPEC_PAGES_OUT; }
+SPEC_DEVINL int held_page(int e) { return sits_out(e) ? -2 - SPEC_PAGES_OUT - e : e < -1 ? -2 - e : e; }
+
 // The pass's slot check: len + n within the capacity and, for a paged cache,
 // every page covering slots [0, len + n) a valid page id.  0 when it fits,
 // else the status bit to raise.

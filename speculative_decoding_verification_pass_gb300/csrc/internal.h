@@ -321,8 +321,8 @@ extern "C" int spec_internal_lm_head(const spec_model* m, const uint16_t* d_hidd
                                      int32_t* status, int max_vocab, int max_grid, void* stream);
 namespace spec {
 
-cudaError_t launch_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, int32_t* status,
-                            cudaStream_t stream, bool pdl);
+cudaError_t launch_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, const int32_t* table,
+                            int max_pages, int32_t* status, cudaStream_t stream, bool pdl);
 
 // ------------------------------------------------------------- draft trees
 constexpr int kTreeMaxNodes = 64;  // one 64-bit ancestor mask per node

@@ -24,12 +24,6 @@ namespace {
 constexpr int kT = 1024;
 constexpr int kW = kT / 32;
 
-// A table entry is a page, -1, or -2 - page: held, but not to be written to (a
-// partly filled page that others hold too).  Passes refuse the latter as a page
-// outside the pool.
-SPEC_DEVINL int held_page(int e) { return e < -1 ? -2 - e : e; }
-SPEC_DEVINL int guarded(int page) { return -2 - page; }
-
 struct Scratch {
   int32_t *writers, *keeper, *taken;  // [n_pages]
   int32_t *need, *first, *copy;       // [B]
@@ -129,6 +123,12 @@ SPEC_DEVINL int give_back(const PagesParams& p, int b, int from, int to) {
   return freed;
 }
 
+// Sequence b, of `base` pages by its length, gets no pass: its last page says so, until a reservation serves it.
+SPEC_DEVINL void sit_out(const PagesParams& p, int b, int base) {
+  int32_t* e = p.table + static_cast<long long>(b) * p.max_pages + base - 1;
+  if (base) *e = sat_out(held_page(*e));
+}
+
 // The `want` lowest free pages, in order, to list; how many there are.
 SPEC_DEVINL int lowest_free(const PagesParams& p, int want, int32_t* list, int* red) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -174,8 +174,12 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PagesParams p, 
     const int base = bad ? 0 : pages_for(L);
     if (!bad && (m < base || m > p.max_pages || !entries_ok(p, b, max(base - 1, 0), m))) bad = SPEC_DEV_BAD_PAGE;
     if (bad) {
+      const int last = L > 0 && L <= cap ? pages_for(L) : 0;  // (its books may be sound: then it sits the pass out)
+      const bool mark = bad == SPEC_DEV_KV_OVERFLOW && last && m >= last && m <= p.max_pages &&
+                        entries_ok(p, b, last - 1, last);
       if (lane == 0) {
         set_status(p.status, bad);
+        if (mark) sit_out(p, b, last);
         s.need[b] = -1;
       }
       continue;
@@ -244,8 +248,12 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PagesParams p, 
     if (c > 0 && at + c > there) {
       if (lane == 0) {
         set_status(p.status, SPEC_DEV_NO_PAGES);
-        if (copy) row[base - 1] = guarded(pg);
+        sit_out(p, b, base);
       }
+      continue;
+    }
+    if ((d_n ? d_n[b] : n) == 0) {  // (of pages returned alone, without counts by sequence, marks stay as they are)
+      if (lane == 0 && d_n) sit_out(p, b, base);
       continue;
     }
     for (int i = lane; i < need; i += 32) {
@@ -254,7 +262,7 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PagesParams p, 
       p.ref[q] = 1;
     }
     if (lane == 0) {
-      if (writes) row[base - 1] = pg;
+      if (base && !copy) row[base - 1] = writes ? pg : held_page(row[base - 1]);
       if (copy) {
         const int q = s.taken[at], i = atomicAdd(&s_moves, 1);
         row[base - 1] = q;
@@ -314,13 +322,13 @@ __global__ void __launch_bounds__(kT) pages_fork_kernel(const PagesParams p, int
     int32_t *from = p.table + static_cast<long long>(a) * p.max_pages,
             *to = p.table + static_cast<long long>(b) * p.max_pages;
     for (int j = lane; j < base; j += 32) {
-      const int pg = held_page(from[j]);
+      const int e = from[j], pg = held_page(e);
       atomicAdd(p.ref + pg, 1);
       // a partly filled page is shared now: not to be written to by either (several forks of one source
-      // put the same word there)
-      const bool part = j == base - 1 && L % kPageSlots;
+      // put the same word there); what sits out does so twice
+      const bool out = j == base - 1 && sits_out(e), part = j == base - 1 && L % kPageSlots && !out;
       if (part) from[j] = guarded(pg);
-      to[j] = part ? guarded(pg) : pg;
+      to[j] = out ? e : part ? guarded(pg) : pg;
     }
     if (lane == 0) {
       if (freed) atomicAdd(&s_freed, freed);
@@ -460,7 +468,7 @@ __global__ void __launch_bounds__(kCopyThreads) pages_move_kernel(const PageMove
         if (to < 0)
           set_status(m.status, SPEC_DEV_BAD_PAGE);  // a page that nobody holds by the counts
         else
-          row[j] = e < 0 ? guarded(to) : to;
+          row[j] = sits_out(e) ? sat_out(to) : e < 0 ? guarded(to) : to;
       }
     }
   }

@@ -24,6 +24,10 @@ def _ints(x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+def _held(e):
+    return e if e >= -1 else -2 - e if e > -2 - sb.PAGES_OUT else -2 - sb.PAGES_OUT - e
+
+
 class Round:
     """A cache with its device pool, a model, and the passes on them."""
 
@@ -58,9 +62,9 @@ class Round:
 
     def bytes_of(self, b, slots):
         """What sequence b's first `slots` slots hold, k and v (and the scales of their blocks)."""
-        row = self.kv.table[b].tolist()
-        rows = [row[t // 64] for t in range(slots)]
-        page, at = torch.tensor(rows, device="cuda"), torch.arange(slots, device="cuda") % 64
+        row = [_held(e) for e in self.kv.table[b].tolist()]
+        page = torch.tensor([row[t // 64] for t in range(slots)], dtype=torch.long, device="cuda")
+        at = torch.arange(slots, device="cuda") % 64
         out = [t.view(torch.uint8)[:, page, :, at].cpu() for t in (self.kv.k, self.kv.v)]
         if self.kv8:
             blocks = torch.arange(0, slots, 16, device="cuda")
@@ -101,3 +105,116 @@ def test_a_pass_right_behind_a_compaction(kv8, schedule, monkeypatch):
         r.close()
     for a, b in zip(*runs):
         assert torch.equal(a, b)
+
+
+def _same(a, b):
+    return len(a) == len(b) and all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("schedule", ["persistent", "per_step"])
+@pytest.mark.parametrize("kv8", [False, True])
+def test_a_short_pool_loses_no_tokens(kv8, schedule, monkeypatch):
+    """Reserve, pass and rollback with pages for one of three: the others keep lengths and rows, and their next pass is
+    that of a pool that never ran short."""
+    if schedule == "per_step":
+        monkeypatch.setenv("SPEC_FORWARD_PERSISTENT", "0")
+    prompt, first, second = _tokens(1, 3, 60), _tokens(2, 3, 5), _tokens(3, 3, 5)
+    last = []
+    for pages in (4, 12):
+        r = Round(kv8, 3, pages, 4)
+        r.reserve(60)
+        r.forward(prompt)
+        if pages == 4:
+            held = [r.bytes_of(b, 60) for b in (1, 2)]
+            r.reserve(5)
+            assert r.status() == sb.DEV_NO_PAGES and r.pages.waiting().tolist() == [False, True, True]
+            r.forward(first)
+            assert r.status() == sb.DEV_BAD_PAGE
+            r.truncate([2, 1, 0], 4)
+            assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [63, 60, 60]
+            if kv8:  # the same of a tree's commit: the root and three accepted nodes
+                sb.spec_kv8_tree_commit(CFG, r.kv, _ints([[1, 2, 4, -1, -1]] * 3), _ints([0, 3, 3]), 5, r.ws)
+                assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [59, 60, 60]
+            r.reserve(0)  # pages returned alone: it changes nothing for those that wait
+            assert r.status() == 0 and r.pages.waiting().tolist() == [False, True, True]
+            assert all(_same(x, r.bytes_of(b, 60)) for x, b in zip(held, (1, 2)))
+        sb.spec_pages_free(r.pages, _ints([0]), r.ws)
+        r.reserve([0, 5, 5])
+        assert r.status() == 0 and r.pages.waiting().tolist() == [True, False, False]
+        z = r.forward(second)
+        assert r.kv.len.tolist() == [0, 65, 65]
+        last.append(z[1:].clone())
+        r.close()
+    assert torch.equal(*last)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_sequences_without_slots_sit_the_pass_out(kv8):
+    """No slots asked for, with room in the last page and without, a last page that is full, one that a longer sequence
+    holds too after a rollback, and a sequence at its capacity: nothing is written for them, nothing dropped."""
+    r = Round(kv8, 6, 40, 3)
+    lens = [70, 10, 61, 128, 70, 190]
+    r.reserve(lens)
+    r.kv.k.view(torch.uint8).random_(0, 120)
+    r.kv.v.view(torch.uint8).random_(0, 120)
+    r.kv.len.copy_(_ints(lens))
+    sb.spec_pages_fork(r.pages, _ints([0]), _ints([4]), r.ws)
+    r.kv.len[4] = 60
+    held = [r.bytes_of(b, x) for b, x in enumerate([0, 10, 61, 128, 60, 190])]
+    r.reserve([5, 0, 0, 0, 0, 5])
+    assert r.status() == sb.DEV_KV_OVERFLOW and r.pages.waiting().tolist() == [False] + [True] * 5
+    r.forward(_tokens(4, 6, 5))
+    assert r.status() & ~sb.DEV_KV_OVERFLOW == sb.DEV_BAD_PAGE
+    r.truncate([1, 0, 0, 0, 0, 0], 4)
+    assert r.status() == sb.DEV_BAD_PAGE
+    assert r.kv.len.tolist() == [72, 10, 61, 128, 60, 190]
+    r.reserve([0, 5, 5, 5, 5, 2])  # a copy of what sequence 4 shares, and pages of their own for the others
+    assert r.status() == 0 and r.pages.waiting().tolist() == [True] + [False] * 5
+    for b, x in enumerate([0, 10, 61, 128, 60, 190]):
+        assert b == 0 or _same(held[b], r.bytes_of(b, x)), b
+    r.forward(_tokens(5, 6, 2))
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [72, 12, 63, 130, 62, 192]
+    r.close()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_forks_and_compaction_keep_who_sits_out(kv8):
+    r = Round(kv8, 4, 6, 3)
+    r.reserve([64, 0, 60, 100])
+    r.kv.len.copy_(_ints([64, 0, 60, 100]))
+    sb.spec_pages_free(r.pages, _ints([2]), r.ws)
+    r.reserve([65, 0, 0, 5])
+    r.reserve([0, 0, 0, 0])
+    assert r.status() == 0 and r.pages.waiting().all()
+    sb.spec_pages_fork(r.pages, _ints([0, 3]), _ints([1, 2]), r.ws)
+    out = [[-2 - sb.PAGES_OUT - 0, -1, -1]] * 2
+    assert r.kv.table.tolist() == out + [[2, -2 - sb.PAGES_OUT - 3, -1]] * 2
+    sb.spec_pages_compact(r.pages, r.ws)
+    t = r.kv.table.tolist()
+    assert t[:2] == out and t[2] == t[3] == [2, -2 - sb.PAGES_OUT - 1, -1] and r.status() == 0
+    r.truncate([0, 0, 0, 0], 4)
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [64, 64, 100, 100]
+    r.reserve(1)  # both of a pair write: a page each past a full one, the first keeps the other, the last copies
+    assert r.status() == 0 and r.pages.waiting().tolist() == [False] * 4
+    assert r.kv.table.tolist() == [[0, 3, -1], [0, 4, -1], [2, 1, -1], [2, 5, -1]]
+    r.close()
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_a_fork_can_still_be_rolled_back(kv8):
+    """The mark of a shared page forbids writes alone."""
+    r = Round(kv8, 2, 6, 3)
+    r.reserve([75, 0])
+    r.kv.len.copy_(_ints([75, 0]))
+    sb.spec_pages_fork(r.pages, _ints([0]), _ints([1]), r.ws)
+    r.truncate([1, 3], 4)
+    assert r.status() == 0 and r.kv.len.tolist() == [72, 74]
+    r.close()
+
+
+def test_pools_of_more_pages_than_marks_tell_apart_are_refused():
+    kv = sb.PagedKVCache(CFG, 1, 1, 1)
+    p = sb.Pages(kv).c()
+    p.n_pages = sb.PAGES_OUT // 2
+    with pytest.raises(sb.SpecError):
+        sb._check(sb.lib().spec_pages_fork(p, 0, None, None, sb.workspace(256).data_ptr(), 1 << 40, None), "fork")
