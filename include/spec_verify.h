@@ -637,8 +637,8 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * len[b] % 64 slots; where every holder is about to write to it, the longest of
  * them (the lowest-numbered of equally long ones) keeps it.  n = 0 without d_n
  * only returns pages (after a rollback).
- * A sequence that the free pages do not cover keeps the pages of its length alone
- * and sets SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or
+ * A sequence that the free pages left by those before it do not cover keeps the
+ * pages of its length alone (they go to later ones that need fewer) and sets SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or
  * whose d_n is negative, keeps what it holds and sets SPEC_DEV_KV_OVERFLOW; one
  * whose d_n is 0 returns pages.  These sit the pass out: their last page is
  * marked in the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages has

@@ -80,8 +80,7 @@ class Pool:
             partial = bool(n[b]) and L % SLOTS > 0
             copy = partial and keeper.get(row[-1]) != b
             c = (pages_for(L + n[b]) - pages_for(L) if n[b] else 0) + copy
-            taken += c
-            if c and taken > len(free):
+            if taken + c > len(free):  # (a later sequence may need less)
                 short.append(b)
                 self.sit_out(b)
                 continue
@@ -89,7 +88,8 @@ class Pool:
                 if by_seq:
                     self.sit_out(b)
                 continue
-            got = free[taken - c:taken]
+            got = free[taken:taken + c]
+            taken += c
             if copy:
                 q = got.pop(0)
                 moves.append((row[-1], q, L % SLOTS))

@@ -237,7 +237,25 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PagesParams p, 
   __syncthreads();
   const int there = lowest_free(p, min(run, p.n_pages), s.taken, red);
   __syncthreads();
-  // 4. the pages are put in place, in order, as long as they last
+  if (run > there) {  // not enough for all: in order, whoever what is left covers (a warp; first: -1 for the others)
+    if (warp == 0) {
+      int taken = 0;
+      for (int b0 = 0; b0 < p.B; b0 += 32) {
+        const int b = b0 + lane;
+        const int c = b < p.B ? max(s.need[b], 0) + s.copy[b] : 0;
+        int first = 0;
+        for (int i = 0; i < 32; ++i) {
+          const int ci = __shfl_sync(0xffffffffu, c, i);
+          const bool fits = taken + ci <= there;
+          if (lane == i) first = fits ? taken : -1;
+          if (fits) taken += ci;
+        }
+        if (b < p.B) s.first[b] = first;
+      }
+    }
+    __syncthreads();
+  }
+  // 4. the pages are put in place
   for (int b = warp; b < p.B; b += kW) {
     const int need = s.need[b];
     if (need < 0) continue;
@@ -245,7 +263,7 @@ __global__ void __launch_bounds__(kT) pages_reserve_kernel(const PagesParams p, 
     int32_t* row = p.table + static_cast<long long>(b) * p.max_pages;
     int pg, key;
     const bool writes = partial(b, &pg, &key);
-    if (c > 0 && at + c > there) {
+    if (at < 0) {
       if (lane == 0) {
         set_status(p.status, SPEC_DEV_NO_PAGES);
         sit_out(p, b, base);

@@ -6,6 +6,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import pool as OP
 from speculative_decoding_verification_pass_gb300 import binding as sb
 from speculative_decoding_verification_pass_gb300 import workloads as wl
 
@@ -218,3 +219,42 @@ def test_pools_of_more_pages_than_marks_tell_apart_are_refused():
     p.n_pages = sb.PAGES_OUT // 2
     with pytest.raises(sb.SpecError):
         sb._check(sb.lib().spec_pages_fork(p, 0, None, None, sb.workspace(256).data_ptr(), 1 << 40, None), "fork")
+
+
+def test_a_demand_that_is_not_met_leaves_the_pages_to_the_others():
+    r = Round(False, 5, 5, 8)
+    r.reserve([6 * 64, 64, 1, 65, 64])
+    assert r.status() == sb.DEV_NO_PAGES and r.pages.waiting().tolist() == [True] + [False] * 4
+    assert [x[:3] for x in r.kv.table.tolist()] == [[-1, -1, -1], [0, -1, -1], [1, -1, -1], [2, 3, -1], [4, -1, -1]]
+    assert r.pages.mapped.tolist() == [0, 1, 1, 2, 1] and r.pages.n_free.item() == 0
+    r.close()
+
+
+@pytest.mark.parametrize("B,N,P", [(40, 60, 9), (300, 170, 6), (2100, 3000, 5)])
+def test_short_pools_against_the_model(B, N, P):
+    """Demands of all sizes on too few pages, copies among them, more sequences than threads."""
+    g = wl.rng(B, 50)
+    kv = sb.PagedKVCache(sb.ModelConfig(1, 128, 2, 1, 128, 100), B, N, P)
+    pages, ws = sb.Pages(kv), sb.workspace(sb.spec_pages_workspace_bytes(B, N, P))
+    m = OP.Pool(B, N, P)
+    served = refused = 0
+    for i in range(12):
+        n = [int(x) for x in g.choice([0, 1, 5, 63, 64, 65, 130, 200], size=B)]
+        sb.spec_pages_reserve(pages, _ints(n), ws)
+        _, short = m.reserve(n)
+        over = any(x + k > P * 64 for x, k in zip(m.len, n))
+        want = (sb.DEV_NO_PAGES if short else 0) | (sb.DEV_KV_OVERFLOW if over else 0)
+        assert sb.spec_device_status(ws)[1] == want
+        m.len = [x + k if b not in short and x + k <= P * 64 else x for b, (x, k) in enumerate(zip(m.len, n))]
+        served, refused = served + B - len(short), refused + len(short)
+        kv.len.copy_(_ints(m.len))
+        gone = [int(b) for b in g.permutation(B)[:B // 3]]
+        left = [b for b in range(B) if b not in gone]
+        src = [int(g.choice(left)) for _ in gone[::2]]
+        sb.spec_pages_free(pages, _ints(gone), ws)
+        sb.spec_pages_fork(pages, _ints(src), _ints(gone[::2]), ws)
+        m.free(gone)
+        assert m.fork(src, gone[::2]) == []
+        assert kv.table.tolist() == m.table() and kv.len.tolist() == m.len
+        assert pages.ref.tolist() == m.ref() and pages.n_free.item() == m.ref().count(0)
+    assert served > B and refused > B
