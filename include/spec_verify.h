@@ -456,7 +456,8 @@ int spec_page_pool_free_pages(const spec_page_pool* pool);
  * workspace of this library as d_ws (its status word is used) and works on
  * the current device; `cfg` gives the layer count and the head shape.
  * Two sequences may share pages that neither appends to (a common prefix); a
- * page that receives rows belongs to one sequence alone.  Pointers that are not
+ * block of 16 slots that receives rows belongs to one sequence alone (the device
+ * page pool sees to it).  Pointers that are not
  * aligned as their element (uint64 8 bytes, other 4) are SPEC_EINVAL.
  *
  * One pass: for each layer spec_kv8_append then spec_kv8_attention, both at
@@ -517,7 +518,10 @@ int spec_rope_table(const spec_rope_config* rope, float* d_table, void* stream);
  * need; when it grows, the rows held are re-rounded at it.  A sequence whose
  * slots pass the capacity or lie on a page id outside the pool sets
  * SPEC_DEV_KV_OVERFLOW / SPEC_DEV_BAD_PAGE and gets nothing written to the
- * cache (its q_out is unspecified).  1 <= n <= 128. */
+ * cache (its q_out is unspecified).  Where a sequence that sits out (device page
+ * pool) holds rows of the same block, the block's scale and those rows stay as they
+ * are: new rows that need a larger one set SPEC_DEV_BAD_PAGE and are held as
+ * +-448 s at most (spec_kv8_advance does not count them).  1 <= n <= 128. */
 int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
                     const void* d_q, int64_t q_ld, const void* d_k, int64_t k_ld, const void* d_v,
                     int64_t v_ld, int is_f32, const int32_t* d_depth,
@@ -647,7 +651,10 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * spec_kv8_tree_commit leave their lengths and rows (SPEC_DEV_BAD_PAGE).  So a
  * round may go on behind a short pool: what the pass and the acceptance put out
  * for a marked sequence is of no account, and the next reservation tries it again
- * at the length that it had.  A sequence with pages that are not of the pool is left
+ * at the length that it had.  In an 8-bit pool one that keeps a partly filled
+ * page waits too (SPEC_DEV_BAD_PAGE from passes, spec_kv8_advance and the rollbacks;
+ * it is not marked) while a marked sequence holds rows of the 16 slots that its next
+ * slot is in, whose scale its new rows could change.  A sequence with pages that are not of the pool is left
  * as it is (SPEC_DEV_BAD_PAGE). */
 int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
                        const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream);

@@ -770,9 +770,18 @@ class Pages:
 
     def waiting(self) -> torch.Tensor:
         """bool [B], on the device: sequences that sit the pass out after the last reservation (not enough pages, no
-        room, or no slots asked for), or hold no page at all."""
-        last = self.kv.table.gather(1, (self.mapped - 1).clamp_(0, self.kv.max_pages - 1).long()[:, None])[:, 0]
-        return (self.mapped <= 0) | (last <= -2 - PAGES_OUT)
+        room, no slots asked for, or, in 8 bits, rows of one that waits in the block of the next slot), or hold no page
+        at all."""
+        kv = self.kv
+        entry = lambda j: kv.table.gather(1, j.clamp(0, kv.max_pages - 1).long()[:, None])[:, 0]
+        last = entry(self.mapped - 1)
+        out = last <= -2 - PAGES_OUT
+        wait = out | (self.mapped <= 0)
+        if isinstance(kv, KV8Cache):
+            same = out & (entry(kv.len // PAGE_SLOTS)[:, None] == -2 - PAGES_OUT - last)
+            rows = kv.len > (kv.len - kv.len % KV8_BLOCK)[:, None]
+            wait |= (kv.len % PAGE_SLOTS > 0) & (same & rows).any(1)
+        return wait
 
     def _device(self, ws) -> int:
         """The books' device, on which the cache's buffers and the workspace lie too."""

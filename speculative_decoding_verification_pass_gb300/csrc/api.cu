@@ -763,6 +763,7 @@ static int verify_forward_impl(const spec_model* m, const int32_t* d_tokens, con
   ep.kv_table = pg.table;  // checked for every slot of the pass, whichever cache it holds
   ep.kv_max_pages = pg.max_pages;
   ep.kv_n_pages = pg.n_pages;
+  ep.kv8 = k8 != nullptr;
   SPEC_CUDA(launch_embed(ep, st, pdl));
 
   GemmParams g0{};
@@ -1580,7 +1581,10 @@ int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) 
 int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws, void* stream) {
   if (const int r = kv8_checks(nullptr, kv)) return r;
   if (!aligned4(d_n_accepted) || !aligned4(d_ws)) return SPEC_EINVAL;
-  return truncate_impl(kv->len, kv->batch, kv->table, kv->max_pages, d_n_accepted, gamma, d_ws, stream);
+  if (!d_n_accepted || !d_ws || gamma < 0) return SPEC_EINVAL;
+  SPEC_CUDA(launch_kv8_truncate(kv->len, d_n_accepted, kv->batch, gamma, kv->table, kv->max_pages,
+                                static_cast<int32_t*>(d_ws), static_cast<cudaStream_t>(stream)));
+  return SPEC_OK;
 }
 
 int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv, const int32_t* d_path,

@@ -91,5 +91,22 @@ SPEC_DEVINL int32_t kv8_fit_warp(int L, int n, const int32_t* table, int max_pag
   return 0;
 }
 
+// A sequence that sits out for want of a page (see spec_pages_reserve) may hold rows on the partly filled page
+// that another goes on with.  Rows are added behind them, but a block's scale that grows re-rounds the rows of
+// its block: a block of which a waiting sequence holds rows is not written to.
+// Do waiting sequences, of the `step` from `first` on, hold slots past `from` (b's own numbers) on the page of b's
+// slot `slot`?
+SPEC_DEVINL bool kv8_waited_for(const int32_t* table, const int32_t* len, int B, int max_pages, int b, int slot,
+                                int from, int first, int step) {
+  const int col = slot / kPageSlots, own = table[static_cast<long long>(b) * max_pages + col];
+  if (own < 0 || own >= SPEC_PAGES_OUT) return false;
+  bool any = false;
+#pragma unroll 4
+  for (int s = first; s < B; s += step)
+    any |= table[static_cast<long long>(s) * max_pages + col] == sat_out(own) && len[s] > from;
+  return any;
+}
+SPEC_DEVINL int kv8_block_of(int slot) { return slot < 0 ? 0 : slot / kKv8Block * kKv8Block; }
+
 }  // namespace
 }  // namespace spec

@@ -3,6 +3,7 @@
 // generator, and constant tables.
 #include "common.cuh"
 #include "internal.h"
+#include "kv8_common.cuh"
 
 namespace spec {
 
@@ -21,9 +22,21 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedParams p) {
   const int m = blockIdx.x;
   if (m == 0) {
     for (int i = threadIdx.x; i < p.n_counters; i += blockDim.x) p.counters[i] = 0;
+    // (a sequence that waits for a page keeps another from writing to the rows they share, see kv8_waited_for)
+    bool waits = false;
+    if (p.kv8)
+      for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
+        const int L = p.len[b];
+        waits |= L > 0 && L <= p.cap &&
+                 sits_out(p.kv_table[static_cast<long long>(b) * p.kv_max_pages + (L - 1) / kPageSlots]);
+      }
+    waits = p.kv8 && __syncthreads_or(waits);
     for (int b = threadIdx.x; b < p.B; b += blockDim.x) {
       const int L = p.len[b];
-      const int32_t bad = seq_fit(L, p.n, p.cap, p.kv_table, p.kv_max_pages, p.kv_n_pages, b);
+      int32_t bad = seq_fit(L, p.n, p.cap, p.kv_table, p.kv_max_pages, p.kv_n_pages, b);
+      if (!bad && waits && L % kPageSlots &&
+          kv8_waited_for(p.kv_table, p.len, p.B, p.kv_max_pages, b, L, kv8_block_of(L), 0, 1))
+        bad = SPEC_DEV_BAD_PAGE;
       p.pos_base[b] = L < 0 ? 0 : L;
       p.seq_ok[b] = bad ? 0 : 1;
       if (!bad)

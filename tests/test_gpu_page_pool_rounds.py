@@ -258,3 +258,83 @@ def test_short_pools_against_the_model(B, N, P):
         assert kv.table.tolist() == m.table() and kv.len.tolist() == m.len
         assert pages.ref.tolist() == m.ref() and pages.n_free.item() == m.ref().count(0)
     assert served > B and refused > B
+
+
+def _shared_and_short(kv8, slots):
+    """A prompt in two sequences that share a partly filled page, a third that fills the pool, and a reservation that has
+    no page for the second's copy."""
+    full = -(-slots // 64)
+    r = Round(kv8, 3, full + 1, 4)
+    r.reserve([slots, 0, 64])
+    r.forward(_tokens(6, 3, slots))  # (sequences 1 and 2 have no room for it)
+    r.status()
+    assert r.kv.len.tolist() == [slots, 0, 0]
+    sb.spec_pages_fork(r.pages, _ints([0]), _ints([1]), r.ws)
+    r.kv.len[2] = 59
+    r.reserve(5)
+    assert r.status() == sb.DEV_NO_PAGES
+    return r
+
+
+def _layer(r, scale, n=5):
+    """Rows of one layer put in by hand: their queries' output is of no account."""
+    d, kvd = CFG.d_model, CFG.d_model // CFG.n_heads * CFG.n_kv_heads
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q, k, v = (scale * torch.randn(3 * n, w, device="cuda", generator=g) for w in (d, kvd, kvd))
+    q_out = torch.empty(3 * n, d, dtype=torch.bfloat16, device="cuda")
+    rope = sb.RopeTable(CFG.head_dim, CFG.rope_theta)
+    for layer in range(CFG.n_layers):
+        sb.spec_kv8_append(CFG, r.kv, layer, n, q, k, v, rope, q_out, r.ws)
+
+
+@pytest.mark.parametrize("slots", [100, 70, 79])
+def test_8_bit_rows_of_a_waiting_sequence_are_not_rounded_again(slots):
+    """The first of two forks keeps the page they share; the other waits for a copy.  Larger values behind its rows
+    would change their block's scale: neither a pass nor an append by hand touches them, and the first waits too."""
+    r = _shared_and_short(True, slots)
+    assert r.pages.waiting().tolist() == [True, True, False]
+    before = r.bytes_of(1, slots)
+    r.forward(_tokens(7, 3, 5))
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 64]
+    r.truncate([0, 0, 4], 4)
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 64]
+    sb.spec_kv8_tree_commit(CFG, r.kv, _ints([[1, 3, -1, -1, -1]] * 3), _ints([2, 2, 0]), 5, r.ws)
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 60]
+    for scale in (1e-3, 1e6):
+        _layer(r, scale)
+        sb.spec_kv8_advance(r.kv, 1, r.ws)
+        assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist()[:2] == [slots, slots]
+        assert _same(before, r.bytes_of(1, slots)) and _same(before, r.bytes_of(0, slots))
+    # pages for both
+    sb.spec_pages_free(r.pages, _ints([2]), r.ws)
+    r.reserve([5, 5, 0])
+    assert r.status() == 0 and r.pages.waiting().tolist() == [False, False, True]
+    assert _same(before, r.bytes_of(0, slots)) and _same(before, r.bytes_of(1, slots))
+    z = r.forward(_tokens(8, 3, 5))
+    assert r.kv.len.tolist() == [slots + 5, slots + 5, 0]
+    # the same in a pool that was never short
+    a = Round(True, 3, 12, 4)
+    a.reserve([slots, slots, 0])
+    a.forward(_ints([_tokens(6, 3, slots)[0].tolist()] * 3))
+    a.reserve([5, 5, 0])
+    assert torch.equal(a.forward(_tokens(8, 3, 5))[:2], z[:2])
+    r.close()
+    a.close()
+
+
+@pytest.mark.parametrize("kv8,slots", [(True, 96), (True, 80), (False, 100), (False, 79)])
+def test_rows_of_a_waiting_sequence_in_blocks_of_their_own(kv8, slots):
+    """Where no scale is shared (a new block, or bf16) the keeper of the page goes on."""
+    r = _shared_and_short(kv8, slots)
+    assert r.pages.waiting().tolist() == [False, True, False]
+    before = r.bytes_of(1, slots)
+    for accepted in (3, 1):
+        r.forward(_tokens(9, 3, 5))
+        assert r.status() == sb.DEV_BAD_PAGE
+        r.truncate([accepted, 0, 0], 4)
+        assert r.status() == sb.DEV_BAD_PAGE
+        r.reserve([5, 5, 0])
+        assert r.status() == sb.DEV_NO_PAGES
+        assert _same(before, r.bytes_of(1, slots))
+    assert r.kv.len.tolist()[:2] == [slots + 6, slots]
+    r.close()
