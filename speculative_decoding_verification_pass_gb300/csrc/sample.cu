@@ -15,7 +15,7 @@
 // (2^-35 of about the largest): sums are exact and the same in any order.  What
 // is left is a weight's own error.  z c (c = log2(e) / T in two parts) is taken
 // with its rounding error by an fma, whole powers leave exactly, and 2^g - 1 is
-// added to 1 as an integer, so that a weight is off by about 2^-26 of itself
+// added to 1 as an integer, so that a weight is off by at most 2^-23.6 of itself
 // (a plain exp2f((z - M) c) by 2^-20 at z - M = -20 T): few draws lie near enough
 // to a border to differ from the same draws in 64 bits.
 //
@@ -683,7 +683,11 @@ struct Row {
       return min(static_cast<int>((M - v) * per), kFar);
     }
     // (MASS) the weight in a bin's middle, in 2^-36 of the largest
-    SPEC_DEVINL float middle(int b) const { return exp2f(36.f - (static_cast<float>(b) + shift) * (1.f / kPerBit)); }
+    SPEC_DEVINL float middle(int b) const {
+      float w;  // (2^7 to 2^36: no number that a plain exp2f would have to look out for)
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(36.f - (static_cast<float>(b) + shift) * (1.f / kPerBit)));
+      return w;
+    }
     // The values between which bin b lies, but for rounding (slack: in bins).
     SPEC_DEVINL float upper(int b, float slack) const {
       if (b <= 0) return INFINITY;
@@ -700,7 +704,7 @@ struct Row {
   SPEC_DEVINL Fine fine_bins(float span) const {
     Fine f;
     f.M = w.M;
-    f.per = MASS ? fminf(w.c_hi, 1e28f) * kPerBit : (span > 0.f && span < 1e30f ? (kFine / 8) / span : 0.f);
+    f.per = MASS ? fminf(w.c_hi, 1e28f) * kPerBit : (span > 0.f && span < 1e30f ? fminf((kFine / 8) / span, 1e30f) : 0.f);
     f.by_sum = !(MASS && w.wide) && fabsf(w.M) * f.per < 3.2e6f && f.per > 1e-25f;
     f.far = f.by_sum ? w.M - __fdividef(static_cast<float>(kFar), f.per) : 0.f;
     f.b0 = __float_as_int(fmaf(w.M, f.per, kRound));
@@ -1158,7 +1162,7 @@ struct Row {
       write_single(row, -1);
       return;
     }
-    if (rs.T == 0.f) {  // the lowest id of the largest
+    if (rs.T < 1.17549435e-38f) {  // (or what would be a subnormal) the lowest id of the largest
       each1([&](int x, float v) {
         if (v == M) atomicMin(&s.lo, static_cast<unsigned>(x));
       });
@@ -1175,7 +1179,8 @@ struct Row {
     w.M = M;
     w.c_hi = c_hi;
     w.c_lo = __fdiv_rn(fmaf(-c_hi, rs.T, 1.44269502f) + 1.92596303e-8f, rs.T);
-    w.wide = !(far < 30000.f) || !(c_hi < 1e30f) || !(c_hi > 1e-25f);
+    // (c below 2^96: the paired steps take a subnormal z as 0, which moves a power by less than 2^-30)
+    w.wide = !(far < 30000.f) || !(c_hi < 7.9e28f) || !(c_hi > 1e-25f);
     w.zlow = w.wide ? 0.f : M - __fdividef(150.f, c_hi);
     w.n0 = __float_as_int(fmaf(M, c_hi, kRound));
     const bool top_k = rs.k > 0 && rs.k < V, top_p = rs.top_p < 1.f, few_k = top_k && rs.k <= nw;
