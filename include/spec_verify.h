@@ -337,8 +337,8 @@ typedef struct {
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
  *               (spec_accept's d_draft_probs); never over the logits.
  * Weights are summed in fixed point, exactly and in any order: a weight is off by
- * about 2^-26 of itself and by 2^-36 of the row's largest, and what
- * is below that is not drawn; probabilities are off by a few fp32 roundings.  The
+ * at most 2^-23.6 of itself and 2^-36 of the row's largest, and what is below
+ * that is not drawn; probabilities are off by at most 2^-21.4 of themselves.  The
  * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
  * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and
  * SPEC_DEV_BAD_PARAM.  Limits: rows <= 65535, vocab <= 262144.  d_ws: any
