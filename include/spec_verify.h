@@ -519,9 +519,9 @@ int spec_rope_table(const spec_rope_config* rope, float* d_table, void* stream);
  * slots pass the capacity or lie on a page id outside the pool sets
  * SPEC_DEV_KV_OVERFLOW / SPEC_DEV_BAD_PAGE and gets nothing written to the
  * cache (its q_out is unspecified).  Where a sequence that sits out (device page
- * pool) holds rows of the same block, the block's scale and those rows stay as they
- * are: new rows that need a larger one set SPEC_DEV_BAD_PAGE and are held as
- * +-448 s at most (spec_kv8_advance does not count them).  1 <= n <= 128. */
+ * pool) holds rows of the same block and its scale would grow, the block stays as it
+ * is and the sequence sits out too (SPEC_DEV_BAD_PAGE; later layers get nothing, and
+ * spec_kv8_advance leaves it).  1 <= n <= 128. */
 int spec_kv8_append(const spec_model_config* cfg, const spec_kv8_cache* kv, int layer, int n,
                     const void* d_q, int64_t q_ld, const void* d_k, int64_t k_ld, const void* d_v,
                     int64_t v_ld, int is_f32, const int32_t* d_depth,
@@ -651,10 +651,12 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * spec_kv8_tree_commit leave their lengths and rows (SPEC_DEV_BAD_PAGE).  So a
  * round may go on behind a short pool: what the pass and the acceptance put out
  * for a marked sequence is of no account, and the next reservation tries it again
- * at the length that it had.  In an 8-bit pool one that keeps a partly filled
- * page waits too (SPEC_DEV_BAD_PAGE from passes, spec_kv8_advance and the rollbacks;
- * it is not marked) while a marked sequence holds rows of the 16 slots that its next
- * slot is in, whose scale its new rows could change.  A sequence with pages that are not of the pool is left
+ * at the length that it had.  In an 8-bit pool one that keeps a partly filled page
+ * may have to wait too: while a marked sequence holds rows of the 16 slots that its
+ * next slot is in, whose scale new rows could change, spec_verify_forward_kv8 marks
+ * and refuses it in the same way, and spec_kv8_append does where the scale would
+ * grow.  (These alone write to the table besides the calls of the pool, and only
+ * there.)  A sequence with pages that are not of the pool is left
  * as it is (SPEC_DEV_BAD_PAGE). */
 int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
                        const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream);

@@ -1581,10 +1581,7 @@ int spec_kv8_advance(const spec_kv8_cache* kv, int n, void* d_ws, void* stream) 
 int spec_kv8_truncate(const spec_kv8_cache* kv, const int32_t* d_n_accepted, int gamma, void* d_ws, void* stream) {
   if (const int r = kv8_checks(nullptr, kv)) return r;
   if (!aligned4(d_n_accepted) || !aligned4(d_ws)) return SPEC_EINVAL;
-  if (!d_n_accepted || !d_ws || gamma < 0) return SPEC_EINVAL;
-  SPEC_CUDA(launch_kv8_truncate(kv->len, d_n_accepted, kv->batch, gamma, kv->table, kv->max_pages,
-                                static_cast<int32_t*>(d_ws), static_cast<cudaStream_t>(stream)));
-  return SPEC_OK;
+  return truncate_impl(kv->len, kv->batch, kv->table, kv->max_pages, d_n_accepted, gamma, d_ws, stream);
 }
 
 int spec_kv8_tree_commit(const spec_model_config* cfg, const spec_kv8_cache* kv, const int32_t* d_path,

@@ -407,8 +407,6 @@ struct Kv8CommitParams {
 cudaError_t launch_kv8_commit(const Kv8CommitParams& p, cudaStream_t stream);
 cudaError_t launch_kv8_advance(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,
                                int32_t* status, cudaStream_t stream);
-cudaError_t launch_kv8_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, const int32_t* table,
-                                int max_pages, int32_t* status, cudaStream_t stream);
 cudaError_t launch_kv8_rope(float2* dst, int rd, double theta, double factor, double low, double high, int orig_len,
                             cudaStream_t stream);
 

@@ -220,12 +220,16 @@ __global__ void __launch_bounds__(kAppThreads) kv8_append_kernel(const Kv8Append
 #pragma unroll
   for (int k = 0; k < kAppWarps; ++k) amax = fmaxf(amax, s_max[k]);
   uint8_t* codes = (which ? p.vc : p.kc) + map.row(page, h, slot0);
-  float s_new = kv8_scale(amax);
-  // (a pass looks at this once, before its layers)
+  const float s_new = kv8_scale(amax);
+  // (A whole pass looks at this once, before its layers.  `page` was read before another CTA of the sequence may
+  // have marked it.)
   if (kept && s_new > s_held && !p.seq_ok &&
-      __syncthreads_or(kv8_waited_for(p.table, p.base, p.B, p.max_pages, b, L, slot0, threadIdx.x, kAppThreads))) {
-    s_new = s_held;  // rows that a waiting sequence holds stay as they are; the new ones do not count (no advance)
-    if (threadIdx.x == 0) set_status(p.status, SPEC_DEV_BAD_PAGE);
+      __syncthreads_or(kv8_waited_for(p.table, p.base, p.B, p.max_pages, page, L, threadIdx.x, kAppThreads))) {
+    if (threadIdx.x == 0) {
+      set_status(p.status, SPEC_DEV_BAD_PAGE);
+      kv8_sit_out(p.table, p.max_pages, b, L);
+    }
+    return;
   }
   const float s = kept ? fmaxf(s_new, s_held) : s_new;
   const float s_old = kept ? s_held : s;
@@ -286,12 +290,7 @@ SPEC_DEVINL int32_t kv8_path_bad(const Kv8CommitParams& p, int b, int len, int m
   if (__any_sync(0xffffffffu, bad)) return SPEC_DEV_BAD_TREE;
   if (len < p.n) return SPEC_DEV_KV_OVERFLOW;
   int page;
-  if (const int32_t r = kv8_fit_warp(len - p.n, p.n, p.table, p.max_pages, p.n_pages, b, len - p.n, &page)) return r;
-  // a pass that was refused for a waiting sequence's rows: len is the length before it
-  return __any_sync(0xffffffffu, kv8_waited_for(p.table, p.len, p.B, p.max_pages, b, len - 1,
-                                                kv8_block_of(len - p.n), lane, 32))
-             ? SPEC_DEV_BAD_PAGE
-             : 0;
+  return kv8_fit_warp(len - p.n, p.n, p.table, p.max_pages, p.n_pages, b, len - p.n, &page);
 }
 
 template <int HD>
@@ -409,7 +408,6 @@ __global__ void kv8_advance_kernel(int32_t* len, const int32_t* table, int B, in
     bool out = false;
 #pragma unroll 4
     for (int j = lane; j < np; j += 32) out |= row[j] < 0 || row[j] >= n_pages;
-    if (L % kPageSlots) out |= kv8_waited_for(table, len, B, max_pages, b, L, kv8_block_of(L), lane, 32);
     if (__any_sync(0xffffffffu, out)) bad = SPEC_DEV_BAD_PAGE;
   }
   if (lane) return;
@@ -417,30 +415,6 @@ __global__ void kv8_advance_kernel(int32_t* len, const int32_t* table, int B, in
     set_status(status, bad);
   else
     len[b] = L + n;
-}
-
-// The rollback as truncate_kernel's; a warp per sequence, which sees whether the pass was refused for a waiting
-// sequence's rows as well.
-__global__ void kv8_truncate_kernel(int32_t* len, const int32_t* n_acc, int B, int gamma, const int32_t* table,
-                                    int max_pages, int32_t* status) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int b = blockIdx.x * (blockDim.x / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
-  if (b >= B) return;
-  const int n = n_acc[b], l = len[b];
-  int32_t bad = 0;
-  if (n < 0 || n > gamma) bad = SPEC_DEV_BAD_NACC;
-  if (!bad && l > 0 && l <= max_pages * kPageSlots &&
-      (sits_out(table[static_cast<long long>(b) * max_pages + (l - 1) / kPageSlots]) ||
-       __any_sync(0xffffffffu,
-                  kv8_waited_for(table, len, B, max_pages, b, l - 1, kv8_block_of(l - gamma - 1), lane, 32))))
-    bad = SPEC_DEV_BAD_PAGE;
-  if (!bad && l < gamma - n) bad = SPEC_DEV_KV_OVERFLOW;
-  if (lane) return;
-  if (bad)
-    set_status(status, bad);
-  else
-    len[b] = l - (gamma - n);
 }
 
 template <class... A>
@@ -481,13 +455,6 @@ cudaError_t launch_kv8_commit(const Kv8CommitParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
   }
   return launch_dep(kv8_commit_len_kernel, dim3((p.B + 3) / 4), 128, stream, p);
-}
-
-cudaError_t launch_kv8_truncate(int32_t* len, const int32_t* n_acc, int B, int gamma, const int32_t* table,
-                                int max_pages, int32_t* status, cudaStream_t stream) {
-  if (B == 0) return cudaSuccess;
-  return launch_dep(kv8_truncate_kernel, dim3((B + 3) / 4), 128, stream, len, n_acc, B, gamma, table, max_pages,
-                    status);
 }
 
 cudaError_t launch_kv8_advance(int32_t* len, const int32_t* table, int B, int n, int max_pages, int n_pages,

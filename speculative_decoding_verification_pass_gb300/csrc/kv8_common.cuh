@@ -93,20 +93,25 @@ SPEC_DEVINL int32_t kv8_fit_warp(int L, int n, const int32_t* table, int max_pag
 
 // A sequence that sits out for want of a page (see spec_pages_reserve) may hold rows on the partly filled page
 // that another goes on with.  Rows are added behind them, but a block's scale that grows re-rounds the rows of
-// its block: a block of which a waiting sequence holds rows is not written to.
-// Do waiting sequences, of the `step` from `first` on, hold slots past `from` (b's own numbers) on the page of b's
-// slot `slot`?
-SPEC_DEVINL bool kv8_waited_for(const int32_t* table, const int32_t* len, int B, int max_pages, int b, int slot,
-                                int from, int first, int step) {
-  const int col = slot / kPageSlots, own = table[static_cast<long long>(b) * max_pages + col];
-  if (own < 0 || own >= SPEC_PAGES_OUT) return false;
+// its block; so a block of which a waiting sequence holds rows keeps its scale, or the other sits out too.
+// Do waiting sequences (every `step`th from `first` on) hold rows of the block that a sequence's next slot L, on
+// page `own`, is in?
+SPEC_DEVINL bool kv8_waited_for(const int32_t* table, const int32_t* len, int B, int max_pages, int own, int L,
+                                int first, int step) {
+  if (L % kKv8Block == 0 || own < 0 || own >= SPEC_PAGES_OUT) return false;
   bool any = false;
 #pragma unroll 4
   for (int s = first; s < B; s += step)
-    any |= table[static_cast<long long>(s) * max_pages + col] == sat_out(own) && len[s] > from;
+    any |= table[static_cast<long long>(s) * max_pages + L / kPageSlots] == sat_out(own) &&
+           len[s] > L / kKv8Block * kKv8Block;
   return any;
 }
-SPEC_DEVINL int kv8_block_of(int slot) { return slot < 0 ? 0 : slot / kKv8Block * kKv8Block; }
+// Sequence b, whose next slot is L, sits out until a reservation serves it.  (Where one waits, a device page pool
+// keeps the table, so that it can be written to.)
+SPEC_DEVINL void kv8_sit_out(const int32_t* table, int max_pages, int b, int L) {
+  int32_t* e = const_cast<int32_t*>(table) + static_cast<long long>(b) * max_pages + L / kPageSlots;
+  if (*e >= 0) *e = sat_out(*e);
+}
 
 }  // namespace
 }  // namespace spec

@@ -35,8 +35,11 @@ __global__ void __launch_bounds__(256) embed_kernel(const EmbedParams p) {
       const int L = p.len[b];
       int32_t bad = seq_fit(L, p.n, p.cap, p.kv_table, p.kv_max_pages, p.kv_n_pages, b);
       if (!bad && waits && L % kPageSlots &&
-          kv8_waited_for(p.kv_table, p.len, p.B, p.kv_max_pages, b, L, kv8_block_of(L), 0, 1))
+          kv8_waited_for(p.kv_table, p.len, p.B, p.kv_max_pages,
+                         p.kv_table[static_cast<long long>(b) * p.kv_max_pages + L / kPageSlots], L, 0, 1)) {
         bad = SPEC_DEV_BAD_PAGE;
+        kv8_sit_out(p.kv_table, p.kv_max_pages, b, L);
+      }
       p.pos_base[b] = L < 0 ? 0 : L;
       p.seq_ok[b] = bad ? 0 : 1;
       if (!bad)

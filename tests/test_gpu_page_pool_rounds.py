@@ -287,24 +287,35 @@ def _layer(r, scale, n=5):
         sb.spec_kv8_append(CFG, r.kv, layer, n, q, k, v, rope, q_out, r.ws)
 
 
+@pytest.mark.parametrize("by_hand", [False, True])
 @pytest.mark.parametrize("slots", [100, 70, 79])
-def test_8_bit_rows_of_a_waiting_sequence_are_not_rounded_again(slots):
+def test_8_bit_rows_of_a_waiting_sequence_are_not_rounded_again(slots, by_hand):
     """The first of two forks keeps the page they share; the other waits for a copy.  Larger values behind its rows
-    would change their block's scale: neither a pass nor an append by hand touches them, and the first waits too."""
+    would change their block's scale: neither a pass nor appends by hand touch them, and the first waits too."""
     r = _shared_and_short(True, slots)
     assert r.pages.waiting().tolist() == [True, True, False]
     before = r.bytes_of(1, slots)
-    r.forward(_tokens(7, 3, 5))
-    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 64]
-    r.truncate([0, 0, 4], 4)
-    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 64]
-    sb.spec_kv8_tree_commit(CFG, r.kv, _ints([[1, 3, -1, -1, -1]] * 3), _ints([2, 2, 0]), 5, r.ws)
-    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, 60]
-    for scale in (1e-3, 1e6):
-        _layer(r, scale)
+    if by_hand:
+        _layer(r, 1e-3)  # (values that need no larger scale change nothing)
+        assert r.status() == sb.DEV_BAD_PAGE and r.kv.table[0].min() == -1
+        assert _same(before, r.bytes_of(1, slots))
+        _layer(r, 1e6)
         sb.spec_kv8_advance(r.kv, 1, r.ws)
-        assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist()[:2] == [slots, slots]
-        assert _same(before, r.bytes_of(1, slots)) and _same(before, r.bytes_of(0, slots))
+    else:
+        r.forward(_tokens(7, 3, 5))
+    assert r.status() == sb.DEV_BAD_PAGE
+    lens = [slots, slots, 60 if by_hand else 64]
+    assert r.kv.len.tolist() == lens and r.pages.waiting().tolist() == [True, True, False]
+    r.truncate([0, 0, 4], 4)
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == lens
+    sb.spec_kv8_tree_commit(CFG, r.kv, _ints([[1, 3, -1, -1, -1]] * 3), _ints([2, 2, 0]), 5, r.ws)
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist() == [slots, slots, lens[2] - 4]
+    assert _same(before, r.bytes_of(1, slots)) and _same(before, r.bytes_of(0, slots))
+    r.reserve([5, 5, 0])  # as short as before: tried again, the first keeps the page
+    assert r.status() == sb.DEV_NO_PAGES and r.kv.table[0].min() == -1
+    r.forward(_tokens(7, 3, 5))
+    assert r.status() == sb.DEV_BAD_PAGE and r.kv.len.tolist()[:2] == [slots, slots]
+    assert _same(before, r.bytes_of(1, slots)) and _same(before, r.bytes_of(0, slots))
     # pages for both
     sb.spec_pages_free(r.pages, _ints([2]), r.ws)
     r.reserve([5, 5, 0])
