@@ -351,7 +351,10 @@ int spec_sample(const void* d_logits, int64_t ld, int is_bf16, int rows, int voc
  * is kept, else -inf (both of one type; d_out may be d_logits with out_ld = ld).
  * Applied to the target's rows before spec_accept or spec_tree_accept (with the
  * same T, and top_p 1), whose drafts were drawn by spec_sample with the same
- * parameters: the truncation then is the same on both sides.  A row without a
+ * parameters: the truncation then is the same on both sides.  (What is kept stays
+ * z, not z / T, and an acceptance takes one T for its batch: top-k, top-p and min-p
+ * may differ by sequence within it, sequences of another T go to a call of their
+ * own.)  A row without a
  * logit above -inf, or with a set out of range, is copied (NaN as -inf) and sets
  * the status bit as above. */
 int spec_filter_logits(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab,
@@ -645,8 +648,8 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * pages of its length alone (they go to later ones that need fewer) and sets SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or
  * whose d_n is negative, keeps what it holds and sets SPEC_DEV_KV_OVERFLOW; one
  * whose d_n is 0 returns pages.  These sit the pass out: their last page is
- * marked in the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages has
- * nothing to mark), passes refuse them (SPEC_DEV_BAD_PAGE), nothing is written to
+ * marked in the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages, as one
+ * that was freed, has nothing to mark and nothing to lose), passes refuse them (SPEC_DEV_BAD_PAGE), nothing is written to
  * their pages, and spec_paged_kv_truncate, spec_kv8_truncate and
  * spec_kv8_tree_commit leave their lengths and rows (SPEC_DEV_BAD_PAGE).  So a
  * round may go on behind a short pool: what the pass and the acceptance put out

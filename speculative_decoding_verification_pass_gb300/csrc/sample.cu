@@ -1369,7 +1369,8 @@ cudaError_t launch_trunc(TruncParams p, int sms, cudaStream_t stream) {
   // every 512 groups: a row alone takes the less time the more share it.  Of so many rows that their CTAs
   // take turns, fewer: what a cluster's CTAs wait for one another costs more then than reading the row
   // again from the caches, and the more so the longer a row's chain of passes (a filter's is shorter).
-  // Rows of 128256, us with eight / four / two CTAs a row:
+  // fp32 rows of 128256, us with eight / four / two CTAs a row (bf16 rows go by the same rule, as they are
+  // kept as fp32: 320 of them 183, 184 and 156 us for the three lines below, with two, two and four CTAs):
   //                            38 rows           64                152               320
   //   draws, top-p alone       43 / 38 / 43      56 / 43 / 50      115 / 85 / 68     232 / 168 / 144
   //   draws, mixed, probs      31 / 38 / 52      43 / 40 / 53      91 / 83 / 85      163 / 129 / 136
