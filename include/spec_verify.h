@@ -337,8 +337,10 @@ typedef struct {
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
  *               (spec_accept's d_draft_probs); never over the logits.
  * Weights are summed in fixed point, exactly and in any order: a weight is off by
- * at most 2^-23.6 of itself and 2^-36 of the row's largest, and what is below
- * that is not drawn; probabilities are off by at most 2^-21.4 of themselves.  The
+ * at most 2^-23.6 of itself and 2^-35.5 of the row's largest, and what is below
+ * that is not drawn; probabilities are off by at most 2^-21.4 of themselves and,
+ * through the total, vocab x 2^-35.5 (a row of which one id outweighs all others by
+ * that much: its tail has no part in the total).  The
  * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
  * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and
  * SPEC_DEV_BAD_PARAM.  Limits: rows <= 65535, vocab <= 262144.  d_ws: any

@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import sample as OS
 from speculative_decoding_verification_pass_gb300 import binding as sb
 from speculative_decoding_verification_pass_gb300 import workloads as wl
 from test_gpu_sample import _cuda, _f32, _rows, check
@@ -96,3 +97,19 @@ def test_rows_whose_bins_are_by_difference(far):
     z = 2.0 * T[:, None] * g.standard_normal((len(par), V))
     z += (far * T * np.log(2.0) - z.max(1))[:, None]
     check(z.astype(np.float32), par, seed=6, draws=4)
+
+
+@pytest.mark.parametrize("V", [183325, 262144])
+@pytest.mark.parametrize("gap", [20.0, 24.0, 25.0, 25.8, 27.0, 40.0])
+def test_tails_below_the_units_of_the_sum(V, gap):
+    """One id and a quarter of a million others, each about a unit of the sum or less: half a unit, 2^-35.5 of the
+    largest, times V on the total, beside what a probability is off by itself."""
+    z = (0.2 * wl.rng(7, 65).standard_normal((2, V))).astype(np.float32)
+    z[:, 4] = gap
+    probs = torch.empty(2, V, device="cuda")
+    tok = torch.empty(2, 2, dtype=torch.int32, device="cuda")
+    sb.spec_sample(_cuda(z), sb.Sampling(), _cuda(np.float32([[0.5, 0.9], [0.1, 0.99]])), tok, sb.workspace(256),
+                   probs=probs)
+    for got, x in zip(probs.double().cpu().numpy(), z):
+        np.testing.assert_allclose(got, OS.truncate(x, 1.0).p, rtol=2.0 ** -21.4 + V * 2.0 ** -35.5)
+    assert gap < 24 or (tok == 4).all()
