@@ -778,9 +778,11 @@ class Pages:
         out = last <= -2 - PAGES_OUT
         wait = out | (self.mapped <= 0)
         if isinstance(kv, KV8Cache):
-            same = out & (entry(kv.len // PAGE_SLOTS)[:, None] == -2 - PAGES_OUT - last)
-            rows = kv.len > (kv.len - kv.len % KV8_BLOCK)[:, None]
-            wait |= (kv.len % PAGE_SLOTS > 0) & (same & rows).any(1)
+            top = kv.n_pages - 1  # of each page: the longest that waits for a copy of it
+            held = torch.zeros_like(self.ref).scatter_reduce_(0, (-2 - PAGES_OUT - last).clamp(0, top).long(),
+                                                              torch.where(out, kv.len, 0), "amax")
+            own = entry(kv.len // PAGE_SLOTS)
+            wait |= (own >= 0) & (held[own.clamp(0, top).long()] > kv.len - kv.len % KV8_BLOCK)
         return wait
 
     def _device(self, ws) -> int:

@@ -1,4 +1,4 @@
-"""The device page pool within rounds, on a GPU: passes right behind the calls
+"""The device page pool around passes, on a GPU: passes right behind the calls
 that write the tables, pools that run short in the middle of a round, and
 sequences that sit one out.
 """
