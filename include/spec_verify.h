@@ -336,13 +336,13 @@ typedef struct {
  *               id order, exceeds u * total;
  *   d_probs     fp32 rows, probs_ld apart, or NULL: the distribution drawn from
  *               (spec_accept's d_draft_probs); never over the logits.
- * Weights are summed in fixed point, exactly and in any order: a weight is off by
- * at most 2^-23.6 of itself and 2^-35.5 of the row's largest, and what is below
- * that is not drawn; probabilities are off by at most 2^-21.4 of themselves and,
- * through the total, vocab x 2^-35.5 (a row of which one id outweighs all others by
- * that much: its tail has no part in the total).  The
- * same call gives the same bits.  A row without a logit above -inf gets tokens -1,
- * probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and
+ * Weights are summed in fixed point, exactly and in any order: a weight is off
+ * by at most 2^-23.6 of itself and 2^-35.5 of the row's largest, and what is
+ * below that is not drawn; probabilities are off by at most 2^-21.4 of
+ * themselves and, through the total, vocab x 2^-35.5 (a row of which one id
+ * outweighs all others by that much: its tail has no part in the total).  The
+ * same call gives the same bits.  A row without a logit above -inf gets tokens
+ * -1, probabilities 0 and SPEC_DEV_EMPTY_MASK; a set out of range the same and
  * SPEC_DEV_BAD_PARAM.  Limits: rows <= 65535, vocab <= 262144.  d_ws: any
  * workspace of this library (its status word is used). */
 int spec_sample(const void* d_logits, int64_t ld, int is_bf16, int rows, int vocab, const spec_sampling* sampling,
@@ -647,30 +647,33 @@ int spec_pages_init(const spec_pages* pages, void* stream);
  * them (the lowest-numbered of equally long ones) keeps it.  n = 0 without d_n
  * only returns pages (after a rollback).
  * A sequence that the free pages left by those before it do not cover keeps the
- * pages of its length alone (they go to later ones that need fewer) and sets SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or
- * whose d_n is negative, keeps what it holds and sets SPEC_DEV_KV_OVERFLOW; one
- * whose d_n is 0 returns pages.  These sit the pass out: their last page is
- * marked in the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages, as one
- * that was freed, has nothing to mark and nothing to lose), passes refuse them (SPEC_DEV_BAD_PAGE), nothing is written to
- * their pages, and spec_paged_kv_truncate, spec_kv8_truncate and
- * spec_kv8_tree_commit leave their lengths and rows (SPEC_DEV_BAD_PAGE).  So a
- * round may go on behind a short pool: what the pass and the acceptance put out
- * for a marked sequence is of no account, and the next reservation tries it again
- * at the length that it had.  In an 8-bit pool one that keeps a partly filled page
- * may have to wait too: while a marked sequence holds rows of the 16 slots that its
- * next slot is in, whose scale new rows could change, spec_verify_forward_kv8 marks
- * and refuses it in the same way, and spec_kv8_append does where the scale would
- * grow.  (These alone write to the table besides the calls of the pool, and only
- * there.)  A sequence with pages that are not of the pool is left
- * as it is (SPEC_DEV_BAD_PAGE). */
+ * pages of its length alone (they go to later ones that need fewer) and sets
+ * SPEC_DEV_NO_PAGES; one that the slots would take past the capacity, or whose
+ * d_n is negative, keeps what it holds and sets SPEC_DEV_KV_OVERFLOW; one whose
+ * d_n is 0 returns pages.  These sit the pass out: their last page is marked in
+ * the table (-2 - SPEC_PAGES_OUT - page; a sequence without pages, as one that
+ * was freed, has nothing to mark and nothing to lose), passes refuse them
+ * (SPEC_DEV_BAD_PAGE), nothing is written to their pages, and
+ * spec_paged_kv_truncate, spec_kv8_truncate and spec_kv8_tree_commit leave their
+ * lengths and rows (SPEC_DEV_BAD_PAGE).  So a round may go on behind a short
+ * pool: what the pass and the acceptance put out for a marked sequence is of no
+ * account, and the next reservation tries it again at the length that it had.
+ * In an 8-bit pool one that keeps a partly filled page may have to wait too:
+ * while a marked sequence holds rows of the 16 slots that its next slot is in,
+ * whose scale new rows could change, spec_verify_forward_kv8 marks and refuses
+ * it in the same way, and spec_kv8_append does where the scale would grow.
+ * (These alone write to the table besides the calls of the pool, and only
+ * there.)  A sequence with pages that are not of the pool is left as it is
+ * (SPEC_DEV_BAD_PAGE). */
 int spec_pages_reserve(const spec_model_config* cfg, const spec_pages* pages, const spec_page_data* data, int n,
                        const int32_t* d_n, void* d_ws, size_t ws_bytes, void* stream);
 
 /* Sequence d_dst[i] becomes a second d_src[i], i < n <= 65535: it returns its pages and
  * shares the source's up to its length.  Nothing is copied until one of them is
  * reserved for; a partly filled last page is marked in both rows as not to be
- * written to until then (a source that sits passes out: its second does too).  Pairs out of range, to itself, with a destination
- * given twice or one that is a source too, are left out (SPEC_DEV_BAD_SEQ). */
+ * written to until then (a source that sits passes out: its second does too).
+ * Pairs out of range, to itself, with a destination given twice or one that is a
+ * source too, are left out (SPEC_DEV_BAD_SEQ). */
 int spec_pages_fork(const spec_pages* pages, int n, const int32_t* d_src, const int32_t* d_dst, void* d_ws,
                     size_t ws_bytes, void* stream);
 
